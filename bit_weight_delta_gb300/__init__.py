@@ -12,7 +12,9 @@ bf16 tensors are torch.bfloat16; the packed sign matrix is torch.uint8
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 
 import torch
@@ -46,6 +48,11 @@ CACHE_EXPORTED = (
 KMERGE_EXPORTED = (
     "bd_kmerge_create", "bd_kmerge_destroy", "bd_kmerge_request", "bd_kmerge_commit",
     "bd_kmerge_entry_of", "bd_kmerge_entry_info", "bd_kmerge_get_stats",
+)
+
+BLOCK_EXPORTED = (
+    "bitdelta_add_norm", "bitdelta_kv_append", "bitdelta_attention_plan_bytes",
+    "bitdelta_attention_plan", "bitdelta_attention_workspace_bytes", "bitdelta_attention",
 )
 
 
@@ -135,6 +142,17 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.bd_kmerge_get_stats.argtypes = [p, ctypes.POINTER(_KMergeStats)]
     for name in KMERGE_EXPORTED:
         getattr(lib, name).restype = st
+    f32 = ctypes.c_float
+    lib.bitdelta_add_norm.argtypes = [p, i64, i64, p, p, st, p, i64, f32, f32, p, p, i32, p, p,
+                                      i32, p, p]
+    lib.bitdelta_kv_append.argtypes = [p, p, p, i64, i32, st, p, p, p, p]
+    lib.bitdelta_attention_plan.argtypes = [p, p, sz, p]
+    lib.bitdelta_attention.argtypes = [p, p, sz, p, p, p, f32, p, p, p, sz, p]
+    for name in BLOCK_EXPORTED:
+        getattr(lib, name).restype = st
+    for name in ("bitdelta_attention_plan_bytes", "bitdelta_attention_workspace_bytes"):
+        getattr(lib, name).argtypes = [p]
+        getattr(lib, name).restype = sz
     _lib = lib
     return lib
 
@@ -574,3 +592,213 @@ class KMergePool:
             self.close()
         except Exception:
             pass
+
+
+# ------------------------------------------------------------------ decoder block
+
+
+def norm_table(weights):
+    """Device array of pointers to bf16 [d] norm weights: slot 0 the base
+    model's, slot v variant v's.  The returned tensor object keeps the weights
+    alive."""
+    weights = [_dev(w, torch.bfloat16, "norm weight") for w in weights]
+    table = torch.tensor([w.data_ptr() for w in weights], dtype=torch.int64,
+                         device=weights[0].device)
+    table.weights = weights
+    return table
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _on(stream):
+    """Outputs made inside a call belong to the stream that writes them."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _raw_stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def bitdelta_add_norm(y, residual=None, pre_table=None, post_table=None, gate=None,
+                      scale: float = 1.0, eps: float = 1e-5, seg_offsets=None, seg_variant=None,
+                      residual_out=None, out=None, stream=None):
+    """h = residual + scale·gate·b with b = y or RMSNorm(y; w_post), and
+    x = RMSNorm(h; w_pre), row by row of y [..., d].  Returns (h, x).
+
+    pre_table / post_table come from norm_table(); with seg_offsets and
+    seg_variant (int32, as in bitdelta_linear_grouped) a row takes its
+    segment's variant's weights, else slot 0.  Rows of no segment are not
+    written.  residual: bf16 or fp32 (None: zero, h is then bf16); gate: bf16
+    [d] or like y.  residual_out may be residual itself."""
+    _dev(y, torch.bfloat16, "y")
+    if pre_table is None:
+        raise ValueError("pre_table is required")
+    d = y.shape[-1]
+    rows = y.numel() // d if d else 0
+    rtype = torch.bfloat16 if residual is None else residual.dtype
+    if rtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"residual must be bfloat16 or float32, got {rtype}")
+    for t, name in ((residual, "residual"), (residual_out, "residual_out")):
+        if t is not None and _dev(t, rtype, name).shape != y.shape:
+            raise ValueError(f"{name} must have the shape of y")
+    if out is not None and _dev(out, torch.bfloat16, "out").shape != y.shape:
+        raise ValueError("out must have the shape of y")
+    gate_stride = 0
+    if gate is not None:
+        _dev(gate, torch.bfloat16, "gate")
+        if gate.shape == y.shape and gate.dim() > 1:
+            gate_stride = d
+        elif gate.shape != (d,):
+            raise ValueError("gate must be [d] or have the shape of y")
+    _dev(pre_table, torch.int64, "pre_table")
+    n_tab = pre_table.numel()
+    if post_table is not None and _dev(post_table, torch.int64, "post_table").numel() != n_tab:
+        raise ValueError("pre_table and post_table must have the same number of slots")
+    n_seg = 0
+    if (seg_offsets is None) != (seg_variant is None):
+        raise ValueError("seg_offsets and seg_variant go together")
+    if seg_offsets is not None:
+        n_seg = _dev(seg_variant, torch.int32, "seg_variant").numel()
+        if _dev(seg_offsets, torch.int32, "seg_offsets").numel() != n_seg + 1:
+            raise ValueError("seg_offsets must have one entry more than seg_variant")
+    with _on(stream):
+        if residual_out is None:
+            residual_out = torch.empty_like(y, dtype=rtype)
+        if out is None:
+            out = torch.empty_like(y)
+    code = load().bitdelta_add_norm(
+        y.data_ptr(), rows, d, _addr(residual), residual_out.data_ptr(),
+        1 if rtype is torch.float32 else 0, _addr(gate), gate_stride, scale, eps,
+        pre_table.data_ptr(), _addr(post_table), n_tab, _addr(seg_offsets), _addr(seg_variant),
+        n_seg, out.data_ptr(), _raw_stream(stream))
+    if code:
+        _check("bitdelta_add_norm", code)
+    return residual_out, out
+
+
+class _AttentionBatch(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int64), ("n_seq", ctypes.c_int32),
+                ("max_q_len", ctypes.c_int32), ("max_kv_len", ctypes.c_int32),
+                ("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_pages", ctypes.c_int64), ("table_stride", ctypes.c_int64),
+                ("seq_offsets", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("n_group", ctypes.c_int32),
+                ("group_offsets", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p)]
+
+
+class AttentionBatch:
+    """A step's sequences over a page table, and the attention's plan for them.
+
+    seq_offsets int32 [n_seq+1], kv_len int32 [n_seq] (keys including the
+    step's own tokens) and page_table int32 [n_seq, width] are CUDA tensors;
+    group_offsets int32 [n_group+1] and prefix_len int32 [n_group] name
+    consecutive sequences that share their first positions' pages.  The
+    constructor computes the plan (stream-ordered, on the device); it holds for
+    every layer of the step.  After writing new lengths into the same tensors,
+    call plan() again.  The batch owns one workspace: attention calls that can
+    overlap on the GPU need batches of their own."""
+
+    def __init__(self, seq_offsets, kv_len, page_table, n_tokens: int, max_q_len: int,
+                 max_kv_len: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
+                 page_size: int, group_offsets=None, prefix_len=None, stream=None):
+        n_seq = _dev(kv_len, torch.int32, "kv_len").numel()
+        if _dev(seq_offsets, torch.int32, "seq_offsets").numel() != n_seq + 1:
+            raise ValueError("seq_offsets must have one entry more than kv_len")
+        _dev(page_table, torch.int32, "page_table")
+        if page_table.dim() != 2 or page_table.shape[0] != n_seq:
+            raise ValueError("page_table must be [n_seq, pages]")
+        if (group_offsets is None) != (prefix_len is None):
+            raise ValueError("group_offsets and prefix_len go together")
+        n_group = 0
+        if group_offsets is not None:
+            n_group = _dev(prefix_len, torch.int32, "prefix_len").numel()
+            if _dev(group_offsets, torch.int32, "group_offsets").numel() != n_group + 1:
+                raise ValueError("group_offsets must have one entry more than prefix_len")
+        self._keep = (seq_offsets, kv_len, page_table, group_offsets, prefix_len)
+        self.head_dim, self.n_q_heads, self.n_kv_heads = head_dim, n_q_heads, n_kv_heads
+        self.page_size, self.n_tokens = page_size, n_tokens
+        self._c = _AttentionBatch(
+            n_tokens, n_seq, max_q_len, max_kv_len, n_q_heads, n_kv_heads, head_dim, page_size, 0,
+            page_table.shape[1], seq_offsets.data_ptr(), kv_len.data_ptr(),
+            page_table.data_ptr(), n_group, _addr(group_offsets), _addr(prefix_len))
+        self._ref = ctypes.addressof(self._c)
+        lib = load()
+        with _on(stream):
+            self._plan = torch.empty(lib.bitdelta_attention_plan_bytes(self._ref),
+                                     dtype=torch.uint8, device=kv_len.device)
+            self._ws = torch.empty(lib.bitdelta_attention_workspace_bytes(self._ref),
+                                   dtype=torch.uint8, device=kv_len.device)
+        self._plan_args = (self._plan.data_ptr(), self._plan.numel())
+        self._ws_args = (self._ws.data_ptr(), self._ws.numel())
+        self._q_shape = (n_tokens, n_q_heads, head_dim)
+        self._qkv_shape = (n_tokens, (n_q_heads + 2 * n_kv_heads) * head_dim)
+        self._scale = 1.0 / math.sqrt(head_dim) if head_dim > 0 else 1.0
+        self.plan(stream)
+
+    def plan(self, stream=None) -> None:
+        """Compute the plan from the lengths now in the batch's tensors."""
+        _check("bitdelta_attention_plan", load().bitdelta_attention_plan(
+            self._ref, *self._plan_args, _raw_stream(stream)))
+
+    def _cache(self, k_pages, v_pages) -> None:
+        _dev(k_pages, torch.bfloat16, "k_pages")
+        _dev(v_pages, torch.bfloat16, "v_pages")
+        if (k_pages.shape != v_pages.shape or
+                k_pages.shape[1:] != (self.n_kv_heads, self.page_size, self.head_dim)):
+            raise ValueError("k_pages and v_pages must be [n_pages, n_kv_heads, page_size, "
+                             "head_dim]")
+        self._c.n_pages = k_pages.shape[0]
+
+
+def bitdelta_kv_append(batch: AttentionBatch, qkv, rope, k_pages, v_pages,
+                       interleaved: bool = False, out=None, stream=None):
+    """Rotates the query and key heads of qkv [n_tokens, (n_q_heads +
+    2·n_kv_heads)·head_dim] by their tokens' positions, appends keys and values
+    to the cache and returns the queries [n_tokens, n_q_heads, head_dim].
+
+    rope: fp32 [positions, rot_dim], cosines then sines (None: no rotation);
+    interleaved rotates neighbours (2i, 2i+1) instead of halves."""
+    if _dev(qkv, torch.bfloat16, "qkv").shape != batch._qkv_shape:
+        raise ValueError(f"qkv must be {batch._qkv_shape}")
+    batch._cache(k_pages, v_pages)
+    rows, rot = (0, 0) if rope is None else _dev(rope, torch.float32, "rope").shape
+    if out is None:
+        with _on(stream):
+            out = torch.empty(batch._q_shape, dtype=torch.bfloat16, device=qkv.device)
+    elif _dev(out, torch.bfloat16, "out").shape != batch._q_shape:
+        raise ValueError(f"out must be {batch._q_shape}")
+    code = load().bitdelta_kv_append(
+        batch._ref, qkv.data_ptr(), _addr(rope), rows, rot, 1 if interleaved else 0,
+        k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), _raw_stream(stream))
+    if code:
+        _check("bitdelta_kv_append", code)
+    return out
+
+
+def bitdelta_attention(batch: AttentionBatch, q, k_pages, v_pages, scale: float | None = None,
+                       out=None, lse=None, stream=None):
+    """Causal attention of q [n_tokens, n_q_heads, head_dim] over the cache.
+    Returns (out, lse): bf16 like q, and fp32 [n_tokens, n_q_heads].  scale
+    defaults to 1/sqrt(head_dim)."""
+    if _dev(q, torch.bfloat16, "q").shape != batch._q_shape:
+        raise ValueError(f"q must be {batch._q_shape}")
+    batch._cache(k_pages, v_pages)
+    with _on(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        elif _dev(out, torch.bfloat16, "out").shape != batch._q_shape:
+            raise ValueError(f"out must be {batch._q_shape}")
+        if lse is None:
+            lse = torch.empty(batch._q_shape[:2], dtype=torch.float32, device=q.device)
+        elif _dev(lse, torch.float32, "lse").shape != batch._q_shape[:2]:
+            raise ValueError(f"lse must be {batch._q_shape[:2]}")
+    code = load().bitdelta_attention(
+        batch._ref, *batch._plan_args, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+        batch._scale if scale is None else scale, out.data_ptr(), lse.data_ptr(),
+        *batch._ws_args, _raw_stream(stream))
+    if code:
+        _check("bitdelta_attention", code)
+    return out, lse

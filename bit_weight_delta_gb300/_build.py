@@ -19,7 +19,8 @@ BUILD_DIR = os.path.join(ROOT, "_build", "bitdelta")
 LIB_PATH = os.path.join(HERE, "libbitdelta.so")
 
 SOURCES = ["abi.cu", "compress.cu", "reconstruct.cu", "gemv.cu", "gemm_pair.cu", "cache.cu",
-           "kmerge.cu", "similarity.cu", "monosoup.cu"]
+           "kmerge.cu", "similarity.cu", "monosoup.cu", "add_norm.cu", "kv_append.cu",
+           "attention.cu"]
 HEADERS = ["common.cuh", "kernels.h", "gemm_common.cuh", "split_schedule.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
@@ -36,6 +37,7 @@ def _inputs_mtime() -> float:
     paths.append(os.path.join(INCLUDE, "bitdelta.h"))
     paths.append(os.path.join(INCLUDE, "bitdelta_cache.h"))
     paths.append(os.path.join(INCLUDE, "bitdelta_kmerge.h"))
+    paths.append(os.path.join(INCLUDE, "bitdelta_block.h"))
     paths.append(os.path.abspath(__file__))
     return max(os.path.getmtime(p) for p in paths)
 
