@@ -1,112 +1,532 @@
-// attention.cu — causal attention of ragged query runs over the paged cache
-// (bitdelta_attention) and its plan (bitdelta_attention_plan).
-//
-//   out[t, h] = Σ_{p ≤ pos(t)} softmax_p(scale · q[t, h]·k_p) · v_p
-//
-// One warp per token and query head: its lanes hold the head's elements, a
-// score is one warp reduction, and the running maximum m, denominator l and
-// sum o of the softmax are rescaled by 2^(m_old − m_new) as m grows, so every
-// key is visited once.
+// attention.cu — causal attention of ragged query runs over the paged cache:
+// the C entry points, the plan kernel and the combine kernel.  attention.cuh
+// says how the work is divided; attn_decode.cu and attn_tile.cu do it.
 #include <climits>
 #include <cmath>
 #include <cstdint>
 
-#include "bitdelta_block.h"
-#include "kernels.h"
+#include "attention.cuh"
 
 namespace bd {
 int check_attention_batch(const bd_attention_batch* b);
+
 namespace {
+size_t pad256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+bool off(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) != 0; }
+}  // namespace
 
-struct AttnArgs {
-  bd_attention_batch b;
-  const int32_t* tok_seq;
-  const uint16_t *q, *k_pages, *v_pages;
-  float scale_log2;
-  uint16_t* out;
-  float* lse;
-  DevCtx ctx;
-};
-
-size_t plan_bytes_of(const bd_attention_batch& b) {
-  return (static_cast<size_t>(b.n_tokens) * 4 + 255) & ~static_cast<size_t>(255);
+AttnLayout attn_layout(const bd_attention_batch& b, int num_sms) {
+  AttnLayout L{};
+  L.g = b.n_q_heads / b.n_kv_heads;
+  L.half_tok = kHalfRows / L.g;
+  const int64_t tile_tok = 2 * L.half_tok;
+  // Short runs have at most 16 rows (one mma.sync row tile), or 32 where a
+  // single token already has more than 16, or no sequence has more than 32.
+  const int64_t max_rows = static_cast<int64_t>(b.max_q_len) * L.g;
+  L.d_rows = L.g > 16 || (max_rows > 16 && max_rows <= 32) ? 32 : 16;
+  L.use_decode = true;  // every batch may hold short runs
+  L.use_tile = max_rows > L.d_rows || b.n_group > 0;
+  L.d_ctas = 2 * num_sms;
+  L.t_ctas = num_sms;
+  const int64_t T = b.n_tokens;
+  const int64_t long_seqs =
+      max_rows > L.d_rows ? (T * L.g / (L.d_rows + 1) < b.n_seq ? T * L.g / (L.d_rows + 1) : b.n_seq)
+                          : 0;
+  L.max_tiles = 0;
+  if (max_rows > L.d_rows) L.max_tiles += T / tile_tok + long_seqs;
+  const int64_t prefix_tiles = b.n_group > 0 ? T / tile_tok + b.n_group : 0;
+  L.max_tiles += prefix_tiles;
+  // pieces: at most one per tile plus one per CTA of the launch (the plan cuts
+  // tiles longer than the CTAs' even share)
+  L.max_entries = L.use_tile ? L.max_tiles + L.t_ctas : 0;
+  // slots: the pieces of cut tiles (at most two per CTA), with groups every
+  // prefix piece and every own piece of a member
+  L.t_slots = L.use_tile ? 2 * L.t_ctas + (b.n_group > 0 ? L.max_tiles * b.n_kv_heads : 0) : 0;
+  size_t o = pad256(sizeof(PlanHeader));
+  const auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += pad256(bytes);
+    return at;
+  };
+  L.o_tok_seq = take(4 * static_cast<size_t>(T));
+  L.o_seq = take(sizeof(SeqRec) * static_cast<size_t>(b.n_seq));
+  L.o_start = take(4 * static_cast<size_t>(L.d_ctas));
+  L.o_group = take(4 * static_cast<size_t>(b.n_group));
+  L.o_run = take(4 * (static_cast<size_t>(b.n_seq) + b.n_group + 1));
+  L.o_tile_slot = take(4 * static_cast<size_t>(L.max_tiles));
+  L.o_tile_ns = take(4 * static_cast<size_t>(L.max_tiles));
+  L.o_entry = take(sizeof(TileEntry) * static_cast<size_t>(L.max_entries));
+  L.o_comb = take(4 * static_cast<size_t>(T));
+  L.plan_bytes = o;
+  o = 0;
+  const size_t d_rows = static_cast<size_t>(L.d_ctas) * 2 * L.d_rows;
+  L.w_d_o = take(d_rows * b.head_dim * 4);
+  L.w_d_ml = take(d_rows * 8);
+  const size_t r_rows = b.n_group > 0 ? static_cast<size_t>(T) * b.n_q_heads : 0;
+  L.w_r_o = take(r_rows * b.head_dim * 4);
+  L.w_r_ml = take(r_rows * 8);
+  const size_t t_rows = static_cast<size_t>(L.t_slots) * 2 * kHalfRows;
+  L.w_t_o = take(t_rows * b.head_dim * 4);
+  L.w_t_ml = take(t_rows * 8);
+  L.ws_bytes = o;
+  return L;
 }
 
-// tok_seq[t]: the sequence of token t, −1 for a token of none.
-__global__ void plan_kernel(bd_attention_batch b, int32_t* tok_seq, DevCtx ctx) {
+namespace {
+
+// ------------------------------------------------------------------ plan
+
+constexpr int kPlanThreads = 1024;
+constexpr int kLenBuckets = 1024;
+
+// Exclusive prefix sum over the CTA; *total receives the sum.
+__device__ int64_t block_scan(int64_t v, int64_t* s_warp, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t inc = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t o = __shfl_up_sync(0xFFFFFFFFu, inc, off);
+    if (lane >= off) inc += o;
+  }
+  __syncthreads();  // s_warp of an earlier call has been read
+  if (lane == 31) s_warp[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t w = s_warp[lane];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t o = __shfl_up_sync(0xFFFFFFFFu, w, off);
+      if (lane >= off) w += o;
+    }
+    s_warp[lane] = w;
+  }
+  __syncthreads();
+  *total = s_warp[31];
+  return inc - v + (warp > 0 ? s_warp[warp - 1] : 0);
+}
+
+// One CTA.  Every phase walks sequences, runs or tiles with all threads; what
+// later kernels read is a function of the lengths alone (the order of equally
+// long pieces is not, and decides only which CTA runs them).
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
+  __shared__ int64_t s_warp[32];
+  __shared__ int s_hist[kLenBuckets];
+  __shared__ unsigned long long s_blocks;
+  __shared__ int s_comb;
+  const bd_attention_batch& b = p.b;
+  const AttnLayout& L = p.L;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kWarps = kPlanThreads / 32;
+  PlanHeader* hd = reinterpret_cast<PlanHeader*>(p.plan);
+  int32_t* tok_seq = reinterpret_cast<int32_t*>(p.plan + L.o_tok_seq);
+  SeqRec* seqs = reinterpret_cast<SeqRec*>(p.plan + L.o_seq);
+  int32_t* starts = reinterpret_cast<int32_t*>(p.plan + L.o_start);
+  int32_t* prefix = reinterpret_cast<int32_t*>(p.plan + L.o_group);
+  int32_t* run_tile0 = reinterpret_cast<int32_t*>(p.plan + L.o_run);
+  int32_t* tile_slot = reinterpret_cast<int32_t*>(p.plan + L.o_tile_slot);
+  int32_t* tile_ns = reinterpret_cast<int32_t*>(p.plan + L.o_tile_ns);
+  TileEntry* entries = reinterpret_cast<TileEntry*>(p.plan + L.o_entry);
+  int32_t* comb = reinterpret_cast<int32_t*>(p.plan + L.o_comb);
+  const int tile_tok = 2 * L.half_tok;
+  const int n_run = L.use_tile ? b.n_seq + b.n_group : 0;
   griddep_wait();
+  if (tid == 0) {
+    s_blocks = 0;
+    s_comb = 0;
+  }
+  for (int i = tid; i < kLenBuckets; i += kPlanThreads) s_hist[i] = 0;
+
+  // The tables' bounds.  A table that breaks them plans no work: every row is
+  // then written as a row without keys.
   int bad = 0;
-  for (int s = threadIdx.x; s < b.n_seq; s += blockDim.x) {
+  for (int s = tid; s < b.n_seq; s += kPlanThreads) {
     const int a = b.seq_offsets[s], e = b.seq_offsets[s + 1], kv = b.kv_len[s];
     bad |= a < 0 || e < a || e > b.n_tokens || e - a > b.max_q_len || kv < 0 ||
            kv > b.max_kv_len || kv > b.table_stride * b.page_size;
   }
+  for (int g = tid; g < b.n_group; g += kPlanThreads) {
+    const int a = b.group_offsets[g], e = b.group_offsets[g + 1];
+    bad |= a < 0 || e < a || e > b.n_seq || b.prefix_len[g] < 0;
+  }
   bad = __syncthreads_or(bad);
-  if (bad && threadIdx.x == 0) record_error(ctx, kErrBounds);
-  for (int64_t t = threadIdx.x; t < b.n_tokens; t += blockDim.x) tok_seq[t] = -1;
-  __syncthreads();
-  if (bad) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int s = warp; s < b.n_seq; s += blockDim.x >> 5)
-    for (int t = b.seq_offsets[s] + lane; t < b.seq_offsets[s + 1]; t += 32) tok_seq[t] = s;
-}
-
-template <int D>
-__global__ void __launch_bounds__(128) attention_rows_kernel(const AttnArgs p) {
-  constexpr int E = D / 32;
-  const bd_attention_batch& b = p.b;
-  griddep_wait();
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (r >= b.n_tokens * b.n_q_heads) return;
-  const int64_t t = r / b.n_q_heads;
-  const int h = static_cast<int>(r % b.n_q_heads);
-  const int kvh = h / (b.n_q_heads / b.n_kv_heads);
-  const int seq = p.tok_seq[t];
-  int64_t keys = 0;
-  if (seq >= 0) keys = static_cast<int64_t>(b.kv_len[seq]) - (b.seq_offsets[seq + 1] - t) + 1;
-  float q[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __uint_as_float(static_cast<uint32_t>(p.q[r * D + e * 32 + lane]) << 16);
-    o[e] = 0.f;
+  for (int64_t t = tid; t < b.n_tokens; t += kPlanThreads) {
+    tok_seq[t] = -1;
+    if (bad) comb[t] = static_cast<int32_t>(t);
   }
-  for (int64_t k = 0; k < keys; ++k) {
-    int64_t page = b.page_table[static_cast<int64_t>(seq) * b.table_stride + k / b.page_size];
-    if (page < 0 || page >= b.n_pages) {
-      if (lane == 0) record_error(p.ctx, kErrBounds);
-      break;
+  if (bad) {
+    if (tid == 0) {
+      record_error(p.ctx, kErrBounds);
+      *hd = PlanHeader{0, 1, 0, static_cast<int32_t>(b.n_tokens)};
     }
-    const int64_t row = (page * b.n_kv_heads + kvh) * b.page_size + k % b.page_size;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      s = fmaf(q[e],
-               __uint_as_float(static_cast<uint32_t>(p.k_pages[row * D + e * 32 + lane]) << 16),
-               s);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
-    s *= p.scale_log2;
-    const float mn = fmaxf(m, s);
-    const float f = exp2f(m - mn), w = exp2f(s - mn);
-    m = mn;
-    l = fmaf(l, f, w);
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      o[e] = fmaf(o[e], f,
-                  w * __uint_as_float(static_cast<uint32_t>(p.v_pages[row * D + e * 32 + lane])
-                                      << 16));
+    return;
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-    p.out[r * D + e * 32 + lane] =
-        static_cast<uint16_t>(pack_bf16x2_rn(o[e] * inv, 0.f) & 0xFFFFu);
-  if (p.lse != nullptr && lane == 0)
-    p.lse[r] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  for (int s = tid; s < b.n_seq; s += kPlanThreads) {
+    SeqRec r{};
+    r.tok0 = b.seq_offsets[s];
+    r.q_len = b.seq_offsets[s + 1] - r.tok0;
+    r.kv_len = b.kv_len[s];
+    r.group = -1;
+    seqs[s] = r;
+  }
+  __syncthreads();
+  for (int s = warp; s < b.n_seq; s += kWarps)
+    for (int t = lane; t < seqs[s].q_len; t += 32) tok_seq[seqs[s].tok0 + t] = s;
+
+  // A group's prefix, cut to what every member has before its first query
+  // token and to whole pages.  Two or three sequences of few rows read it by
+  // themselves: the decode kernel is then as fast as the join.
+  for (int g = warp; g < b.n_group; g += kWarps) {
+    const int a = b.group_offsets[g], e = b.group_offsets[g + 1];
+    int len = b.prefix_len[g];
+    for (int s = a + lane; s < e; s += 32) {
+      const int before = seqs[s].kv_len - seqs[s].q_len;
+      len = before < len ? before : len;
+    }
+    len = __reduce_min_sync(0xFFFFFFFFu, len);
+    len = len > 0 ? len / b.page_size * b.page_size : 0;
+    const int64_t rows =
+        e > a ? static_cast<int64_t>(b.seq_offsets[e] - b.seq_offsets[a]) * L.g : 0;
+    if (e - a < 2 || (e - a < 4 && rows <= 32)) len = 0;
+    if (lane == 0) prefix[g] = len;
+    if (len > 0)
+      for (int s = a + lane; s < e; s += 32) {
+        seqs[s].k0 = len;
+        seqs[s].group = g;
+      }
+  }
+  __syncthreads();
+
+  // Decode units: every 64 own keys of a short run, once per key head.
+  int64_t carry = 0;
+  for (int base = 0; base < b.n_seq; base += kPlanThreads) {
+    const int s = base + tid;
+    int64_t n = 0;
+    if (s < b.n_seq) {
+      const SeqRec r = seqs[s];
+      const int rows = r.q_len * L.g;
+      if (rows > 0 && rows <= L.d_rows) n = (r.kv_len - r.k0 + kUnitKeys - 1) / kUnitKeys;
+    }
+    int64_t sum;
+    const int64_t at = carry + block_scan(n * b.n_kv_heads, s_warp, &sum);
+    if (s < b.n_seq) {
+      seqs[s].unit0 = at;
+      seqs[s].units = static_cast<int32_t>(n);
+    }
+    carry += sum;
+  }
+  const int64_t d_units = carry;
+  const int64_t d_per = d_units > 0 ? (d_units + L.d_ctas - 1) / L.d_ctas : 1;
+  __syncthreads();
+  // The sequence in which each CTA's units begin.
+  for (int s = tid; s < b.n_seq; s += kPlanThreads) {
+    const SeqRec r = seqs[s];
+    const int64_t end = r.unit0 + static_cast<int64_t>(r.units) * b.n_kv_heads;
+    for (int64_t c = (r.unit0 + d_per - 1) / d_per; c * d_per < end; ++c)
+      starts[c] = s;
+  }
+
+  // Tiles of the long runs: sequences, then groups.
+  carry = 0;
+  for (int base = 0; base < n_run; base += kPlanThreads) {
+    const int r = base + tid;
+    int64_t n = 0;
+    if (r < b.n_seq) {
+      const SeqRec q = seqs[r];
+      if (q.q_len * static_cast<int64_t>(L.g) > L.d_rows)
+        n = (q.q_len + tile_tok - 1) / tile_tok;
+    } else if (r < n_run && prefix[r - b.n_seq] > 0) {
+      const int g = r - b.n_seq;
+      const int toks =
+          b.seq_offsets[b.group_offsets[g + 1]] - b.seq_offsets[b.group_offsets[g]];
+      n = (toks + tile_tok - 1) / tile_tok;
+    }
+    int64_t sum;
+    const int64_t at = carry + block_scan(n, s_warp, &sum);
+    if (r < n_run) run_tile0[r] = static_cast<int32_t>(at);
+    carry += sum;
+  }
+  const int n_tiles = static_cast<int>(carry);
+  if (tid == 0 && n_run > 0) run_tile0[n_run] = n_tiles;
+  __syncthreads();
+
+  // Tile i of run r without its piece: what it covers and its blocks.
+  const auto tile_of = [&](int r, int i, int* blocks) {
+    TileEntry e{};
+    int first, toks;
+    if (r < b.n_seq) {
+      const SeqRec q = seqs[r];
+      first = q.tok0;
+      toks = q.q_len;
+      e.seq = r;
+      e.k_lo = q.k0;
+      e.causal = q.kv_len - (q.tok0 + q.q_len) + 1;
+    } else {
+      const int g = r - b.n_seq, s0 = b.group_offsets[g];
+      first = seqs[s0].tok0;
+      toks = b.seq_offsets[b.group_offsets[g + 1]] - first;
+      e.seq = s0;
+      e.causal = 1 << 30;
+    }
+    e.tok0 = first + i * tile_tok;
+    e.n_tok = toks - i * tile_tok < tile_tok ? toks - i * tile_tok : tile_tok;
+    if (r < b.n_seq) {
+      const int kv = seqs[r].kv_len;
+      e.k_hi = e.tok0 + e.n_tok - 1 + e.causal;  // what the tile's last token sees
+      e.tail = (e.k_hi + 15) / 16 * 16 > kv;
+    } else {
+      e.k_hi = prefix[r - b.n_seq];
+    }
+    *blocks = e.k_hi > e.k_lo ? (e.k_hi - e.k_lo + kTileKeys - 1) / kTileKeys : 0;
+    return e;
+  };
+  for (int r = warp; r < n_run; r += kWarps) {
+    const int t0 = run_tile0[r], t1 = run_tile0[r + 1];
+    for (int i = t0 + lane; i < t1; i += 32) {
+      int nb;
+      tile_of(r, i - t0, &nb);
+      atomicAdd(&s_blocks, static_cast<unsigned long long>(nb));
+    }
+  }
+  __syncthreads();
+  // Tiles longer than the CTAs' even share are cut into pieces of that share.
+  const int64_t share =
+      (static_cast<int64_t>(s_blocks) * b.n_kv_heads + L.t_ctas - 1) / L.t_ctas;
+  const int piece = static_cast<int>(share < 2 ? 2 : share);
+  // slots first (a scan over tiles, which belong to runs: by tile index)
+  for (int r = warp; r < n_run; r += kWarps) {
+    const int t0 = run_tile0[r], t1 = run_tile0[r + 1];
+    const bool parts = r >= b.n_seq || (t1 > t0 && seqs[r].group >= 0);
+    for (int i = t0 + lane; i < t1; i += 32) {
+      int nb;
+      tile_of(r, i - t0, &nb);
+      const int ns = (nb + piece - 1) / piece;
+      tile_ns[i] = ns;
+      tile_slot[i] = ns > 1 || (parts && ns > 0) ? 0 : -1;
+      for (int j = 0; j < ns; ++j) {
+        const int len = j + 1 < ns ? piece : nb - j * piece;
+        atomicAdd(&s_hist[len < kLenBuckets ? len : kLenBuckets - 1], 1);
+      }
+    }
+  }
+  __syncthreads();
+  carry = 0;
+  for (int base = 0; base < n_tiles; base += kPlanThreads) {
+    const int i = base + tid;
+    const int64_t n = i < n_tiles && tile_slot[i] >= 0 ? tile_ns[i] : 0;
+    int64_t sum;
+    const int64_t at = carry + block_scan(n, s_warp, &sum);
+    if (n > 0) tile_slot[i] = static_cast<int32_t>(at);
+    carry += sum;
+  }
+  const bool over = carry * b.n_kv_heads > L.t_slots;  // attn_layout's bound: cannot happen
+  // The longest pieces first: bucket offsets in descending order of length.
+  {
+    const int len = kLenBuckets - 1 - tid;
+    int64_t sum;
+    const int64_t at = block_scan(s_hist[len], s_warp, &sum);
+    carry = sum;
+    __syncthreads();
+    s_hist[len] = static_cast<int>(at);
+  }
+  const int n_entries = static_cast<int>(carry);
+  const bool fits = !over && n_entries <= L.max_entries;
+  __syncthreads();
+  for (int r = warp; r < n_run && fits; r += kWarps) {
+    const int t0 = run_tile0[r], t1 = run_tile0[r + 1];
+    for (int i = t0 + lane; i < t1; i += 32) {
+      int nb;
+      TileEntry e = tile_of(r, i - t0, &nb);
+      const int ns = tile_ns[i], slot = tile_slot[i];
+      for (int j = 0; j < ns; ++j) {
+        e.b0 = j * piece;
+        e.b1 = j + 1 < ns ? e.b0 + piece : nb;
+        e.slot = slot < 0 ? -1 : slot + j;
+        const int len = e.b1 - e.b0;
+        entries[atomicAdd(&s_hist[len < kLenBuckets ? len : kLenBuckets - 1], 1)] = e;
+      }
+    }
+  }
+
+  // Tokens whose rows are joined, or have no keys at all.
+  for (int64_t t = tid; t < b.n_tokens; t += kPlanThreads) {
+    const int s = tok_seq[t];
+    bool join = true;
+    if (s >= 0) {
+      const SeqRec r = seqs[s];
+      if (r.q_len * static_cast<int64_t>(L.g) > L.d_rows) {
+        const int i = run_tile0[s] + static_cast<int>(t - r.tok0) / tile_tok;
+        join = tile_slot[i] >= 0 || tile_ns[i] == 0;
+      } else if (r.units > 0 && r.group < 0) {
+        // final where no head's units are cut between CTAs
+        join = false;
+        for (int h = 0; h < b.n_kv_heads && !join; ++h) {
+          const int64_t u0 = r.unit0 + static_cast<int64_t>(h) * r.units;
+          join = u0 / d_per != (u0 + r.units - 1) / d_per;
+        }
+      }
+    }
+    if (join) comb[atomicAdd(&s_comb, 1)] = static_cast<int32_t>(t);
+  }
+  __syncthreads();
+  if (tid == 0) {
+    if (!fits) record_error(p.ctx, kErrBounds);
+    *hd = PlanHeader{d_units, d_per, fits ? n_entries : 0, s_comb};
+  }
 }
 
-bool off(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) != 0; }
+// ------------------------------------------------------------------ combine
+
+constexpr int kCombThreads = 256;
+
+// One CTA per (token, key head) of the plan's list: the rows' partial results
+// joined in a fixed order.  Thread e takes row e % g and elements 4·(e / g) ..
+// + 3, so neighbouring threads read neighbouring rows of a slot.
+__global__ void __launch_bounds__(kCombThreads) combine_kernel(const AttnArgs p) {
+  const bd_attention_batch& b = p.b;
+  const AttnLayout& L = p.L;
+  const int g = L.g, D = b.head_dim;
+  griddep_wait();
+  griddep_launch_dependents();
+  const PlanHeader hd = *p.header();
+  const int tile_tok = 2 * L.half_tok;
+  const int64_t n_work = static_cast<int64_t>(hd.n_comb) * b.n_kv_heads;
+  for (int64_t w = blockIdx.x; w < n_work; w += gridDim.x) {
+    const int t = p.comb()[w / b.n_kv_heads];
+    const int kvh = static_cast<int>(w % b.n_kv_heads);
+    const int seq = p.tok_seq()[t];
+    // up to two families of parts: slots s_i = first + i·step of `rows` rows,
+    // the token's first row at row0
+    struct Family {
+      uint8_t *o, *ml;
+      int64_t first, step;
+      int n, rows, row0;
+    };
+    Family f[2] = {};
+    int64_t d_c0 = -1;  // decode parts: CTAs d_c0 .., the first in its slot 1
+    if (seq >= 0) {
+      const SeqRec r = p.seqs()[seq];
+      const int x = t - r.tok0;
+      if (static_cast<int64_t>(r.q_len) * g > L.d_rows) {
+        const int i = p.run_tile0()[seq] + x / tile_tok;
+        const int y = x % tile_tok;
+        f[0] = Family{p.ws + L.w_t_o, p.ws + L.w_t_ml,
+                      static_cast<int64_t>(p.tile_slot()[i]) * b.n_kv_heads + kvh, b.n_kv_heads,
+                      p.tile_ns()[i], 2 * kHalfRows,
+                      y / L.half_tok * kHalfRows + y % L.half_tok * g};
+      } else if (r.units > 0) {
+        const int64_t u0 = r.unit0 + static_cast<int64_t>(kvh) * r.units;
+        const int64_t c0 = u0 / hd.d_per, c1 = (u0 + r.units - 1) / hd.d_per;
+        if (c1 > c0) {
+          d_c0 = c0;
+          f[0] = Family{p.ws + L.w_d_o, p.ws + L.w_d_ml, 2 * c0, 2, static_cast<int>(c1 - c0) + 1,
+                        L.d_rows, x * g};
+        } else if (r.group >= 0) {
+          f[0] = Family{p.ws + L.w_r_o, p.ws + L.w_r_ml,
+                        static_cast<int64_t>(t) * b.n_kv_heads + kvh, 0, 1, g, 0};
+        }
+        // else: written by the decode kernel (another head of the token is cut)
+        else {
+          continue;
+        }
+      }
+      if (r.group >= 0) {
+        const int y0 = t - p.seqs()[b.group_offsets[r.group]].tok0;
+        const int i = p.run_tile0()[b.n_seq + r.group] + y0 / tile_tok;
+        const int y = y0 % tile_tok;
+        f[1] = Family{p.ws + L.w_t_o, p.ws + L.w_t_ml,
+                      static_cast<int64_t>(p.tile_slot()[i]) * b.n_kv_heads + kvh, b.n_kv_heads,
+                      p.tile_ns()[i], 2 * kHalfRows,
+                      y / L.half_tok * kHalfRows + y % L.half_tok * g};
+      }
+    }
+    for (int e = threadIdx.x; e < g * (D / 4); e += kCombThreads) {
+      const int row = e % g, d4 = e / g;
+      float top = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll 4
+        for (int i = 0; i < f[k].n; ++i) {
+          const int64_t slot = f[k].first + i * f[k].step + (k == 0 && i == 0 && d_c0 >= 0 ? 1 : 0);
+          top = fmaxf(top, part_ml(f[k].ml, slot, f[k].rows)[f[k].row0 + row].x);
+        }
+      const float ref = top == -INFINITY ? 0.f : top;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      float l = 0.f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll 4
+        for (int i = 0; i < f[k].n; ++i) {
+          const int64_t slot = f[k].first + i * f[k].step + (k == 0 && i == 0 && d_c0 >= 0 ? 1 : 0);
+          const float2 ml = part_ml(f[k].ml, slot, f[k].rows)[f[k].row0 + row];
+          const float4 v =
+              part_o(f[k].o, slot, f[k].rows, D)[static_cast<int64_t>(d4) * f[k].rows + f[k].row0 + row];
+          const float s = ex2(ml.x - ref);
+          l = fmaf(ml.y, s, l);
+          o.x = fmaf(v.x, s, o.x);
+          o.y = fmaf(v.y, s, o.y);
+          o.z = fmaf(v.z, s, o.z);
+          o.w = fmaf(v.w, s, o.w);
+        }
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const int64_t at = static_cast<int64_t>(t) * b.n_q_heads + kvh * g + row;
+      reinterpret_cast<uint2*>(p.out + at * D)[d4] =
+          make_uint2(pack_bf16x2_rn(o.x * inv, o.y * inv), pack_bf16x2_rn(o.z * inv, o.w * inv));
+      if (d4 == 0 && p.lse != nullptr)
+        p.lse[at] = l > 0.f ? (ref + log2f(l)) * kLn2 : -INFINITY;
+    }
+  }
+}
+
+int fill_args(const bd_attention_batch* batch, AttnArgs* p) {
+  int sms = 0;
+  const int st = current_device_context(&p->ctx, &sms);
+  if (st != BD_OK) return st;
+  p->b = *batch;
+  p->L = attn_layout(*batch, sms);
+  return BD_OK;
+}
+
+// Plan and workspace sizes need the device's SM count; without a device they
+// are those of a GB300.
+AttnLayout sized_layout(const bd_attention_batch* batch) {
+  DevCtx ctx;
+  int sms = 0;
+  if (current_device_context(&ctx, &sms) != BD_OK) sms = 152;
+  return attn_layout(*batch, sms);
+}
+
+bd_status run_attention(AttnArgs& p, cudaStream_t s) {
+  const bd_attention_batch& b = p.b;
+  const uint64_t D = static_cast<uint64_t>(b.head_dim), H = static_cast<uint64_t>(b.n_q_heads);
+  const uint64_t rows =
+      static_cast<uint64_t>(b.n_pages) * b.n_kv_heads * static_cast<uint64_t>(b.page_size);
+  const uint64_t kdims[3] = {64, rows, D / 64};
+  const uint64_t kstr[2] = {2 * D, 128};
+  CUtensorMap tk, tv;
+  if (p.L.use_tile) {
+    const uint32_t box[3] = {64, static_cast<uint32_t>(b.page_size), 1};
+    const uint64_t qdims[3] = {D, H, static_cast<uint64_t>(b.n_tokens)};
+    const uint64_t qstr[2] = {2 * D, 2 * D * H};
+    const uint32_t qbox[3] = {64, static_cast<uint32_t>(p.L.g),
+                              static_cast<uint32_t>(p.L.half_tok)};
+    CUtensorMap tq;
+    if (!encode_tmap_bf16_3d(&tk, p.k_pages, kdims, kstr, box) ||
+        !encode_tmap_bf16_3d(&tv, p.v_pages, kdims, kstr, box) ||
+        !encode_tmap_bf16_3d(&tq, p.q, qdims, qstr, qbox))
+      return BD_ERR_CUDA;
+    if (launch_attn_tile(p, tq, tk, tv, s) != cudaSuccess) return BD_ERR_CUDA;
+  }
+  const uint32_t box[3] = {64, 16, static_cast<uint32_t>(D / 64)};
+  if (!encode_tmap_bf16_3d(&tk, p.k_pages, kdims, kstr, box) ||
+      !encode_tmap_bf16_3d(&tv, p.v_pages, kdims, kstr, box))
+    return BD_ERR_CUDA;
+  if (launch_attn_decode(p, tk, tv, s) != cudaSuccess) return BD_ERR_CUDA;
+  const int64_t work = b.n_tokens * b.n_kv_heads;
+  const int64_t most = 4 * static_cast<int64_t>(p.L.t_ctas);
+  const cudaError_t e = launch_pdl(combine_kernel, dim3(static_cast<unsigned>(work < most ? work : most)),
+                                   dim3(kCombThreads), 0, s, p);
+  return e == cudaSuccess ? BD_OK : BD_ERR_CUDA;
+}
 
 }  // namespace
 }  // namespace bd
@@ -115,7 +535,7 @@ extern "C" {
 
 size_t bitdelta_attention_plan_bytes(const bd_attention_batch* batch) {
   if (bd::check_attention_batch(batch) != BD_OK) return 0;
-  return bd::plan_bytes_of(*batch);
+  return bd::sized_layout(batch).plan_bytes;
 }
 
 bd_status bitdelta_attention_plan(const bd_attention_batch* batch, void* plan, size_t plan_bytes,
@@ -123,21 +543,20 @@ bd_status bitdelta_attention_plan(const bd_attention_batch* batch, void* plan, s
   int st = bd::check_attention_batch(batch);
   if (st != BD_OK) return static_cast<bd_status>(st);
   if (batch->n_tokens == 0 || batch->n_seq == 0) return BD_OK;
-  if (!plan || plan_bytes < bd::plan_bytes_of(*batch)) return BD_ERR_WORKSPACE;
+  if (!plan) return BD_ERR_WORKSPACE;
   if (bd::off(plan, 256)) return BD_ERR_MISALIGNED;
-  bd::DevCtx ctx;
-  int sms = 0;
-  if ((st = bd::current_device_context(&ctx, &sms)) != BD_OK) return static_cast<bd_status>(st);
-  const cudaError_t e =
-      bd::launch_pdl(bd::plan_kernel, dim3(1), dim3(1024), 0,
-                     reinterpret_cast<cudaStream_t>(stream), *batch,
-                     static_cast<int32_t*>(plan), ctx);
+  bd::AttnArgs p{};
+  if ((st = bd::fill_args(batch, &p)) != BD_OK) return static_cast<bd_status>(st);
+  if (plan_bytes < p.L.plan_bytes) return BD_ERR_WORKSPACE;
+  p.plan = static_cast<uint8_t*>(plan);
+  const cudaError_t e = bd::launch_pdl(bd::plan_kernel, dim3(1), dim3(bd::kPlanThreads), 0,
+                                       reinterpret_cast<cudaStream_t>(stream), p);
   return e == cudaSuccess ? BD_OK : BD_ERR_CUDA;
 }
 
 size_t bitdelta_attention_workspace_bytes(const bd_attention_batch* batch) {
-  (void)batch;
-  return 0;
+  if (bd::check_attention_batch(batch) != BD_OK) return 0;
+  return bd::sized_layout(batch).ws_bytes;
 }
 
 bd_status bitdelta_attention(const bd_attention_batch* batch, const void* plan, size_t plan_bytes,
@@ -148,32 +567,25 @@ bd_status bitdelta_attention(const bd_attention_batch* batch, const void* plan, 
   if (st != BD_OK) return static_cast<bd_status>(st);
   if (!(scale > 0.f) || std::isinf(scale)) return BD_ERR_INVALID_ARG;
   if (batch->n_tokens == 0 || batch->n_seq == 0) return BD_OK;
-  if (!q || !k_pages || !v_pages || !out) return BD_ERR_INVALID_ARG;
-  if (!plan || plan_bytes < bd::plan_bytes_of(*batch)) return BD_ERR_WORKSPACE;
-  const size_t need = bitdelta_attention_workspace_bytes(batch);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return BD_ERR_WORKSPACE;
+  if (!q || !k_pages || !v_pages || !out || batch->n_pages < 1) return BD_ERR_INVALID_ARG;
+  if (!plan || !workspace) return BD_ERR_WORKSPACE;
   if (bd::off(q, 16) || bd::off(k_pages, 16) || bd::off(v_pages, 16) || bd::off(out, 16) ||
       bd::off(lse, 4) || bd::off(plan, 256) || bd::off(workspace, 256))
     return BD_ERR_MISALIGNED;
+  const size_t tables = sizeof(bd::PlanHeader);  // no plan is smaller
+  if (plan_bytes < tables) return BD_ERR_WORKSPACE;
   bd::AttnArgs p{};
-  int sms = 0;
-  if ((st = bd::current_device_context(&p.ctx, &sms)) != BD_OK) return static_cast<bd_status>(st);
-  p.b = *batch;
-  p.tok_seq = static_cast<const int32_t*>(plan);
+  if ((st = bd::fill_args(batch, &p)) != BD_OK) return static_cast<bd_status>(st);
+  if (plan_bytes < p.L.plan_bytes || workspace_bytes < p.L.ws_bytes) return BD_ERR_WORKSPACE;
+  p.plan = static_cast<uint8_t*>(const_cast<void*>(plan));
+  p.ws = static_cast<uint8_t*>(workspace);
   p.q = q;
   p.k_pages = k_pages;
   p.v_pages = v_pages;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.out = out;
   p.lse = lse;
-  const int64_t rows = batch->n_tokens * batch->n_q_heads;
-  const dim3 grid(static_cast<unsigned>((rows + 3) / 4));
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e =
-      batch->head_dim == 128
-          ? bd::launch_pdl(bd::attention_rows_kernel<128>, grid, dim3(128), 0, s, p)
-          : bd::launch_pdl(bd::attention_rows_kernel<64>, grid, dim3(128), 0, s, p);
-  return e == cudaSuccess ? BD_OK : BD_ERR_CUDA;
+  return bd::run_attention(p, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

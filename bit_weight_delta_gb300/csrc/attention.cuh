@@ -1,0 +1,155 @@
+// attention.cuh — what the attention's kernels share: the plan's layout, the
+// partial results' layout and the launchers.
+//
+// A batch's work falls in two kinds of run.  Short runs (a sequence with at
+// most d_rows query rows per key head, i.e. query tokens x query heads per key
+// head) go to the decode kernel, whose time is reading the cache.  Long runs go
+// to the tile kernel, on the tensor cores: sequences with more rows, over their
+// own keys, and groups of sequences, over their shared prefix.  Rows whose keys
+// are spread over several pieces (a key range cut over CTAs, a prefix and an
+// own part) are joined by the combine kernel from partial results
+//   o = Σ 2^(s − m)·v,  l = Σ 2^(s − m),  m      (s in units of log2)
+// as Σ 2^(m_i − M)·o_i / Σ 2^(m_i − M)·l_i with M = max m_i.
+#pragma once
+
+#include <cstdint>
+
+#include "bitdelta_block.h"
+#include "kernels.h"
+
+namespace bd {
+
+constexpr int kTileKeys = 128;   // keys per block of the tile kernel
+constexpr int kHalfRows = 128;   // rows per half of its 256-row tile (tensor-memory lanes)
+constexpr int kUnitKeys = 64;    // keys per unit of the decode kernel's split
+constexpr int kDecodeWarps = 4;
+
+struct PlanHeader {
+  int64_t d_units;    // units of the decode kernel, all sequences and key heads
+  int64_t d_per;      // units per CTA
+  int32_t t_entries;  // pieces of the tile kernel (each once per key head)
+  int32_t n_comb;     // tokens whose rows the combine kernel writes
+};
+
+// One sequence, as the decode kernel and the combine kernel see it.
+struct SeqRec {
+  int64_t unit0;      // first of its decode units (key head h: + h · units per head)
+  int32_t units;      // decode units per key head (0: none, or a tile-kernel run)
+  int32_t tok0, q_len, kv_len;
+  int32_t k0;         // first own key (the shared prefix ends there)
+  int32_t group;      // group whose prefix it reads, or −1
+};
+
+// One piece of the tile kernel's work: a tile of query tokens by a range of
+// 128-key blocks.
+struct TileEntry {
+  int32_t tok0, n_tok;   // query tokens
+  int32_t seq;           // whose page-table row is read
+  int32_t k_lo, k_hi;    // keys of the tile; block b starts at k_lo + 128·b
+  int32_t causal;        // token t sees keys below min(k_hi, t + causal)
+  int32_t b0, b1;        // blocks of this piece
+  int32_t slot;          // partial slot (times n_kv_heads plus head), or −1: final
+  int32_t tail;          // values past k_hi in its 16-key step may hold anything
+  int32_t pad0, pad1;
+};
+
+// Sizes that the host fixes for a batch, and where everything lies.
+struct AttnLayout {
+  int32_t g;             // query heads per key head
+  int32_t half_tok;      // tokens per half tile
+  int32_t d_rows;        // rows up to which a run is short
+  int32_t d_ctas, t_ctas;
+  bool use_decode, use_tile;
+  int64_t max_tiles, max_entries, t_slots;
+  // plan
+  size_t o_tok_seq, o_seq, o_start, o_group, o_run, o_tile_slot, o_tile_ns, o_entry, o_comb;
+  size_t plan_bytes;
+  // workspace: O then (m, l) of each
+  size_t w_d_o, w_d_ml, w_r_o, w_r_ml, w_t_o, w_t_ml;
+  size_t ws_bytes;
+};
+AttnLayout attn_layout(const bd_attention_batch& b, int num_sms);
+
+struct AttnArgs {
+  bd_attention_batch b;
+  AttnLayout L;
+  uint8_t* plan;
+  uint8_t* ws;
+  const uint16_t *q, *k_pages, *v_pages;
+  float scale_log2;
+  uint16_t* out;
+  float* lse;
+  DevCtx ctx;
+
+  __host__ __device__ const PlanHeader* header() const {
+    return reinterpret_cast<const PlanHeader*>(plan);
+  }
+  __host__ __device__ const int32_t* tok_seq() const {
+    return reinterpret_cast<const int32_t*>(plan + L.o_tok_seq);
+  }
+  __host__ __device__ const SeqRec* seqs() const {
+    return reinterpret_cast<const SeqRec*>(plan + L.o_seq);
+  }
+  __host__ __device__ const int32_t* starts() const {
+    return reinterpret_cast<const int32_t*>(plan + L.o_start);
+  }
+  __host__ __device__ const int32_t* run_tile0() const {
+    return reinterpret_cast<const int32_t*>(plan + L.o_run);
+  }
+  __host__ __device__ const int32_t* tile_slot() const {
+    return reinterpret_cast<const int32_t*>(plan + L.o_tile_slot);
+  }
+  __host__ __device__ const int32_t* tile_ns() const {
+    return reinterpret_cast<const int32_t*>(plan + L.o_tile_ns);
+  }
+  __host__ __device__ const TileEntry* entries() const {
+    return reinterpret_cast<const TileEntry*>(plan + L.o_entry);
+  }
+  __host__ __device__ const int32_t* comb() const {
+    return reinterpret_cast<const int32_t*>(plan + L.o_comb);
+  }
+};
+
+// Partial results.  A slot of R rows holds o as [D/4][R] float4 (four
+// neighbouring elements of a row together, neighbouring rows next to them) and
+// (m, l) as [R] float2.
+__device__ __forceinline__ float4* part_o(uint8_t* base, int64_t slot, int rows, int dim) {
+  return reinterpret_cast<float4*>(base) + slot * rows * (dim / 4);
+}
+__device__ __forceinline__ float2* part_ml(uint8_t* base, int64_t slot, int rows) {
+  return reinterpret_cast<float2*>(base) + slot * rows;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr float kLn2 = 0.69314718055994531f;
+
+// The running reference m of a row's softmax follows its maximum only in steps
+// of more than this (log2 units): weights are then at most 2^8, sums stay far
+// inside fp32, and the sums are rarely rescaled.
+constexpr float kRescale = 8.f;
+
+cudaError_t launch_attn_decode(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
+                               cudaStream_t s);
+cudaError_t launch_attn_tile(const AttnArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
+                             const CUtensorMap& tv, cudaStream_t s);
+
+// Tensor map of up to 3 dimensions of 16-bit elements in the 128-byte swizzle;
+// strides in bytes of dimensions 1 and 2.
+bool encode_tmap_bf16_3d(CUtensorMap* map, const void* base, const uint64_t (&dims)[3],
+                         const uint64_t (&strides)[2], const uint32_t (&box)[3]);
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, uint64_t* bar, int32_t x,
+                                            int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_addr(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+}  // namespace bd
