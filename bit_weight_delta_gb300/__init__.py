@@ -12,7 +12,6 @@ bf16 tensors are torch.bfloat16; the packed sign matrix is torch.uint8
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -612,13 +611,31 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _on(stream):
-    """Outputs made inside a call belong to the stream that writes them."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+# The current stream's handle without building a Stream object: a decode step's
+# calls are a few microseconds each, and the object alone costs about three.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _raw_stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+def _raw_stream(stream, t):
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_raw_stream is not None:
+        return _current_raw_stream(t.get_device())
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _new(shape, dtype, like, stream):
+    """An output of a call; it belongs to the stream that writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _out(t, shape, dtype, name):
+    if _dev(t, dtype, name).shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    return t
 
 
 def bitdelta_add_norm(y, residual=None, pre_table=None, post_table=None, gate=None,
@@ -635,25 +652,26 @@ def bitdelta_add_norm(y, residual=None, pre_table=None, post_table=None, gate=No
     _dev(y, torch.bfloat16, "y")
     if pre_table is None:
         raise ValueError("pre_table is required")
-    d = y.shape[-1]
-    rows = y.numel() // d if d else 0
-    rtype = torch.bfloat16 if residual is None else residual.dtype
-    if rtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"residual must be bfloat16 or float32, got {rtype}")
-    for t, name in ((residual, "residual"), (residual_out, "residual_out")):
-        if t is not None and _dev(t, rtype, name).shape != y.shape:
-            raise ValueError(f"{name} must have the shape of y")
-    if out is not None and _dev(out, torch.bfloat16, "out").shape != y.shape:
-        raise ValueError("out must have the shape of y")
+    shape = y.shape
+    d = shape[-1]
+    rtype = torch.bfloat16
+    if residual is not None:
+        rtype = residual.dtype
+        if rtype is not torch.bfloat16 and rtype is not torch.float32:
+            raise ValueError(f"residual must be bfloat16 or float32, got {rtype}")
+        _out(residual, shape, rtype, "residual")
+    residual_out = (_new(shape, rtype, y, stream) if residual_out is None else
+                    _out(residual_out, shape, rtype, "residual_out"))
+    out = (_new(shape, torch.bfloat16, y, stream) if out is None else
+           _out(out, shape, torch.bfloat16, "out"))
     gate_stride = 0
     if gate is not None:
         _dev(gate, torch.bfloat16, "gate")
-        if gate.shape == y.shape and gate.dim() > 1:
+        if gate.dim() > 1 and gate.shape == shape:
             gate_stride = d
         elif gate.shape != (d,):
             raise ValueError("gate must be [d] or have the shape of y")
-    _dev(pre_table, torch.int64, "pre_table")
-    n_tab = pre_table.numel()
+    n_tab = _dev(pre_table, torch.int64, "pre_table").numel()
     if post_table is not None and _dev(post_table, torch.int64, "post_table").numel() != n_tab:
         raise ValueError("pre_table and post_table must have the same number of slots")
     n_seg = 0
@@ -663,16 +681,11 @@ def bitdelta_add_norm(y, residual=None, pre_table=None, post_table=None, gate=No
         n_seg = _dev(seg_variant, torch.int32, "seg_variant").numel()
         if _dev(seg_offsets, torch.int32, "seg_offsets").numel() != n_seg + 1:
             raise ValueError("seg_offsets must have one entry more than seg_variant")
-    with _on(stream):
-        if residual_out is None:
-            residual_out = torch.empty_like(y, dtype=rtype)
-        if out is None:
-            out = torch.empty_like(y)
     code = load().bitdelta_add_norm(
-        y.data_ptr(), rows, d, _addr(residual), residual_out.data_ptr(),
+        y.data_ptr(), y.numel() // d if d else 0, d, _addr(residual), residual_out.data_ptr(),
         1 if rtype is torch.float32 else 0, _addr(gate), gate_stride, scale, eps,
         pre_table.data_ptr(), _addr(post_table), n_tab, _addr(seg_offsets), _addr(seg_variant),
-        n_seg, out.data_ptr(), _raw_stream(stream))
+        n_seg, out.data_ptr(), _raw_stream(stream, y))
     if code:
         _check("bitdelta_add_norm", code)
     return residual_out, out
@@ -726,31 +739,29 @@ class AttentionBatch:
             page_table.data_ptr(), n_group, _addr(group_offsets), _addr(prefix_len))
         self._ref = ctypes.addressof(self._c)
         lib = load()
-        with _on(stream):
-            self._plan = torch.empty(lib.bitdelta_attention_plan_bytes(self._ref),
-                                     dtype=torch.uint8, device=kv_len.device)
-            self._ws = torch.empty(lib.bitdelta_attention_workspace_bytes(self._ref),
-                                   dtype=torch.uint8, device=kv_len.device)
+        self._plan = _new(lib.bitdelta_attention_plan_bytes(self._ref), torch.uint8, kv_len, stream)
+        self._ws = _new(lib.bitdelta_attention_workspace_bytes(self._ref), torch.uint8, kv_len,
+                        stream)
         self._plan_args = (self._plan.data_ptr(), self._plan.numel())
         self._ws_args = (self._ws.data_ptr(), self._ws.numel())
-        self._q_shape = (n_tokens, n_q_heads, head_dim)
-        self._qkv_shape = (n_tokens, (n_q_heads + 2 * n_kv_heads) * head_dim)
+        self._q_shape = torch.Size((n_tokens, n_q_heads, head_dim))
+        self._lse_shape = self._q_shape[:2]
+        self._page_shape = torch.Size((n_kv_heads, page_size, head_dim))
+        self._qkv_shape = torch.Size((n_tokens, (n_q_heads + 2 * n_kv_heads) * head_dim))
         self._scale = 1.0 / math.sqrt(head_dim) if head_dim > 0 else 1.0
         self.plan(stream)
 
     def plan(self, stream=None) -> None:
         """Compute the plan from the lengths now in the batch's tensors."""
         _check("bitdelta_attention_plan", load().bitdelta_attention_plan(
-            self._ref, *self._plan_args, _raw_stream(stream)))
+            self._ref, *self._plan_args, _raw_stream(stream, self._plan)))
 
     def _cache(self, k_pages, v_pages) -> None:
-        _dev(k_pages, torch.bfloat16, "k_pages")
-        _dev(v_pages, torch.bfloat16, "v_pages")
-        if (k_pages.shape != v_pages.shape or
-                k_pages.shape[1:] != (self.n_kv_heads, self.page_size, self.head_dim)):
+        shape = _dev(k_pages, torch.bfloat16, "k_pages").shape
+        if _dev(v_pages, torch.bfloat16, "v_pages").shape != shape or shape[1:] != self._page_shape:
             raise ValueError("k_pages and v_pages must be [n_pages, n_kv_heads, page_size, "
                              "head_dim]")
-        self._c.n_pages = k_pages.shape[0]
+        self._c.n_pages = shape[0]
 
 
 def bitdelta_kv_append(batch: AttentionBatch, qkv, rope, k_pages, v_pages,
@@ -761,18 +772,14 @@ def bitdelta_kv_append(batch: AttentionBatch, qkv, rope, k_pages, v_pages,
 
     rope: fp32 [positions, rot_dim], cosines then sines (None: no rotation);
     interleaved rotates neighbours (2i, 2i+1) instead of halves."""
-    if _dev(qkv, torch.bfloat16, "qkv").shape != batch._qkv_shape:
-        raise ValueError(f"qkv must be {batch._qkv_shape}")
+    _out(qkv, batch._qkv_shape, torch.bfloat16, "qkv")
     batch._cache(k_pages, v_pages)
     rows, rot = (0, 0) if rope is None else _dev(rope, torch.float32, "rope").shape
-    if out is None:
-        with _on(stream):
-            out = torch.empty(batch._q_shape, dtype=torch.bfloat16, device=qkv.device)
-    elif _dev(out, torch.bfloat16, "out").shape != batch._q_shape:
-        raise ValueError(f"out must be {batch._q_shape}")
+    out = (_new(batch._q_shape, torch.bfloat16, qkv, stream) if out is None else
+           _out(out, batch._q_shape, torch.bfloat16, "out"))
     code = load().bitdelta_kv_append(
         batch._ref, qkv.data_ptr(), _addr(rope), rows, rot, 1 if interleaved else 0,
-        k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), _raw_stream(stream))
+        k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), _raw_stream(stream, qkv))
     if code:
         _check("bitdelta_kv_append", code)
     return out
@@ -783,22 +790,16 @@ def bitdelta_attention(batch: AttentionBatch, q, k_pages, v_pages, scale: float 
     """Causal attention of q [n_tokens, n_q_heads, head_dim] over the cache.
     Returns (out, lse): bf16 like q, and fp32 [n_tokens, n_q_heads].  scale
     defaults to 1/sqrt(head_dim)."""
-    if _dev(q, torch.bfloat16, "q").shape != batch._q_shape:
-        raise ValueError(f"q must be {batch._q_shape}")
+    _out(q, batch._q_shape, torch.bfloat16, "q")
     batch._cache(k_pages, v_pages)
-    with _on(stream):
-        if out is None:
-            out = torch.empty_like(q)
-        elif _dev(out, torch.bfloat16, "out").shape != batch._q_shape:
-            raise ValueError(f"out must be {batch._q_shape}")
-        if lse is None:
-            lse = torch.empty(batch._q_shape[:2], dtype=torch.float32, device=q.device)
-        elif _dev(lse, torch.float32, "lse").shape != batch._q_shape[:2]:
-            raise ValueError(f"lse must be {batch._q_shape[:2]}")
+    out = (_new(batch._q_shape, torch.bfloat16, q, stream) if out is None else
+           _out(out, batch._q_shape, torch.bfloat16, "out"))
+    lse = (_new(batch._lse_shape, torch.float32, q, stream) if lse is None else
+           _out(lse, batch._lse_shape, torch.float32, "lse"))
     code = load().bitdelta_attention(
         batch._ref, *batch._plan_args, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
         batch._scale if scale is None else scale, out.data_ptr(), lse.data_ptr(),
-        *batch._ws_args, _raw_stream(stream))
+        *batch._ws_args, _raw_stream(stream, q))
     if code:
         _check("bitdelta_attention", code)
     return out, lse

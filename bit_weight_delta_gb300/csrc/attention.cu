@@ -50,13 +50,13 @@ AttnLayout attn_layout(const bd_attention_batch& b, int num_sms) {
   };
   L.o_tok_seq = take(4 * static_cast<size_t>(T));
   L.o_seq = take(sizeof(SeqRec) * static_cast<size_t>(b.n_seq));
-  L.o_start = take(4 * static_cast<size_t>(L.d_ctas));
+  L.o_start = take(sizeof(DecodeStart) * static_cast<size_t>(L.d_ctas));
   L.o_group = take(4 * static_cast<size_t>(b.n_group));
   L.o_run = take(4 * (static_cast<size_t>(b.n_seq) + b.n_group + 1));
   L.o_tile_slot = take(4 * static_cast<size_t>(L.max_tiles));
   L.o_tile_ns = take(4 * static_cast<size_t>(L.max_tiles));
   L.o_entry = take(sizeof(TileEntry) * static_cast<size_t>(L.max_entries));
-  L.o_comb = take(4 * static_cast<size_t>(T));
+  L.o_comb = take(sizeof(CombItem) * static_cast<size_t>(T));
   L.plan_bytes = o;
   o = 0;
   const size_t d_rows = static_cast<size_t>(L.d_ctas) * 2 * L.d_rows;
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
   __shared__ int64_t s_warp[32];
   __shared__ int s_hist[kLenBuckets];
   __shared__ unsigned long long s_blocks;
-  __shared__ int s_comb;
+  __shared__ int s_comb, s_longest;
   const bd_attention_batch& b = p.b;
   const AttnLayout& L = p.L;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -120,19 +120,20 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
   PlanHeader* hd = reinterpret_cast<PlanHeader*>(p.plan);
   int32_t* tok_seq = reinterpret_cast<int32_t*>(p.plan + L.o_tok_seq);
   SeqRec* seqs = reinterpret_cast<SeqRec*>(p.plan + L.o_seq);
-  int32_t* starts = reinterpret_cast<int32_t*>(p.plan + L.o_start);
+  DecodeStart* starts = reinterpret_cast<DecodeStart*>(p.plan + L.o_start);
   int32_t* prefix = reinterpret_cast<int32_t*>(p.plan + L.o_group);
   int32_t* run_tile0 = reinterpret_cast<int32_t*>(p.plan + L.o_run);
   int32_t* tile_slot = reinterpret_cast<int32_t*>(p.plan + L.o_tile_slot);
   int32_t* tile_ns = reinterpret_cast<int32_t*>(p.plan + L.o_tile_ns);
   TileEntry* entries = reinterpret_cast<TileEntry*>(p.plan + L.o_entry);
-  int32_t* comb = reinterpret_cast<int32_t*>(p.plan + L.o_comb);
+  CombItem* comb = reinterpret_cast<CombItem*>(p.plan + L.o_comb);
   const int tile_tok = 2 * L.half_tok;
   const int n_run = L.use_tile ? b.n_seq + b.n_group : 0;
   griddep_wait();
   if (tid == 0) {
     s_blocks = 0;
     s_comb = 0;
+    s_longest = 0;
   }
   for (int i = tid; i < kLenBuckets; i += kPlanThreads) s_hist[i] = 0;
 
@@ -151,9 +152,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
   bad = __syncthreads_or(bad);
   for (int64_t t = tid; t < b.n_tokens; t += kPlanThreads) {
     tok_seq[t] = -1;
-    if (bad) comb[t] = static_cast<int32_t>(t);
+    if (bad) {
+      CombItem it{};
+      it.tok = static_cast<int32_t>(t);
+      comb[t] = it;
+    }
   }
   if (bad) {
+    for (int c = tid; c < L.d_ctas; c += kPlanThreads) starts[c].lo = starts[c].hi = 0;
     if (tid == 0) {
       record_error(p.ctx, kErrBounds);
       *hd = PlanHeader{0, 1, 0, static_cast<int32_t>(b.n_tokens)};
@@ -217,13 +223,20 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
   const int64_t d_units = carry;
   const int64_t d_per = d_units > 0 ? (d_units + L.d_ctas - 1) / L.d_ctas : 1;
   __syncthreads();
-  // The sequence in which each CTA's units begin.
+  // Where each CTA's units begin.
   for (int s = tid; s < b.n_seq; s += kPlanThreads) {
-    const SeqRec r = seqs[s];
-    const int64_t end = r.unit0 + static_cast<int64_t>(r.units) * b.n_kv_heads;
-    for (int64_t c = (r.unit0 + d_per - 1) / d_per; c * d_per < end; ++c)
-      starts[c] = s;
+    DecodeStart st{};
+    st.r = seqs[s];
+    st.seq = s;
+    const int64_t end = st.r.unit0 + static_cast<int64_t>(st.r.units) * b.n_kv_heads;
+    for (int64_t c = (st.r.unit0 + d_per - 1) / d_per; c * d_per < end; ++c) {
+      st.lo = c * d_per;
+      st.hi = st.lo + d_per < d_units ? st.lo + d_per : d_units;
+      starts[c] = st;
+    }
   }
+  for (int64_t c = (d_units + d_per - 1) / d_per + tid; c < L.d_ctas; c += kPlanThreads)
+    starts[c].lo = starts[c].hi = 0;
 
   // Tiles of the long runs: sequences, then groups.
   carry = 0;
@@ -285,12 +298,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
       int nb;
       tile_of(r, i - t0, &nb);
       atomicAdd(&s_blocks, static_cast<unsigned long long>(nb));
+      atomicMax(&s_longest, nb);
     }
   }
   __syncthreads();
-  // Tiles longer than the CTAs' even share are cut into pieces of that share.
-  const int64_t share =
-      (static_cast<int64_t>(s_blocks) * b.n_kv_heads + L.t_ctas - 1) / L.t_ctas;
+  // Where the longest tile exceeds the CTAs' even share by more than a quarter
+  // and by more than 4 blocks, tiles longer than the share are cut into pieces
+  // of that share.  Below that the join of the pieces costs more than the
+  // uneven end: 256 tiles of up to 20 blocks with a share of 17 took 55 µs and
+  // 32 µs more for the join when cut.
+  int64_t share = (static_cast<int64_t>(s_blocks) * b.n_kv_heads + L.t_ctas - 1) / L.t_ctas;
+  if (s_longest <= share + (share / 4 > 4 ? share / 4 : 4)) share = s_longest;
   const int piece = static_cast<int>(share < 2 ? 2 : share);
   // slots first (a scan over tiles, which belong to runs: by tile index)
   for (int r = warp; r < n_run; r += kWarps) {
@@ -351,21 +369,39 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
   for (int64_t t = tid; t < b.n_tokens; t += kPlanThreads) {
     const int s = tok_seq[t];
     bool join = true;
+    CombItem it{};
+    it.tok = static_cast<int32_t>(t);
     if (s >= 0) {
       const SeqRec r = seqs[s];
+      const int x = it.tok - r.tok0;
       if (r.q_len * static_cast<int64_t>(L.g) > L.d_rows) {
-        const int i = run_tile0[s] + static_cast<int>(t - r.tok0) / tile_tok;
+        const int i = run_tile0[s] + x / tile_tok, y = x % tile_tok;
         join = tile_slot[i] >= 0 || tile_ns[i] == 0;
-      } else if (r.units > 0 && r.group < 0) {
-        // final where no head's units are cut between CTAs
-        join = false;
-        for (int h = 0; h < b.n_kv_heads && !join; ++h) {
-          const int64_t u0 = r.unit0 + static_cast<int64_t>(h) * r.units;
-          join = u0 / d_per != (u0 + r.units - 1) / d_per;
+        it.own_slot = tile_slot[i];
+        it.own_ns = tile_ns[i];
+        it.own_row = y / L.half_tok * kHalfRows + y % L.half_tok * L.g;
+      } else if (r.units > 0) {
+        it.unit0 = r.unit0;
+        it.units = r.units;
+        it.own_row = x * L.g;
+        if (r.group < 0) {
+          // final where no head's units are cut between CTAs
+          join = false;
+          for (int h = 0; h < b.n_kv_heads && !join; ++h) {
+            const int64_t u0 = r.unit0 + static_cast<int64_t>(h) * r.units;
+            join = u0 / d_per != (u0 + r.units - 1) / d_per;
+          }
         }
       }
+      if (r.group >= 0) {
+        const int z = it.tok - seqs[b.group_offsets[r.group]].tok0;
+        const int i = run_tile0[b.n_seq + r.group] + z / tile_tok, y = z % tile_tok;
+        it.pre_slot = tile_slot[i];
+        it.pre_ns = tile_ns[i];
+        it.pre_row = y / L.half_tok * kHalfRows + y % L.half_tok * L.g;
+      }
     }
-    if (join) comb[atomicAdd(&s_comb, 1)] = static_cast<int32_t>(t);
+    if (join) comb[atomicAdd(&s_comb, 1)] = it;
   }
   __syncthreads();
   if (tid == 0) {
@@ -377,103 +413,136 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
 // ------------------------------------------------------------------ combine
 
 constexpr int kCombThreads = 256;
+constexpr int kCombD4 = 8;     // float4 columns of a row per CTA
+constexpr int kCombBatch = 4;  // parts that a thread has in flight
 
-// One CTA per (token, key head) of the plan's list: the rows' partial results
-// joined in a fixed order.  Thread e takes row e % g and elements 4·(e / g) ..
-// + 3, so neighbouring threads read neighbouring rows of a slot.
+// One CTA per (token, key head, 32 columns) of the plan's list.  A row's parts
+// are dealt to the thread groups of the CTA, which join them in a fixed order
+// with a running maximum and meet in shared memory: the join is one load of the
+// item and about parts / (groups · 4) rounds of independent loads.  Neighbouring
+// threads read neighbouring rows of a slot.
 __global__ void __launch_bounds__(kCombThreads) combine_kernel(const AttnArgs p) {
+  __shared__ float4 s_o[kCombThreads];
+  __shared__ float2 s_ml[kCombThreads];
   const bd_attention_batch& b = p.b;
   const AttnLayout& L = p.L;
-  const int g = L.g, D = b.head_dim;
+  const int g = L.g, D = b.head_dim, H = b.n_kv_heads;
+  const int slices = D / (4 * kCombD4);
+  const int groups = kCombThreads / (kCombD4 * g);
+  const int row = threadIdx.x % g, q = threadIdx.x / g;
+  const int col = q % kCombD4, grp = q / kCombD4;
   griddep_wait();
   griddep_launch_dependents();
   const PlanHeader hd = *p.header();
-  const int tile_tok = 2 * L.half_tok;
-  const int64_t n_work = static_cast<int64_t>(hd.n_comb) * b.n_kv_heads;
+  const int64_t n_work = static_cast<int64_t>(hd.n_comb) * H * slices;
   for (int64_t w = blockIdx.x; w < n_work; w += gridDim.x) {
-    const int t = p.comb()[w / b.n_kv_heads];
-    const int kvh = static_cast<int>(w % b.n_kv_heads);
-    const int seq = p.tok_seq()[t];
-    // up to two families of parts: slots s_i = first + i·step of `rows` rows,
-    // the token's first row at row0
-    struct Family {
-      uint8_t *o, *ml;
-      int64_t first, step;
-      int n, rows, row0;
-    };
-    Family f[2] = {};
-    int64_t d_c0 = -1;  // decode parts: CTAs d_c0 .., the first in its slot 1
-    if (seq >= 0) {
-      const SeqRec r = p.seqs()[seq];
-      const int x = t - r.tok0;
-      if (static_cast<int64_t>(r.q_len) * g > L.d_rows) {
-        const int i = p.run_tile0()[seq] + x / tile_tok;
-        const int y = x % tile_tok;
-        f[0] = Family{p.ws + L.w_t_o, p.ws + L.w_t_ml,
-                      static_cast<int64_t>(p.tile_slot()[i]) * b.n_kv_heads + kvh, b.n_kv_heads,
-                      p.tile_ns()[i], 2 * kHalfRows,
-                      y / L.half_tok * kHalfRows + y % L.half_tok * g};
-      } else if (r.units > 0) {
-        const int64_t u0 = r.unit0 + static_cast<int64_t>(kvh) * r.units;
-        const int64_t c0 = u0 / hd.d_per, c1 = (u0 + r.units - 1) / hd.d_per;
-        if (c1 > c0) {
-          d_c0 = c0;
-          f[0] = Family{p.ws + L.w_d_o, p.ws + L.w_d_ml, 2 * c0, 2, static_cast<int>(c1 - c0) + 1,
-                        L.d_rows, x * g};
-        } else if (r.group >= 0) {
-          f[0] = Family{p.ws + L.w_r_o, p.ws + L.w_r_ml,
-                        static_cast<int64_t>(t) * b.n_kv_heads + kvh, 0, 1, g, 0};
-        }
-        // else: written by the decode kernel (another head of the token is cut)
-        else {
-          continue;
-        }
+    const CombItem it = p.comb()[w / (H * slices)];
+    const int kvh = static_cast<int>(w / slices % H);
+    const int d4 = static_cast<int>(w % slices) * kCombD4 + col;
+    // own parts: slot first + i·step (the very first one slot later for decode
+    // parts: their first CTA holds them as its last run), `rows` rows each
+    int64_t first = 0, step = H;
+    int n_own = it.own_ns, rows = 2 * kHalfRows, own_row = it.own_row, skip = 0;
+    uint8_t *o_base = p.ws + L.w_t_o, *ml_base = p.ws + L.w_t_ml;
+    if (it.units > 0) {
+      const int64_t u0 = it.unit0 + static_cast<int64_t>(kvh) * it.units;
+      const int64_t c0 = u0 / hd.d_per, c1 = (u0 + it.units - 1) / hd.d_per;
+      if (c1 > c0) {
+        first = 2 * c0;
+        step = 2;
+        skip = 1;
+        n_own = static_cast<int>(c1 - c0) + 1;
+        rows = L.d_rows;
+        o_base = p.ws + L.w_d_o;
+        ml_base = p.ws + L.w_d_ml;
+      } else {
+        if (it.pre_ns == 0) continue;  // final already; another head of the token is cut
+        first = static_cast<int64_t>(it.tok) * H + kvh;
+        n_own = 1;
+        rows = g;
+        own_row = 0;
+        o_base = p.ws + L.w_r_o;
+        ml_base = p.ws + L.w_r_ml;
       }
-      if (r.group >= 0) {
-        const int y0 = t - p.seqs()[b.group_offsets[r.group]].tok0;
-        const int i = p.run_tile0()[b.n_seq + r.group] + y0 / tile_tok;
-        const int y = y0 % tile_tok;
-        f[1] = Family{p.ws + L.w_t_o, p.ws + L.w_t_ml,
-                      static_cast<int64_t>(p.tile_slot()[i]) * b.n_kv_heads + kvh, b.n_kv_heads,
-                      p.tile_ns()[i], 2 * kHalfRows,
-                      y / L.half_tok * kHalfRows + y % L.half_tok * g};
+    } else {
+      first = static_cast<int64_t>(it.own_slot) * H + kvh;
+    }
+    const int n = n_own + it.pre_ns;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (grp < groups) {
+      for (int i0 = grp; i0 < n; i0 += groups * kCombBatch) {
+        float2 ml[kCombBatch];
+        float4 v[kCombBatch];
+#pragma unroll
+        for (int k = 0; k < kCombBatch; ++k) {
+          const int i = i0 + k * groups;
+          ml[k] = make_float2(-INFINITY, 0.f);
+          v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i < n_own) {
+            const int64_t slot = first + i * step + (i == 0 ? skip : 0);
+            ml[k] = part_ml(ml_base, slot, rows)[own_row + row];
+            v[k] = part_o(o_base, slot, rows, D)[static_cast<int64_t>(d4) * rows + own_row + row];
+          } else if (i < n) {
+            const int64_t slot = static_cast<int64_t>(it.pre_slot + (i - n_own)) * H + kvh;
+            ml[k] = part_ml(p.ws + L.w_t_ml, slot, 2 * kHalfRows)[it.pre_row + row];
+            v[k] = part_o(p.ws + L.w_t_o, slot, 2 * kHalfRows,
+                          D)[static_cast<int64_t>(d4) * 2 * kHalfRows + it.pre_row + row];
+          }
+        }
+        float top = m;
+#pragma unroll
+        for (int k = 0; k < kCombBatch; ++k) top = fmaxf(top, ml[k].x);
+        const float ref = top == -INFINITY ? 0.f : top;
+        const float f = ex2(m - ref);
+        l *= f;
+        o.x *= f;
+        o.y *= f;
+        o.z *= f;
+        o.w *= f;
+#pragma unroll
+        for (int k = 0; k < kCombBatch; ++k) {
+          const float s = ex2(ml[k].x - ref);
+          l = fmaf(ml[k].y, s, l);
+          o.x = fmaf(v[k].x, s, o.x);
+          o.y = fmaf(v[k].y, s, o.y);
+          o.z = fmaf(v[k].z, s, o.z);
+          o.w = fmaf(v[k].w, s, o.w);
+        }
+        m = top;
       }
     }
-    for (int e = threadIdx.x; e < g * (D / 4); e += kCombThreads) {
-      const int row = e % g, d4 = e / g;
-      float top = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll 4
-        for (int i = 0; i < f[k].n; ++i) {
-          const int64_t slot = f[k].first + i * f[k].step + (k == 0 && i == 0 && d_c0 >= 0 ? 1 : 0);
-          top = fmaxf(top, part_ml(f[k].ml, slot, f[k].rows)[f[k].row0 + row].x);
-        }
-      const float ref = top == -INFINITY ? 0.f : top;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      float l = 0.f;
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll 4
-        for (int i = 0; i < f[k].n; ++i) {
-          const int64_t slot = f[k].first + i * f[k].step + (k == 0 && i == 0 && d_c0 >= 0 ? 1 : 0);
-          const float2 ml = part_ml(f[k].ml, slot, f[k].rows)[f[k].row0 + row];
-          const float4 v =
-              part_o(f[k].o, slot, f[k].rows, D)[static_cast<int64_t>(d4) * f[k].rows + f[k].row0 + row];
-          const float s = ex2(ml.x - ref);
-          l = fmaf(ml.y, s, l);
-          o.x = fmaf(v.x, s, o.x);
-          o.y = fmaf(v.y, s, o.y);
-          o.z = fmaf(v.z, s, o.z);
-          o.w = fmaf(v.w, s, o.w);
-        }
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const int64_t at = static_cast<int64_t>(t) * b.n_q_heads + kvh * g + row;
-      reinterpret_cast<uint2*>(p.out + at * D)[d4] =
-          make_uint2(pack_bf16x2_rn(o.x * inv, o.y * inv), pack_bf16x2_rn(o.z * inv, o.w * inv));
-      if (d4 == 0 && p.lse != nullptr)
-        p.lse[at] = l > 0.f ? (ref + log2f(l)) * kLn2 : -INFINITY;
+    __syncthreads();  // the last item's values have been read
+    s_o[threadIdx.x] = o;
+    s_ml[threadIdx.x] = make_float2(m, l);
+    __syncthreads();
+    if (grp != 0) continue;
+    const int span = g * kCombD4, most = groups < n ? groups : n;
+    float top = m;
+    for (int k = 1; k < most; ++k) top = fmaxf(top, s_ml[threadIdx.x + k * span].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float f = ex2(m - ref);
+    l *= f;
+    o.x *= f;
+    o.y *= f;
+    o.z *= f;
+    o.w *= f;
+    for (int k = 1; k < most; ++k) {
+      const float2 ml = s_ml[threadIdx.x + k * span];
+      const float4 v = s_o[threadIdx.x + k * span];
+      const float s = ex2(ml.x - ref);
+      l = fmaf(ml.y, s, l);
+      o.x = fmaf(v.x, s, o.x);
+      o.y = fmaf(v.y, s, o.y);
+      o.z = fmaf(v.z, s, o.z);
+      o.w = fmaf(v.w, s, o.w);
     }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int64_t at = static_cast<int64_t>(it.tok) * b.n_q_heads + kvh * g + row;
+    reinterpret_cast<uint2*>(p.out + at * D)[d4] =
+        make_uint2(pack_bf16x2_rn(o.x * inv, o.y * inv), pack_bf16x2_rn(o.z * inv, o.w * inv));
+    if (d4 == 0 && p.lse != nullptr)
+      p.lse[at] = l > 0.f ? (ref + log2f(l)) * kLn2 : -INFINITY;
   }
 }
 
@@ -521,8 +590,8 @@ bd_status run_attention(AttnArgs& p, cudaStream_t s) {
       !encode_tmap_bf16_3d(&tv, p.v_pages, kdims, kstr, box))
     return BD_ERR_CUDA;
   if (launch_attn_decode(p, tk, tv, s) != cudaSuccess) return BD_ERR_CUDA;
-  const int64_t work = b.n_tokens * b.n_kv_heads;
-  const int64_t most = 4 * static_cast<int64_t>(p.L.t_ctas);
+  const int64_t work = b.n_tokens * b.n_kv_heads * (b.head_dim / (4 * kCombD4));
+  const int64_t most = 8 * static_cast<int64_t>(p.L.t_ctas);
   const cudaError_t e = launch_pdl(combine_kernel, dim3(static_cast<unsigned>(work < most ? work : most)),
                                    dim3(kCombThreads), 0, s, p);
   return e == cudaSuccess ? BD_OK : BD_ERR_CUDA;

@@ -40,6 +40,28 @@ struct SeqRec {
   int32_t group;      // group whose prefix it reads, or −1
 };
 
+// Where a CTA of the decode kernel begins: its units [lo, hi) and the sequence
+// that holds lo.  One load, so that the kernel's first page ids are one step
+// away.
+struct DecodeStart {
+  SeqRec r;
+  int64_t lo, hi;
+  int32_t seq, pad[3];
+};
+
+// A token whose rows the combine kernel writes, and where its parts lie.  Own
+// part: tile slots own_slot .. (own_ns of them, rows from own_row), or decode
+// units (units > 0: rows from own_row, the slots following from the head's
+// units).  Prefix part: pre_ns tile slots.
+struct CombItem {
+  int64_t unit0;
+  int32_t units;
+  int32_t tok;
+  int32_t own_slot, own_ns, own_row;
+  int32_t pre_slot, pre_ns, pre_row;
+  int32_t pad[2];
+};
+
 // One piece of the tile kernel's work: a tile of query tokens by a range of
 // 128-key blocks.
 struct TileEntry {
@@ -84,29 +106,17 @@ struct AttnArgs {
   __host__ __device__ const PlanHeader* header() const {
     return reinterpret_cast<const PlanHeader*>(plan);
   }
-  __host__ __device__ const int32_t* tok_seq() const {
-    return reinterpret_cast<const int32_t*>(plan + L.o_tok_seq);
-  }
   __host__ __device__ const SeqRec* seqs() const {
     return reinterpret_cast<const SeqRec*>(plan + L.o_seq);
   }
-  __host__ __device__ const int32_t* starts() const {
-    return reinterpret_cast<const int32_t*>(plan + L.o_start);
-  }
-  __host__ __device__ const int32_t* run_tile0() const {
-    return reinterpret_cast<const int32_t*>(plan + L.o_run);
-  }
-  __host__ __device__ const int32_t* tile_slot() const {
-    return reinterpret_cast<const int32_t*>(plan + L.o_tile_slot);
-  }
-  __host__ __device__ const int32_t* tile_ns() const {
-    return reinterpret_cast<const int32_t*>(plan + L.o_tile_ns);
+  __host__ __device__ const DecodeStart* starts() const {
+    return reinterpret_cast<const DecodeStart*>(plan + L.o_start);
   }
   __host__ __device__ const TileEntry* entries() const {
     return reinterpret_cast<const TileEntry*>(plan + L.o_entry);
   }
-  __host__ __device__ const int32_t* comb() const {
-    return reinterpret_cast<const int32_t*>(plan + L.o_comb);
+  __host__ __device__ const CombItem* comb() const {
+    return reinterpret_cast<const CombItem*>(plan + L.o_comb);
   }
 };
 

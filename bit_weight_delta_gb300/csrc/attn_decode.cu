@@ -116,15 +116,14 @@ __global__ void __launch_bounds__(32 * kDecodeWarps, 2)
   griddep_wait();
   griddep_launch_dependents();
 
-  const PlanHeader hd = *p.header();
-  const int64_t lo = static_cast<int64_t>(blockIdx.x) * hd.d_per;
-  const int64_t hi = lo + hd.d_per < hd.d_units ? lo + hd.d_per : hd.d_units;
-  if (lo >= hi) return;
+  const DecodeStart st = p.starts()[blockIdx.x];
+  const int64_t lo = st.lo;
+  if (lo >= st.hi) return;
   Walk cons{};
-  cons.seq = p.starts()[blockIdx.x];
-  cons.r = p.seqs()[cons.seq];
+  cons.seq = st.seq;
+  cons.r = st.r;
   cons.at = lo;
-  cons.end = hi;
+  cons.end = st.hi;
   Walk prod = cons;
   const int g = p.L.g;
   const int page_shift = 31 - __clz(b.page_size);
