@@ -46,8 +46,9 @@ struct Cfg {
   static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kOffKv = kQBytes;
   static constexpr int kOffBar = kOffKv + kStages * kStageBytes;
-  // q_full, q_empty, s_full[2], p_full[2], o_full[2], tail, drain, kv_full[], kv_empty[]
-  static constexpr int kBars = 10 + 2 * kStages;
+  // q_full, q_empty, s_full[2], p_full[2][2], o_full[2], tail, drain, kv_full[],
+  // kv_empty[]
+  static constexpr int kBars = 12 + 2 * kStages;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kSmem = kOffMisc + 16 + 1024;  // with slack for alignment
 };
@@ -131,6 +132,44 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
 }
 constexpr uint32_t kIdescB_MN = 1u << 16;  // instruction descriptor: B is MN-major
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Two fp32 values in one 64-bit register and the paired operations on them.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+               : "=r"(p));
+  return p != 0;
+}
+// Bounded wait of a whole warp, with one answer for all its lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const DevCtx& ctx,
+                                          volatile int* abort) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, ctx, abort));
+}
+
 // The pieces of one CTA in turn, each fetched while the one before it runs.
 struct Pieces {
   const AttnArgs& p;
@@ -188,10 +227,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* q_empty = q_full + 1;
   uint64_t* s_full = q_full + 2;
   uint64_t* p_full = q_full + 4;
-  uint64_t* o_full = q_full + 6;
-  uint64_t* tail_bar = q_full + 8;
-  uint64_t* drain_bar = q_full + 9;
-  uint64_t* kv_full = q_full + 10;
+  uint64_t* o_full = q_full + 8;
+  uint64_t* tail_bar = q_full + 10;
+  uint64_t* drain_bar = q_full + 11;
+  uint64_t* kv_full = q_full + 12;
   uint64_t* kv_empty = kv_full + C::kStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
@@ -204,7 +243,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(q_empty, 1);
     for (int h = 0; h < 2; ++h) {
       mbar_init(&s_full[h], 1);
-      mbar_init(&p_full[h], 4);
+      mbar_init(&p_full[2 * h], 4);
+      mbar_init(&p_full[2 * h + 1], 4);
       mbar_init(&o_full[h], 1);
     }
     mbar_init(tail_bar, 1);
@@ -254,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float mref = -INFINITY, l = 0.f;
       for (int j = e.b0; j < end; ++j) {
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&s_full[h], s_phase, p.ctx, abort));
+        ok = warp_wait(&s_full[h], s_phase, p.ctx, abort);
         if (!ok) break;
         s_phase ^= 1u;
         tc_fence_after();
@@ -273,9 +313,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         float top[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          top[c] = __uint_as_float(s[c][0]);
+          top[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
 #pragma unroll
-          for (int x = 1; x < 32; ++x) top[c] = fmaxf(top[c], __uint_as_float(s[c][x]));
+          for (int x = 2; x < 32; x += 2)
+            top[c] = max3(top[c], __uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1]));
         }
         const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
         if (__any_sync(0xFFFFFFFFu, mx > mref + kRescale)) {
@@ -299,33 +340,42 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float ref = mref == -INFINITY ? 0.f : mref;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        // weights two at a time: the row maximum and the sum are then half the
+        // instructions of the scalar form
+        const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), ref2 = pack2(-ref, -ref);
+        uint64_t sum[2] = {0u, 0u};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t w[16];
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
-            const float a = ex2(fmaf(__uint_as_float(s[c][2 * x]), p.scale_log2, -ref));
-            const float z = ex2(fmaf(__uint_as_float(s[c][2 * x + 1]), p.scale_log2, -ref));
-            sum[(2 * x) & 3] += a;
-            sum[(2 * x + 1) & 3] += z;
+            float a, z;
+            unpack2(fma2(pack2(__uint_as_float(s[c][2 * x]), __uint_as_float(s[c][2 * x + 1])),
+                         scale2, ref2), a, z);
+            a = ex2(a);
+            z = ex2(z);
+            sum[x & 1] = add2(sum[x & 1], pack2(a, z));
             // rounded to bf16, the tensor core's operand type: 2^-9 of each
             // weight, while l sums them unrounded
             w[x] = pack_bf16x2_rn(a, z);
           }
           tmem_st_x16(t_s + 16u * c, w);
+          if (c & 1) {  // 64 keys' weights are written: their product may start
+            tmem_st_done();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[2 * h + (c >> 1)]);
+          }
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_st_done();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[h]);
+        float l0, l1;
+        unpack2(add2(sum[0], sum[1]), l0, l1);
+        l += l0 + l1;
       }
       if (!ok) break;
       // ---- epilogue: the half's rows, final or as a partial result
       const bool any = end > e.b0;
       if (any) {
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&o_full[h], o_phase, p.ctx, abort));
+        ok = warp_wait(&o_full[h], o_phase, p.ctx, abort);
         if (!ok) break;
         o_phase ^= 1u;
         tc_fence_after();
@@ -374,8 +424,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     reg_dec<kOtherRegs>();
-    if (warp == kMmaWarp && lane == 0) {
+    if (warp == kMmaWarp) {
       // ========================================================== MMA issuer
+      // The whole warp walks the pieces, so that descriptors and addresses stay
+      // in uniform registers, and one elected lane issues: with a single-lane
+      // walk each product took about 100 cycles to issue, against 64 to run.
+      const bool lead = elect_one();
       constexpr uint32_t idesc_s = idesc_bf16_f32(128, kTileKeys);
       constexpr uint32_t idesc_o = idesc_bf16_f32(128, D) | kIdescB_MN;
       const uint32_t q_base = smem_addr(smem);
@@ -384,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int64_t fill = 0;  // ring position of the current block's K
       bool ok = true, issued = false;
       const auto wait_fill = [&](int64_t f) {
-        return mbar_wait(&kv_full[f % C::kStages],
+        return warp_wait(&kv_full[f % C::kStages],
                          static_cast<uint32_t>((f / C::kStages) & 1), p.ctx, abort);
       };
       Pieces pieces(p);
@@ -392,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int kvh;
       while (ok && pieces.take(e, kvh)) {
         const int end[2] = {half_end(e, 0, half_tok), half_end(e, 1, half_tok)};
-        ok = mbar_wait(q_full, q_phase, p.ctx, abort);
+        ok = warp_wait(q_full, q_phase, p.ctx, abort);
         q_phase ^= 1u;
         for (int j = e.b0; ok && j <= e.b1; ++j) {
           bool have_v = false, have_k = false;
@@ -400,20 +454,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (j > e.b0 && j - 1 < end[h]) {  // O += P·V of block j − 1
               if (!have_v) ok = wait_fill(fill - 1);
               have_v = true;
-              ok = ok && mbar_wait(&p_full[h], p_phase[h], p.ctx, abort);
+              ok = ok && warp_wait(&p_full[2 * h], p_phase[h], p.ctx, abort);
               if (!ok) break;
-              p_phase[h] ^= 1u;
               tc_fence_after();
               const uint64_t vd =
                   sdesc_mn_sw128(kv_base + static_cast<uint32_t>((fill - 1) % C::kStages) *
                                                C::kStageBytes);
               const int left = e.k_hi - e.k_lo - (j - 1) * kTileKeys;
               const int steps = left >= kTileKeys ? kTileKeys / 16 : (left + 15) / 16;
-              for (int k = 0; k < steps; ++k)
-                mma_ts(tmem + 256u + 128u * h, tmem + 128u * h + 8u * k, vd + 128u * k, idesc_o,
-                       j - 1 > e.b0 || k > 0 ? 1u : 0u);
+              const uint32_t t_o = tmem + 256u + 128u * h, t_p = tmem + 128u * h;
+              const uint32_t acc = j - 1 > e.b0 ? 1u : 0u;
+              // the weights of the block's first 64 keys, then of the others
+              if (lead) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  if (k < steps)
+                    mma_ts(t_o, t_p + 8u * k, vd + 128u * k, idesc_o, k > 0 ? 1u : acc);
+              }
               issued = true;
-              if (j == end[h]) mma_commit(&o_full[h]);
+              ok = warp_wait(&p_full[2 * h + 1], p_phase[h], p.ctx, abort);
+              if (!ok) break;
+              p_phase[h] ^= 1u;
+              tc_fence_after();
+              if (lead) {
+#pragma unroll
+                for (int k = 4; k < 8; ++k)
+                  if (k < steps) mma_ts(t_o, t_p + 8u * k, vd + 128u * k, idesc_o, 1u);
+                if (j == end[h]) mma_commit(&o_full[h]);
+              }
             }
             if (j < e.b1 && j < end[h]) {  // S = Q·Kᵀ of block j
               if (!have_k) ok = wait_fill(fill);
@@ -423,26 +491,32 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint64_t qd = sdesc_k_sw128(q_base + static_cast<uint32_t>(h) * C::kStageBytes);
               const uint64_t kd = sdesc_k_sw128(
                   kv_base + static_cast<uint32_t>(fill % C::kStages) * C::kStageBytes);
+              if (lead) {
 #pragma unroll
-              for (int k = 0; k < D / 16; ++k) {
-                const uint64_t step = static_cast<uint64_t>((k >> 2) * (kPanel >> 4) + 2 * (k & 3));
-                mma_ss(tmem + 128u * h, qd + step, kd + step, idesc_s, k > 0 ? 1u : 0u);
+                for (int k = 0; k < D / 16; ++k) {
+                  const uint64_t step =
+                      static_cast<uint64_t>((k >> 2) * (kPanel >> 4) + 2 * (k & 3));
+                  mma_ss(tmem + 128u * h, qd + step, kd + step, idesc_s, k > 0 ? 1u : 0u);
+                }
               }
               issued = true;
-              mma_commit(&s_full[h]);
+              if (lead) mma_commit(&s_full[h]);
             }
           }
           if (!ok) break;
-          if (j > e.b0) mma_commit(&kv_empty[(fill - 1) % C::kStages]);
-          if (j < e.b1) mma_commit(&kv_empty[fill % C::kStages]);
-          if (j == e.b1 - 1) mma_commit(q_empty);
+          if (lead) {
+            if (j > e.b0) mma_commit(&kv_empty[(fill - 1) % C::kStages]);
+            if (j < e.b1) mma_commit(&kv_empty[fill % C::kStages]);
+            if (j == e.b1 - 1) mma_commit(q_empty);
+          }
           if (j < e.b1) fill += 2;
         }
       }
       if (issued) {
-        mma_commit(drain_bar);
+        if (lead) mma_commit(drain_bar);
         mbar_wait(drain_bar, 0, p.ctx, nullptr);
       }
+      __syncwarp();
     } else if (warp == kTmaWarp) {
       // ========================================================== TMA producer
       const int page_shift = 31 - __clz(b.page_size);
@@ -456,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const auto load_block = [&](const CUtensorMap* map, int page, int n_pg, int kvh, int zero0) {
         const int s = static_cast<int>(fill % C::kStages);
         const uint32_t ph = static_cast<uint32_t>((fill / C::kStages) & 1);
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&kv_empty[s], ph ^ 1u, p.ctx, abort));
+        ok = warp_wait(&kv_empty[s], ph ^ 1u, p.ctx, abort);
         if (!ok) return;
         uint8_t* dst = smem + C::kOffKv + s * C::kStageBytes;
         uint64_t* bar = zero0 >= 0 ? tail_bar : &kv_full[s];
@@ -475,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (zero0 >= 0) {
           // Values past the last key may be anything, and zero weights do not
           // cancel a NaN: clear them up to the end of their 16-key step.
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait(tail_bar, tail_phase, p.ctx, abort));
+          ok = warp_wait(tail_bar, tail_phase, p.ctx, abort);
           tail_phase ^= 1u;
           const int n = ((zero0 + 15) / 16 * 16 - zero0) * 8;
           for (int x = lane; x < n * C::kPanels; x += 32)
@@ -506,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return id;
         };
         int page = page_of(e.b0);
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(q_empty, q_phase, p.ctx, abort));
+        ok = warp_wait(q_empty, q_phase, p.ctx, abort);
         q_phase ^= 1u;
         if (!ok) break;
         const int halves = e.n_tok > half_tok ? 2 : 1;
