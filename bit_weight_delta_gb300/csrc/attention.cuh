@@ -139,9 +139,11 @@ __device__ __forceinline__ float ex2(float x) {
 constexpr float kLn2 = 0.69314718055994531f;
 
 // The running reference m of a row's softmax follows its maximum only in steps
-// of more than this (log2 units): weights are then at most 2^8, sums stay far
-// inside fp32, and the sums are rarely rescaled.
-constexpr float kRescale = 8.f;
+// of more than this (log2 units).  Any reference within the exponents' range
+// gives the same relative precision (weights are fp32 and bf16, sums fp32): a
+// row's weights are at most 2^40 and 2^30 of them, times |v|, stay inside fp32,
+// and the sums are seldom rescaled.
+constexpr float kRescale = 40.f;
 
 cudaError_t launch_attn_decode(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
                                cudaStream_t s);

@@ -11,11 +11,11 @@
 //   O += P·V   (128 x D, fp32, in tensor memory; P from tensor memory).
 // The two halves take turns: while one half's warpgroup works on its weights,
 // the tensor core runs the other half's products.  O is rescaled only when a
-// row's maximum has grown by more than 2^8 since the last time.
+// row's maximum has left the reference's range (kRescale).
 //
 // Tensor memory (512 columns): S/P of half h at 128·h, O of half h at 256 +
-// 128·h.  Warps: 0-3 and 4-7 the halves' softmax and epilogue, 8 the MMA
-// issuer, 9 the TMA producer (10, 11 idle).  Q, K and V lie in shared memory in
+// 128·h.  Warps: 0-3 and 4-7 the halves' softmax and epilogue, 8 and 9
+// their MMA issuers, 10 and 11 the TMA producers of Q and K, and of V.  Q, K and V lie in shared memory in
 // the 128-byte swizzle, 64 columns (128 bytes) of 128 rows per 16 KB panel; K
 // is the K-major B operand, V (keys x D as stored) the MN-major one.
 //
@@ -29,8 +29,8 @@ namespace bd {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kMmaWarp = 8;
-constexpr int kTmaWarp = 9;
+constexpr int kMmaWarp = 8;  // and the next one: a half each
+constexpr int kTmaWarp = 10;  // K and Q; the next one V
 constexpr int kPanel = kTileKeys * 128;  // 128 rows x 128 bytes
 // 384 threads launch with 168 registers each; the two softmax warpgroups take
 // 208 and leave 88 for the third: 2·208 + 88 = 3·168.
@@ -45,10 +45,11 @@ struct Cfg {
   static constexpr int kQBytes = 2 * kPanels * kPanel;
   static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kOffKv = kQBytes;
-  static constexpr int kOffBar = kOffKv + kStages * kStageBytes;
-  // q_full, q_empty, s_full[2], p_full[2][2], o_full[2], tail, drain, kv_full[],
-  // kv_empty[]
-  static constexpr int kBars = 12 + 2 * kStages;
+  static constexpr int kOffOut = kOffKv + kStages * kStageBytes;  // 4 KB per softmax warp
+  static constexpr int kOffBar = kOffOut + 8 * 4096;
+  // q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], tail, drain[2],
+  // turn[2], kv_full[], kv_empty[]
+  static constexpr int kBars = 17 + 2 * kStages;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kSmem = kOffMisc + 16 + 1024;  // with slack for alignment
 };
@@ -170,37 +171,43 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, ctx, abort));
 }
 
-// The pieces of one CTA in turn, each fetched while the one before it runs.
+// The pieces of one CTA in turn.  Every role calls fetch() for the next piece
+// while it works on the current one (loads and a division off the path between
+// two pieces) and take() when it is done.
 struct Pieces {
-  const AttnArgs& p;
-  int64_t n, k;
+  const TileEntry* entries;
+  int n, heads, k = 0, next_h = 0;
+  bool has = false;
   TileEntry next;
-  int next_h;
-  bool has;
   __device__ __forceinline__ explicit Pieces(const AttnArgs& a)
-      : p(a), n(static_cast<int64_t>(a.header()->t_entries) * a.b.n_kv_heads), k(0) {
-    fetch();
+      : entries(a.entries()), heads(a.b.n_kv_heads) {
+    // the first entry's address does not depend on how many there are (the
+    // plan's table has at least one per CTA), so the two loads overlap
+    const int32_t count = *const_cast<const volatile int32_t*>(&a.header()->t_entries);
+    load(static_cast<int>(blockIdx.x));
+    n = count * heads;
+    has = static_cast<int>(blockIdx.x) < n;
+    k = 1;
+  }
+  __device__ __forceinline__ void load(int i) {
+    const int q = static_cast<int>(static_cast<unsigned>(i) / static_cast<unsigned>(heads));
+    const int4* src = reinterpret_cast<const int4*>(entries + q);
+    const int4 x = __ldg(src), y = __ldg(src + 1), z = __ldg(src + 2);
+    next = TileEntry{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, 0, 0};
+    next_h = i - q * heads;
   }
   __device__ __forceinline__ void fetch() {
-    const int64_t c = blockIdx.x, w = gridDim.x;
-    const int64_t i = k * w + ((k & 1) ? w - 1 - c : c);
+    const int c = static_cast<int>(blockIdx.x), w = static_cast<int>(gridDim.x);
+    const int i = k * w + ((k & 1) ? w - 1 - c : c);
     has = i < n;
-    if (has) {
-      const int4* src = reinterpret_cast<const int4*>(p.entries() + i / p.b.n_kv_heads);
-      const int4 x = __ldg(src), y = __ldg(src + 1), z = __ldg(src + 2);
-      next = TileEntry{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, 0, 0};
-      next_h = static_cast<int>(i % p.b.n_kv_heads);
-    }
+    if (has) load(i);
     ++k;
   }
-  __device__ __forceinline__ bool take(TileEntry& e, int& h) {
-    // later rounds hold shorter rows of pieces: once one is missing in an
-    // even round none follows; a missing odd-round piece likewise
-    if (!has) return false;
+  // once a piece is missing in one round, none follows in a later one
+  __device__ __forceinline__ bool take(TileEntry& e, int& h) const {
     e = next;
     h = next_h;
-    fetch();
-    return true;
+    return has;
   }
 };
 
@@ -224,34 +231,39 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  uint64_t* q_empty = q_full + 1;
-  uint64_t* s_full = q_full + 2;
-  uint64_t* p_full = q_full + 4;
-  uint64_t* o_full = q_full + 8;
-  uint64_t* tail_bar = q_full + 10;
-  uint64_t* drain_bar = q_full + 11;
-  uint64_t* kv_full = q_full + 12;
+  uint64_t* q_empty = q_full + 2;
+  uint64_t* s_full = q_full + 4;
+  uint64_t* p_full = q_full + 6;
+  uint64_t* o_full = q_full + 10;
+  uint64_t* tail_bar = q_full + 12;
+  uint64_t* drain_bar = q_full + 13;
+  uint64_t* turn = q_full + 15;
+  uint64_t* kv_full = q_full + 17;
   uint64_t* kv_empty = kv_full + C::kStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   const bd_attention_batch& b = p.b;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (a value from lane 0 is known to be the same in all lanes)
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
+  const int lane = threadIdx.x & 31;
   const int half_tok = p.L.half_tok, g = p.L.g;
 
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
     for (int h = 0; h < 2; ++h) {
+      mbar_init(&q_full[h], 1);
+      mbar_init(&q_empty[h], 1);
       mbar_init(&s_full[h], 1);
       mbar_init(&p_full[2 * h], 4);
       mbar_init(&p_full[2 * h + 1], 4);
       mbar_init(&o_full[h], 1);
+      mbar_init(&turn[h], 1);
     }
     mbar_init(tail_bar, 1);
-    mbar_init(drain_bar, 1);
+    mbar_init(&drain_bar[0], 1);
+    mbar_init(&drain_bar[1], 1);
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&kv_full[s], 1);
-      mbar_init(&kv_empty[s], 1);
+      mbar_init(&kv_empty[s], 2);
     }
     *abort = 0;
     fence_mbar_init();
@@ -265,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   griddep_wait();
   griddep_launch_dependents();
 
@@ -310,6 +322,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int x = 0; x < 32; ++x)
               if (32 * c + x >= seen) s[c][x] = 0xFF800000u;  // −inf
         }
+        // Weights two at a time (paired fp32 operations: half the instructions),
+        // relative to a reference that follows the row's maximum lazily.
+        // (Forming the first weights before the maximum is known, to be redone
+        // where it moves, measured 15% slower.)
+        const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
+        uint64_t sum[2] = {0u, 0u};
+        const auto weigh = [&](int c, uint64_t ref2) {
+          uint32_t w[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            float a, z;
+            unpack2(fma2(pack2(__uint_as_float(s[c][2 * x]), __uint_as_float(s[c][2 * x + 1])),
+                         scale2, ref2), a, z);
+            a = ex2(a);
+            z = ex2(z);
+            sum[x & 1] = add2(sum[x & 1], pack2(a, z));
+            // rounded to bf16, the tensor core's operand type: 2^-9 of each
+            // weight, while l sums them unrounded
+            w[x] = pack_bf16x2_rn(a, z);
+          }
+          tmem_st_x16(t_s + 16u * c, w);
+        };
+        const auto done = [&](int part) {  // 64 keys' weights are written
+          tmem_st_done();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * h + part]);
+        };
         float top[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -340,38 +380,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float ref = mref == -INFINITY ? 0.f : mref;
-        // weights two at a time: the row maximum and the sum are then half the
-        // instructions of the scalar form
-        const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), ref2 = pack2(-ref, -ref);
-        uint64_t sum[2] = {0u, 0u};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[16];
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            float a, z;
-            unpack2(fma2(pack2(__uint_as_float(s[c][2 * x]), __uint_as_float(s[c][2 * x + 1])),
-                         scale2, ref2), a, z);
-            a = ex2(a);
-            z = ex2(z);
-            sum[x & 1] = add2(sum[x & 1], pack2(a, z));
-            // rounded to bf16, the tensor core's operand type: 2^-9 of each
-            // weight, while l sums them unrounded
-            w[x] = pack_bf16x2_rn(a, z);
-          }
-          tmem_st_x16(t_s + 16u * c, w);
-          if (c & 1) {  // 64 keys' weights are written: their product may start
-            tmem_st_done();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[2 * h + (c >> 1)]);
-          }
-        }
+        const uint64_t ref2 = pack2(-ref, -ref);
+        weigh(0, ref2);
+        weigh(1, ref2);
+        done(0);
+        weigh(2, ref2);
+        weigh(3, ref2);
+        done(1);
         float l0, l1;
         unpack2(add2(sum[0], sum[1]), l0, l1);
         l += l0 + l1;
       }
       if (!ok) break;
+      pieces.fetch();
       // ---- epilogue: the half's rows, final or as a partial result
       const bool any = end > e.b0;
       if (any) {
@@ -380,37 +401,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         o_phase ^= 1u;
         tc_fence_after();
       }
-      const int64_t at = (static_cast<int64_t>(e.tok0) + i) * b.n_q_heads + kvh * g + row_head;
       const float inv = l > 0.f ? 1.f / l : 0.f;
+      const int row_at = i * b.n_q_heads + row_head;  // the row's head in the tile's tokens
+      const int64_t tile_at = static_cast<int64_t>(e.tok0) * b.n_q_heads + kvh * g;
       const int64_t slot = static_cast<int64_t>(e.slot) * b.n_kv_heads + kvh;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
+#pragma unroll 1  // code that runs once a piece: kept short for the instruction cache
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t o[2][32];
         if (any) {
-          tmem_ld_32x32b_x32(t_o + 32u * c, o);
+          tmem_ld_32x32b_x32(t_o + 64u * c, o[0]);
+          tmem_ld_32x32b_x32(t_o + 64u * c + 32u, o[1]);
           tmem_ld_wait();
         } else {
 #pragma unroll
-          for (int x = 0; x < 32; ++x) o[x] = 0u;
+          for (int x = 0; x < 32; ++x) o[0][x] = o[1][x] = 0u;
         }
-        if (live && e.slot < 0) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + at * D) + 4 * c;
+        if (e.slot < 0) {
+          // Through shared memory (swizzled), so that a store instruction
+          // covers whole 128-byte lines of four rows: with a row per lane the
+          // 32 lines of each store took 3 µs a piece.
+          uint8_t* mine = smem + C::kOffOut + warp * 4096;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t v[4];
+          for (int x = 0; x < 8; ++x) {
+            const uint32_t* v = &o[x >> 2][8 * (x & 3)];
+            uint32_t w[4];
 #pragma unroll
             for (int y = 0; y < 4; ++y)
-              v[y] = pack_bf16x2_rn(__uint_as_float(o[8 * x + 2 * y]) * inv,
-                                    __uint_as_float(o[8 * x + 2 * y + 1]) * inv);
-            dst[x] = make_uint4(v[0], v[1], v[2], v[3]);
+              w[y] = pack_bf16x2_rn(__uint_as_float(v[2 * y]) * inv,
+                                    __uint_as_float(v[2 * y + 1]) * inv);
+            *reinterpret_cast<uint4*>(mine + lane * 128 + ((x ^ (lane & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
           }
+          __syncwarp();
+          int at[8];
+          uint4 v[8];
+          const int chunk = lane & 7;
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const int row = 4 * x + (lane >> 3);
+            at[x] = __shfl_sync(0xFFFFFFFFu, live ? row_at : -1, row);
+            v[x] = *reinterpret_cast<const uint4*>(mine + row * 128 + ((chunk ^ (row & 7)) << 4));
+          }
+          uint16_t* dst = p.out + tile_at * D + 64 * c + 8 * chunk;
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            if (at[x] >= 0) *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(at[x]) * D) = v[x];
+          __syncwarp();
         } else if (live) {
           float4* dst = part_o(p.ws + p.L.w_t_o, slot, 2 * kHalfRows, D) + h * kHalfRows + r;
 #pragma unroll
-          for (int x = 0; x < 8; ++x)
-            dst[(8 * c + x) * 2 * kHalfRows] =
-                make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
-                            __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
+          for (int x = 0; x < 16; ++x) {
+            const uint32_t* v = &o[x >> 3][4 * (x & 7)];
+            dst[(16 * c + x) * 2 * kHalfRows] =
+                make_float4(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]),
+                            __uint_as_float(v[3]));
+          }
         }
         __syncwarp();
       }
@@ -418,200 +463,212 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (e.slot >= 0)
           part_ml(p.ws + p.L.w_t_ml, slot, 2 * kHalfRows)[h * kHalfRows + r] = make_float2(mref, l);
         else if (p.lse != nullptr)
-          p.lse[at] = l > 0.f ? (mref + log2f(l)) * kLn2 : -INFINITY;
+          p.lse[tile_at + row_at] = l > 0.f ? (mref + log2f(l)) * kLn2 : -INFINITY;
       }
       tc_fence_before();  // O has been read before the next piece's first P is signalled
     }
   } else {
     reg_dec<kOtherRegs>();
-    if (warp == kMmaWarp) {
-      // ========================================================== MMA issuer
-      // The whole warp walks the pieces, so that descriptors and addresses stay
-      // in uniform registers, and one elected lane issues: with a single-lane
-      // walk each product took about 100 cycles to issue, against 64 to run.
+    if (warp < kTmaWarp) {
+      // ========================================================== MMA issuers
+      // A warp per half, so that one half's waits do not hold up the other's
+      // products, and a turn that they pass to and fro with each block's two
+      // products.  Without it the halves' products interleave, their softmaxes
+      // then run side by side on the same schedulers, and a block takes a
+      // quarter longer (3450 cycles against 2810).  The whole warp walks the
+      // pieces, which keeps descriptors and addresses in uniform registers, and
+      // one elected lane issues: with a single-lane walk a product took about
+      // 100 cycles to issue, against 64 to run.
+      const int h = warp - kMmaWarp;
       const bool lead = elect_one();
       constexpr uint32_t idesc_s = idesc_bf16_f32(128, kTileKeys);
       constexpr uint32_t idesc_o = idesc_bf16_f32(128, D) | kIdescB_MN;
-      const uint32_t q_base = smem_addr(smem);
       const uint32_t kv_base = smem_addr(smem + C::kOffKv);
-      uint32_t q_phase = 0, p_phase[2] = {0, 0};
-      int64_t fill = 0;  // ring position of the current block's K
+      const uint32_t t_s = tmem + 128u * h, t_o = tmem + 256u + 128u * h;
+      const uint64_t qd = sdesc_k_sw128(smem_addr(smem) + static_cast<uint32_t>(h) * C::kStageBytes);
+      uint32_t q_phase = 0, p_phase = 0, my_turn = h == 0 ? 1u : 0u;
+      int stage = 0, v_stage = 1;      // of the current K, of the last block's V
+      uint32_t phase = 0, v_phase = 0;
       bool ok = true, issued = false;
-      const auto wait_fill = [&](int64_t f) {
-        return warp_wait(&kv_full[f % C::kStages],
-                         static_cast<uint32_t>((f / C::kStages) & 1), p.ctx, abort);
-      };
       Pieces pieces(p);
       TileEntry e;
       int kvh;
       while (ok && pieces.take(e, kvh)) {
-        const int end[2] = {half_end(e, 0, half_tok), half_end(e, 1, half_tok)};
-        ok = warp_wait(q_full, q_phase, p.ctx, abort);
-        q_phase ^= 1u;
-        for (int j = e.b0; ok && j <= e.b1; ++j) {
-          bool have_v = false, have_k = false;
-          for (int h = 0; h < 2 && ok; ++h) {
-            if (j > e.b0 && j - 1 < end[h]) {  // O += P·V of block j − 1
-              if (!have_v) ok = wait_fill(fill - 1);
-              have_v = true;
-              ok = ok && warp_wait(&p_full[2 * h], p_phase[h], p.ctx, abort);
-              if (!ok) break;
-              tc_fence_after();
-              const uint64_t vd =
-                  sdesc_mn_sw128(kv_base + static_cast<uint32_t>((fill - 1) % C::kStages) *
-                                               C::kStageBytes);
-              const int left = e.k_hi - e.k_lo - (j - 1) * kTileKeys;
-              const int steps = left >= kTileKeys ? kTileKeys / 16 : (left + 15) / 16;
-              const uint32_t t_o = tmem + 256u + 128u * h, t_p = tmem + 128u * h;
-              const uint32_t acc = j - 1 > e.b0 ? 1u : 0u;
-              // the weights of the block's first 64 keys, then of the others
-              if (lead) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  if (k < steps)
-                    mma_ts(t_o, t_p + 8u * k, vd + 128u * k, idesc_o, k > 0 ? 1u : acc);
-              }
-              issued = true;
-              ok = warp_wait(&p_full[2 * h + 1], p_phase[h], p.ctx, abort);
-              if (!ok) break;
-              p_phase[h] ^= 1u;
-              tc_fence_after();
-              if (lead) {
-#pragma unroll
-                for (int k = 4; k < 8; ++k)
-                  if (k < steps) mma_ts(t_o, t_p + 8u * k, vd + 128u * k, idesc_o, 1u);
-                if (j == end[h]) mma_commit(&o_full[h]);
-              }
-            }
-            if (j < e.b1 && j < end[h]) {  // S = Q·Kᵀ of block j
-              if (!have_k) ok = wait_fill(fill);
-              have_k = true;
-              if (!ok) break;
-              tc_fence_after();
-              const uint64_t qd = sdesc_k_sw128(q_base + static_cast<uint32_t>(h) * C::kStageBytes);
-              const uint64_t kd = sdesc_k_sw128(
-                  kv_base + static_cast<uint32_t>(fill % C::kStages) * C::kStageBytes);
-              if (lead) {
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                  const uint64_t step =
-                      static_cast<uint64_t>((k >> 2) * (kPanel >> 4) + 2 * (k & 3));
-                  mma_ss(tmem + 128u * h, qd + step, kd + step, idesc_s, k > 0 ? 1u : 0u);
-                }
-              }
-              issued = true;
-              if (lead) mma_commit(&s_full[h]);
-            }
-          }
+        const int b0 = __shfl_sync(0xFFFFFFFFu, e.b0, 0), b1 = __shfl_sync(0xFFFFFFFFu, e.b1, 0);
+        const int end = __shfl_sync(0xFFFFFFFFu, half_end(e, h, half_tok), 0);
+        // keys from the last block on
+        int left = __shfl_sync(0xFFFFFFFFu, e.k_hi - e.k_lo, 0) - b0 * kTileKeys + kTileKeys;
+        if (end > b0) {
+          ok = warp_wait(&q_full[h], q_phase, p.ctx, abort);
+          q_phase ^= 1u;
+        }
+        for (int j = b0; ok; ++j) {
+          const bool more = j < b1, back = j > b0;
+          if (more) ok = warp_wait(&kv_full[stage], phase, p.ctx, abort);
+          if (back) ok = ok && warp_wait(&kv_full[v_stage], v_phase, p.ctx, abort);
+          if (back && j <= end) ok = ok && warp_wait(&p_full[2 * h], p_phase, p.ctx, abort);
+          ok = ok && warp_wait(&turn[h], my_turn, p.ctx, abort);
           if (!ok) break;
-          if (lead) {
-            if (j > e.b0) mma_commit(&kv_empty[(fill - 1) % C::kStages]);
-            if (j < e.b1) mma_commit(&kv_empty[fill % C::kStages]);
-            if (j == e.b1 - 1) mma_commit(q_empty);
+          my_turn ^= 1u;
+          if (back && j <= end) {  // O += P·V of block j − 1
+            const uint64_t vd =
+                sdesc_mn_sw128(kv_base + static_cast<uint32_t>(v_stage) * C::kStageBytes);
+            const int steps = left >= kTileKeys ? kTileKeys / 16 : (left + 15) / 16;
+            const uint32_t acc = j > b0 + 1 ? 1u : 0u;
+            // the weights of the block's first 64 keys, then of the others
+            tc_fence_after();
+            issued = true;
+            if (lead) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (k < steps)
+                  mma_ts(t_o, t_s + 8u * k, vd + 128u * k, idesc_o, k > 0 ? 1u : acc);
+            }
+            if (!(ok = warp_wait(&p_full[2 * h + 1], p_phase, p.ctx, abort))) break;
+            p_phase ^= 1u;
+            tc_fence_after();
+            if (lead) {
+#pragma unroll
+              for (int k = 4; k < 8; ++k)
+                if (k < steps) mma_ts(t_o, t_s + 8u * k, vd + 128u * k, idesc_o, 1u);
+              if (j == end) mma_commit(&o_full[h]);
+            }
           }
-          if (j < e.b1) fill += 2;
+          if (more && j < end) {  // S = Q·Kᵀ of block j
+            const uint64_t kd =
+                sdesc_k_sw128(kv_base + static_cast<uint32_t>(stage) * C::kStageBytes);
+            tc_fence_after();
+            issued = true;
+            if (lead) {
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const uint64_t step = static_cast<uint64_t>((k >> 2) * (kPanel >> 4) + 2 * (k & 3));
+                mma_ss(t_s, qd + step, kd + step, idesc_s, k > 0 ? 1u : 0u);
+              }
+              mma_commit(&s_full[h]);
+              if (j == end - 1) mma_commit(&q_empty[h]);
+            }
+          }
+          if (lead) {
+            mbar_arrive(&turn[h ^ 1]);
+            if (back) mma_commit(&kv_empty[v_stage]);
+            if (more) mma_commit(&kv_empty[stage]);
+          }
+          if (j == b0) pieces.fetch();
+          if (!more) break;
+          left -= kTileKeys;
+          v_stage = stage + 1;
+          v_phase = phase;
+          stage += 2;
+          if (stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
       }
       if (issued) {
-        if (lead) mma_commit(drain_bar);
-        mbar_wait(drain_bar, 0, p.ctx, nullptr);
+        if (lead) mma_commit(&drain_bar[h]);
+        mbar_wait(&drain_bar[h], 0, p.ctx, nullptr);
       }
       __syncwarp();
-    } else if (warp == kTmaWarp) {
-      // ========================================================== TMA producer
+    } else {
+      // ========================================================== TMA producers
+      // K blocks (and the pieces' Q rows) go to the ring's even stages, V blocks
+      // to the odd ones, by a warp each: with 16-token pages a block is 16
+      // copies, and one warp for both took longer than the products.
+      const bool is_v = warp != kTmaWarp;
+      const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
       const int page_shift = 31 - __clz(b.page_size);
-      const int64_t cache_rows = b.n_pages * b.n_kv_heads * b.page_size;
-      int64_t fill = 0;
-      uint32_t q_phase = 1, tail_phase = 0;
-      int64_t q_loads = 0;
+      // rows of the cache's tensor map fit 31 bits (checked on the host)
+      const int cache_rows = static_cast<int>(b.n_pages * b.n_kv_heads * b.page_size);
+      const int per = kTileKeys >> page_shift;  // pages per block, at most 8
+      int fill = 0, stage = is_v ? 1 : 0;
+      uint32_t phase = 1, q_phase[2] = {1, 1}, tail_phase = 0;
       bool ok = true;
-      // One K or V block into the next stage: lanes 0 .. panels·pages − 1 load
-      // a page's panel each.
-      const auto load_block = [&](const CUtensorMap* map, int page, int n_pg, int kvh, int zero0) {
-        const int s = static_cast<int>(fill % C::kStages);
-        const uint32_t ph = static_cast<uint32_t>((fill / C::kStages) & 1);
-        ok = warp_wait(&kv_empty[s], ph ^ 1u, p.ctx, abort);
-        if (!ok) return;
-        uint8_t* dst = smem + C::kOffKv + s * C::kStageBytes;
-        uint64_t* bar = zero0 >= 0 ? tail_bar : &kv_full[s];
-        if (lane == 0)
-          mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n_pg * b.page_size * 128 * C::kPanels));
-        __syncwarp();
-        const int pg = lane / C::kPanels, panel = lane % C::kPanels;
-        const int id = __shfl_sync(0xFFFFFFFFu, page, pg & 7);
-        if (pg < n_pg) {
-          const int64_t row =
-              id < 0 ? cache_rows
-                     : (static_cast<int64_t>(id) * b.n_kv_heads + kvh) * b.page_size;
-          tma_load_3d(dst + panel * kPanel + pg * b.page_size * 128, map, bar, 0,
-                      static_cast<int32_t>(row), panel);
-        }
-        if (zero0 >= 0) {
-          // Values past the last key may be anything, and zero weights do not
-          // cancel a NaN: clear them up to the end of their 16-key step.
-          ok = warp_wait(tail_bar, tail_phase, p.ctx, abort);
-          tail_phase ^= 1u;
-          const int n = ((zero0 + 15) / 16 * 16 - zero0) * 8;
-          for (int x = lane; x < n * C::kPanels; x += 32)
-            *reinterpret_cast<uint4*>(dst + x / n * kPanel + zero0 * 128 + x % n * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&kv_full[s]);
-        }
-        ++fill;
-      };
       Pieces pieces(p);
       TileEntry e;
       int kvh;
       while (ok && pieces.take(e, kvh)) {
         const int32_t* table = b.page_table + static_cast<int64_t>(e.seq) * b.table_stride;
-        const int per = kTileKeys >> page_shift;  // pages per block, at most 8
         const auto page_of = [&](int j) {
           const int key = e.k_lo + j * kTileKeys + ((lane & 7) << page_shift);
-          int id = -1;
-          if ((lane & 7) < per && key < e.k_hi && j < e.b1) {
-            id = table[key >> page_shift];
-            if (id < 0 || id >= b.n_pages) {
-              record_error(p.ctx, kErrBounds);
-              id = -1;
-            }
-          }
-          return id;
+          // not looked at before its block is loaded, a block later
+          return (lane & 7) < per && key < e.k_hi && j < e.b1 ? table[key >> page_shift] : -1;
         };
         int page = page_of(e.b0);
-        ok = warp_wait(q_empty, q_phase, p.ctx, abort);
-        q_phase ^= 1u;
-        if (!ok) break;
-        const int halves = e.n_tok > half_tok ? 2 : 1;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(q_full,
-                                static_cast<uint32_t>(halves * C::kPanels * half_tok * g * 128));
-          for (int h = 0; h < halves; ++h)
-            for (int c = 0; c < C::kPanels; ++c)
-              tma_load_3d(smem + (h * C::kPanels + c) * kPanel, &tmap_q, q_full, 64 * c, kvh * g,
-                          e.tok0 + h * half_tok);
-        }
-        ++q_loads;
-        __syncwarp();
-        for (int j = e.b0; j < e.b1 && ok; ++j) {
+        for (int j = e.b0; j < e.b1; ++j) {
           const int left = e.k_hi - e.k_lo - j * kTileKeys;
           const int n_pg = left >= kTileKeys ? per : (left + b.page_size - 1) >> page_shift;
+          // keys of the block from which on values may be anything, or −1
+          const int zero0 = is_v && e.tail && left <= kTileKeys && left % 16 != 0 ? left : -1;
           const int next = page_of(j + 1);
-          load_block(&tmap_k, page, n_pg, kvh, -1);
+          if (!(ok = warp_wait(&kv_empty[stage], phase, p.ctx, abort))) break;
+          uint8_t* dst = smem + C::kOffKv + stage * C::kStageBytes;
+          uint64_t* bar = zero0 >= 0 ? tail_bar : &kv_full[stage];
+          if (lane == 0)
+            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n_pg * b.page_size * 128 * C::kPanels));
+          __syncwarp();
+          // lanes 0 .. panels · pages − 1 load a page's panel each
+          const int pg = lane / C::kPanels, panel = lane % C::kPanels;
+          const int id = __shfl_sync(0xFFFFFFFFu, page, pg & 7);
+          if (pg < n_pg) {
+            // a page outside the cache reads as zeros (rows past the tensor)
+            const bool in = id >= 0 && id < b.n_pages;
+            if (!in) record_error(p.ctx, kErrBounds);
+            tma_load_3d(dst + panel * kPanel + pg * b.page_size * 128, map, bar, 0,
+                        in ? (id * b.n_kv_heads + kvh) << page_shift : cache_rows, panel);
+          }
+          __syncwarp();
+          if (zero0 >= 0) {
+            // Zero weights do not cancel a NaN: the values past the last key
+            // are cleared up to the end of their 16-key step.
+            ok = warp_wait(tail_bar, tail_phase, p.ctx, abort);
+            tail_phase ^= 1u;
+            const int n = ((zero0 + 15) / 16 * 16 - zero0) * 8;
+            for (int x = lane; x < n * C::kPanels; x += 32)
+              *reinterpret_cast<uint4*>(dst + x / n * kPanel + zero0 * 128 + x % n * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&kv_full[stage]);
+          }
+          ++fill;
+          stage += 2;
+          if (stage >= C::kStages) {
+            stage -= C::kStages;
+            phase ^= 1u;
+          }
           if (!ok) break;
-          load_block(&tmap_v, page, n_pg, kvh,
-                     e.tail && left <= kTileKeys && left % 16 != 0 ? left : -1);
+          if (j == e.b0) {
+            // the halves' rows, each as soon as its last product has read it
+            for (int h = 0; h < 2 && ok && !is_v; ++h) {
+              if (half_end(e, h, half_tok) <= e.b0) continue;
+              if (!(ok = warp_wait(&q_empty[h], q_phase[h], p.ctx, abort))) break;
+              q_phase[h] ^= 1u;
+              if (lane == 0) {
+                mbar_arrive_expect_tx(&q_full[h],
+                                      static_cast<uint32_t>(C::kPanels * half_tok * g * 128));
+                for (int c = 0; c < C::kPanels; ++c)
+                  tma_load_3d(smem + (h * C::kPanels + c) * kPanel, &tmap_q, &q_full[h], 64 * c,
+                              kvh * g, e.tok0 + h * half_tok);
+              }
+              __syncwarp();
+            }
+            if (!ok) break;
+            pieces.fetch();
+          }
           page = next;
         }
       }
       // See every issued load land (bounded, also after an abort).
       if (lane == 0) {
-        for (int64_t f = fill > C::kStages ? fill - C::kStages : 0; f < fill; ++f)
-          mbar_wait(&kv_full[f % C::kStages], static_cast<uint32_t>((f / C::kStages) & 1), p.ctx,
-                    nullptr);
-        if (q_loads > 0)
-          mbar_wait(q_full, static_cast<uint32_t>((q_loads - 1) & 1), p.ctx, nullptr);
+        constexpr int kMine = C::kStages / 2;
+        for (int f = fill > kMine ? fill - kMine : 0; f < fill; ++f)
+          mbar_wait(&kv_full[2 * (f % kMine) + (is_v ? 1 : 0)],
+                    static_cast<uint32_t>((f / kMine) & 1), p.ctx, nullptr);
+        // q_phase[h] == 1: no load yet, or an even number; the last one's phase
+        // is q_phase[h] in either case
+        for (int h = 0; h < 2 && !is_v; ++h) mbar_wait(&q_full[h], q_phase[h], p.ctx, nullptr);
       }
       __syncwarp();
     }
