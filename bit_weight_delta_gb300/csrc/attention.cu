@@ -24,9 +24,9 @@ AttnLayout attn_layout(const bd_attention_batch& b, int num_sms) {
   // single token already has more than 16, or no sequence has more than 32.
   const int64_t max_rows = static_cast<int64_t>(b.max_q_len) * L.g;
   L.d_rows = L.g > 16 || (max_rows > 16 && max_rows <= 32) ? 32 : 16;
-  L.use_decode = true;  // every batch may hold short runs
   L.use_tile = max_rows > L.d_rows || b.n_group > 0;
   L.d_ctas = 2 * num_sms;
+  L.d_warps = 8 * num_sms;
   L.t_ctas = num_sms;
   const int64_t T = b.n_tokens;
   const int64_t long_seqs =
@@ -50,7 +50,7 @@ AttnLayout attn_layout(const bd_attention_batch& b, int num_sms) {
   };
   L.o_tok_seq = take(4 * static_cast<size_t>(T));
   L.o_seq = take(sizeof(SeqRec) * static_cast<size_t>(b.n_seq));
-  L.o_start = take(sizeof(DecodeStart) * static_cast<size_t>(L.d_ctas));
+  L.o_start = take(sizeof(DecodeStart) * static_cast<size_t>(L.d_warps));
   L.o_group = take(4 * static_cast<size_t>(b.n_group));
   L.o_run = take(4 * (static_cast<size_t>(b.n_seq) + b.n_group + 1));
   L.o_tile_slot = take(4 * static_cast<size_t>(L.max_tiles));
@@ -59,7 +59,7 @@ AttnLayout attn_layout(const bd_attention_batch& b, int num_sms) {
   L.o_comb = take(sizeof(CombItem) * static_cast<size_t>(T));
   L.plan_bytes = o;
   o = 0;
-  const size_t d_rows = static_cast<size_t>(L.d_ctas) * 2 * L.d_rows;
+  const size_t d_rows = static_cast<size_t>(L.d_warps) * 2 * L.d_rows;
   L.w_d_o = take(d_rows * b.head_dim * 4);
   L.w_d_ml = take(d_rows * 8);
   const size_t r_rows = b.n_group > 0 ? static_cast<size_t>(T) * b.n_q_heads : 0;
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
   __shared__ int64_t s_warp[32];
   __shared__ int s_hist[kLenBuckets];
   __shared__ unsigned long long s_blocks;
-  __shared__ int s_comb, s_longest;
+  __shared__ int s_comb, s_longest, s_parts;
   const bd_attention_batch& b = p.b;
   const AttnLayout& L = p.L;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
     s_blocks = 0;
     s_comb = 0;
     s_longest = 0;
+    s_parts = 0;
   }
   for (int i = tid; i < kLenBuckets; i += kPlanThreads) s_hist[i] = 0;
 
@@ -143,7 +144,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
   for (int s = tid; s < b.n_seq; s += kPlanThreads) {
     const int a = b.seq_offsets[s], e = b.seq_offsets[s + 1], kv = b.kv_len[s];
     bad |= a < 0 || e < a || e > b.n_tokens || e - a > b.max_q_len || kv < 0 ||
-           kv > b.max_kv_len || kv > b.table_stride * b.page_size;
+           kv > b.max_kv_len || kv > b.table_stride * b.page_size ||
+           static_cast<int64_t>(kv) * b.n_kv_heads > INT32_MAX;
   }
   for (int g = tid; g < b.n_group; g += kPlanThreads) {
     const int a = b.group_offsets[g], e = b.group_offsets[g + 1];
@@ -159,10 +161,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
     }
   }
   if (bad) {
-    for (int c = tid; c < L.d_ctas; c += kPlanThreads) starts[c].lo = starts[c].hi = 0;
+    for (int c = tid; c < L.d_warps; c += kPlanThreads) starts[c].lo = starts[c].hi = 0;
     if (tid == 0) {
       record_error(p.ctx, kErrBounds);
-      *hd = PlanHeader{0, 1, 0, static_cast<int32_t>(b.n_tokens)};
+      *hd = PlanHeader{0, 1, 1, 0, 0, static_cast<int32_t>(b.n_tokens), 0};
     }
     return;
   }
@@ -202,7 +204,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
   }
   __syncthreads();
 
-  // Decode units: every 64 own keys of a short run, once per key head.
+  // Decode units: every 16 own keys of a short run, once per key head.
   int64_t carry = 0;
   for (int base = 0; base < b.n_seq; base += kPlanThreads) {
     const int s = base + tid;
@@ -221,22 +223,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
     carry += sum;
   }
   const int64_t d_units = carry;
-  const int64_t d_per = d_units > 0 ? (d_units + L.d_ctas - 1) / L.d_ctas : 1;
   __syncthreads();
-  // Where each CTA's units begin.
-  for (int s = tid; s < b.n_seq; s += kPlanThreads) {
-    DecodeStart st{};
-    st.r = seqs[s];
-    st.seq = s;
-    const int64_t end = st.r.unit0 + static_cast<int64_t>(st.r.units) * b.n_kv_heads;
-    for (int64_t c = (st.r.unit0 + d_per - 1) / d_per; c * d_per < end; ++c) {
-      st.lo = c * d_per;
-      st.hi = st.lo + d_per < d_units ? st.lo + d_per : d_units;
-      starts[c] = st;
-    }
-  }
-  for (int64_t c = (d_units + d_per - 1) / d_per + tid; c < L.d_ctas; c += kPlanThreads)
-    starts[c].lo = starts[c].hi = 0;
 
   // Tiles of the long runs: sequences, then groups.
   carry = 0;
@@ -302,12 +289,47 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
     }
   }
   __syncthreads();
+  // CTAs per role, so that both end at about the same time: a block of 256 rows
+  // takes about 1.5 µs of an SM (1.1 at 64-element heads) and a piece 3 µs on
+  // top, a CTA reads keys and values at about 80 bytes per ns.  A batch of 64
+  // ragged decode rows and four 512-token chunks took 117 µs with the two kinds
+  // of work one after the other.
+  const int64_t t_blocks = static_cast<int64_t>(s_blocks) * b.n_kv_heads;
+  int n_tile = 0, n_dec = L.d_ctas;
+  if (L.use_tile) {
+    const float t_cost = static_cast<float>(t_blocks) * (b.head_dim == 128 ? 1.5f : 1.1f) +
+                         3.f * static_cast<float>(n_tiles) * b.n_kv_heads;
+    const float d_cost = static_cast<float>(d_units) * (kUnitKeys * 4.f / 80e3f) * b.head_dim;
+    n_dec = d_units == 0 ? 0
+                         : static_cast<int>(L.t_ctas * d_cost / (t_cost + d_cost) + 0.5f);
+    if (d_units > 0 && n_dec < 1) n_dec = 1;
+    if (t_blocks > 0 && n_dec > L.t_ctas - 1) n_dec = L.t_ctas - 1;
+    n_tile = L.t_ctas - n_dec;
+  }
+  const int warps = L.use_tile ? kTileDecodeWarps : kDecodeWarps;
+  int64_t d_per = n_dec > 0 ? (d_units + n_dec * warps - 1) / (n_dec * warps) : 1;
+  d_per = d_per > kMinUnits ? d_per : kMinUnits;
+  // Where each decode warp's units begin.
+  for (int s = tid; s < b.n_seq; s += kPlanThreads) {
+    DecodeStart st{};
+    st.r = seqs[s];
+    st.seq = s;
+    const int64_t end = st.r.unit0 + static_cast<int64_t>(st.r.units) * b.n_kv_heads;
+    for (int64_t c = (st.r.unit0 + d_per - 1) / d_per; c * d_per < end; ++c) {
+      st.lo = c * d_per;
+      st.hi = st.lo + d_per < d_units ? st.lo + d_per : d_units;
+      starts[c] = st;
+    }
+  }
+  for (int64_t c = (d_units + d_per - 1) / d_per + tid; c < L.d_warps; c += kPlanThreads)
+    starts[c].lo = starts[c].hi = 0;
+
   // Where the longest tile exceeds the CTAs' even share by more than a quarter
   // and by more than 4 blocks, tiles longer than the share are cut into pieces
   // of that share.  Below that the join of the pieces costs more than the
   // uneven end: 256 tiles of up to 20 blocks with a share of 17 took 55 µs and
   // 32 µs more for the join when cut.
-  int64_t share = (static_cast<int64_t>(s_blocks) * b.n_kv_heads + L.t_ctas - 1) / L.t_ctas;
+  int64_t share = n_tile == 0 ? 0 : (t_blocks + n_tile - 1) / n_tile;
   if (s_longest <= share + (share / 4 > 4 ? share / 4 : 4)) share = s_longest;
   const int piece = static_cast<int>(share < 2 ? 2 : share);
   // slots first (a scan over tiles, which belong to runs: by tile index)
@@ -374,8 +396,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
     if (s >= 0) {
       const SeqRec r = seqs[s];
       const int x = it.tok - r.tok0;
+      int parts = 0;
       if (r.q_len * static_cast<int64_t>(L.g) > L.d_rows) {
         const int i = run_tile0[s] + x / tile_tok, y = x % tile_tok;
+        parts = tile_ns[i];
         join = tile_slot[i] >= 0 || tile_ns[i] == 0;
         it.own_slot = tile_slot[i];
         it.own_ns = tile_ns[i];
@@ -384,14 +408,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
         it.unit0 = r.unit0;
         it.units = r.units;
         it.own_row = x * L.g;
-        if (r.group < 0) {
-          // final where no head's units are cut between CTAs
-          join = false;
-          for (int h = 0; h < b.n_kv_heads && !join; ++h) {
-            const int64_t u0 = r.unit0 + static_cast<int64_t>(h) * r.units;
-            join = u0 / d_per != (u0 + r.units - 1) / d_per;
-          }
+        for (int h = 0; h < b.n_kv_heads; ++h) {
+          const int64_t u0 = r.unit0 + static_cast<int64_t>(h) * r.units;
+          const int n = decode_parts(u0, u0 + r.units, d_units, d_per, warps).count();
+          parts = n > parts ? n : parts;
         }
+        join = r.group >= 0 || parts > 1;  // final where no head's units are cut
       }
       if (r.group >= 0) {
         const int z = it.tok - seqs[b.group_offsets[r.group]].tok0;
@@ -399,73 +421,72 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
         it.pre_slot = tile_slot[i];
         it.pre_ns = tile_ns[i];
         it.pre_row = y / L.half_tok * kHalfRows + y % L.half_tok * L.g;
+        parts += it.pre_ns;
       }
+      if (join) atomicMax(&s_parts, parts);
     }
     if (join) comb[atomicAdd(&s_comb, 1)] = it;
   }
   __syncthreads();
   if (tid == 0) {
     if (!fits) record_error(p.ctx, kErrBounds);
-    *hd = PlanHeader{d_units, d_per, fits ? n_entries : 0, s_comb};
+    *hd = PlanHeader{d_units, static_cast<int32_t>(d_per), warps, fits ? n_entries : 0, n_tile, s_comb, s_parts};
   }
 }
 
 // ------------------------------------------------------------------ combine
 
 constexpr int kCombThreads = 256;
-constexpr int kCombD4 = 8;     // float4 columns of a row per CTA
 constexpr int kCombBatch = 4;  // parts that a thread has in flight
 
-// One CTA per (token, key head, 32 columns) of the plan's list.  A row's parts
-// are dealt to the thread groups of the CTA, which join them in a fixed order
-// with a running maximum and meet in shared memory: the join is one load of the
-// item and about parts / (groups · 4) rounds of independent loads.  Neighbouring
-// threads read neighbouring rows of a slot.
+// One CTA per (token, key head) of the plan's list, or per 32 columns of one
+// where rows have many parts.  A row's parts are dealt to the thread groups of
+// the CTA, which join them in a fixed order with a running maximum and meet in
+// shared memory: the join is one load of the item and about parts / (groups ·
+// 4) rounds of independent loads.  Neighbouring threads read neighbouring rows
+// of a slot.
 __global__ void __launch_bounds__(kCombThreads) combine_kernel(const AttnArgs p) {
   __shared__ float4 s_o[kCombThreads];
   __shared__ float2 s_ml[kCombThreads];
   const bd_attention_batch& b = p.b;
   const AttnLayout& L = p.L;
   const int g = L.g, D = b.head_dim, H = b.n_kv_heads;
-  const int slices = D / (4 * kCombD4);
-  const int groups = kCombThreads / (kCombD4 * g);
-  const int row = threadIdx.x % g, q = threadIdx.x / g;
-  const int col = q % kCombD4, grp = q / kCombD4;
   griddep_wait();
   griddep_launch_dependents();
   const PlanHeader hd = *p.header();
+  const int slices = hd.most_parts <= 2 * kCombBatch && g * (D / 4) <= kCombThreads ? 1 : D / 32;
+  const int cols = D / 4 / slices;  // float4 columns per CTA
+  const int groups = kCombThreads / (cols * g);
+  const int row = threadIdx.x % g, q = threadIdx.x / g;
+  const int col = q % cols, grp = q / cols;
   const int64_t n_work = static_cast<int64_t>(hd.n_comb) * H * slices;
   for (int64_t w = blockIdx.x; w < n_work; w += gridDim.x) {
     const CombItem it = p.comb()[w / (H * slices)];
     const int kvh = static_cast<int>(w / slices % H);
-    const int d4 = static_cast<int>(w % slices) * kCombD4 + col;
-    // own parts: slot first + i·step (the very first one slot later for decode
-    // parts: their first CTA holds them as its last run), `rows` rows each
-    int64_t first = 0, step = H;
-    int n_own = it.own_ns, rows = 2 * kHalfRows, own_row = it.own_row, skip = 0;
+    const int d4 = static_cast<int>(w % slices) * cols + col;
+    // own parts: tile slots own_slot .. (times heads plus head), decode parts,
+    // or the one part of a run that a warp or CTA did alone
+    DecodeParts dp{};
+    int64_t first = static_cast<int64_t>(it.own_slot) * H + kvh;
+    int n_own = it.own_ns, rows = 2 * kHalfRows, own_row = it.own_row;
+    const bool cut = it.units > 0;
     uint8_t *o_base = p.ws + L.w_t_o, *ml_base = p.ws + L.w_t_ml;
-    if (it.units > 0) {
+    if (cut) {
       const int64_t u0 = it.unit0 + static_cast<int64_t>(kvh) * it.units;
-      const int64_t c0 = u0 / hd.d_per, c1 = (u0 + it.units - 1) / hd.d_per;
-      if (c1 > c0) {
-        first = 2 * c0;
-        step = 2;
-        skip = 1;
-        n_own = static_cast<int>(c1 - c0) + 1;
+      dp = decode_parts(u0, u0 + it.units, hd.d_units, hd.d_per, hd.d_warps);
+      n_own = dp.count();
+      if (n_own > 1) {
         rows = L.d_rows;
         o_base = p.ws + L.w_d_o;
         ml_base = p.ws + L.w_d_ml;
       } else {
         if (it.pre_ns == 0) continue;  // final already; another head of the token is cut
         first = static_cast<int64_t>(it.tok) * H + kvh;
-        n_own = 1;
         rows = g;
         own_row = 0;
         o_base = p.ws + L.w_r_o;
         ml_base = p.ws + L.w_r_ml;
       }
-    } else {
-      first = static_cast<int64_t>(it.own_slot) * H + kvh;
     }
     const int n = n_own + it.pre_ns;
     float m = -INFINITY, l = 0.f;
@@ -480,7 +501,7 @@ __global__ void __launch_bounds__(kCombThreads) combine_kernel(const AttnArgs p)
           ml[k] = make_float2(-INFINITY, 0.f);
           v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (i < n_own) {
-            const int64_t slot = first + i * step + (i == 0 ? skip : 0);
+            const int64_t slot = cut && n_own > 1 ? dp.slot(i) : first + static_cast<int64_t>(i) * H;
             ml[k] = part_ml(ml_base, slot, rows)[own_row + row];
             v[k] = part_o(o_base, slot, rows, D)[static_cast<int64_t>(d4) * rows + own_row + row];
           } else if (i < n) {
@@ -512,12 +533,14 @@ __global__ void __launch_bounds__(kCombThreads) combine_kernel(const AttnArgs p)
         m = top;
       }
     }
+    if (groups > 1) {
     __syncthreads();  // the last item's values have been read
     s_o[threadIdx.x] = o;
     s_ml[threadIdx.x] = make_float2(m, l);
     __syncthreads();
+    }
     if (grp != 0) continue;
-    const int span = g * kCombD4, most = groups < n ? groups : n;
+    const int span = g * cols, most = groups < n ? groups : n;
     float top = m;
     for (int k = 1; k < most; ++k) top = fmaxf(top, s_ml[threadIdx.x + k * span].x);
     const float ref = top == -INFINITY ? 0.f : top;
@@ -571,26 +594,26 @@ bd_status run_attention(AttnArgs& p, cudaStream_t s) {
       static_cast<uint64_t>(b.n_pages) * b.n_kv_heads * static_cast<uint64_t>(b.page_size);
   const uint64_t kdims[3] = {64, rows, D / 64};
   const uint64_t kstr[2] = {2 * D, 128};
-  CUtensorMap tk, tv;
+  const uint32_t box16[3] = {64, 16, static_cast<uint32_t>(D / 64)};
+  TileMaps m;
+  if (!encode_tmap_bf16_3d(&m.dk, p.k_pages, kdims, kstr, box16) ||
+      !encode_tmap_bf16_3d(&m.dv, p.v_pages, kdims, kstr, box16))
+    return BD_ERR_CUDA;
   if (p.L.use_tile) {
     const uint32_t box[3] = {64, static_cast<uint32_t>(b.page_size), 1};
     const uint64_t qdims[3] = {D, H, static_cast<uint64_t>(b.n_tokens)};
     const uint64_t qstr[2] = {2 * D, 2 * D * H};
     const uint32_t qbox[3] = {64, static_cast<uint32_t>(p.L.g),
                               static_cast<uint32_t>(p.L.half_tok)};
-    CUtensorMap tq;
-    if (!encode_tmap_bf16_3d(&tk, p.k_pages, kdims, kstr, box) ||
-        !encode_tmap_bf16_3d(&tv, p.v_pages, kdims, kstr, box) ||
-        !encode_tmap_bf16_3d(&tq, p.q, qdims, qstr, qbox))
+    if (!encode_tmap_bf16_3d(&m.k, p.k_pages, kdims, kstr, box) ||
+        !encode_tmap_bf16_3d(&m.v, p.v_pages, kdims, kstr, box) ||
+        !encode_tmap_bf16_3d(&m.q, p.q, qdims, qstr, qbox))
       return BD_ERR_CUDA;
-    if (launch_attn_tile(p, tq, tk, tv, s) != cudaSuccess) return BD_ERR_CUDA;
-  }
-  const uint32_t box[3] = {64, 16, static_cast<uint32_t>(D / 64)};
-  if (!encode_tmap_bf16_3d(&tk, p.k_pages, kdims, kstr, box) ||
-      !encode_tmap_bf16_3d(&tv, p.v_pages, kdims, kstr, box))
+    if (launch_attn_tile(p, m, s) != cudaSuccess) return BD_ERR_CUDA;
+  } else if (launch_attn_decode(p, m.dk, m.dv, s) != cudaSuccess) {
     return BD_ERR_CUDA;
-  if (launch_attn_decode(p, tk, tv, s) != cudaSuccess) return BD_ERR_CUDA;
-  const int64_t work = b.n_tokens * b.n_kv_heads * (b.head_dim / (4 * kCombD4));
+  }
+  const int64_t work = b.n_tokens * b.n_kv_heads * (b.head_dim / 32);
   const int64_t most = 8 * static_cast<int64_t>(p.L.t_ctas);
   const cudaError_t e = launch_pdl(combine_kernel, dim3(static_cast<unsigned>(work < most ? work : most)),
                                    dim3(kCombThreads), 0, s, p);

@@ -3,9 +3,12 @@
 //
 // A batch's work falls in two kinds of run.  Short runs (a sequence with at
 // most d_rows query rows per key head, i.e. query tokens x query heads per key
-// head) go to the decode kernel, whose time is reading the cache.  Long runs go
-// to the tile kernel, on the tensor cores: sequences with more rows, over their
-// own keys, and groups of sequences, over their shared prefix.  Rows whose keys
+// head) are the decode role's, whose time is reading the cache.  Long runs are
+// the tile role's, on the tensor cores: sequences with more rows, over their
+// own keys, and groups of sequences, over their shared prefix.  A batch that
+// can only hold short runs runs the decode kernel; any other the tile kernel,
+// some of whose CTAs take the decode role, as many as the plan finds that the
+// two kinds of work end together.  Rows whose keys
 // are spread over several pieces (a key range cut over CTAs, a prefix and an
 // own part) are joined by the combine kernel from partial results
 //   o = Σ 2^(s − m)·v,  l = Σ 2^(s − m),  m      (s in units of log2)
@@ -21,15 +24,66 @@ namespace bd {
 
 constexpr int kTileKeys = 128;   // keys per block of the tile kernel
 constexpr int kHalfRows = 128;   // rows per half of its 256-row tile (tensor-memory lanes)
-constexpr int kUnitKeys = 64;    // keys per unit of the decode kernel's split
-constexpr int kDecodeWarps = 4;
+constexpr int kUnitKeys = 16;    // keys per unit of the decode role's split
+constexpr int kDecodeWarps = 4;      // warps per CTA of the decode kernel
+constexpr int kTileDecodeWarps = 8;  // of the tile kernel's decode role
+constexpr int kMinUnits = 4;     // units per warp at least: a part costs a row's sums
 
 struct PlanHeader {
   int64_t d_units;    // units of the decode kernel, all sequences and key heads
-  int64_t d_per;      // units per CTA
+  int32_t d_per;      // units per warp
+  int32_t d_warps;    // warps per CTA
   int32_t t_entries;  // pieces of the tile kernel (each once per key head)
+  int32_t t_ctas;     // CTAs of its launch that take pieces; the others take units
   int32_t n_comb;     // tokens whose rows the combine kernel writes
+  int32_t most_parts; // of any of their rows
 };
+
+// The decode role's parts of a run of units [u0, u1), out of `total` units cut
+// into `per` per warp and `w` warps per CTA.  A CTA whose whole range lies in
+// one run works on it with all its warps and leaves one part; elsewhere each
+// warp has a range, and parts, of its own.  A run's parts are thus those of the
+// warps of its first CTA, one of each CTA in between, and those of the warps of
+// its last CTA.  A part's slot is 2·warp, plus one where the run begins inside
+// the range of its warp (a warp has at most one part that began earlier and one
+// that goes on).
+struct DecodeParts {
+  int64_t g0;        // first warp (or first warp of the first CTA)
+  int64_t mid0;      // first warp of the CTAs in between
+  int64_t last0;     // first warp of the last parts
+  int na, nb, nc;    // parts of the first CTA, in between, of the last CTA
+  int w, first_odd;  // warps per CTA; 1 where the first part's slot is the odd one
+  __host__ __device__ int count() const { return na + nb + nc; }
+  __host__ __device__ int64_t slot(int i) const {
+    if (i < na) return 2 * (g0 + i) + (i == 0 ? first_odd : 0);
+    if (i < na + nb) return 2 * (mid0 + static_cast<int64_t>(i - na) * w);
+    return 2 * (last0 + (i - na - nb));
+  }
+};
+__host__ __device__ inline DecodeParts decode_parts(int64_t u0, int64_t u1, int64_t total,
+                                                    int64_t per, int w) {
+  DecodeParts d{};
+  const int64_t span = per * w, c0 = u0 / span, c1 = (u1 - 1) / span;
+  const int64_t end0 = (c0 + 1) * span < total ? (c0 + 1) * span : total;
+  const int64_t end1 = (c1 + 1) * span < total ? (c1 + 1) * span : total;
+  const int64_t w0 = u0 / per, w1 = (u1 - 1) / per;
+  d.w = w;
+  if (u0 <= c0 * span && u1 >= end0) {  // all of the first CTA
+    d.g0 = c0 * w;
+    d.na = 1;
+  } else {
+    d.g0 = w0;
+    d.na = static_cast<int>((c0 == c1 ? w1 : (c0 + 1) * w - 1) - w0) + 1;
+    d.first_odd = 1;
+  }
+  if (c1 > c0) {
+    d.mid0 = (c0 + 1) * w;
+    d.nb = static_cast<int>(c1 - c0 - 1);
+    d.last0 = c1 * w;
+    d.nc = u1 >= end1 ? 1 : static_cast<int>(w1 - c1 * w) + 1;
+  }
+  return d;
+}
 
 // One sequence, as the decode kernel and the combine kernel see it.
 struct SeqRec {
@@ -40,9 +94,8 @@ struct SeqRec {
   int32_t group;      // group whose prefix it reads, or −1
 };
 
-// Where a CTA of the decode kernel begins: its units [lo, hi) and the sequence
-// that holds lo.  One load, so that the kernel's first page ids are one step
-// away.
+// Where a warp of the decode role begins: its units [lo, hi) and the sequence
+// that holds lo.  One load, so that its first page ids are one step away.
 struct DecodeStart {
   SeqRec r;
   int64_t lo, hi;
@@ -80,8 +133,10 @@ struct AttnLayout {
   int32_t g;             // query heads per key head
   int32_t half_tok;      // tokens per half tile
   int32_t d_rows;        // rows up to which a run is short
-  int32_t d_ctas, t_ctas;
-  bool use_decode, use_tile;
+  int32_t d_ctas;        // CTAs of the decode kernel
+  int32_t d_warps;       // warps that take the decode role in either kernel, at most
+  int32_t t_ctas;        // CTAs of the tile kernel
+  bool use_tile;
   int64_t max_tiles, max_entries, t_slots;
   // plan
   size_t o_tok_seq, o_seq, o_start, o_group, o_run, o_tile_slot, o_tile_ns, o_entry, o_comb;
@@ -147,8 +202,12 @@ constexpr float kRescale = 40.f;
 
 cudaError_t launch_attn_decode(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
                                cudaStream_t s);
-cudaError_t launch_attn_tile(const AttnArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
-                             const CUtensorMap& tv, cudaStream_t s);
+// Tensor maps of the query rows, of the cache in boxes of a page's panel (tile
+// role) and in boxes of 16 keys (decode role).
+struct TileMaps {
+  CUtensorMap q, k, v, dk, dv;
+};
+cudaError_t launch_attn_tile(const AttnArgs& a, const TileMaps& maps, cudaStream_t s);
 
 // Tensor map of up to 3 dimensions of 16-bit elements in the 128-byte swizzle;
 // strides in bytes of dimensions 1 and 2.

@@ -1,456 +1,28 @@
-// attn_decode.cu — attention of short query runs (a decode step's single
-// tokens, or a few tokens) over the paged cache.
-//
-// A run has at most 16·RT rows per key head (query tokens x query heads per
-// key head), so each key and value byte feeds few products and the kernel's
-// floor is reading the cache once.  The batch's keys, in units of 64, key head
-// by key head and sequence by sequence, are cut evenly over the CTAs; a run
-// cut between CTAs leaves partial results that the combine kernel joins.
-//
-// Within a CTA the four warps take 16-key tiles in turn, each from its own
-// ring of stages that it fills itself by TMA (one box of 16 keys for K, one
-// for V, in the 128-byte swizzle), so warps never wait for one another but at
-// the end of a run.  Scores are mma.sync m16n8k16 products of the rows with 16
-// keys; the softmax statistics and the output stay in registers; at the end of
-// a run the four warps' results are joined in shared memory.
-#include <cstdint>
-
-#include "attention.cuh"
+// attn_decode.cu — the decode kernel: two CTAs of four warps per SM over a batch
+// of short runs alone (attn_decode.cuh).
+#include "attn_decode.cuh"
 
 namespace bd {
 namespace {
 
-template <int D, int RT>
-struct Cfg {
-  static constexpr int kRows = 16 * RT;
-  static constexpr int kKv = 16 * D * 2;  // K (or V) bytes of a stage
-  static constexpr int kStage = 2 * kKv;
-  // Two CTAs per SM: rings of 96 KB (64 KB for 32 rows, whose join needs more)
-  static constexpr int kStages = (RT == 1 ? 24576 : 16384) / kStage;
-  static constexpr int kMerge = kRows * D * 4;  // one warp's o
-  static constexpr int kOffMerge = kDecodeWarps * kStages * kStage;
-  static constexpr int kOffM = kOffMerge + 2 * kMerge;             // [warps][rows] m
-  static constexpr int kOffL = kOffM + kDecodeWarps * kRows * 4;   // [2][rows] l
-  static constexpr int kOffBar = kOffL + 2 * kRows * 4;
-  static constexpr int kSmem = kOffBar + kDecodeWarps * kStages * 8 + 16;
-};
-
-__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-__device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// A walk over the runs in a CTA's range of units.
-struct Walk {
-  SeqRec r;
-  int seq, h;          // current run
-  int64_t at, end;     // next unit, end of the CTA's range
-  int t0, t1;          // the run's 16-key tiles in the range
-  int64_t u0;          // the run's first unit
-  bool whole;          // the range holds all of the run
-};
-
-// The run at w.at; false at the end of the range.
-__device__ __forceinline__ bool next_run(const AttnArgs& p, Walk& w) {
-  if (w.at >= w.end) return false;
-  while (true) {  // units beyond the current sequence belong to a later one
-    const int64_t rel = w.at - w.r.unit0;
-    if (rel < static_cast<int64_t>(w.r.units) * p.b.n_kv_heads) {
-      w.h = static_cast<int>(rel / w.r.units);
-      break;
-    }
-    if (++w.seq >= p.b.n_seq) return false;
-    w.r = p.seqs()[w.seq];
-  }
-  w.u0 = w.r.unit0 + static_cast<int64_t>(w.h) * w.r.units;
-  const int64_t stop = w.u0 + w.r.units < w.end ? w.u0 + w.r.units : w.end;
-  w.whole = w.at == w.u0 && stop == w.u0 + w.r.units;
-  constexpr int kPer = kUnitKeys / 16;
-  w.t0 = static_cast<int>(w.at - w.u0) * kPer;
-  const int tiles = (w.r.kv_len - w.r.k0 + 15) / 16;
-  w.t1 = static_cast<int>(stop - w.u0) * kPer;
-  w.t1 = w.t1 < tiles ? w.t1 : tiles;
-  w.at = stop;
-  return true;
-}
+constexpr int kWarps = kDecodeWarps;
 
 template <int D, int RT>
-__global__ void __launch_bounds__(32 * kDecodeWarps, 2)
+__global__ void __launch_bounds__(32 * kWarps, 2)
     attn_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
                        const __grid_constant__ CUtensorMap tmap_v, const AttnArgs p) {
-  using C = Cfg<D, RT>;
-  constexpr int kKSteps = D / 16;
   extern __shared__ __align__(1024) uint8_t smem[];
-  const bd_attention_batch& b = p.b;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g8 = lane >> 2, t4 = lane & 3;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar) + warp * C::kStages;
-  volatile int* abort = reinterpret_cast<volatile int*>(smem + C::kOffBar +
-                                                        kDecodeWarps * C::kStages * 8);
-  uint8_t* ring = smem + warp * C::kStages * C::kStage;
-  float* s_m = reinterpret_cast<float*>(smem + C::kOffM);
-  float* s_l = reinterpret_cast<float*>(smem + C::kOffL);
-  if (lane == 0)
-    for (int s = 0; s < C::kStages; ++s) mbar_init(&bars[s], 1);
+  attn_decode::init<D, RT, kWarps>(smem, warp, lane);
   if (threadIdx.x == 0) {
-    *abort = 0;
     prefetch_tmap(&tmap_k);
     prefetch_tmap(&tmap_v);
   }
-  fence_mbar_init();
   __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
-
-  const DecodeStart st = p.starts()[blockIdx.x];
-  const int64_t lo = st.lo;
-  if (lo >= st.hi) return;
-  Walk cons{};
-  cons.seq = st.seq;
-  cons.r = st.r;
-  cons.at = lo;
-  cons.end = st.hi;
-  Walk prod = cons;
-  const int g = p.L.g;
-  const int page_shift = 31 - __clz(b.page_size);
-  const int64_t cache_rows = b.n_pages * b.n_kv_heads * b.page_size;
-
-  // ---- producer: the warp's tiles t0 + warp, + 4, ... of every run in turn
-  int p_tile = 0, p_end = 0, p_page = 0, p_have = 0;
-  int p_stage = 0;
-  const auto issue = [&]() {
-    while (p_tile >= p_end) {
-      if (!next_run(p, prod)) return;
-      p_tile = prod.t0 + warp;
-      p_end = prod.t1;
-      p_have = 32;
-    }
-    if (p_have == 32) {  // page ids of the next 32 tiles, one per lane
-      const int tile = p_tile + kDecodeWarps * lane;
-      p_page = -1;
-      if (tile < p_end) {
-        p_page = b.page_table[static_cast<int64_t>(prod.seq) * b.table_stride +
-                              ((prod.r.k0 + 16 * tile) >> page_shift)];
-        if (p_page < 0 || p_page >= b.n_pages) {
-          record_error(p.ctx, kErrBounds);
-          p_page = -1;
-        }
-      }
-      p_have = 0;
-    }
-    const int page = __shfl_sync(0xFFFFFFFFu, p_page, p_have);
-    if (lane == 0) {
-      const int key = prod.r.k0 + 16 * p_tile;
-      // a page outside the cache reads as zeros (rows past the tensor)
-      const int64_t row =
-          page < 0 ? cache_rows
-                   : (static_cast<int64_t>(page) * b.n_kv_heads + prod.h) * b.page_size +
-                         (key & (b.page_size - 1));
-      uint8_t* dst = ring + p_stage * C::kStage;
-      mbar_arrive_expect_tx(&bars[p_stage], C::kStage);
-      tma_load_3d(dst, &tmap_k, &bars[p_stage], 0, static_cast<int32_t>(row), 0);
-      tma_load_3d(dst + C::kKv, &tmap_v, &bars[p_stage], 0, static_cast<int32_t>(row), 0);
-    }
-    ++p_have;
-    p_tile += kDecodeWarps;
-    p_stage = p_stage + 1 == C::kStages ? 0 : p_stage + 1;
-  };
-  for (int s = 0; s < C::kStages; ++s) issue();
-
-  int stage = 0;
-  uint32_t phase = 0;
-  bool ok = true;
-  while (next_run(p, cons)) {
-    const SeqRec r = cons.r;
-    const int rows = r.q_len * g;
-    const int pos0 = r.kv_len - r.q_len;  // the first token's position
-    uint32_t qf[RT][kKSteps][4];
-    int limit[RT][2];                     // keys below it are seen by rows g8, g8 + 8
-#pragma unroll
-    for (int m = 0; m < RT; ++m) {
-      const uint16_t* src[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = 16 * m + 8 * e + g8;
-        limit[m][e] = row < rows ? pos0 + row / g + 1 : 0;
-        src[e] = row < rows ? p.q + (static_cast<int64_t>(r.tok0 + row / g) * b.n_q_heads +
-                                     cons.h * g + row % g) * D + 2 * t4
-                            : nullptr;
-      }
-#pragma unroll
-      for (int k = 0; k < kKSteps; ++k)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint16_t* s = src[x & 1];
-          qf[m][k][x] =
-              s ? __ldg(reinterpret_cast<const uint32_t*>(s + 16 * k + 8 * (x >> 1))) : 0u;
-        }
-    }
-    float o[RT][D / 8][4], mref[RT][2], l[RT][2];
-#pragma unroll
-    for (int m = 0; m < RT; ++m) {
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) o[m][n][x] = 0.f;
-      mref[m][0] = mref[m][1] = -INFINITY;
-      l[m][0] = l[m][1] = 0.f;
-    }
-
-    for (int tile = cons.t0 + warp; tile < cons.t1; tile += kDecodeWarps) {
-      ok = ok && mbar_wait(&bars[stage], phase, p.ctx, abort);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) break;
-      const uint32_t kb = smem_addr(ring + stage * C::kStage);
-      const uint32_t vb = kb + C::kKv;
-      const int key0 = r.k0 + 16 * tile;
-      float s[RT][2][4];
-#pragma unroll
-      for (int m = 0; m < RT; ++m)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) s[m][n][x] = 0.f;
-      {
-        const int tok = (lane & 7) + ((lane & 16) ? 8 : 0), sel = (lane >> 3) & 1;
-#pragma unroll
-        for (int k = 0; k < kKSteps; ++k) {
-          uint32_t kf[4];
-          ldsm_x4(kf, kb + (k >> 2) * 2048 + tok * 128 +
-                          (((((k & 3) << 1) + sel) ^ (tok & 7)) << 4));
-#pragma unroll
-          for (int m = 0; m < RT; ++m) {
-            mma16816(s[m][0], qf[m][k], kf[0], kf[1]);
-            mma16816(s[m][1], qf[m][k], kf[2], kf[3]);
-          }
-        }
-      }
-      const bool edge = key0 + 16 > pos0 + 1;  // some row does not see all 16 keys
-      if (edge) {
-#pragma unroll
-        for (int m = 0; m < RT; ++m)
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (key0 + 8 * n + 2 * t4 + (x & 1) >= limit[m][x >> 1]) s[m][n][x] = -INFINITY;
-      }
-      uint32_t pf[RT][4];
-#pragma unroll
-      for (int m = 0; m < RT; ++m) {
-        float top[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          top[e] = fmaxf(fmaxf(s[m][0][2 * e], s[m][0][2 * e + 1]),
-                         fmaxf(s[m][1][2 * e], s[m][1][2 * e + 1]));
-          top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 1));
-          top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 2)) * p.scale_log2;
-        }
-        const bool move = top[0] > mref[m][0] + kRescale || top[1] > mref[m][1] + kRescale;
-        if (__any_sync(0xFFFFFFFFu, move)) {
-          float f[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float mn = fmaxf(mref[m][e], top[e]);
-            f[e] = mn == -INFINITY ? 1.f : ex2(mref[m][e] - mn);
-            mref[m][e] = mn;
-            l[m][e] *= f[e];
-          }
-#pragma unroll
-          for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) o[m][n][x] *= f[x >> 1];
-        }
-        float w[2][4];
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float ref = mref[m][x >> 1] == -INFINITY ? 0.f : mref[m][x >> 1];
-            w[n][x] = ex2(fmaf(s[m][n][x], p.scale_log2, -ref));
-            l[m][x >> 1] += w[n][x];
-          }
-        // the weights as the A operand of the product with V, rounded to bf16:
-        // the tensor core's operand type, 2^-9 of each weight
-        pf[m][0] = pack_bf16x2_rn(w[0][0], w[0][1]);
-        pf[m][1] = pack_bf16x2_rn(w[0][2], w[0][3]);
-        pf[m][2] = pack_bf16x2_rn(w[1][0], w[1][1]);
-        pf[m][3] = pack_bf16x2_rn(w[1][2], w[1][3]);
-      }
-      {
-        const int tok = lane & 15, sel = lane >> 4;
-        // values past kv_len may be anything and must not meet a zero weight
-        uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-        const bool tail = key0 + 16 > r.kv_len;
-        if (tail) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int k = key0 + 8 * e + 2 * t4;
-            keep[e] = (k < r.kv_len ? 0xFFFFu : 0u) | (k + 1 < r.kv_len ? 0xFFFF0000u : 0u);
-          }
-        }
-#pragma unroll
-        for (int d = 0; d < kKSteps; ++d) {
-          uint32_t vf[4];
-          ldsm_x4_t(vf, vb + (d >> 2) * 2048 + tok * 128 +
-                            (((((d & 3) << 1) + sel) ^ (tok & 7)) << 4));
-          if (tail) {
-            vf[0] &= keep[0];
-            vf[1] &= keep[1];
-            vf[2] &= keep[0];
-            vf[3] &= keep[1];
-          }
-#pragma unroll
-          for (int m = 0; m < RT; ++m) {
-            mma16816(o[m][2 * d], pf[m], vf[0], vf[1]);
-            mma16816(o[m][2 * d + 1], pf[m], vf[2], vf[3]);
-          }
-        }
-      }
-      __syncwarp();  // every lane has read the stage
-      issue();
-      if (++stage == C::kStages) {
-        stage = 0;
-        phase ^= 1u;
-      }
-    }
-
-    // ---- join the four warps: m, then o and l relative to the common m
-#pragma unroll
-    for (int m = 0; m < RT; ++m)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        l[m][e] += __shfl_xor_sync(0xFFFFFFFFu, l[m][e], 1);
-        l[m][e] += __shfl_xor_sync(0xFFFFFFFFu, l[m][e], 2);
-        if (t4 == 0) s_m[warp * C::kRows + 16 * m + 8 * e + g8] = mref[m][e];
-      }
-    __syncthreads();
-#pragma unroll
-    for (int m = 0; m < RT; ++m) {
-      float f[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = 16 * m + 8 * e + g8;
-        float top = s_m[row];
-#pragma unroll
-        for (int w = 1; w < kDecodeWarps; ++w) top = fmaxf(top, s_m[w * C::kRows + row]);
-        f[e] = top == -INFINITY ? 1.f : ex2(mref[m][e] - top);
-        mref[m][e] = top;
-        l[m][e] *= f[e];
-      }
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) o[m][n][x] *= f[x >> 1];
-    }
-    const auto put = [&](int slot) {
-      float4* d = reinterpret_cast<float4*>(smem + C::kOffMerge + slot * C::kMerge) + lane;
-#pragma unroll
-      for (int m = 0; m < RT; ++m)
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-          d[(m * (D / 8) + n) * 32] = make_float4(o[m][n][0], o[m][n][1], o[m][n][2], o[m][n][3]);
-      if (t4 == 0)
-#pragma unroll
-        for (int m = 0; m < RT; ++m)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) s_l[slot * C::kRows + 16 * m + 8 * e + g8] = l[m][e];
-    };
-    const auto add = [&](int slot) {
-      const float4* d =
-          reinterpret_cast<const float4*>(smem + C::kOffMerge + slot * C::kMerge) + lane;
-#pragma unroll
-      for (int m = 0; m < RT; ++m) {
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          const float4 v = d[(m * (D / 8) + n) * 32];
-          o[m][n][0] += v.x;
-          o[m][n][1] += v.y;
-          o[m][n][2] += v.z;
-          o[m][n][3] += v.w;
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) l[m][e] += s_l[slot * C::kRows + 16 * m + 8 * e + g8];
-      }
-    };
-    if (warp >= 2) put(warp - 2);
-    __syncthreads();
-    if (warp < 2) add(warp);
-    if (warp == 1) put(1);
-    __syncthreads();
-    if (warp != 0) continue;
-    add(1);
-
-    // ---- final rows, or a partial result
-    const bool last = cons.whole && r.group < 0;
-    uint8_t *po, *pml;
-    int64_t slot;
-    int part_rows;
-    if (cons.whole) {
-      po = p.ws + p.L.w_r_o;
-      pml = p.ws + p.L.w_r_ml;
-      part_rows = g;
-    } else {
-      // a cut run is the CTA's last one (it begins here) or its first
-      slot = 2 * static_cast<int64_t>(blockIdx.x) + (cons.u0 >= lo ? 1 : 0);
-      po = p.ws + p.L.w_d_o;
-      pml = p.ws + p.L.w_d_ml;
-      part_rows = p.L.d_rows;
-    }
-#pragma unroll
-    for (int m = 0; m < RT; ++m)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = 16 * m + 8 * e + g8;
-        if (row >= rows) continue;
-        const int64_t tok = r.tok0 + row / g;
-        const int64_t at = tok * b.n_q_heads + cons.h * g + row % g;
-        if (last) {
-          const float inv = l[m][e] > 0.f ? 1.f / l[m][e] : 0.f;
-          uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + at * D) + t4;
-#pragma unroll
-          for (int n = 0; n < D / 8; ++n)
-            dst[4 * n] = pack_bf16x2_rn(o[m][n][2 * e] * inv, o[m][n][2 * e + 1] * inv);
-          if (t4 == 0 && p.lse != nullptr)
-            p.lse[at] = l[m][e] > 0.f ? (mref[m][e] + log2f(l[m][e])) * kLn2 : -INFINITY;
-          continue;
-        }
-        int part_row = row;
-        if (cons.whole) {
-          slot = tok * b.n_kv_heads + cons.h;
-          part_row = row % g;
-        }
-        float2* dst = reinterpret_cast<float2*>(part_o(po, slot, part_rows, D));
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          const int d = 8 * n + 2 * t4;
-          dst[(static_cast<int64_t>(d >> 2) * part_rows + part_row) * 2 + ((d >> 1) & 1)] =
-              make_float2(o[m][n][2 * e], o[m][n][2 * e + 1]);
-        }
-        if (t4 == 0)
-          part_ml(pml, slot, part_rows)[part_row] = make_float2(mref[m][e], l[m][e]);
-      }
-  }
-  // After a wait that gave up, loads may still be in flight: see them land.
-  if (!ok)
-    for (int s = 0; s < C::kStages; ++s) {
-      const int i = (stage + s) % C::kStages;
-      mbar_wait(&bars[i], phase ^ (stage + s >= C::kStages ? 1u : 0u), p.ctx, nullptr);
-    }
+  attn_decode::run<D, RT, kWarps>(tmap_k, tmap_v, p, smem, warp, lane,
+                                  static_cast<int>(blockIdx.x));
 }
 
 template <int D, int RT>
@@ -464,13 +36,13 @@ cudaError_t launch(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& 
     std::lock_guard<std::mutex> lock(host_cache_mutex());
     if (!done[dev & 63]) {
       e = cudaFuncSetAttribute(attn_decode_kernel<D, RT>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, RT>::kSmem);
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, attn_decode::Cfg<D, RT, kWarps>::kSmem);
       if (e != cudaSuccess) return e;
       done[dev & 63] = true;
     }
   }
-  return launch_pdl(attn_decode_kernel<D, RT>, dim3(a.L.d_ctas), dim3(32 * kDecodeWarps),
-                    Cfg<D, RT>::kSmem, s, tk, tv, a);
+  return launch_pdl(attn_decode_kernel<D, RT>, dim3(a.L.d_ctas), dim3(32 * kWarps),
+                    attn_decode::Cfg<D, RT, kWarps>::kSmem, s, tk, tv, a);
 }
 
 }  // namespace

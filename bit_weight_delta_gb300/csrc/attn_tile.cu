@@ -23,7 +23,7 @@
 // which evens out their lengths without a counter.
 #include <cstdint>
 
-#include "attention.cuh"
+#include "attn_decode.cuh"
 
 namespace bd {
 namespace {
@@ -36,6 +36,9 @@ constexpr int kPanel = kTileKeys * 128;  // 128 rows x 128 bytes
 // 208 and leave 88 for the third: 2·208 + 88 = 3·168.
 constexpr int kSoftmaxRegs = 208;
 constexpr int kOtherRegs = 88;
+// CTAs of the decode role: eight warps of 232, 2·232 + 40 = 3·168.
+constexpr int kDecodeRegs = 232;
+constexpr int kIdleRegs = 40;
 constexpr uint32_t kTmemCols = 512;
 
 template <int D>
@@ -176,7 +179,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
 // two pieces) and take() when it is done.
 struct Pieces {
   const TileEntry* entries;
-  int n, heads, k = 0, next_h = 0;
+  int n, w, heads, k = 0, next_h = 0;  // w: CTAs that take pieces
   bool has = false;
   TileEntry next;
   __device__ __forceinline__ explicit Pieces(const AttnArgs& a)
@@ -184,6 +187,7 @@ struct Pieces {
     // the first entry's address does not depend on how many there are (the
     // plan's table has at least one per CTA), so the two loads overlap
     const int32_t count = *const_cast<const volatile int32_t*>(&a.header()->t_entries);
+    w = *const_cast<const volatile int32_t*>(&a.header()->t_ctas);
     load(static_cast<int>(blockIdx.x));
     n = count * heads;
     has = static_cast<int>(blockIdx.x) < n;
@@ -197,7 +201,7 @@ struct Pieces {
     next_h = i - q * heads;
   }
   __device__ __forceinline__ void fetch() {
-    const int c = static_cast<int>(blockIdx.x), w = static_cast<int>(gridDim.x);
+    const int c = static_cast<int>(blockIdx.x);
     const int i = k * w + ((k & 1) ? w - 1 - c : c);
     has = i < n;
     if (has) load(i);
@@ -221,12 +225,11 @@ __device__ __forceinline__ int half_end(const TileEntry& e, int h, int half_tok)
   return nb < e.b1 ? nb : e.b1;
 }
 
-template <int D>
+template <int D, int RT>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_tile_kernel(const __grid_constant__ CUtensorMap tmap_q,
-                     const __grid_constant__ CUtensorMap tmap_k,
-                     const __grid_constant__ CUtensorMap tmap_v, const AttnArgs p) {
+    attn_tile_kernel(const __grid_constant__ TileMaps maps, const AttnArgs p) {
   using C = Cfg<D>;
+  const CUtensorMap &tmap_q = maps.q, &tmap_k = maps.k, &tmap_v = maps.v;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -281,7 +284,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_wait();
   griddep_launch_dependents();
 
-  if (warp < 8) {
+  const int n_tile = p.header()->t_ctas;
+  if (static_cast<int>(blockIdx.x) >= n_tile) {
+    // ============================================================ decode role
+    __syncthreads();  // everyone has read the tensor-memory address
+    attn_decode::init<D, RT, kTileDecodeWarps>(smem, warp, lane);
+    __syncthreads();
+    if (warp < kTileDecodeWarps) {
+      reg_inc<kDecodeRegs>();
+      attn_decode::run<D, RT, kTileDecodeWarps>(maps.dk, maps.dv, p, smem, warp, lane,
+                                            static_cast<int>(blockIdx.x) - n_tile);
+    } else {
+      reg_dec<kIdleRegs>();
+    }
+  } else if (warp < 8) {
     // ============================================================ softmax
     reg_inc<kSoftmaxRegs>();
     const int h = warp >> 2;
@@ -680,9 +696,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D>
-cudaError_t launch(const AttnArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
-                   const CUtensorMap& tv, cudaStream_t s) {
+template <int D, int RT>
+cudaError_t launch(const AttnArgs& a, const TileMaps& maps, cudaStream_t s) {
+  constexpr int kDecodeSmem = attn_decode::Cfg<D, RT, kTileDecodeWarps>::kSmem + 1024;
+  constexpr int kSmem = Cfg<D>::kSmem > kDecodeSmem ? Cfg<D>::kSmem : kDecodeSmem;
+  static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
   static bool done[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -690,21 +708,21 @@ cudaError_t launch(const AttnArgs& a, const CUtensorMap& tq, const CUtensorMap& 
   {
     std::lock_guard<std::mutex> lock(host_cache_mutex());
     if (!done[dev & 63]) {
-      e = cudaFuncSetAttribute(attn_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               Cfg<D>::kSmem);
+      e = cudaFuncSetAttribute(attn_tile_kernel<D, RT>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
       if (e != cudaSuccess) return e;
       done[dev & 63] = true;
     }
   }
-  return launch_pdl(attn_tile_kernel<D>, dim3(a.L.t_ctas), dim3(kThreads), Cfg<D>::kSmem, s, tq,
-                    tk, tv, a);
+  return launch_pdl(attn_tile_kernel<D, RT>, dim3(a.L.t_ctas), dim3(kThreads), kSmem, s, maps, a);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_tile(const AttnArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
-                             const CUtensorMap& tv, cudaStream_t s) {
-  return a.b.head_dim == 128 ? launch<128>(a, tq, tk, tv, s) : launch<64>(a, tq, tk, tv, s);
+cudaError_t launch_attn_tile(const AttnArgs& a, const TileMaps& maps, cudaStream_t s) {
+  if (a.b.head_dim == 128)
+    return a.L.d_rows == 16 ? launch<128, 1>(a, maps, s) : launch<128, 2>(a, maps, s);
+  return a.L.d_rows == 16 ? launch<64, 1>(a, maps, s) : launch<64, 2>(a, maps, s);
 }
 
 }  // namespace bd
