@@ -624,12 +624,19 @@ def _raw_stream(stream, t):
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
-def _new(shape, dtype, like, stream):
+def _new(shape, dtype, device, stream):
     """An output of a call; it belongs to the stream that writes it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _new_like(t, stream):
+    if stream is None:
+        return torch.empty_like(t)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t)
 
 
 def _out(t, shape, dtype, name):
@@ -660,10 +667,9 @@ def bitdelta_add_norm(y, residual=None, pre_table=None, post_table=None, gate=No
         if rtype is not torch.bfloat16 and rtype is not torch.float32:
             raise ValueError(f"residual must be bfloat16 or float32, got {rtype}")
         _out(residual, shape, rtype, "residual")
-    residual_out = (_new(shape, rtype, y, stream) if residual_out is None else
-                    _out(residual_out, shape, rtype, "residual_out"))
-    out = (_new(shape, torch.bfloat16, y, stream) if out is None else
-           _out(out, shape, torch.bfloat16, "out"))
+    residual_out = (_new_like(y if residual is None else residual, stream)
+                    if residual_out is None else _out(residual_out, shape, rtype, "residual_out"))
+    out = _new_like(y, stream) if out is None else _out(out, shape, torch.bfloat16, "out")
     gate_stride = 0
     if gate is not None:
         _dev(gate, torch.bfloat16, "gate")
@@ -739,9 +745,11 @@ class AttentionBatch:
             page_table.data_ptr(), n_group, _addr(group_offsets), _addr(prefix_len))
         self._ref = ctypes.addressof(self._c)
         lib = load()
-        self._plan = _new(lib.bitdelta_attention_plan_bytes(self._ref), torch.uint8, kv_len, stream)
-        self._ws = _new(lib.bitdelta_attention_workspace_bytes(self._ref), torch.uint8, kv_len,
-                        stream)
+        self._plan = _new(lib.bitdelta_attention_plan_bytes(self._ref), torch.uint8, kv_len.device,
+                          stream)
+        self._ws = _new(lib.bitdelta_attention_workspace_bytes(self._ref), torch.uint8,
+                        kv_len.device, stream)
+        self._device = kv_len.device
         self._plan_args = (self._plan.data_ptr(), self._plan.numel())
         self._ws_args = (self._ws.data_ptr(), self._ws.numel())
         self._q_shape = torch.Size((n_tokens, n_q_heads, head_dim))
@@ -775,7 +783,7 @@ def bitdelta_kv_append(batch: AttentionBatch, qkv, rope, k_pages, v_pages,
     _out(qkv, batch._qkv_shape, torch.bfloat16, "qkv")
     batch._cache(k_pages, v_pages)
     rows, rot = (0, 0) if rope is None else _dev(rope, torch.float32, "rope").shape
-    out = (_new(batch._q_shape, torch.bfloat16, qkv, stream) if out is None else
+    out = (_new(batch._q_shape, torch.bfloat16, batch._device, stream) if out is None else
            _out(out, batch._q_shape, torch.bfloat16, "out"))
     code = load().bitdelta_kv_append(
         batch._ref, qkv.data_ptr(), _addr(rope), rows, rot, 1 if interleaved else 0,
@@ -792,9 +800,9 @@ def bitdelta_attention(batch: AttentionBatch, q, k_pages, v_pages, scale: float 
     defaults to 1/sqrt(head_dim)."""
     _out(q, batch._q_shape, torch.bfloat16, "q")
     batch._cache(k_pages, v_pages)
-    out = (_new(batch._q_shape, torch.bfloat16, q, stream) if out is None else
+    out = (_new_like(q, stream) if out is None else
            _out(out, batch._q_shape, torch.bfloat16, "out"))
-    lse = (_new(batch._lse_shape, torch.float32, q, stream) if lse is None else
+    lse = (_new(batch._lse_shape, torch.float32, batch._device, stream) if lse is None else
            _out(lse, batch._lse_shape, torch.float32, "lse"))
     code = load().bitdelta_attention(
         batch._ref, *batch._plan_args, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),

@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
   }
   __syncthreads();
   // CTAs per role, so that both end at about the same time: a block of 256 rows
-  // takes about 1.5 µs of an SM (1.1 at 64-element heads) and a piece 3 µs on
+  // takes about 1.5 µs of an SM (1.1 at 64-element heads) and a piece 5 µs on
   // top, a CTA reads keys and values at about 80 bytes per ns.  A batch of 64
   // ragged decode rows and four 512-token chunks took 117 µs with the two kinds
   // of work one after the other.
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
   int n_tile = 0, n_dec = L.d_ctas;
   if (L.use_tile) {
     const float t_cost = static_cast<float>(t_blocks) * (b.head_dim == 128 ? 1.5f : 1.1f) +
-                         3.f * static_cast<float>(n_tiles) * b.n_kv_heads;
+                         5.f * static_cast<float>(n_tiles) * b.n_kv_heads;
     const float d_cost = static_cast<float>(d_units) * (kUnitKeys * 4.f / 80e3f) * b.head_dim;
     n_dec = d_units == 0 ? 0
                          : static_cast<int>(L.t_ctas * d_cost / (t_cost + d_cost) + 0.5f);
@@ -330,8 +330,27 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
   // uneven end: 256 tiles of up to 20 blocks with a share of 17 took 55 µs and
   // 32 µs more for the join when cut.
   int64_t share = n_tile == 0 ? 0 : (t_blocks + n_tile - 1) / n_tile;
-  if (s_longest <= share + (share / 4 > 4 ? share / 4 : 4)) share = s_longest;
-  const int piece = static_cast<int>(share < 2 ? 2 : share);
+  const bool cut = s_longest > share + (share / 4 > 4 ? share / 4 : 4);
+  if (!cut) share = s_longest;
+  int piece = static_cast<int>(share < 2 ? 2 : share);
+  if (cut && static_cast<int64_t>(n_tiles) * b.n_kv_heads <= n_tile) {
+    // Few tiles: the shortest pieces that are one per CTA, so that none takes a
+    // remainder on top of a full piece (each thread tries one length).
+    __syncthreads();
+    if (tid == 0) s_longest = INT_MAX;
+    for (int r = warp; r < n_run; r += kWarps)
+      for (int i = run_tile0[r] + lane; i < run_tile0[r + 1]; i += 32) {
+        int nb;
+        tile_of(r, i - run_tile0[r], &nb);
+        tile_ns[i] = nb;
+      }
+    __syncthreads();
+    int64_t pieces = 0;
+    for (int i = 0; i < n_tiles; ++i) pieces += (tile_ns[i] + piece + tid - 1) / (piece + tid);
+    if (pieces * b.n_kv_heads <= n_tile) atomicMin(&s_longest, piece + tid);
+    __syncthreads();
+    if (s_longest < INT_MAX) piece = s_longest;
+  }
   // slots first (a scan over tiles, which belong to runs: by tile index)
   for (int r = warp; r < n_run; r += kWarps) {
     const int t0 = run_tile0[r], t1 = run_tile0[r + 1];
@@ -437,31 +456,41 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
 // ------------------------------------------------------------------ combine
 
 constexpr int kCombThreads = 256;
+constexpr int kCombCtas = 4;   // per SM, and in the launch: one round, no second wave
 constexpr int kCombBatch = 4;  // parts that a thread has in flight
 
-// One CTA per (token, key head) of the plan's list, or per 32 columns of one
-// where rows have many parts.  A row's parts are dealt to the thread groups of
+// One CTA per (token, key head) of the plan's list, or per slice of its columns
+// where there are few.  A row's parts are dealt to the thread groups of
 // the CTA, which join them in a fixed order with a running maximum and meet in
 // shared memory: the join is one load of the item and about parts / (groups ·
 // 4) rounds of independent loads.  Neighbouring threads read neighbouring rows
 // of a slot.
-__global__ void __launch_bounds__(kCombThreads) combine_kernel(const AttnArgs p) {
+__global__ void __launch_bounds__(kCombThreads, kCombCtas) combine_kernel(const AttnArgs p) {
   __shared__ float4 s_o[kCombThreads];
   __shared__ float2 s_ml[kCombThreads];
   const bd_attention_batch& b = p.b;
   const AttnLayout& L = p.L;
   const int g = L.g, D = b.head_dim, H = b.n_kv_heads;
-  griddep_wait();
-  griddep_launch_dependents();
+  // The plan is older than the kernel that this one waits for, which has itself
+  // waited for it before it let this one start: its header and this CTA's first
+  // item are fetched while that kernel ends.
   const PlanHeader hd = *p.header();
-  const int slices = hd.most_parts <= 2 * kCombBatch && g * (D / 4) <= kCombThreads ? 1 : D / 32;
+  // as many column slices as one round of CTAs takes, at least what fits a CTA
+  int slices = D / 32;
+  while (slices > 1 && g * (D / 4) * 2 <= kCombThreads * slices &&
+         static_cast<int64_t>(hd.n_comb) * H * slices > gridDim.x)
+    slices >>= 1;
   const int cols = D / 4 / slices;  // float4 columns per CTA
   const int groups = kCombThreads / (cols * g);
   const int row = threadIdx.x % g, q = threadIdx.x / g;
   const int col = q % cols, grp = q / cols;
-  const int64_t n_work = static_cast<int64_t>(hd.n_comb) * H * slices;
-  for (int64_t w = blockIdx.x; w < n_work; w += gridDim.x) {
-    const CombItem it = p.comb()[w / (H * slices)];
+  const int n_work = hd.n_comb * H * slices;
+  CombItem it{};
+  if (static_cast<int>(blockIdx.x) < n_work) it = p.comb()[blockIdx.x / (H * slices)];
+  griddep_wait();
+  griddep_launch_dependents();
+  for (int w = static_cast<int>(blockIdx.x); w < n_work; w += gridDim.x) {
+    if (w != static_cast<int>(blockIdx.x)) it = p.comb()[w / (H * slices)];
     const int kvh = static_cast<int>(w / slices % H);
     const int d4 = static_cast<int>(w % slices) * cols + col;
     // own parts: tile slots own_slot .. (times heads plus head), decode parts,
@@ -614,7 +643,7 @@ bd_status run_attention(AttnArgs& p, cudaStream_t s) {
     return BD_ERR_CUDA;
   }
   const int64_t work = b.n_tokens * b.n_kv_heads * (b.head_dim / 32);
-  const int64_t most = 8 * static_cast<int64_t>(p.L.t_ctas);
+  const int64_t most = kCombCtas * static_cast<int64_t>(p.L.t_ctas);
   const cudaError_t e = launch_pdl(combine_kernel, dim3(static_cast<unsigned>(work < most ? work : most)),
                                    dim3(kCombThreads), 0, s, p);
   return e == cudaSuccess ? BD_OK : BD_ERR_CUDA;

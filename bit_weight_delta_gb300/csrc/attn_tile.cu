@@ -421,58 +421,58 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row_at = i * b.n_q_heads + row_head;  // the row's head in the tile's tokens
       const int64_t tile_at = static_cast<int64_t>(e.tok0) * b.n_q_heads + kvh * g;
       const int64_t slot = static_cast<int64_t>(e.slot) * b.n_kv_heads + kvh;
-#pragma unroll 1  // code that runs once a piece: kept short for the instruction cache
+      // (code that runs once a piece: kept short for the instruction cache)
+      uint8_t* mine = smem + C::kOffOut + warp * 4096;
+#pragma unroll 1
       for (int c = 0; c < D / 64; ++c) {
-        uint32_t o[2][32];
-        if (any) {
-          tmem_ld_32x32b_x32(t_o + 64u * c, o[0]);
-          tmem_ld_32x32b_x32(t_o + 64u * c + 32u, o[1]);
-          tmem_ld_wait();
-        } else {
+#pragma unroll 1
+        for (int x = 0; x < 4; ++x) {  // 16 columns
+          uint32_t o[16];
+          if (any) {
+            tmem_ld_x16(t_o + 64u * c + 16u * x, o);
+            tmem_ld_wait();
+          } else {
 #pragma unroll
-          for (int x = 0; x < 32; ++x) o[0][x] = o[1][x] = 0u;
-        }
-        if (e.slot < 0) {
-          // Through shared memory (swizzled), so that a store instruction
-          // covers whole 128-byte lines of four rows: with a row per lane the
-          // 32 lines of each store took 3 µs a piece.
-          uint8_t* mine = smem + C::kOffOut + warp * 4096;
+            for (int y = 0; y < 16; ++y) o[y] = 0u;
+          }
+          if (e.slot < 0) {
+            // Through shared memory (swizzled), so that a store instruction
+            // covers whole 128-byte lines of four rows: with a row per lane the
+            // 32 lines of each store took 3 µs a piece.
+            uint32_t w[8];
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const uint32_t* v = &o[x >> 2][8 * (x & 3)];
-            uint32_t w[4];
+            for (int y = 0; y < 8; ++y)
+              w[y] = pack_bf16x2_rn(__uint_as_float(o[2 * y]) * inv,
+                                    __uint_as_float(o[2 * y + 1]) * inv);
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+              *reinterpret_cast<uint4*>(mine + lane * 128 + (((2 * x + y) ^ (lane & 7)) << 4)) =
+                  make_uint4(w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
+          } else if (live) {
+            float4* dst = part_o(p.ws + p.L.w_t_o, slot, 2 * kHalfRows, D) + h * kHalfRows + r +
+                          (16 * c + 4 * x) * 2 * kHalfRows;
 #pragma unroll
             for (int y = 0; y < 4; ++y)
-              w[y] = pack_bf16x2_rn(__uint_as_float(v[2 * y]) * inv,
-                                    __uint_as_float(v[2 * y + 1]) * inv);
-            *reinterpret_cast<uint4*>(mine + lane * 128 + ((x ^ (lane & 7)) << 4)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
+              dst[y * 2 * kHalfRows] =
+                  make_float4(__uint_as_float(o[4 * y]), __uint_as_float(o[4 * y + 1]),
+                              __uint_as_float(o[4 * y + 2]), __uint_as_float(o[4 * y + 3]));
           }
           __syncwarp();
-          int at[8];
-          uint4 v[8];
-          const int chunk = lane & 7;
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const int row = 4 * x + (lane >> 3);
-            at[x] = __shfl_sync(0xFFFFFFFFu, live ? row_at : -1, row);
-            v[x] = *reinterpret_cast<const uint4*>(mine + row * 128 + ((chunk ^ (row & 7)) << 4));
-          }
-          uint16_t* dst = p.out + tile_at * D + 64 * c + 8 * chunk;
-#pragma unroll
-          for (int x = 0; x < 8; ++x)
-            if (at[x] >= 0) *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(at[x]) * D) = v[x];
-          __syncwarp();
-        } else if (live) {
-          float4* dst = part_o(p.ws + p.L.w_t_o, slot, 2 * kHalfRows, D) + h * kHalfRows + r;
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            const uint32_t* v = &o[x >> 3][4 * (x & 7)];
-            dst[(16 * c + x) * 2 * kHalfRows] =
-                make_float4(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]),
-                            __uint_as_float(v[3]));
-          }
         }
+        if (e.slot >= 0) continue;
+        int at[8];
+        uint4 v[8];
+        const int chunk = lane & 7;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const int row = 4 * x + (lane >> 3);
+          at[x] = __shfl_sync(0xFFFFFFFFu, live ? row_at : -1, row);
+          v[x] = *reinterpret_cast<const uint4*>(mine + row * 128 + ((chunk ^ (row & 7)) << 4));
+        }
+        uint16_t* dst = p.out + tile_at * D + 64 * c + 8 * chunk;
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          if (at[x] >= 0) *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(at[x]) * D) = v[x];
         __syncwarp();
       }
       if (live) {
