@@ -78,8 +78,10 @@ __device__ __forceinline__ const uint16_t* weights_of(const uint16_t* const* tab
 }
 
 // C chunks of 8 elements per thread.
+// (32 registers where they do, so that rows of 8192 stay two to an SM; the
+// weights are fetched late for that.)
 template <int C, bool kF32>
-__global__ void __launch_bounds__(1024) add_norm_kernel(const NormArgs p) {
+__global__ void __launch_bounds__(1024, C == 1 ? 2 : 1) add_norm_kernel(const NormArgs p) {
   __shared__ float s_post[32], s_pre[32];
   __shared__ int s_seg;
   const int64_t row = blockIdx.x;
@@ -130,14 +132,6 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const NormArgs p) {
     }
   }
   const uint16_t* w_pre = p.pre_table ? weights_of(p.pre_table, slot, p.ctx) : nullptr;
-  uint4 wv[C];
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int i = c * blockDim.x + tid;
-    // 0x3F80 is one
-    wv[c] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
-    if (i < n8 && w_pre != nullptr) wv[c] = ldg_v4(reinterpret_cast<const uint4*>(w_pre) + i);
-  }
 
   float inv_post = 1.f;
   const uint16_t* w_post = nullptr;
@@ -198,6 +192,14 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const NormArgs p) {
     }
   }
   if (p.x_out == nullptr) return;
+  uint4 wv[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int i = c * blockDim.x + tid;
+    // 0x3F80 is one
+    wv[c] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+    if (i < n8 && w_pre != nullptr) wv[c] = ldg_v4(reinterpret_cast<const uint4*>(w_pre) + i);
+  }
   const float inv = rsqrtf(block_sum(ss, s_pre) / static_cast<float>(p.d) + p.eps);
 #pragma unroll
   for (int c = 0; c < C; ++c) {

@@ -155,6 +155,16 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack2_bf16(uint64_t v) {
+  float lo, hi;
+  unpack2(v, lo, hi);
+  return pack_bf16x2_rn(lo, hi);
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -418,6 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       const float inv = l > 0.f ? 1.f / l : 0.f;
+      const uint64_t inv2 = pack2(inv, inv);
       const int row_at = i * b.n_q_heads + row_head;  // the row's head in the tile's tokens
       const int64_t tile_at = static_cast<int64_t>(e.tok0) * b.n_q_heads + kvh * g;
       const int64_t slot = static_cast<int64_t>(e.slot) * b.n_kv_heads + kvh;
@@ -442,8 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t w[8];
 #pragma unroll
             for (int y = 0; y < 8; ++y)
-              w[y] = pack_bf16x2_rn(__uint_as_float(o[2 * y]) * inv,
-                                    __uint_as_float(o[2 * y + 1]) * inv);
+              w[y] = pack2_bf16(mul2(pack2(__uint_as_float(o[2 * y]), __uint_as_float(o[2 * y + 1])),
+                                     inv2));
 #pragma unroll
             for (int y = 0; y < 2; ++y)
               *reinterpret_cast<uint4*>(mine + lane * 128 + (((2 * x + y) ^ (lane & 7)) << 4)) =
