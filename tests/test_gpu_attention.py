@@ -315,3 +315,46 @@ def test_refusals():
             c.make(**over)
     with pytest.raises(ValueError):
         c.make(prefix_len=torch.zeros(1, dtype=torch.int32).cuda())
+
+
+def test_ranges_cut_in_every_way():
+    """Very unlike lengths: runs that span many CTAs, runs that share one with others, and
+    runs of one tile, in one batch; alone, and beside prompts in the same launch."""
+    rng = np.random.default_rng(17)
+    short = [(1, 30000)] + [(1, int(k)) for k in rng.integers(1, 40, 60)] + [(1, 9000), (2, 17),
+                                                                            (1, 4096), (1, 1)]
+    c = Case(short, 8, 2, 64, 64, seed=17)
+    c.check(*c.run())
+    c = Case(short[:40] + [(300, 700)] + short[40:], 8, 2, 64, 64, seed=18)
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_random_batches(seed):
+    """Random heads, pages, groups, query and key lengths."""
+    rng = np.random.default_rng(1000 + seed)
+    hq, hkv = [(8, 1), (8, 8), (6, 2), (10, 2), (12, 4), (32, 1), (28, 4), (24, 8)][seed % 8]
+    dim, page = [64, 128][int(rng.integers(2))], [16, 32, 64, 128][int(rng.integers(4))]
+    lens, groups = [], []
+    for _ in range(int(rng.integers(0, 3))):
+        prefix, n = page * int(rng.integers(0, 900 // page + 2)), int(rng.integers(1, 24))
+        groups.append((n, prefix))
+        for _ in range(n):
+            q = int(rng.choice([1, 1, 1, 2, 5, 40]))
+            lens.append((q, prefix + q + int(rng.integers(0, 300))))
+    for _ in range(int(rng.integers(1, 30))):
+        q = int(rng.choice([0, 1, 1, 1, 3, 17, 100, 260]))
+        lens.append((q, max(0, q + int(rng.integers(-2, 900)))))
+    c = Case(lens, hq, hkv, dim, page, groups=groups, seed=seed, std=float(rng.uniform(0.3, 2.5)),
+             extra_tokens=int(rng.integers(0, 3)))
+    c.check(*c.run())
+
+
+def test_one_token_everywhere():
+    """The smallest batch."""
+    for dim in (64, 128):
+        c = Case([(1, 1)], 1, 1, dim, 16, seed=19)
+        out, lse = c.run()
+        c.check(out, lse)
+        want = c.vp[c.table[0, 0], 0, 0]
+        assert torch.equal(out[0, 0], want)          # its own value, weight one
