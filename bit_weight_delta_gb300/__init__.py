@@ -717,8 +717,8 @@ class AttentionBatch:
     consecutive sequences that share their first positions' pages.  The
     constructor computes the plan (stream-ordered, on the device); it holds for
     every layer of the step.  After writing new lengths into the same tensors,
-    call plan() again.  The batch owns one workspace: attention calls that can
-    overlap on the GPU need batches of their own."""
+    call plan() again.  The batch owns one plan and workspace: attention calls
+    that can overlap on the GPU need batches of their own."""
 
     def __init__(self, seq_offsets, kv_len, page_table, n_tokens: int, max_q_len: int,
                  max_kv_len: int, n_q_heads: int, n_kv_heads: int, head_dim: int,

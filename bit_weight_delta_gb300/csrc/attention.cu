@@ -29,9 +29,11 @@ AttnLayout attn_layout(const bd_attention_batch& b, int num_sms) {
   L.d_warps = 8 * num_sms;
   L.t_ctas = num_sms;
   const int64_t T = b.n_tokens;
-  const int64_t long_seqs =
-      max_rows > L.d_rows ? (T * L.g / (L.d_rows + 1) < b.n_seq ? T * L.g / (L.d_rows + 1) : b.n_seq)
-                          : 0;
+  int64_t long_seqs = 0;  // at most
+  if (max_rows > L.d_rows) {
+    long_seqs = T * L.g / (L.d_rows + 1);
+    long_seqs = long_seqs < b.n_seq ? long_seqs : b.n_seq;
+  }
   L.max_tiles = 0;
   if (max_rows > L.d_rows) L.max_tiles += T / tile_tok + long_seqs;
   const int64_t prefix_tiles = b.n_group > 0 ? T / tile_tok + b.n_group : 0;
@@ -164,7 +166,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
     for (int c = tid; c < L.d_warps; c += kPlanThreads) starts[c].lo = starts[c].hi = 0;
     if (tid == 0) {
       record_error(p.ctx, kErrBounds);
-      *hd = PlanHeader{0, 1, 1, 0, 0, static_cast<int32_t>(b.n_tokens), 0};
+      *hd = PlanHeader{0, 1, 1, 0, 0, static_cast<int32_t>(b.n_tokens), 0, 0, 0};
     }
     return;
   }
@@ -290,18 +292,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
   }
   __syncthreads();
   // CTAs per role, so that both end at about the same time: a block of 256 rows
-  // takes about 1.5 µs of an SM (1.1 at 64-element heads) and a piece 5 µs on
+  // takes about 1.4 µs of an SM (1 at 64-element heads) and a piece 5 µs on
   // top, a CTA reads keys and values at about 80 bytes per ns.  A batch of 64
   // ragged decode rows and four 512-token chunks took 117 µs with the two kinds
   // of work one after the other.
   const int64_t t_blocks = static_cast<int64_t>(s_blocks) * b.n_kv_heads;
   int n_tile = 0, n_dec = L.d_ctas;
   if (L.use_tile) {
-    const float t_cost = static_cast<float>(t_blocks) * (b.head_dim == 128 ? 1.5f : 1.1f) +
+    const float t_cost = static_cast<float>(t_blocks) * (b.head_dim == 128 ? 1.4f : 1.f) +
                          5.f * static_cast<float>(n_tiles) * b.n_kv_heads;
     const float d_cost = static_cast<float>(d_units) * (kUnitKeys * 4.f / 80e3f) * b.head_dim;
     n_dec = d_units == 0 ? 0
-                         : static_cast<int>(L.t_ctas * d_cost / (t_cost + d_cost) + 0.5f);
+                         : static_cast<int>(ceilf(L.t_ctas * d_cost / (t_cost + d_cost)));
     if (d_units > 0 && n_dec < 1) n_dec = 1;
     if (t_blocks > 0 && n_dec > L.t_ctas - 1) n_dec = L.t_ctas - 1;
     n_tile = L.t_ctas - n_dec;
@@ -449,14 +451,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
   __syncthreads();
   if (tid == 0) {
     if (!fits) record_error(p.ctx, kErrBounds);
-    *hd = PlanHeader{d_units, static_cast<int32_t>(d_per), warps, fits ? n_entries : 0, n_tile, s_comb, s_parts};
+    *hd = PlanHeader{d_units, static_cast<int32_t>(d_per), warps, fits ? n_entries : 0,
+                     n_tile,  s_comb, s_parts, n_tile, 0};
   }
 }
 
 // ------------------------------------------------------------------ combine
 
-constexpr int kCombThreads = 256;
-constexpr int kCombCtas = 4;   // per SM, and in the launch: one round, no second wave
+constexpr int kCombThreads = 128;
+constexpr int kCombCtas = 8;   // per SM, and in the launch: one round, no second wave
 constexpr int kCombBatch = 4;  // parts that a thread has in flight
 
 // One CTA per (token, key head) of the plan's list, or per slice of its columns
@@ -476,7 +479,7 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtas) combine_kernel(const 
   // item are fetched while that kernel ends.
   const PlanHeader hd = *p.header();
   // as many column slices as one round of CTAs takes, at least what fits a CTA
-  int slices = D / 32;
+  int slices = D / 16;
   while (slices > 1 && g * (D / 4) * 2 <= kCombThreads * slices &&
          static_cast<int64_t>(hd.n_comb) * H * slices > gridDim.x)
     slices >>= 1;
@@ -489,8 +492,12 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtas) combine_kernel(const 
   if (static_cast<int>(blockIdx.x) < n_work) it = p.comb()[blockIdx.x / (H * slices)];
   griddep_wait();
   griddep_launch_dependents();
+  // the tile kernel has dealt its pieces: its counter for the next call
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.piece_counter() = hd.t_ctas;
+  CombItem ahead = it;
   for (int w = static_cast<int>(blockIdx.x); w < n_work; w += gridDim.x) {
-    if (w != static_cast<int>(blockIdx.x)) it = p.comb()[w / (H * slices)];
+    it = ahead;
+    if (w + static_cast<int>(gridDim.x) < n_work) ahead = p.comb()[(w + gridDim.x) / (H * slices)];
     const int kvh = static_cast<int>(w / slices % H);
     const int d4 = static_cast<int>(w % slices) * cols + col;
     // own parts: tile slots own_slot .. (times heads plus head), decode parts,
@@ -530,7 +537,8 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtas) combine_kernel(const 
           ml[k] = make_float2(-INFINITY, 0.f);
           v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (i < n_own) {
-            const int64_t slot = cut && n_own > 1 ? dp.slot(i) : first + static_cast<int64_t>(i) * H;
+            const int64_t slot =
+                cut && n_own > 1 ? dp.slot(i) : first + static_cast<int64_t>(i) * H;
             ml[k] = part_ml(ml_base, slot, rows)[own_row + row];
             v[k] = part_o(o_base, slot, rows, D)[static_cast<int64_t>(d4) * rows + own_row + row];
           } else if (i < n) {
@@ -563,10 +571,10 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtas) combine_kernel(const 
       }
     }
     if (groups > 1) {
-    __syncthreads();  // the last item's values have been read
-    s_o[threadIdx.x] = o;
-    s_ml[threadIdx.x] = make_float2(m, l);
-    __syncthreads();
+      __syncthreads();  // the last item's values have been read
+      s_o[threadIdx.x] = o;
+      s_ml[threadIdx.x] = make_float2(m, l);
+      __syncthreads();
     }
     if (grp != 0) continue;
     const int span = g * cols, most = groups < n ? groups : n;
@@ -642,10 +650,10 @@ bd_status run_attention(AttnArgs& p, cudaStream_t s) {
   } else if (launch_attn_decode(p, m.dk, m.dv, s) != cudaSuccess) {
     return BD_ERR_CUDA;
   }
-  const int64_t work = b.n_tokens * b.n_kv_heads * (b.head_dim / 32);
+  const int64_t work = b.n_tokens * b.n_kv_heads * (b.head_dim / 16);
   const int64_t most = kCombCtas * static_cast<int64_t>(p.L.t_ctas);
-  const cudaError_t e = launch_pdl(combine_kernel, dim3(static_cast<unsigned>(work < most ? work : most)),
-                                   dim3(kCombThreads), 0, s, p);
+  const dim3 grid(static_cast<unsigned>(work < most ? work : most));
+  const cudaError_t e = launch_pdl(combine_kernel, grid, dim3(kCombThreads), 0, s, p);
   return e == cudaSuccess ? BD_OK : BD_ERR_CUDA;
 }
 
@@ -680,7 +688,7 @@ size_t bitdelta_attention_workspace_bytes(const bd_attention_batch* batch) {
   return bd::sized_layout(batch).ws_bytes;
 }
 
-bd_status bitdelta_attention(const bd_attention_batch* batch, const void* plan, size_t plan_bytes,
+bd_status bitdelta_attention(const bd_attention_batch* batch, void* plan, size_t plan_bytes,
                              const uint16_t* q, const uint16_t* k_pages, const uint16_t* v_pages,
                              float scale, uint16_t* out, float* lse, void* workspace,
                              size_t workspace_bytes, bd_stream_t stream) {
@@ -698,7 +706,7 @@ bd_status bitdelta_attention(const bd_attention_batch* batch, const void* plan, 
   bd::AttnArgs p{};
   if ((st = bd::fill_args(batch, &p)) != BD_OK) return static_cast<bd_status>(st);
   if (plan_bytes < p.L.plan_bytes || workspace_bytes < p.L.ws_bytes) return BD_ERR_WORKSPACE;
-  p.plan = static_cast<uint8_t*>(const_cast<void*>(plan));
+  p.plan = static_cast<uint8_t*>(plan);
   p.ws = static_cast<uint8_t*>(workspace);
   p.q = q;
   p.k_pages = k_pages;

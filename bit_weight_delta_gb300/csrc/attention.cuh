@@ -37,6 +37,8 @@ struct PlanHeader {
   int32_t t_ctas;     // CTAs of its launch that take pieces; the others take units
   int32_t n_comb;     // tokens whose rows the combine kernel writes
   int32_t most_parts; // of any of their rows
+  int32_t next_piece; // the tile kernel's dealing: t_ctas between calls
+  int32_t pad;
 };
 
 // The decode role's parts of a run of units [u0, u1), out of `total` units cut
@@ -160,6 +162,9 @@ struct AttnArgs {
 
   __host__ __device__ const PlanHeader* header() const {
     return reinterpret_cast<const PlanHeader*>(plan);
+  }
+  __device__ int* piece_counter() const {
+    return &reinterpret_cast<PlanHeader*>(plan)->next_piece;
   }
   __host__ __device__ const SeqRec* seqs() const {
     return reinterpret_cast<const SeqRec*>(plan + L.o_seq);

@@ -36,7 +36,8 @@ cudaError_t launch(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& 
     std::lock_guard<std::mutex> lock(host_cache_mutex());
     if (!done[dev & 63]) {
       e = cudaFuncSetAttribute(attn_decode_kernel<D, RT>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, attn_decode::Cfg<D, RT, kWarps>::kSmem);
+                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               attn_decode::Cfg<D, RT, kWarps>::kSmem);
       if (e != cudaSuccess) return e;
       done[dev & 63] = true;
     }

@@ -355,66 +355,66 @@ __device__ __forceinline__ void run(const CUtensorMap& tmap_k, const CUtensorMap
         if (together && t4 == 0) s_m[warp * C::kRows + 16 * m + 8 * e + g8] = mref[m][e];
       }
     if (together) {
-    // ---- join the warps: m, then o and l relative to the common m
-    sync_warps<W>();
+      // ---- join the warps: m, then o and l relative to the common m
+      sync_warps<W>();
 #pragma unroll
-    for (int m = 0; m < RT; ++m) {
-      float f[2];
+      for (int m = 0; m < RT; ++m) {
+        float f[2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = 16 * m + 8 * e + g8;
-        float top = s_m[row];
+        for (int e = 0; e < 2; ++e) {
+          const int row = 16 * m + 8 * e + g8;
+          float top = s_m[row];
 #pragma unroll
-        for (int w = 1; w < W; ++w) top = fmaxf(top, s_m[w * C::kRows + row]);
-        f[e] = top == -INFINITY ? 1.f : ex2(mref[m][e] - top);
-        mref[m][e] = top;
-        l[m][e] *= f[e];
-      }
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) o[m][n][x] *= f[x >> 1];
-    }
-    const auto put = [&](int slot) {
-      float4* d = reinterpret_cast<float4*>(smem + C::kOffMerge + slot * C::kMerge) + lane;
-#pragma unroll
-      for (int m = 0; m < RT; ++m)
+          for (int w = 1; w < W; ++w) top = fmaxf(top, s_m[w * C::kRows + row]);
+          f[e] = top == -INFINITY ? 1.f : ex2(mref[m][e] - top);
+          mref[m][e] = top;
+          l[m][e] *= f[e];
+        }
 #pragma unroll
         for (int n = 0; n < D / 8; ++n)
-          d[(m * (D / 8) + n) * 32] = make_float4(o[m][n][0], o[m][n][1], o[m][n][2], o[m][n][3]);
-      if (t4 == 0)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) o[m][n][x] *= f[x >> 1];
+      }
+      const auto put = [&](int slot) {
+        float4* d = reinterpret_cast<float4*>(smem + C::kOffMerge + slot * C::kMerge) + lane;
 #pragma unroll
         for (int m = 0; m < RT; ++m)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) s_l[slot * C::kRows + 16 * m + 8 * e + g8] = l[m][e];
-    };
-    const auto add = [&](int slot) {
-      const float4* d =
-          reinterpret_cast<const float4*>(smem + C::kOffMerge + slot * C::kMerge) + lane;
+          for (int n = 0; n < D / 8; ++n)
+            d[(m * (D / 8) + n) * 32] = make_float4(o[m][n][0], o[m][n][1], o[m][n][2], o[m][n][3]);
+        if (t4 == 0)
 #pragma unroll
-      for (int m = 0; m < RT; ++m) {
+          for (int m = 0; m < RT; ++m)
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          const float4 v = d[(m * (D / 8) + n) * 32];
-          o[m][n][0] += v.x;
-          o[m][n][1] += v.y;
-          o[m][n][2] += v.z;
-          o[m][n][3] += v.w;
+            for (int e = 0; e < 2; ++e) s_l[slot * C::kRows + 16 * m + 8 * e + g8] = l[m][e];
+      };
+      const auto add = [&](int slot) {
+        const float4* d =
+            reinterpret_cast<const float4*>(smem + C::kOffMerge + slot * C::kMerge) + lane;
+#pragma unroll
+        for (int m = 0; m < RT; ++m) {
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) {
+            const float4 v = d[(m * (D / 8) + n) * 32];
+            o[m][n][0] += v.x;
+            o[m][n][1] += v.y;
+            o[m][n][2] += v.z;
+            o[m][n][3] += v.w;
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) l[m][e] += s_l[slot * C::kRows + 16 * m + 8 * e + g8];
         }
+      };
+      // halves of the remaining warps, one onto the other; a warp's slot is one
+      // that nobody but itself has still to read
 #pragma unroll
-        for (int e = 0; e < 2; ++e) l[m][e] += s_l[slot * C::kRows + 16 * m + 8 * e + g8];
+      for (int half = W / 2; half >= 1; half /= 2) {
+        const int first = half == W / 2 ? W / 2 : 0;
+        if (warp >= half && warp < 2 * half) put(warp - first);
+        sync_warps<W>();
+        if (warp < half) add(warp + half - first);
       }
-    };
-    // halves of the remaining warps, one onto the other; a warp's slot is one
-    // that nobody but itself has still to read
-#pragma unroll
-    for (int half = W / 2; half >= 1; half /= 2) {
-      const int first = half == W / 2 ? W / 2 : 0;
-      if (warp >= half && warp < 2 * half) put(warp - first);
-      sync_warps<W>();
-      if (warp < half) add(warp + half - first);
-    }
-    if (warp != 0) continue;
+      if (warp != 0) continue;
     }
 
     // ---- final rows, or a partial result

@@ -14,13 +14,15 @@
 // row's maximum has left the reference's range (kRescale).
 //
 // Tensor memory (512 columns): S/P of half h at 128·h, O of half h at 256 +
-// 128·h.  Warps: 0-3 and 4-7 the halves' softmax and epilogue, 8 and 9
-// their MMA issuers, 10 and 11 the TMA producers of Q and K, and of V.  Q, K and V lie in shared memory in
-// the 128-byte swizzle, 64 columns (128 bytes) of 128 rows per 16 KB panel; K
-// is the K-major B operand, V (keys x D as stored) the MN-major one.
+// 128·h.  Warps: 0-3 and 4-7 the halves' softmax and epilogue, 8 and 9 their
+// MMA issuers, 10 and 11 the TMA producers of Q and K, and of V.  Q, K and V
+// lie in shared memory in the 128-byte swizzle, 64 columns (128 bytes) of 128
+// rows per 16 KB panel; K is the K-major B operand, V (keys x D as stored) the
+// MN-major one.
 //
-// Pieces (plan.entries, longest first) are dealt to the CTAs back and forth,
-// which evens out their lengths without a counter.
+// Pieces (the plan's list, longest first) are dealt to the CTAs as they come: a
+// batch of 256 pieces of 1 to 20 blocks ended within 3% on all CTAs, where a
+// fixed deal back and forth left a tail of 9%.
 #include <cstdint>
 
 #include "attn_decode.cuh"
@@ -40,6 +42,7 @@ constexpr int kOtherRegs = 88;
 constexpr int kDecodeRegs = 232;
 constexpr int kIdleRegs = 40;
 constexpr uint32_t kTmemCols = 512;
+constexpr int kPieceBytes = 64;
 
 template <int D>
 struct Cfg {
@@ -51,10 +54,11 @@ struct Cfg {
   static constexpr int kOffOut = kOffKv + kStages * kStageBytes;  // 4 KB per softmax warp
   static constexpr int kOffBar = kOffOut + 8 * 4096;
   // q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], tail, drain[2],
-  // turn[2], kv_full[], kv_empty[]
-  static constexpr int kBars = 17 + 2 * kStages;
-  static constexpr int kOffMisc = kOffBar + kBars * 8;
-  static constexpr int kSmem = kOffMisc + 16 + 1024;  // with slack for alignment
+  // turn[2], piece_full[2], piece_empty[2], kv_full[], kv_empty[]
+  static constexpr int kBars = 21 + 2 * kStages;
+  static constexpr int kOffMisc = (kOffBar + kBars * 8 + 15) / 16 * 16;
+  static constexpr int kOffPiece = kOffMisc + 16;
+  static constexpr int kSmem = kOffPiece + 2 * kPieceBytes + 1024;  // with slack for alignment
 };
 
 template <int N>
@@ -184,46 +188,37 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, ctx, abort));
 }
 
-// The pieces of one CTA in turn.  Every role calls fetch() for the next piece
-// while it works on the current one (loads and a division off the path between
-// two pieces) and take() when it is done.
+// A piece as the roles read it from shared memory: kvh < 0 ends the work.
+struct Piece {
+  TileEntry e;
+  int kvh, pad[3];
+};
+static_assert(sizeof(Piece) == kPieceBytes, "four 16-byte words");
+
+// The CTA's pieces in turn, two slots of shared memory that the K producer
+// fills (one piece ahead) and every other warp of the tile role empties.
 struct Pieces {
-  const TileEntry* entries;
-  int n, w, heads, k = 0, next_h = 0;  // w: CTAs that take pieces
-  bool has = false;
-  TileEntry next;
-  __device__ __forceinline__ explicit Pieces(const AttnArgs& a)
-      : entries(a.entries()), heads(a.b.n_kv_heads) {
-    // the first entry's address does not depend on how many there are (the
-    // plan's table has at least one per CTA), so the two loads overlap
-    const int32_t count = *const_cast<const volatile int32_t*>(&a.header()->t_entries);
-    w = *const_cast<const volatile int32_t*>(&a.header()->t_ctas);
-    load(static_cast<int>(blockIdx.x));
-    n = count * heads;
-    has = static_cast<int>(blockIdx.x) < n;
-    k = 1;
-  }
-  __device__ __forceinline__ void load(int i) {
-    const int q = static_cast<int>(static_cast<unsigned>(i) / static_cast<unsigned>(heads));
-    const int4* src = reinterpret_cast<const int4*>(entries + q);
-    const int4 x = __ldg(src), y = __ldg(src + 1), z = __ldg(src + 2);
-    next = TileEntry{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, 0, 0};
-    next_h = i - q * heads;
-  }
-  __device__ __forceinline__ void fetch() {
-    const int c = static_cast<int>(blockIdx.x);
-    const int i = k * w + ((k & 1) ? w - 1 - c : c);
-    has = i < n;
-    if (has) load(i);
-    ++k;
-  }
-  // once a piece is missing in one round, none follows in a later one
-  __device__ __forceinline__ bool take(TileEntry& e, int& h) const {
-    e = next;
-    h = next_h;
-    return has;
+  const Piece* slots;
+  uint64_t *full, *empty;
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ bool take(TileEntry& e, int& kvh, const DevCtx& ctx,
+                                       volatile int* abort) {
+    if (!warp_wait(&full[slot], phase, ctx, abort)) return false;
+    const int4* src = reinterpret_cast<const int4*>(slots + slot);
+    const int4 x = src[0], y = src[1], z = src[2];
+    e = TileEntry{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, 0, 0};
+    kvh = slots[slot].kvh;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[slot]);
+    if (++slot == 2) {
+      slot = 0;
+      phase ^= 1u;
+    }
+    return kvh >= 0;
   }
 };
+constexpr int kPieceReaders = 11;  // 8 softmax warps, 2 issuers, the V producer
 
 // Blocks of half h in a piece: [b0, end), empty when end <= b0.
 __device__ __forceinline__ int half_end(const TileEntry& e, int h, int half_tok) {
@@ -251,7 +246,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* tail_bar = q_full + 12;
   uint64_t* drain_bar = q_full + 13;
   uint64_t* turn = q_full + 15;
-  uint64_t* kv_full = q_full + 17;
+  uint64_t* piece_full = q_full + 17;
+  uint64_t* piece_empty = q_full + 19;
+  uint64_t* kv_full = q_full + 21;
+  Piece* piece_slots = reinterpret_cast<Piece*>(smem + C::kOffPiece);
   uint64_t* kv_empty = kv_full + C::kStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
@@ -270,6 +268,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&p_full[2 * h + 1], 4);
       mbar_init(&o_full[h], 1);
       mbar_init(&turn[h], 1);
+      mbar_init(&piece_full[h], 1);
+      mbar_init(&piece_empty[h], kPieceReaders);
     }
     mbar_init(tail_bar, 1);
     mbar_init(&drain_bar[0], 1);
@@ -317,11 +317,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t_o = tmem + lanes + 256u + 128u * h;
     const int row_tok = r / g, row_head = r - row_tok * g;
     uint32_t s_phase = 0, o_phase = 0;
-    Pieces pieces(p);
+    Pieces pieces{piece_slots, piece_full, piece_empty};
     TileEntry e;
     int kvh;
     bool ok = true;
-    while (ok && pieces.take(e, kvh)) {
+    while (ok && pieces.take(e, kvh, p.ctx, abort)) {
       const int end = half_end(e, h, half_tok);
       const int i = h * half_tok + row_tok;                      // token of the tile
       const bool live = row_tok < half_tok && i < e.n_tok;       // a row that exists
@@ -350,8 +350,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // Weights two at a time (paired fp32 operations: half the instructions),
         // relative to a reference that follows the row's maximum lazily.
-        // (Forming the first weights before the maximum is known, to be redone
-        // where it moves, measured 15% slower.)
+        // (Forming the first weights with the reference as it stands, before the
+        // block's maximum is known, and again where it moves, measured no faster
+        // on long prompts and 3-5% slower on batches of short pieces.)
         const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
         uint64_t sum[2] = {0u, 0u};
         const auto weigh = [&](int c, uint64_t ref2) {
@@ -418,7 +419,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += l0 + l1;
       }
       if (!ok) break;
-      pieces.fetch();
       // ---- epilogue: the half's rows, final or as a partial result
       const bool any = end > e.b0;
       if (any) {
@@ -453,8 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t w[8];
 #pragma unroll
             for (int y = 0; y < 8; ++y)
-              w[y] = pack2_bf16(mul2(pack2(__uint_as_float(o[2 * y]), __uint_as_float(o[2 * y + 1])),
-                                     inv2));
+              w[y] = pack2_bf16(mul2(
+                  pack2(__uint_as_float(o[2 * y]), __uint_as_float(o[2 * y + 1])), inv2));
 #pragma unroll
             for (int y = 0; y < 2; ++y)
               *reinterpret_cast<uint4*>(mine + lane * 128 + (((2 * x + y) ^ (lane & 7)) << 4)) =
@@ -512,15 +512,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t idesc_o = idesc_bf16_f32(128, D) | kIdescB_MN;
       const uint32_t kv_base = smem_addr(smem + C::kOffKv);
       const uint32_t t_s = tmem + 128u * h, t_o = tmem + 256u + 128u * h;
-      const uint64_t qd = sdesc_k_sw128(smem_addr(smem) + static_cast<uint32_t>(h) * C::kStageBytes);
+      const uint64_t qd =
+          sdesc_k_sw128(smem_addr(smem) + static_cast<uint32_t>(h) * C::kStageBytes);
       uint32_t q_phase = 0, p_phase = 0, my_turn = h == 0 ? 1u : 0u;
       int stage = 0, v_stage = 1;      // of the current K, of the last block's V
       uint32_t phase = 0, v_phase = 0;
       bool ok = true, issued = false;
-      Pieces pieces(p);
+      Pieces pieces{piece_slots, piece_full, piece_empty};
       TileEntry e;
       int kvh;
-      while (ok && pieces.take(e, kvh)) {
+      while (ok && pieces.take(e, kvh, p.ctx, abort)) {
         const int b0 = __shfl_sync(0xFFFFFFFFu, e.b0, 0), b1 = __shfl_sync(0xFFFFFFFFu, e.b1, 0);
         const int end = __shfl_sync(0xFFFFFFFFu, half_end(e, h, half_tok), 0);
         // keys from the last block on
@@ -581,7 +582,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (back) mma_commit(&kv_empty[v_stage]);
             if (more) mma_commit(&kv_empty[stage]);
           }
-          if (j == b0) pieces.fetch();
           if (!more) break;
           left -= kTileKeys;
           v_stage = stage + 1;
@@ -612,10 +612,58 @@ __global__ void __launch_bounds__(kThreads, 1)
       int fill = 0, stage = is_v ? 1 : 0;
       uint32_t phase = 1, q_phase[2] = {1, 1}, tail_phase = 0;
       bool ok = true;
-      Pieces pieces(p);
-      TileEntry e;
-      int kvh;
-      while (ok && pieces.take(e, kvh)) {
+      // The K producer also deals the pieces: the first by the CTA's index, then
+      // the next of the list (longest first) once it has loaded all of the
+      // current one, about two blocks before that ends.  (Drawn earlier, a CTA
+      // with a long piece takes another long one.)  The counter starts at the
+      // number of CTAs, set by the plan and again by the kernel that joins the
+      // parts.
+      const int n_pieces = p.header()->t_entries * b.n_kv_heads;
+      int* counter = p.piece_counter();
+      int put_slot = 0;
+      uint32_t put_phase = 1;
+      const auto read_piece = [&](int i, TileEntry& e, int& kvh) {
+        kvh = -1;
+        if (i >= n_pieces) return;
+        const int q = static_cast<int>(static_cast<unsigned>(i) /
+                                       static_cast<unsigned>(b.n_kv_heads));
+        const int4* src = reinterpret_cast<const int4*>(p.entries() + q);
+        const int4 x = __ldg(src), y = __ldg(src + 1), z = __ldg(src + 2);
+        e = TileEntry{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, 0, 0};
+        kvh = i - q * b.n_kv_heads;
+      };
+      const auto put = [&](const TileEntry& e, int kvh) {
+        if (!warp_wait(&piece_empty[put_slot], put_phase, p.ctx, abort)) return false;
+        if (lane == 0) {
+          int4* dst = reinterpret_cast<int4*>(piece_slots + put_slot);
+          dst[0] = make_int4(e.tok0, e.n_tok, e.seq, e.k_lo);
+          dst[1] = make_int4(e.k_hi, e.causal, e.b0, e.b1);
+          dst[2] = make_int4(e.slot, e.tail, 0, 0);
+          piece_slots[put_slot].kvh = kvh;
+          mbar_arrive(&piece_full[put_slot]);
+        }
+        __syncwarp();
+        if (++put_slot == 2) {
+          put_slot = 0;
+          put_phase ^= 1u;
+        }
+        return true;
+      };
+      Pieces pieces{piece_slots, piece_full, piece_empty};
+      TileEntry e, next_e;
+      int kvh, next_kvh = -1;
+      if (!is_v) {
+        read_piece(static_cast<int>(blockIdx.x), next_e, next_kvh);
+        ok = put(next_e, next_kvh);
+      }
+      while (ok) {
+        if (is_v) {
+          if (!pieces.take(e, kvh, p.ctx, abort)) break;
+        } else {
+          e = next_e;
+          kvh = next_kvh;
+          if (kvh < 0) break;
+        }
         const int32_t* table = b.page_table + static_cast<int64_t>(e.seq) * b.table_stride;
         const auto page_of = [&](int j) {
           const int key = e.k_lo + j * kTileKeys + ((lane & 7) << page_shift);
@@ -633,7 +681,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* dst = smem + C::kOffKv + stage * C::kStageBytes;
           uint64_t* bar = zero0 >= 0 ? tail_bar : &kv_full[stage];
           if (lane == 0)
-            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n_pg * b.page_size * 128 * C::kPanels));
+            mbar_arrive_expect_tx(
+                bar, static_cast<uint32_t>(n_pg * b.page_size * 128 * C::kPanels));
           __syncwarp();
           // lanes 0 .. panels · pages − 1 load a page's panel each
           const int pg = lane / C::kPanels, panel = lane % C::kPanels;
@@ -682,9 +731,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               __syncwarp();
             }
             if (!ok) break;
-            pieces.fetch();
           }
           page = next;
+        }
+        if (ok && !is_v) {
+          int drawn = 0;
+          if (lane == 0) drawn = atomicAdd(counter, 1);
+          read_piece(__shfl_sync(0xFFFFFFFFu, drawn, 0), next_e, next_kvh);
+          ok = put(next_e, next_kvh);
         }
       }
       // See every issued load land (bounded, also after an abort).

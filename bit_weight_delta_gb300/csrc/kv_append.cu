@@ -149,7 +149,8 @@ int check_attention_batch(const bd_attention_batch* b) {
   if (b->n_q_heads % b->n_kv_heads != 0 || b->n_q_heads / b->n_kv_heads > 32 ||
       b->n_q_heads > 1024 || (b->head_dim != 64 && b->head_dim != 128) ||
       (b->page_size != 16 && b->page_size != 32 && b->page_size != 64 && b->page_size != 128) ||
-      b->n_tokens > (1 << 26) || b->n_tokens * b->n_kv_heads > (1 << 28) || b->n_seq > (1 << 20) || b->n_group > b->n_seq ||
+      b->n_tokens > (1 << 26) || b->n_tokens * b->n_kv_heads > (1 << 28) ||
+      b->n_seq > (1 << 20) || b->n_group > b->n_seq ||
       b->n_pages > 0x7FFFFFFF / b->n_kv_heads / b->page_size || b->table_stride > 0x7FFFFFFF ||
       b->max_kv_len > (1 << 30))
     return BD_ERR_UNSUPPORTED_SHAPE;

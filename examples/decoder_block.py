@@ -42,7 +42,8 @@ class Block:
             base = normal(d_out, d_in, std=d_in ** -0.5)
             packs = []
             for _ in range(variants):
-                tuned = (base.float() + normal(d_out, d_in, std=0.05 * d_in ** -0.5)).to(torch.bfloat16)
+                delta = normal(d_out, d_in, std=0.05 * d_in ** -0.5)
+                tuned = (base.float() + delta).to(torch.bfloat16)
                 packs.append(bd.bitdelta_compress(base, tuned, per_row=True))
             self.linears[name] = (base, packs, bd.variant_tables(
                 [p for p, _ in packs], [a for _, a in packs], device))
@@ -91,7 +92,8 @@ def main():
     prompts, steps, variant = [512, 300, 77, 1], 8, [0, 1, 2, 1]
     width = -(-(max(prompts) + steps) // page)
     table = int32([[s * width + i for i in range(width)] for s in range(len(prompts))])
-    k_pages = torch.empty((len(prompts) * width, hkv, page, dim), dtype=torch.bfloat16, device="cuda")
+    k_pages = torch.empty((len(prompts) * width, hkv, page, dim), dtype=torch.bfloat16,
+                          device="cuda")
     v_pages = torch.empty_like(k_pages)
     rope = rope_table(max(prompts) + steps, dim)
     lens = list(prompts)
@@ -101,8 +103,8 @@ def main():
             lens = [n + 1 for n in lens]
         offsets = [sum(q_len[:i]) for i in range(len(q_len) + 1)]
         seg = (int32(offsets), int32(variant), max(q_len))
-        batch = bd.AttentionBatch(seg[0], int32(lens), table, offsets[-1], max(q_len), max(lens), hq,
-                                  hkv, dim, page)
+        batch = bd.AttentionBatch(seg[0], int32(lens), table, offsets[-1], max(q_len), max(lens),
+                                  hq, hkv, dim, page)
         h = torch.randn((offsets[-1], hidden), device="cuda")
         block.forward(h, seg, batch, rope, k_pages, v_pages)          # warm
         a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)

@@ -89,7 +89,9 @@ bd_status bitdelta_add_norm(const uint16_t* y, int64_t M, int64_t d, const void*
  * once for the whole group, through the first member's row.  The attention's
  * definition does not change; sequences outside every group share nothing.
  *
- * n_q_heads must be a multiple of n_kv_heads, at most 32 times as many;
+ * n_q_heads must be a multiple of n_kv_heads, at most 32 times as many and at
+ * most 1024; n_tokens · n_kv_heads at most 2^28, kv_len · n_kv_heads and n_pages
+ * · n_kv_heads · page_size below 2^31;
  * query head h reads key head h / (n_q_heads / n_kv_heads).  head_dim 64 or
  * 128; page_size 16, 32, 64 or 128.  max_q_len and max_kv_len are host bounds
  * of the lengths in device memory; a table that breaks them, or is not
@@ -119,8 +121,8 @@ typedef struct {
  * rounded once.  rope: fp32 [rope_rows, rot_dim], per position rot_dim/2
  * cosines, then rot_dim/2 sines.  Query heads go to q_out bf16 [n_tokens,
  * n_q_heads, head_dim], key and value heads to the token's place in the cache.
- * A token at a negative position (kv_len < q_len) is padding: its query is
- * zero and nothing is appended.  A position past rope_rows or past the page
+ * A token at a negative position (kv_len < q_len), or of no sequence, is
+ * padding: its query is zero and nothing is appended.  A position past rope_rows or past the page
  * table's row, or a page outside [0, n_pages), sets BD_ERR_DEVICE_BOUNDS; the
  * query is then zero and nothing is appended for that token.
  * rot_dim: a multiple of 16, 0 .. head_dim.
@@ -152,14 +154,15 @@ bd_status bitdelta_attention_plan(const bd_attention_batch* batch, void* plan, s
  * gives zeros and an lse of −inf.  Positions past a sequence's kv_len are
  * never read as values, whatever the page holds there; within kv_len, keys
  * and values are expected finite.
- *   plan         as made by bitdelta_attention_plan for the same batch.
+ *   plan         as made by bitdelta_attention_plan for the same batch.  A call
+ *                uses a counter in it and leaves it as it was.
  *   workspace    device memory of bitdelta_attention_workspace_bytes(batch)
- *                bytes on a 256-byte boundary (NULL when that is 0); calls
- *                that can overlap on the GPU need workspaces of their own.
+ *                bytes on a 256-byte boundary.
+ *   Calls that can overlap on the GPU need plans and workspaces of their own.
  * scale must be positive and finite.
  */
 size_t bitdelta_attention_workspace_bytes(const bd_attention_batch* batch);
-bd_status bitdelta_attention(const bd_attention_batch* batch, const void* plan, size_t plan_bytes,
+bd_status bitdelta_attention(const bd_attention_batch* batch, void* plan, size_t plan_bytes,
                              const uint16_t* q, const uint16_t* k_pages, const uint16_t* v_pages,
                              float scale, uint16_t* out, float* lse, void* workspace,
                              size_t workspace_bytes, bd_stream_t stream);
