@@ -13,7 +13,6 @@ bf16 tensors are torch.bfloat16; the packed sign matrix is torch.uint8
 from __future__ import annotations
 
 import ctypes
-import math
 import os
 
 import torch
@@ -611,38 +610,30 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-# The current stream's handle without building a Stream object: a decode step's
-# calls are a few microseconds each, and the object alone costs about three.
-_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+def _raw_stream(stream, device):
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
 
 
-def _raw_stream(stream, t):
-    if stream is not None:
-        return stream.cuda_stream
-    if _current_raw_stream is not None:
-        return _current_raw_stream(t.get_device())
-    return torch.cuda.current_stream(t.device).cuda_stream
+def _empty(n: int, device, stream):
+    """n bytes that belong to the stream that will use them."""
+    with torch.cuda.stream(stream):          # None: the current one
+        return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _new(shape, dtype, device, stream):
-    """An output of a call; it belongs to the stream that writes it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+_native = None
 
 
-def _new_like(t, stream):
-    if stream is None:
-        return torch.empty_like(t)
-    with torch.cuda.stream(stream):
-        return torch.empty_like(t)
-
-
-def _out(t, shape, dtype, name):
-    if _dev(t, dtype, name).shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}")
-    return t
+def _load_native():
+    """The C++ side of the calls below (csrc/binding.cpp): argument checks,
+    output allocation and the call of the C entry point of the same name."""
+    global _native
+    if _native is None:
+        lib = load()
+        from . import _binding as native
+        native.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+            "bitdelta_add_norm", "bitdelta_kv_append", "bitdelta_attention")))
+        _native = native
+    return _native
 
 
 def bitdelta_add_norm(y, residual=None, pre_table=None, post_table=None, gate=None,
@@ -656,45 +647,15 @@ def bitdelta_add_norm(y, residual=None, pre_table=None, post_table=None, gate=No
     segment's variant's weights, else slot 0.  Rows of no segment are not
     written.  residual: bf16 or fp32 (None: zero, h is then bf16); gate: bf16
     [d] or like y.  residual_out may be residual itself."""
-    _dev(y, torch.bfloat16, "y")
-    if pre_table is None:
-        raise ValueError("pre_table is required")
-    shape = y.shape
-    d = shape[-1]
-    rtype = torch.bfloat16
-    if residual is not None:
-        rtype = residual.dtype
-        if rtype is not torch.bfloat16 and rtype is not torch.float32:
-            raise ValueError(f"residual must be bfloat16 or float32, got {rtype}")
-        _out(residual, shape, rtype, "residual")
-    residual_out = (_new_like(y if residual is None else residual, stream)
-                    if residual_out is None else _out(residual_out, shape, rtype, "residual_out"))
-    out = _new_like(y, stream) if out is None else _out(out, shape, torch.bfloat16, "out")
-    gate_stride = 0
-    if gate is not None:
-        _dev(gate, torch.bfloat16, "gate")
-        if gate.dim() > 1 and gate.shape == shape:
-            gate_stride = d
-        elif gate.shape != (d,):
-            raise ValueError("gate must be [d] or have the shape of y")
-    n_tab = _dev(pre_table, torch.int64, "pre_table").numel()
-    if post_table is not None and _dev(post_table, torch.int64, "post_table").numel() != n_tab:
-        raise ValueError("pre_table and post_table must have the same number of slots")
-    n_seg = 0
-    if (seg_offsets is None) != (seg_variant is None):
-        raise ValueError("seg_offsets and seg_variant go together")
-    if seg_offsets is not None:
-        n_seg = _dev(seg_variant, torch.int32, "seg_variant").numel()
-        if _dev(seg_offsets, torch.int32, "seg_offsets").numel() != n_seg + 1:
-            raise ValueError("seg_offsets must have one entry more than seg_variant")
-    code = load().bitdelta_add_norm(
-        y.data_ptr(), y.numel() // d if d else 0, d, _addr(residual), residual_out.data_ptr(),
-        1 if rtype is torch.float32 else 0, _addr(gate), gate_stride, scale, eps,
-        pre_table.data_ptr(), _addr(post_table), n_tab, _addr(seg_offsets), _addr(seg_variant),
-        n_seg, out.data_ptr(), _raw_stream(stream, y))
-    if code:
-        _check("bitdelta_add_norm", code)
-    return residual_out, out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return bitdelta_add_norm(y, residual, pre_table, post_table, gate, scale, eps,
+                                     seg_offsets, seg_variant, residual_out, out)
+    r = (_native or _load_native()).add_norm(y, residual, pre_table, post_table, gate, scale, eps,
+                                         seg_offsets, seg_variant, residual_out, out)
+    if type(r) is int:
+        _check("bitdelta_add_norm", r)
+    return r
 
 
 class _AttentionBatch(ctypes.Structure):
@@ -737,39 +698,22 @@ class AttentionBatch:
             if _dev(group_offsets, torch.int32, "group_offsets").numel() != n_group + 1:
                 raise ValueError("group_offsets must have one entry more than prefix_len")
         self._keep = (seq_offsets, kv_len, page_table, group_offsets, prefix_len)
-        self.head_dim, self.n_q_heads, self.n_kv_heads = head_dim, n_q_heads, n_kv_heads
-        self.page_size, self.n_tokens = page_size, n_tokens
         self._c = _AttentionBatch(
             n_tokens, n_seq, max_q_len, max_kv_len, n_q_heads, n_kv_heads, head_dim, page_size, 0,
             page_table.shape[1], seq_offsets.data_ptr(), kv_len.data_ptr(),
             page_table.data_ptr(), n_group, _addr(group_offsets), _addr(prefix_len))
         self._ref = ctypes.addressof(self._c)
         lib = load()
-        self._plan = _new(lib.bitdelta_attention_plan_bytes(self._ref), torch.uint8, kv_len.device,
-                          stream)
-        self._ws = _new(lib.bitdelta_attention_workspace_bytes(self._ref), torch.uint8,
-                        kv_len.device, stream)
-        self._device = kv_len.device
-        self._plan_args = (self._plan.data_ptr(), self._plan.numel())
-        self._ws_args = (self._ws.data_ptr(), self._ws.numel())
-        self._q_shape = torch.Size((n_tokens, n_q_heads, head_dim))
-        self._lse_shape = self._q_shape[:2]
-        self._page_shape = torch.Size((n_kv_heads, page_size, head_dim))
-        self._qkv_shape = torch.Size((n_tokens, (n_q_heads + 2 * n_kv_heads) * head_dim))
-        self._scale = 1.0 / math.sqrt(head_dim) if head_dim > 0 else 1.0
+        self._plan = _empty(lib.bitdelta_attention_plan_bytes(self._ref), kv_len.device, stream)
+        self._ws = _empty(lib.bitdelta_attention_workspace_bytes(self._ref), kv_len.device, stream)
+        self._args = (self._ref, self._plan.data_ptr(), self._plan.numel(), self._ws.data_ptr(),
+                      self._ws.numel())
         self.plan(stream)
 
     def plan(self, stream=None) -> None:
         """Compute the plan from the lengths now in the batch's tensors."""
         _check("bitdelta_attention_plan", load().bitdelta_attention_plan(
-            self._ref, *self._plan_args, _raw_stream(stream, self._plan)))
-
-    def _cache(self, k_pages, v_pages) -> None:
-        shape = _dev(k_pages, torch.bfloat16, "k_pages").shape
-        if _dev(v_pages, torch.bfloat16, "v_pages").shape != shape or shape[1:] != self._page_shape:
-            raise ValueError("k_pages and v_pages must be [n_pages, n_kv_heads, page_size, "
-                             "head_dim]")
-        self._c.n_pages = shape[0]
+            *self._args[:3], _raw_stream(stream, self._plan.device)))
 
 
 def bitdelta_kv_append(batch: AttentionBatch, qkv, rope, k_pages, v_pages,
@@ -780,17 +724,13 @@ def bitdelta_kv_append(batch: AttentionBatch, qkv, rope, k_pages, v_pages,
 
     rope: fp32 [positions, rot_dim], cosines then sines (None: no rotation);
     interleaved rotates neighbours (2i, 2i+1) instead of halves."""
-    _out(qkv, batch._qkv_shape, torch.bfloat16, "qkv")
-    batch._cache(k_pages, v_pages)
-    rows, rot = (0, 0) if rope is None else _dev(rope, torch.float32, "rope").shape
-    out = (_new(batch._q_shape, torch.bfloat16, batch._device, stream) if out is None else
-           _out(out, batch._q_shape, torch.bfloat16, "out"))
-    code = load().bitdelta_kv_append(
-        batch._ref, qkv.data_ptr(), _addr(rope), rows, rot, 1 if interleaved else 0,
-        k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), _raw_stream(stream, qkv))
-    if code:
-        _check("bitdelta_kv_append", code)
-    return out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return bitdelta_kv_append(batch, qkv, rope, k_pages, v_pages, interleaved, out)
+    r = (_native or _load_native()).kv_append(batch._ref, qkv, rope, k_pages, v_pages, interleaved, out)
+    if type(r) is int:
+        _check("bitdelta_kv_append", r)
+    return r
 
 
 def bitdelta_attention(batch: AttentionBatch, q, k_pages, v_pages, scale: float | None = None,
@@ -798,16 +738,10 @@ def bitdelta_attention(batch: AttentionBatch, q, k_pages, v_pages, scale: float 
     """Causal attention of q [n_tokens, n_q_heads, head_dim] over the cache.
     Returns (out, lse): bf16 like q, and fp32 [n_tokens, n_q_heads].  scale
     defaults to 1/sqrt(head_dim)."""
-    _out(q, batch._q_shape, torch.bfloat16, "q")
-    batch._cache(k_pages, v_pages)
-    out = (_new_like(q, stream) if out is None else
-           _out(out, batch._q_shape, torch.bfloat16, "out"))
-    lse = (_new(batch._lse_shape, torch.float32, batch._device, stream) if lse is None else
-           _out(lse, batch._lse_shape, torch.float32, "lse"))
-    code = load().bitdelta_attention(
-        batch._ref, *batch._plan_args, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-        batch._scale if scale is None else scale, out.data_ptr(), lse.data_ptr(),
-        *batch._ws_args, _raw_stream(stream, q))
-    if code:
-        _check("bitdelta_attention", code)
-    return out, lse
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return bitdelta_attention(batch, q, k_pages, v_pages, scale, out, lse)
+    r = (_native or _load_native()).attention(*batch._args, q, k_pages, v_pages, scale, out, lse)
+    if type(r) is int:
+        _check("bitdelta_attention", r)
+    return r

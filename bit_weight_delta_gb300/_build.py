@@ -1,4 +1,5 @@
-"""In-tree build of libbitdelta.so (sm_103a) with nvcc.
+"""In-tree build of libbitdelta.so (sm_103a) with nvcc, and of the Python binding
+of the decoder-block operators (_binding.so) with g++ on torch's headers.
 
 Each .cu file compiles to an object in parallel, then nvcc links the shared
 library next to this file.  The CUDA runtime is linked statically; the driver
@@ -10,6 +11,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import os
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -17,6 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build", "bitdelta")
 LIB_PATH = os.path.join(HERE, "libbitdelta.so")
+BINDING_PATH = os.path.join(HERE, "_binding.so")
+BINDING_SOURCE = "binding.cpp"
 
 SOURCES = ["abi.cu", "compress.cu", "reconstruct.cu", "gemv.cu", "gemm_pair.cu", "cache.cu",
            "kmerge.cu", "similarity.cu", "monosoup.cu", "add_norm.cu", "kv_append.cu",
@@ -33,7 +37,7 @@ def _nvcc() -> str:
 
 
 def _inputs_mtime() -> float:
-    paths = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
+    paths = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + [BINDING_SOURCE]]
     paths.append(os.path.join(INCLUDE, "bitdelta.h"))
     paths.append(os.path.join(INCLUDE, "bitdelta_cache.h"))
     paths.append(os.path.join(INCLUDE, "bitdelta_kmerge.h"))
@@ -42,8 +46,29 @@ def _inputs_mtime() -> float:
     return max(os.path.getmtime(p) for p in paths)
 
 
+def _build_binding() -> None:
+    import torch
+    base = os.path.dirname(torch.__file__)
+    lib = os.path.join(base, "lib")
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE,
+           "-I", os.path.join(base, "include"),
+           "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           os.path.join(CSRC, BINDING_SOURCE), "-o", tmp, "-L", lib, "-lc10", "-ltorch_cpu",
+           "-ltorch_python", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_PATH)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    if not force and os.path.exists(LIB_PATH) and os.path.getmtime(LIB_PATH) >= _inputs_mtime():
+    newest = _inputs_mtime()
+    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= newest
+                         for p in (LIB_PATH, BINDING_PATH)):
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     nvcc = _nvcc()
@@ -59,8 +84,10 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             print(r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_build_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        binding.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
