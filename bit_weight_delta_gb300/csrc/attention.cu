@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
     for (int c = tid; c < L.d_warps; c += kPlanThreads) starts[c].lo = starts[c].hi = 0;
     if (tid == 0) {
       record_error(p.ctx, kErrBounds);
-      *hd = PlanHeader{0, 1, 1, 0, 0, static_cast<int32_t>(b.n_tokens), 0, 0, 0};
+      *hd = PlanHeader{0, 1, 1, 0, 0, static_cast<int32_t>(b.n_tokens), 0, 0};
     }
     return;
   }
@@ -219,10 +219,24 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
     int64_t sum;
     const int64_t at = carry + block_scan(n * b.n_kv_heads, s_warp, &sum);
     if (s < b.n_seq) {
-      seqs[s].unit0 = at;
+      seqs[s].unit0 = static_cast<int32_t>(at);
       seqs[s].units = static_cast<int32_t>(n);
     }
     carry += sum;
+  }
+  // Units are counted in 31 bits; more (2^35 keys times key heads) plan nothing.
+  if (carry > INT32_MAX) {
+    for (int64_t t = tid; t < b.n_tokens; t += kPlanThreads) {
+      CombItem it{};
+      it.tok = static_cast<int32_t>(t);
+      comb[t] = it;
+    }
+    for (int c = tid; c < L.d_warps; c += kPlanThreads) starts[c].lo = starts[c].hi = 0;
+    if (tid == 0) {
+      record_error(p.ctx, kErrBounds);
+      *hd = PlanHeader{0, 1, 1, 0, 0, static_cast<int32_t>(b.n_tokens), 0, 0};
+    }
+    return;
   }
   const int64_t d_units = carry;
   __syncthreads();
@@ -318,8 +332,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
     st.seq = s;
     const int64_t end = st.r.unit0 + static_cast<int64_t>(st.r.units) * b.n_kv_heads;
     for (int64_t c = (st.r.unit0 + d_per - 1) / d_per; c * d_per < end; ++c) {
-      st.lo = c * d_per;
-      st.hi = st.lo + d_per < d_units ? st.lo + d_per : d_units;
+      st.lo = static_cast<int32_t>(c * d_per);
+      st.hi = static_cast<int32_t>(st.lo + d_per < d_units ? st.lo + d_per : d_units);
       starts[c] = st;
     }
   }
@@ -430,7 +444,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
         it.units = r.units;
         it.own_row = x * L.g;
         for (int h = 0; h < b.n_kv_heads; ++h) {
-          const int64_t u0 = r.unit0 + static_cast<int64_t>(h) * r.units;
+          const uint32_t u0 = r.unit0 + h * r.units;
           const int n = decode_parts(u0, u0 + r.units, d_units, d_per, warps).count();
           parts = n > parts ? n : parts;
         }
@@ -451,8 +465,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
   __syncthreads();
   if (tid == 0) {
     if (!fits) record_error(p.ctx, kErrBounds);
-    *hd = PlanHeader{d_units, static_cast<int32_t>(d_per), warps, fits ? n_entries : 0,
-                     n_tile,  s_comb, s_parts, n_tile, 0};
+    *hd = PlanHeader{static_cast<int32_t>(d_units), static_cast<int32_t>(d_per), warps,
+                     fits ? n_entries : 0, n_tile, s_comb, s_parts, n_tile};
   }
 }
 
@@ -488,42 +502,67 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtas) combine_kernel(const 
   const int row = threadIdx.x % g, q = threadIdx.x / g;
   const int col = q % cols, grp = q / cols;
   const int n_work = hd.n_comb * H * slices;
-  CombItem it{};
-  if (static_cast<int>(blockIdx.x) < n_work) it = p.comb()[blockIdx.x / (H * slices)];
+  // An item's own parts: tile slots own_slot .. (times heads plus head), decode
+  // parts, or the one part of a run that a warp or CTA did alone; none to join
+  // where that part is final already (another head of the token is cut).
+  struct Work {
+    CombItem it;
+    DecodeParts dp;
+    int64_t first;
+    int kvh, d4, n_own, rows, own_row;
+    bool cut, skip;
+    uint8_t *o, *ml;
+  };
+  const auto prepare = [&](const CombItem& it, int w) {
+    Work k;
+    k.it = it;
+    k.kvh = static_cast<int>(static_cast<uint32_t>(w) / static_cast<uint32_t>(slices) %
+                             static_cast<uint32_t>(H));
+    k.d4 = static_cast<int>(static_cast<uint32_t>(w) % static_cast<uint32_t>(slices)) * cols + col;
+    k.first = static_cast<int64_t>(it.own_slot) * H + k.kvh;
+    k.n_own = it.own_ns;
+    k.rows = 2 * kHalfRows;
+    k.own_row = it.own_row;
+    k.o = p.ws + L.w_t_o;
+    k.ml = p.ws + L.w_t_ml;
+    k.cut = k.skip = false;
+    if (it.units > 0) {
+      const uint32_t u0 = it.unit0 + k.kvh * it.units;
+      k.dp = decode_parts(u0, u0 + it.units, hd.d_units, hd.d_per, hd.d_warps);
+      k.n_own = k.dp.count();
+      k.cut = k.n_own > 1;
+      k.skip = !k.cut && it.pre_ns == 0;
+      if (!k.cut) {
+        k.first = static_cast<int64_t>(it.tok) * H + k.kvh;
+        k.own_row = 0;
+      }
+      k.rows = k.cut ? L.d_rows : g;
+      k.o = p.ws + (k.cut ? L.w_d_o : L.w_r_o);
+      k.ml = p.ws + (k.cut ? L.w_d_ml : L.w_r_ml);
+    }
+    return k;
+  };
+  const auto item_of = [&](int w) {
+    return p.comb()[static_cast<uint32_t>(w) / static_cast<uint32_t>(H * slices)];
+  };
+  const int stride = static_cast<int>(gridDim.x);
+  int w = static_cast<int>(blockIdx.x);
+  Work k{};
+  CombItem ahead{};
+  if (w < n_work) k = prepare(item_of(w), w);
+  if (w + stride < n_work) ahead = item_of(w + stride);
   griddep_wait();
   griddep_launch_dependents();
   // the tile kernel has dealt its pieces: its counter for the next call
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.piece_counter() = hd.t_ctas;
-  CombItem ahead = it;
-  for (int w = static_cast<int>(blockIdx.x); w < n_work; w += gridDim.x) {
-    it = ahead;
-    if (w + static_cast<int>(gridDim.x) < n_work) ahead = p.comb()[(w + gridDim.x) / (H * slices)];
-    const int kvh = static_cast<int>(w / slices % H);
-    const int d4 = static_cast<int>(w % slices) * cols + col;
-    // own parts: tile slots own_slot .. (times heads plus head), decode parts,
-    // or the one part of a run that a warp or CTA did alone
-    DecodeParts dp{};
-    int64_t first = static_cast<int64_t>(it.own_slot) * H + kvh;
-    int n_own = it.own_ns, rows = 2 * kHalfRows, own_row = it.own_row;
-    const bool cut = it.units > 0;
-    uint8_t *o_base = p.ws + L.w_t_o, *ml_base = p.ws + L.w_t_ml;
-    if (cut) {
-      const int64_t u0 = it.unit0 + static_cast<int64_t>(kvh) * it.units;
-      dp = decode_parts(u0, u0 + it.units, hd.d_units, hd.d_per, hd.d_warps);
-      n_own = dp.count();
-      if (n_own > 1) {
-        rows = L.d_rows;
-        o_base = p.ws + L.w_d_o;
-        ml_base = p.ws + L.w_d_ml;
-      } else {
-        if (it.pre_ns == 0) continue;  // final already; another head of the token is cut
-        first = static_cast<int64_t>(it.tok) * H + kvh;
-        rows = g;
-        own_row = 0;
-        o_base = p.ws + L.w_r_o;
-        ml_base = p.ws + L.w_r_ml;
-      }
+  for (; w < n_work; w += stride) {
+    if (w != static_cast<int>(blockIdx.x)) {
+      k = prepare(ahead, w);
+      if (w + stride < n_work) ahead = item_of(w + stride);
     }
+    if (k.skip) continue;
+    const CombItem& it = k.it;
+    const int kvh = k.kvh, d4 = k.d4, n_own = k.n_own, rows = k.rows, own_row = k.own_row;
     const int n = n_own + it.pre_ns;
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -532,25 +571,24 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtas) combine_kernel(const 
         float2 ml[kCombBatch];
         float4 v[kCombBatch];
 #pragma unroll
-        for (int k = 0; k < kCombBatch; ++k) {
-          const int i = i0 + k * groups;
-          ml[k] = make_float2(-INFINITY, 0.f);
-          v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int x = 0; x < kCombBatch; ++x) {
+          const int i = i0 + x * groups;
+          ml[x] = make_float2(-INFINITY, 0.f);
+          v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (i < n_own) {
-            const int64_t slot =
-                cut && n_own > 1 ? dp.slot(i) : first + static_cast<int64_t>(i) * H;
-            ml[k] = part_ml(ml_base, slot, rows)[own_row + row];
-            v[k] = part_o(o_base, slot, rows, D)[static_cast<int64_t>(d4) * rows + own_row + row];
+            const int64_t slot = k.cut ? k.dp.slot(i) : k.first + static_cast<int64_t>(i) * H;
+            ml[x] = part_ml(k.ml, slot, rows)[own_row + row];
+            v[x] = part_o(k.o, slot, rows, D)[static_cast<int64_t>(d4) * rows + own_row + row];
           } else if (i < n) {
             const int64_t slot = static_cast<int64_t>(it.pre_slot + (i - n_own)) * H + kvh;
-            ml[k] = part_ml(p.ws + L.w_t_ml, slot, 2 * kHalfRows)[it.pre_row + row];
-            v[k] = part_o(p.ws + L.w_t_o, slot, 2 * kHalfRows,
+            ml[x] = part_ml(p.ws + L.w_t_ml, slot, 2 * kHalfRows)[it.pre_row + row];
+            v[x] = part_o(p.ws + L.w_t_o, slot, 2 * kHalfRows,
                           D)[static_cast<int64_t>(d4) * 2 * kHalfRows + it.pre_row + row];
           }
         }
         float top = m;
 #pragma unroll
-        for (int k = 0; k < kCombBatch; ++k) top = fmaxf(top, ml[k].x);
+        for (int x = 0; x < kCombBatch; ++x) top = fmaxf(top, ml[x].x);
         const float ref = top == -INFINITY ? 0.f : top;
         const float f = ex2(m - ref);
         l *= f;
@@ -559,13 +597,13 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtas) combine_kernel(const 
         o.z *= f;
         o.w *= f;
 #pragma unroll
-        for (int k = 0; k < kCombBatch; ++k) {
-          const float s = ex2(ml[k].x - ref);
-          l = fmaf(ml[k].y, s, l);
-          o.x = fmaf(v[k].x, s, o.x);
-          o.y = fmaf(v[k].y, s, o.y);
-          o.z = fmaf(v[k].z, s, o.z);
-          o.w = fmaf(v[k].w, s, o.w);
+        for (int x = 0; x < kCombBatch; ++x) {
+          const float s = ex2(ml[x].x - ref);
+          l = fmaf(ml[x].y, s, l);
+          o.x = fmaf(v[x].x, s, o.x);
+          o.y = fmaf(v[x].y, s, o.y);
+          o.z = fmaf(v[x].z, s, o.z);
+          o.w = fmaf(v[x].w, s, o.w);
         }
         m = top;
       }

@@ -30,7 +30,7 @@ constexpr int kTileDecodeWarps = 8;  // of the tile kernel's decode role
 constexpr int kMinUnits = 4;     // units per warp at least: a part costs a row's sums
 
 struct PlanHeader {
-  int64_t d_units;    // units of the decode kernel, all sequences and key heads
+  int32_t d_units;    // units of the decode role, all sequences and key heads
   int32_t d_per;      // units per warp
   int32_t d_warps;    // warps per CTA
   int32_t t_entries;  // pieces of the tile kernel (each once per key head)
@@ -38,7 +38,6 @@ struct PlanHeader {
   int32_t n_comb;     // tokens whose rows the combine kernel writes
   int32_t most_parts; // of any of their rows
   int32_t next_piece; // the tile kernel's dealing: t_ctas between calls
-  int32_t pad;
 };
 
 // The decode role's parts of a run of units [u0, u1), out of `total` units cut
@@ -50,58 +49,61 @@ struct PlanHeader {
 // the range of its warp (a warp has at most one part that began earlier and one
 // that goes on).
 struct DecodeParts {
-  int64_t g0;        // first warp (or first warp of the first CTA)
-  int64_t mid0;      // first warp of the CTAs in between
-  int64_t last0;     // first warp of the last parts
+  int g0;            // first warp (or first warp of the first CTA)
+  int mid0;          // first warp of the CTAs in between
+  int last0;         // first warp of the last parts
   int na, nb, nc;    // parts of the first CTA, in between, of the last CTA
   int w, first_odd;  // warps per CTA; 1 where the first part's slot is the odd one
   __host__ __device__ int count() const { return na + nb + nc; }
-  __host__ __device__ int64_t slot(int i) const {
+  __host__ __device__ int slot(int i) const {
     if (i < na) return 2 * (g0 + i) + (i == 0 ? first_odd : 0);
-    if (i < na + nb) return 2 * (mid0 + static_cast<int64_t>(i - na) * w);
+    if (i < na + nb) return 2 * (mid0 + (i - na) * w);
     return 2 * (last0 + (i - na - nb));
   }
 };
-__host__ __device__ inline DecodeParts decode_parts(int64_t u0, int64_t u1, int64_t total,
-                                                    int64_t per, int w) {
+// (Units are counted in 31 bits, which the plan checks: 64-bit divisions took
+// most of a microsecond here.)
+__host__ __device__ inline DecodeParts decode_parts(uint32_t u0, uint32_t u1, uint32_t total,
+                                                    uint32_t per, uint32_t w) {
   DecodeParts d{};
-  const int64_t span = per * w, c0 = u0 / span, c1 = (u1 - 1) / span;
-  const int64_t end0 = (c0 + 1) * span < total ? (c0 + 1) * span : total;
-  const int64_t end1 = (c1 + 1) * span < total ? (c1 + 1) * span : total;
-  const int64_t w0 = u0 / per, w1 = (u1 - 1) / per;
-  d.w = w;
+  const uint32_t w0 = u0 / per, w1 = (u1 - 1) / per, c0 = w0 / w, c1 = w1 / w;
+  const uint32_t span = per * w;
+  const uint32_t end0 = (c0 + 1) * span < total ? (c0 + 1) * span : total;
+  const uint32_t end1 = (c1 + 1) * span < total ? (c1 + 1) * span : total;
+  d.w = static_cast<int>(w);
   if (u0 <= c0 * span && u1 >= end0) {  // all of the first CTA
-    d.g0 = c0 * w;
+    d.g0 = static_cast<int>(c0 * w);
     d.na = 1;
   } else {
-    d.g0 = w0;
+    d.g0 = static_cast<int>(w0);
     d.na = static_cast<int>((c0 == c1 ? w1 : (c0 + 1) * w - 1) - w0) + 1;
     d.first_odd = 1;
   }
   if (c1 > c0) {
-    d.mid0 = (c0 + 1) * w;
+    d.mid0 = static_cast<int>((c0 + 1) * w);
     d.nb = static_cast<int>(c1 - c0 - 1);
-    d.last0 = c1 * w;
+    d.last0 = static_cast<int>(c1 * w);
     d.nc = u1 >= end1 ? 1 : static_cast<int>(w1 - c1 * w) + 1;
   }
   return d;
 }
 
-// One sequence, as the decode kernel and the combine kernel see it.
+// One sequence, as the decode role and the combine kernel see it.
 struct SeqRec {
-  int64_t unit0;      // first of its decode units (key head h: + h · units per head)
-  int32_t units;      // decode units per key head (0: none, or a tile-kernel run)
+  int32_t unit0;      // first of its decode units (key head h: + h · units per head)
+  int32_t units;      // decode units per key head (0: none, or a tile-role run)
   int32_t tok0, q_len, kv_len;
   int32_t k0;         // first own key (the shared prefix ends there)
   int32_t group;      // group whose prefix it reads, or −1
+  int32_t pad;
 };
 
 // Where a warp of the decode role begins: its units [lo, hi) and the sequence
 // that holds lo.  One load, so that its first page ids are one step away.
 struct DecodeStart {
   SeqRec r;
-  int64_t lo, hi;
-  int32_t seq, pad[3];
+  int32_t lo, hi;
+  int32_t seq;
 };
 
 // A token whose rows the combine kernel writes, and where its parts lie.  Own
@@ -109,12 +111,10 @@ struct DecodeStart {
 // units (units > 0: rows from own_row, the slots following from the head's
 // units).  Prefix part: pre_ns tile slots.
 struct CombItem {
-  int64_t unit0;
-  int32_t units;
+  int32_t unit0, units;
   int32_t tok;
   int32_t own_slot, own_ns, own_row;
   int32_t pre_slot, pre_ns, pre_row;
-  int32_t pad[2];
 };
 
 // One piece of the tile kernel's work: a tile of query tokens by a range of

@@ -60,9 +60,9 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 struct Walk {
   SeqRec r;
   int seq, h;          // current run
-  int64_t at, end;     // next unit, end of the CTA's range
+  int at, end;         // next unit, end of the range
   int t0, t1;          // the run's 16-key tiles in the range
-  int64_t u0;          // the run's first unit
+  int u0;              // the run's first unit
   bool whole;          // the range holds all of the run
 };
 
@@ -70,20 +70,20 @@ struct Walk {
 __device__ __forceinline__ bool next_run(const AttnArgs& p, Walk& w) {
   if (w.at >= w.end) return false;
   while (true) {  // units beyond the current sequence belong to a later one
-    const int64_t rel = w.at - w.r.unit0;
-    if (rel < static_cast<int64_t>(w.r.units) * p.b.n_kv_heads) {
+    const int rel = w.at - w.r.unit0;
+    if (rel < w.r.units * p.b.n_kv_heads) {
       w.h = static_cast<int>(static_cast<uint32_t>(rel) / static_cast<uint32_t>(w.r.units));
       break;
     }
     if (++w.seq >= p.b.n_seq) return false;
     w.r = p.seqs()[w.seq];
   }
-  w.u0 = w.r.unit0 + static_cast<int64_t>(w.h) * w.r.units;
-  const int64_t stop = w.u0 + w.r.units < w.end ? w.u0 + w.r.units : w.end;
+  w.u0 = w.r.unit0 + w.h * w.r.units;
+  const int stop = w.u0 + w.r.units < w.end ? w.u0 + w.r.units : w.end;
   w.whole = w.at == w.u0 && stop == w.u0 + w.r.units;
   static_assert(kUnitKeys == 16, "a unit is a tile");
-  w.t0 = static_cast<int>(w.at - w.u0);
-  w.t1 = static_cast<int>(stop - w.u0);
+  w.t0 = w.at - w.u0;
+  w.t1 = stop - w.u0;
   w.at = stop;
   return true;
 }
@@ -127,15 +127,14 @@ __device__ __forceinline__ void run(const CUtensorMap& tmap_k, const CUtensorMap
   const PlanHeader hd = *p.header();
   const DecodeStart st0 = p.starts()[cta * W], mine = p.starts()[cta * W + warp];
   if (st0.lo >= st0.hi) return;
-  const int64_t cta_lo = st0.lo, span = static_cast<int64_t>(hd.d_per) * W;
-  const int64_t cta_hi = cta_lo + span < hd.d_units ? cta_lo + span : hd.d_units;
-  const uint32_t rel = static_cast<uint32_t>(cta_lo - st0.r.unit0);
-  const int64_t run_end = st0.r.unit0 + (rel / static_cast<uint32_t>(st0.r.units) + 1) *
-                                            static_cast<int64_t>(st0.r.units);
-  const bool together = run_end >= cta_hi;
+  const int span = hd.d_per * W;
+  const int cta_hi = st0.lo < hd.d_units - span ? st0.lo + span : hd.d_units;
+  const uint32_t units = static_cast<uint32_t>(st0.r.units);
+  const uint32_t run0 = static_cast<uint32_t>(st0.lo - st0.r.unit0) / units * units;
+  const bool together = st0.r.unit0 + run0 + units >= static_cast<uint32_t>(cta_hi);
   if (!together && mine.lo >= mine.hi) return;
   const int step = together ? W : 1, skew = together ? warp : 0;
-  const int64_t lo = together ? cta_lo : mine.lo;
+  const int lo = together ? st0.lo : mine.lo;
   Walk cons{};
   cons.seq = together ? st0.seq : mine.seq;
   cons.r = together ? st0.r : mine.r;
