@@ -234,13 +234,18 @@ __device__ __forceinline__ void run(const CUtensorMap& tmap_k, const CUtensorMap
       const uint32_t kb = smem_addr(ring + stage * C::kStage);
       const uint32_t vb = kb + C::kKv;
       const int key0 = r.k0 + 16 * tile;
-      float s[RT][2][4];
+      // two chains of products per score, each half as long (for 32 rows their
+      // registers would spill, and the two row tiles are two chains already)
+      constexpr int kChains = RT == 1 ? 2 : 1;
+      float s[RT][2][4], part[kChains][RT][2][4];
 #pragma unroll
-      for (int m = 0; m < RT; ++m)
+      for (int c = 0; c < kChains; ++c)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int m = 0; m < RT; ++m)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) s[m][n][x] = 0.f;
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) part[c][m][n][x] = 0.f;
       {
         const int tok = (lane & 7) + ((lane & 16) ? 8 : 0), sel = (lane >> 3) & 1;
 #pragma unroll
@@ -250,10 +255,18 @@ __device__ __forceinline__ void run(const CUtensorMap& tmap_k, const CUtensorMap
                           (((((k & 3) << 1) + sel) ^ (tok & 7)) << 4));
 #pragma unroll
           for (int m = 0; m < RT; ++m) {
-            mma16816(s[m][0], qf[m][k], kf[0], kf[1]);
-            mma16816(s[m][1], qf[m][k], kf[2], kf[3]);
+            mma16816(part[k % kChains][m][0], qf[m][k], kf[0], kf[1]);
+            mma16816(part[k % kChains][m][1], qf[m][k], kf[2], kf[3]);
           }
         }
+#pragma unroll
+        for (int m = 0; m < RT; ++m)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              s[m][n][x] = kChains == 2 ? part[0][m][n][x] + part[kChains - 1][m][n][x]
+                                        : part[0][m][n][x];
       }
       const bool edge = key0 + 16 > pos0 + 1;  // some row does not see all 16 keys
       if (edge) {
@@ -272,15 +285,17 @@ __device__ __forceinline__ void run(const CUtensorMap& tmap_k, const CUtensorMap
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           top[e] = fmaxf(fmaxf(s[m][0][2 * e], s[m][0][2 * e + 1]),
-                         fmaxf(s[m][1][2 * e], s[m][1][2 * e + 1]));
-          top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 1));
-          top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 2)) * p.scale_log2;
+                         fmaxf(s[m][1][2 * e], s[m][1][2 * e + 1])) * p.scale_log2;
         }
+        // each lane looks at its own scores; the row's maximum is exchanged only
+        // where one of them moves the reference
         const bool move = top[0] > mref[m][0] + kRescale || top[1] > mref[m][1] + kRescale;
         if (__any_sync(0xFFFFFFFFu, move)) {
           float f[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
+            top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 1));
+            top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 2));
             const float mn = fmaxf(mref[m][e], top[e]);
             f[e] = mn == -INFINITY ? 1.f : ex2(mref[m][e] - mn);
             mref[m][e] = mn;
