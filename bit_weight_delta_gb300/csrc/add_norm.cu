@@ -8,6 +8,13 @@
 // last store, so every input is read once and every output written once:
 // the floor is those bytes over the HBM bandwidth.  The two sums of squares
 // are each one warp-shuffle reduction and one exchange through shared memory.
+//
+// Measured: 2112 rows x 4096 with both norms, a gate and an fp32 residual (104
+// MB, 15.6 us at the copy rate) 18.2 us on repeated inputs and 22.1 us on
+// inputs that change (4.7 TB/s): each row's chain of load, sum, exchange, sum
+// and store leaves loads in flight for only part of a CTA's life.  8 rows x
+// 8192: 3.0 us on the GPU, bound by that chain.  Rows streamed through a ring
+// in shared memory by one persistent CTA per SM were slower at every size.
 #include <cstdint>
 
 #include "bitdelta_block.h"

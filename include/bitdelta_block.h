@@ -19,8 +19,8 @@
  * boundary and are contiguous.
  *
  * Stream order: these kernels are launched with programmatic dependent launch
- * and read and write nothing before the kernels ahead of them on the stream
- * have completed.
+ * and touch no tensor of the caller's before the kernels ahead of them on the
+ * stream have completed.
  */
 #ifndef BITDELTA_BLOCK_H_
 #define BITDELTA_BLOCK_H_
