@@ -711,7 +711,7 @@ bd_status bitdelta_attention_plan(const bd_attention_batch* batch, void* plan, s
                                   bd_stream_t stream) {
   int st = bd::check_attention_batch(batch);
   if (st != BD_OK) return static_cast<bd_status>(st);
-  if (batch->n_tokens == 0 || batch->n_seq == 0) return BD_OK;
+  if (batch->n_tokens == 0) return BD_OK;
   if (!plan) return BD_ERR_WORKSPACE;
   if (bd::off(plan, 256)) return BD_ERR_MISALIGNED;
   bd::AttnArgs p{};
@@ -735,7 +735,7 @@ bd_status bitdelta_attention(const bd_attention_batch* batch, void* plan, size_t
   int st = bd::check_attention_batch(batch);
   if (st != BD_OK) return static_cast<bd_status>(st);
   if (!(scale > 0.f) || std::isinf(scale)) return BD_ERR_INVALID_ARG;
-  if (batch->n_tokens == 0 || batch->n_seq == 0) return BD_OK;
+  if (batch->n_tokens == 0) return BD_OK;
   if (!q || !k_pages || !v_pages || !out || batch->n_pages < 1) return BD_ERR_INVALID_ARG;
   if (!plan || !workspace) return BD_ERR_WORKSPACE;
   if (bd::off(q, 16) || bd::off(k_pages, 16) || bd::off(v_pages, 16) || bd::off(out, 16) ||

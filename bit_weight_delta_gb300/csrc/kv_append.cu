@@ -179,7 +179,7 @@ extern "C" bd_status bitdelta_kv_append(const bd_attention_batch* batch, const u
   if (style != BD_ROPE_HALVES && style != BD_ROPE_PAIRS) return BD_ERR_INVALID_ARG;
   if (rope_rows < 0 || rot_dim < 0) return BD_ERR_INVALID_ARG;
   if (rot_dim % 16 != 0 || rot_dim > batch->head_dim) return BD_ERR_UNSUPPORTED_SHAPE;
-  if (batch->n_tokens == 0 || batch->n_seq == 0) return BD_OK;
+  if (batch->n_tokens == 0) return BD_OK;
   if (!qkv || !q_out || !k_pages || !v_pages || (rot_dim > 0 && !rope)) return BD_ERR_INVALID_ARG;
   if (bd::off(qkv, 16) || bd::off(q_out, 16) || bd::off(k_pages, 16) || bd::off(v_pages, 16) ||
       bd::off(rope, 16))

@@ -214,6 +214,18 @@ def test_nothing_to_do():
     assert out.shape == (0, 8, 128) and lse.shape == (0, 8)
 
 
+@pytest.mark.parametrize("max_q", [1, 64])
+def test_tokens_without_any_sequence(max_q):
+    """A batch of padding alone writes zeros, in either kernel."""
+    c = Case([], 8, 2, 128, 16, extra_tokens=5)
+    c.batch = c.make(max_q_len=max_q, max_kv_len=64)
+    out = torch.full((5, 8, 128), NAN, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((5, 8), NAN, device="cuda")
+    c.run(out=out, lse=lse)
+    assert (out == 0).all() and torch.isneginf(lse).all()
+    assert bd.bitdelta_check_error() == 0
+
+
 def test_infinite_and_nan_keys_behind_the_mask():
     """Pages past kv_len and the last page's tail hold NaN in every test here; infinities
     behave the same."""

@@ -103,6 +103,20 @@ def test_no_rope_copies():
     assert torch.equal(kp[table[1, 2], :, 7], qkv[2, 4 * 128:6 * 128].view(2, 128))
 
 
+def test_tokens_without_any_sequence():
+    """A batch of padding alone: zero queries, nothing appended."""
+    empty = torch.zeros(0, dtype=torch.int32, device="cuda")
+    batch = bd.AttentionBatch(torch.zeros(1, dtype=torch.int32, device="cuda"), empty,
+                              empty.view(0, 4), 3, 1, 64, 4, 2, 64, 16)
+    qkv = torch.randn(3, 8 * 64, device="cuda").to(torch.bfloat16)
+    kp = torch.randn(2, 2, 16, 64, device="cuda").to(torch.bfloat16)
+    vp, k0 = kp.clone(), kp.clone()
+    q = torch.full((3, 4, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    bd.bitdelta_kv_append(batch, qkv, None, kp, vp, out=q)
+    assert (q == 0).all() and torch.equal(kp, k0) and torch.equal(vp, k0)
+    assert bd.bitdelta_check_error() == 0
+
+
 def test_places_outside_are_reported_and_left_alone():
     batch, off, kv, table, qkv, rope, kp, vp = make([(2, 20), (1, 5)], 4, 2, 64, 16, rope_rows=19)
     k0, v0 = kp.clone(), vp.clone()
