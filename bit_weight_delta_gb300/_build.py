@@ -58,7 +58,7 @@ def _build_binding() -> None:
            "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            os.path.join(CSRC, BINDING_SOURCE), "-o", tmp, "-L", lib, "-lc10", "-ltorch_cpu",
-           "-ltorch_python", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
+           "-ltorch_python", "-ltorch_cuda", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {BINDING_SOURCE}:\n{r.stdout}\n{r.stderr}")

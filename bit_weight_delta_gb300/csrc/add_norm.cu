@@ -39,6 +39,7 @@ struct NormArgs {
   uint16_t* x_out;
   int64_t M;
   int32_t d;
+  int32_t ahead;  // rows
   DevCtx ctx;
 };
 
@@ -87,7 +88,8 @@ __device__ __forceinline__ const uint16_t* weights_of(const uint16_t* const* tab
 // C chunks of 8 elements per thread.
 // (32 registers where they do, so that rows of 8192 stay two to an SM; the
 // weights are fetched late for that.)
-template <int C, bool kF32>
+// kAhead: each CTA also fetches into L2 a row that one of the next CTAs will take.
+template <int C, bool kF32, bool kAhead>
 __global__ void __launch_bounds__(1024, C == 1 ? 2 : 1) add_norm_kernel(const NormArgs p) {
   __shared__ float s_post[32], s_pre[32];
   __shared__ int s_seg;
@@ -96,6 +98,15 @@ __global__ void __launch_bounds__(1024, C == 1 ? 2 : 1) add_norm_kernel(const No
   const int n8 = p.d >> 3;
   griddep_wait();
   griddep_launch_dependents();
+
+  if constexpr (kAhead) {
+    if (tid == 0 && row + p.ahead < p.M) {
+      const int64_t next = (row + p.ahead) * p.d;
+      prefetch_l2(p.y + next, 2 * p.d);
+      if (p.residual != nullptr)
+        prefetch_l2(static_cast<const uint16_t*>(p.residual) + next, 2 * p.d);
+    }
+  }
 
   uint4 yv[C], gv[C], ra[C], rb[C];
   const uint4* y8 = reinterpret_cast<const uint4*>(p.y + row * p.d);
@@ -220,19 +231,29 @@ __global__ void __launch_bounds__(1024, C == 1 ? 2 : 1) add_norm_kernel(const No
 }
 
 template <int C>
-cudaError_t launch_c(const NormArgs& p, bool f32, int threads, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(p.M));
-  return f32 ? launch_pdl(add_norm_kernel<C, true>, grid, dim3(threads), 0, s, p)
-             : launch_pdl(add_norm_kernel<C, false>, grid, dim3(threads), 0, s, p);
+cudaError_t launch_c(NormArgs p, int sms, bool f32, int threads, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(p.M)), block(threads);
+  if (f32) return launch_pdl(add_norm_kernel<C, true, false>, grid, block, 0, s, p);
+  // Where an SM holds at most two CTAs, their loads stop together while they sum:
+  // with two rounds of CTAs or more, half a round is fetched ahead (2048 rows of
+  // 8192, bf16, 23.9 -> 21.9 us; 1024 of 16384 34.3 -> 30.9; of 6144 21.3 -> 20.7).
+  // More, smaller CTAs cover one another (8192 rows of 1024 16.0 -> 16.4 us, 2048
+  // of 5120 unchanged), fewer rounds leave little to fetch (500 rows of 8192 7.6
+  // -> 7.9), and rows with an fp32 residual lose by it (4096 of 8192 74.3 -> 78.4).
+  const int resident = (C == 1 ? 2048 : 1024) / threads;
+  if (resident > 2 || p.M < 2 * static_cast<int64_t>(sms) * resident)
+    return launch_pdl(add_norm_kernel<C, false, false>, grid, block, 0, s, p);
+  p.ahead = sms * resident / 2;
+  return launch_pdl(add_norm_kernel<C, false, true>, grid, block, 0, s, p);
 }
 
-cudaError_t launch_add_norm(const NormArgs& p, bool f32, cudaStream_t s) {
+cudaError_t launch_add_norm(const NormArgs& p, int sms, bool f32, cudaStream_t s) {
   const int n8 = p.d / 8;
   const auto threads = [&](int c) { return ((n8 + c - 1) / c + 31) / 32 * 32; };
-  if (n8 <= 1024) return launch_c<1>(p, f32, threads(1), s);
-  if (n8 <= 2048) return launch_c<2>(p, f32, threads(2), s);
-  if (n8 <= 4096) return launch_c<4>(p, f32, threads(4), s);
-  return launch_c<8>(p, f32, threads(8), s);
+  if (n8 <= 1024) return launch_c<1>(p, sms, f32, threads(1), s);
+  if (n8 <= 2048) return launch_c<2>(p, sms, f32, threads(2), s);
+  if (n8 <= 4096) return launch_c<4>(p, sms, f32, threads(4), s);
+  return launch_c<8>(p, sms, f32, threads(8), s);
 }
 
 bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
@@ -284,7 +305,7 @@ extern "C" bd_status bitdelta_add_norm(const uint16_t* y, int64_t M, int64_t d,
   p.x_out = x_out;
   p.M = M;
   p.d = static_cast<int32_t>(d);
-  const cudaError_t e = bd::launch_add_norm(p, rtype == BD_RESIDUAL_F32,
+  const cudaError_t e = bd::launch_add_norm(p, sms, rtype == BD_RESIDUAL_F32,
                                             reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? BD_OK : BD_ERR_CUDA;
 }

@@ -94,6 +94,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
 
 // ------------------------------------------------------------------ TMA
 
+// Fetches [p, p + bytes) into L2; p on a 16-byte boundary, bytes a multiple of 16.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(__cvta_generic_to_global(p)),
+               "r"(bytes)
+               : "memory");
+}
+
 // 2D tiled bulk tensor load global -> shared, completing on `bar` (tx bytes).
 // x is the innermost (contiguous) coordinate in elements.
 __device__ __forceinline__ void tma_load_2d(void* dst, const void* tmap, uint64_t* bar, int32_t x,
