@@ -316,10 +316,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
     const float t_cost = static_cast<float>(t_blocks) * (b.head_dim == 128 ? 1.4f : 1.f) +
                          5.f * static_cast<float>(n_tiles) * b.n_kv_heads;
     const float d_cost = static_cast<float>(d_units) * (kUnitKeys * 4.f / 80e3f) * b.head_dim;
+    // (the quotient may round to a little above its bound: both ends are cut)
     n_dec = d_units == 0 ? 0
                          : static_cast<int>(ceilf(L.t_ctas * d_cost / (t_cost + d_cost)));
-    if (d_units > 0 && n_dec < 1) n_dec = 1;
-    if (t_blocks > 0 && n_dec > L.t_ctas - 1) n_dec = L.t_ctas - 1;
+    const int least = d_units > 0 ? 1 : 0, most = L.t_ctas - (t_blocks > 0 ? 1 : 0);
+    n_dec = n_dec < least ? least : (n_dec > most ? most : n_dec);
     n_tile = L.t_ctas - n_dec;
   }
   const int warps = L.use_tile ? kTileDecodeWarps : kDecodeWarps;

@@ -302,6 +302,20 @@ def test_bad_tables_are_reported():
     assert bd.bitdelta_check_error() == 7
 
 
+@pytest.mark.parametrize("units", [33, 66, 132, 264, 528, 565, 607])
+@pytest.mark.parametrize("hq,dim", [(24, 128), (8, 64)])
+def test_groups_that_share_nothing(hq, dim, units):
+    """A batch whose every prefix is empty has work for one of the two roles
+    only: all CTAs and no more are that role's (152·x/x in 32 bits is a little
+    above 152 for these numbers of 16-key units)."""
+    c = Case([(1, 16 * units)], hq, 1, dim, 32, groups=[(1, 0)], seed=23)
+    out, lse = c.run()
+    c.check(out, lse)
+    again, lse2 = c.run()
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    assert bd.bitdelta_check_error() == 0
+
+
 def test_a_prefix_longer_than_a_member_is_cut():
     """prefix_len past a member's earlier context counts only as far as all members have it."""
     lens = [(1, 64 + 1 + i) for i in range(40)]
