@@ -55,6 +55,21 @@ def test_plain_residual(rows, d, rtype):
     assert bd.bitdelta_check_error() == 0
 
 
+@pytest.mark.parametrize("rows,d", [(609, 8192), (700, 6152), (308, 16384), (305, 32776)])
+@pytest.mark.parametrize("residual", ["none", "other", "same"])
+def test_more_rows_than_run_at_once(rows, d, residual):
+    """Wide bf16 rows in several rounds of CTAs, which are fetched ahead; the
+    residual absent, of its own, or updated in place."""
+    g = torch.Generator(device="cuda").manual_seed(rows + d)
+    y, pre = rand(g, rows, d), rand(g, 1, d, std=0.1, mean=1.0)
+    res = None if residual == "none" else rand(g, rows, d, std=2.0)
+    ref = reference(y, res, pre, None, None, 1.0, [0] * rows)
+    h, x = bd.bitdelta_add_norm(y, res, bd.norm_table(list(pre)), eps=EPS,
+                                residual_out=res if residual == "same" else None)
+    check(h, x, *ref, torch.bfloat16)
+    assert bd.bitdelta_check_error() == 0
+
+
 @pytest.mark.parametrize("post", [False, True])
 @pytest.mark.parametrize("gate", ["none", "channel", "row"])
 @pytest.mark.parametrize("rtype", [torch.bfloat16, torch.float32])

@@ -96,6 +96,21 @@ def test_append(hq, hkv, dim, page, rot, pairs):
     assert torch.equal(q, q1) and torch.equal(kp, k1) and torch.equal(vp, v1)
 
 
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("hq,hkv,dim,page,rot", [(6, 2, 128, 16, 128), (3, 1, 64, 64, 32)])
+def test_more_tokens_than_run_at_once(hq, hkv, dim, page, rot, pairs):
+    """Several rounds of CTAs, whose rows are fetched ahead; the last rows end
+    at the tensor's end."""
+    lens = [(1, 40), (1400, 1401), (1, 7), (131, 500)]
+    batch, off, kv, table, qkv, rope, kp, vp = make(lens, hq, hkv, dim, page, seed=rot, rot=rot)
+    ref = reference(off, kv, table, qkv, rope, kp, vp, hq, hkv, dim, page, pairs)
+    q = bd.bitdelta_kv_append(batch, qkv, rope, kp, vp, interleaved=pairs)
+    close(q, ref[0], ref[3], "q")
+    close(kp, ref[1], ref[4], "k")
+    assert np.array_equal(vp.double().cpu().numpy(), ref[2])
+    assert bd.bitdelta_check_error() == 0
+
+
 def test_no_rope_copies():
     batch, off, kv, table, qkv, rope, kp, vp = make([(2, 2), (1, 40)], 4, 2, 128, 16)
     q = bd.bitdelta_kv_append(batch, qkv, None, kp, vp)
