@@ -9,8 +9,8 @@
 // angle's cosines and sines in registers and walks over the heads with it.
 //
 // Measured: 4 prompts of 2048 tokens, 64 query and 8 key heads of 128 (340 MB)
-// 58.3 us, 5.8 TB/s; 64 single tokens and four chunks of 512, 32 query heads
-// (52 MB) 11.7 us; 8 single tokens 3.9 us.
+// 52.6 us, 6.45 TB/s; 64 single tokens and four chunks of 512, 32 query heads
+// (52 MB) 12.3 us; 8 single tokens 3.2 us (3.7 a call from the host).
 #include <cstdint>
 
 #include "bitdelta_block.h"

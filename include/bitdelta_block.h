@@ -153,7 +153,8 @@ bd_status bitdelta_attention_plan(const bd_attention_batch* batch, void* plan, s
  * the product with the values.  A row with no key (a negative position)
  * gives zeros and an lse of −inf.  Positions past a sequence's kv_len are
  * never read as values, whatever the page holds there; within kv_len, keys
- * and values are expected finite.
+ * and values are expected finite, and values below 2^57 (a row's sums are kept
+ * relative to a score that may lie 2^40 below its largest).
  *   plan         as made by bitdelta_attention_plan for the same batch.  A call
  *                uses a counter in it and leaves it as it was.
  *   workspace    device memory of bitdelta_attention_workspace_bytes(batch)
