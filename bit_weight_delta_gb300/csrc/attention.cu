@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
   __shared__ int64_t s_warp[32];
   __shared__ int s_hist[kLenBuckets];
   __shared__ unsigned long long s_blocks;
-  __shared__ int s_comb, s_longest, s_parts;
+  __shared__ int s_comb, s_longest;
   const bd_attention_batch& b = p.b;
   const AttnLayout& L = p.L;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -136,7 +136,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
     s_blocks = 0;
     s_comb = 0;
     s_longest = 0;
-    s_parts = 0;
   }
   for (int i = tid; i < kLenBuckets; i += kPlanThreads) s_hist[i] = 0;
 
@@ -166,7 +165,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
     for (int c = tid; c < L.d_warps; c += kPlanThreads) starts[c].lo = starts[c].hi = 0;
     if (tid == 0) {
       record_error(p.ctx, kErrBounds);
-      *hd = PlanHeader{0, 1, 1, 0, 0, static_cast<int32_t>(b.n_tokens), 0, 0};
+      *hd = PlanHeader{0, 1, 1, 0, 0, static_cast<int32_t>(b.n_tokens), 0};
     }
     return;
   }
@@ -234,7 +233,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
     for (int c = tid; c < L.d_warps; c += kPlanThreads) starts[c].lo = starts[c].hi = 0;
     if (tid == 0) {
       record_error(p.ctx, kErrBounds);
-      *hd = PlanHeader{0, 1, 1, 0, 0, static_cast<int32_t>(b.n_tokens), 0, 0};
+      *hd = PlanHeader{0, 1, 1, 0, 0, static_cast<int32_t>(b.n_tokens), 0};
     }
     return;
   }
@@ -432,10 +431,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
     if (s >= 0) {
       const SeqRec r = seqs[s];
       const int x = it.tok - r.tok0;
-      int parts = 0;
       if (r.q_len * static_cast<int64_t>(L.g) > L.d_rows) {
         const int i = run_tile0[s] + x / tile_tok, y = x % tile_tok;
-        parts = tile_ns[i];
         join = tile_slot[i] >= 0 || tile_ns[i] == 0;
         it.own_slot = tile_slot[i];
         it.own_ns = tile_ns[i];
@@ -444,12 +441,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
         it.unit0 = r.unit0;
         it.units = r.units;
         it.own_row = x * L.g;
-        for (int h = 0; h < b.n_kv_heads; ++h) {
+        join = r.group >= 0;  // else final where no head's units are cut
+        for (int h = 0; h < b.n_kv_heads && !join; ++h) {
           const uint32_t u0 = r.unit0 + h * r.units;
-          const int n = decode_parts(u0, u0 + r.units, d_units, d_per, warps).count();
-          parts = n > parts ? n : parts;
+          join = decode_parts(u0, u0 + r.units, d_units, d_per, warps).count() > 1;
         }
-        join = r.group >= 0 || parts > 1;  // final where no head's units are cut
       }
       if (r.group >= 0) {
         const int z = it.tok - seqs[b.group_offsets[r.group]].tok0;
@@ -457,9 +453,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
         it.pre_slot = tile_slot[i];
         it.pre_ns = tile_ns[i];
         it.pre_row = y / L.half_tok * kHalfRows + y % L.half_tok * L.g;
-        parts += it.pre_ns;
       }
-      if (join) atomicMax(&s_parts, parts);
     }
     if (join) comb[atomicAdd(&s_comb, 1)] = it;
   }
@@ -467,7 +461,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
   if (tid == 0) {
     if (!fits) record_error(p.ctx, kErrBounds);
     *hd = PlanHeader{static_cast<int32_t>(d_units), static_cast<int32_t>(d_per), warps,
-                     fits ? n_entries : 0, n_tile, s_comb, s_parts, n_tile};
+                     fits ? n_entries : 0, n_tile, s_comb, n_tile};
   }
 }
 

@@ -36,7 +36,6 @@ struct PlanHeader {
   int32_t t_entries;  // pieces of the tile kernel (each once per key head)
   int32_t t_ctas;     // CTAs of its launch that take pieces; the others take units
   int32_t n_comb;     // tokens whose rows the combine kernel writes
-  int32_t most_parts; // of any of their rows
   int32_t next_piece; // the tile kernel's dealing: t_ctas between calls
 };
 
