@@ -20,10 +20,17 @@ AttnLayout attn_layout(const bd_attention_batch& b, int num_sms) {
   L.g = b.n_q_heads / b.n_kv_heads;
   L.half_tok = kHalfRows / L.g;
   const int64_t tile_tok = 2 * L.half_tok;
-  // Short runs have at most 16 rows (one mma.sync row tile), or 32 where a
-  // single token already has more than 16, or no sequence has more than 32.
+  // Short runs have at most 16 rows, one mma.sync row tile.  Longer ones are the
+  // tile role's: at 128-element heads its 256-row tile takes a few rows faster
+  // than two row tiles per warp did (8 sequences of 4 tokens, 8 query heads per key
+  // head, 20.4 -> 14.5 us; 256 of them 75 -> 53; 64 single tokens of 32 query heads
+  // per key head 64 -> 60).  At 64 a block's softmax takes twice its loads, and
+  // two row tiles win (64 sequences of 4 tokens over 500 to 8000 keys, 109
+  // against 177 us; 256 single tokens of 20 query heads per key head, 23 against
+  // 30), so runs have up to 32 rows where a single token already has more than
+  // 16, or no sequence has more than 32.
   const int64_t max_rows = static_cast<int64_t>(b.max_q_len) * L.g;
-  L.d_rows = L.g > 16 || (max_rows > 16 && max_rows <= 32) ? 32 : 16;
+  L.d_rows = b.head_dim == 64 && (L.g > 16 || (max_rows > 16 && max_rows <= 32)) ? 32 : 16;
   L.use_tile = max_rows > L.d_rows || b.n_group > 0;
   L.d_ctas = 2 * num_sms;
   L.d_warps = 8 * num_sms;
@@ -40,10 +47,10 @@ AttnLayout attn_layout(const bd_attention_batch& b, int num_sms) {
   L.max_tiles += prefix_tiles;
   // pieces: at most one per tile plus one per CTA of the launch (the plan cuts
   // tiles longer than the CTAs' even share)
-  L.max_entries = L.use_tile ? L.max_tiles + L.t_ctas : 0;
+  L.max_entries = L.use_tile ? L.max_tiles + 2 * L.t_ctas : 0;
   // slots: the pieces of cut tiles (at most two per CTA), with groups every
   // prefix piece and every own piece of a member
-  L.t_slots = L.use_tile ? 2 * L.t_ctas + (b.n_group > 0 ? L.max_tiles * b.n_kv_heads : 0) : 0;
+  L.t_slots = L.use_tile ? 4 * L.t_ctas + (b.n_group > 0 ? L.max_tiles * b.n_kv_heads : 0) : 0;
   size_t o = pad256(sizeof(PlanHeader));
   const auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -351,7 +358,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
   int piece = static_cast<int>(share < 2 ? 2 : share);
   if (cut && static_cast<int64_t>(n_tiles) * b.n_kv_heads <= n_tile) {
     // Few tiles: the shortest pieces that are one per CTA, so that none takes a
-    // remainder on top of a full piece (each thread tries one length).
+    // remainder on top of a full piece (each thread tries one length).  Where that
+    // is far above the share (about as many uneven tiles as CTAs), pieces of half
+    // a share, several per CTA: 128 tiles of 4 to 63 blocks, 90 us with one piece
+    // per CTA, 60 so.
     __syncthreads();
     if (tid == 0) s_longest = INT_MAX;
     for (int r = warp; r < n_run; r += kWarps)
@@ -365,7 +375,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs p) {
     for (int i = 0; i < n_tiles; ++i) pieces += (tile_ns[i] + piece + tid - 1) / (piece + tid);
     if (pieces * b.n_kv_heads <= n_tile) atomicMin(&s_longest, piece + tid);
     __syncthreads();
-    if (s_longest < INT_MAX) piece = s_longest;
+    const int most = static_cast<int>(share + (share / 4 > 4 ? share / 4 : 4));
+    piece = s_longest <= most ? s_longest : (piece + 1) / 2;
   }
   // slots first (a scan over tiles, which belong to runs: by tile index)
   for (int r = warp; r < n_run; r += kWarps) {
@@ -489,16 +500,23 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtas) combine_kernel(const 
   // waited for it before it let this one start: its header and this CTA's first
   // item are fetched while that kernel ends.
   const PlanHeader hd = *p.header();
-  // as many column slices as one round of CTAs takes, at least what fits a CTA
-  int slices = D / 16;
-  while (slices > 1 && g * (D / 4) * 2 <= kCombThreads * slices &&
-         static_cast<int64_t>(hd.n_comb) * H * slices > gridDim.x)
-    slices >>= 1;
-  const int cols = D / 4 / slices;  // float4 columns per CTA
-  const int groups = kCombThreads / (cols * g);
-  const int row = threadIdx.x % g, q = threadIdx.x / g;
-  const int col = q % cols, grp = q / cols;
-  const int n_work = hd.n_comb * H * slices;
+  // As many column slices as one round of CTAs takes, at least what fits a CTA;
+  // and, where few items leave SMs idle, fewer rows for each CTA, so that more
+  // thread groups share the parts (one token of 32 query heads on one key head,
+  // 65536 keys, 57 -> 21 us).
+  const int64_t items = static_cast<int64_t>(hd.n_comb) * H;
+  int slice_bits = D == 128 ? 3 : 2, row_bits = 0;
+  while (slice_bits > 0 && g * (D / 4) * 2 <= kCombThreads << slice_bits &&
+         items << slice_bits > gridDim.x)
+    --slice_bits;
+  while (4 << row_bits < g && items << (slice_bits + row_bits + 1) <= L.d_ctas) ++row_bits;
+  const int cut_bits = slice_bits + row_bits;     // 2^cut_bits CTAs per item
+  const int g_cta = (g + (1 << row_bits) - 1) >> row_bits;
+  const int cols = (D / 4) >> slice_bits;         // float4 columns per CTA
+  const int groups = kCombThreads / (cols * g_cta);
+  const int q = threadIdx.x / g_cta;
+  const int col = q % cols, grp = q / cols, row_in = threadIdx.x % g_cta;
+  const int n_work = static_cast<int>(items << cut_bits);
   // An item's own parts: tile slots own_slot .. (times heads plus head), decode
   // parts, or the one part of a run that a warp or CTA did alone; none to join
   // where that part is final already (another head of the token is cut).
@@ -506,16 +524,16 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtas) combine_kernel(const 
     CombItem it;
     DecodeParts dp;
     int64_t first;
-    int kvh, d4, n_own, rows, own_row;
+    int kvh, d4, row, n_own, rows, own_row;
     bool cut, skip;
     uint8_t *o, *ml;
   };
   const auto prepare = [&](const CombItem& it, int w) {
     Work k;
     k.it = it;
-    k.kvh = static_cast<int>(static_cast<uint32_t>(w) / static_cast<uint32_t>(slices) %
-                             static_cast<uint32_t>(H));
-    k.d4 = static_cast<int>(static_cast<uint32_t>(w) % static_cast<uint32_t>(slices)) * cols + col;
+    k.kvh = static_cast<int>((static_cast<uint32_t>(w) >> cut_bits) % static_cast<uint32_t>(H));
+    k.d4 = (w & ((1 << slice_bits) - 1)) * cols + col;
+    k.row = (w >> slice_bits & ((1 << row_bits) - 1)) * g_cta + row_in;
     k.first = static_cast<int64_t>(it.own_slot) * H + k.kvh;
     k.n_own = it.own_ns;
     k.rows = 2 * kHalfRows;
@@ -540,7 +558,7 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtas) combine_kernel(const 
     return k;
   };
   const auto item_of = [&](int w) {
-    return p.comb()[static_cast<uint32_t>(w) / static_cast<uint32_t>(H * slices)];
+    return p.comb()[(static_cast<uint32_t>(w) >> cut_bits) / static_cast<uint32_t>(H)];
   };
   const int stride = static_cast<int>(gridDim.x);
   int w = static_cast<int>(blockIdx.x);
@@ -559,11 +577,11 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtas) combine_kernel(const 
     }
     if (k.skip) continue;
     const CombItem& it = k.it;
-    const int kvh = k.kvh, d4 = k.d4, n_own = k.n_own, rows = k.rows, own_row = k.own_row;
+    const int kvh = k.kvh, d4 = k.d4, row = k.row, n_own = k.n_own, rows = k.rows, own_row = k.own_row;
     const int n = n_own + it.pre_ns;
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (grp < groups) {
+    if (grp < groups && row < g) {
       for (int i0 = grp; i0 < n; i0 += groups * kCombBatch) {
         float2 ml[kCombBatch];
         float4 v[kCombBatch];
@@ -611,8 +629,8 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtas) combine_kernel(const 
       s_ml[threadIdx.x] = make_float2(m, l);
       __syncthreads();
     }
-    if (grp != 0) continue;
-    const int span = g * cols, most = groups < n ? groups : n;
+    if (grp != 0 || row >= g) continue;
+    const int span = g_cta * cols, most = groups < n ? groups : n;
     float top = m;
     for (int k = 1; k < most; ++k) top = fmaxf(top, s_ml[threadIdx.x + k * span].x);
     const float ref = top == -INFINITY ? 0.f : top;
@@ -685,9 +703,9 @@ bd_status run_attention(AttnArgs& p, cudaStream_t s) {
   } else if (launch_attn_decode(p, m.dk, m.dv, s) != cudaSuccess) {
     return BD_ERR_CUDA;
   }
-  const int64_t work = b.n_tokens * b.n_kv_heads * (b.head_dim / 16);
-  const int64_t most = kCombCtas * static_cast<int64_t>(p.L.t_ctas);
-  const dim3 grid(static_cast<unsigned>(work < most ? work : most));
+  const int64_t items = b.n_tokens * b.n_kv_heads * (b.head_dim / 16);
+  const int64_t few = p.L.d_ctas, most = kCombCtas * static_cast<int64_t>(p.L.t_ctas);
+  const dim3 grid(static_cast<unsigned>(items < few ? few : (items < most ? items : most)));
   const cudaError_t e = launch_pdl(combine_kernel, grid, dim3(kCombThreads), 0, s, p);
   return e == cudaSuccess ? BD_OK : BD_ERR_CUDA;
 }

@@ -51,7 +51,7 @@ cudaError_t launch(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& 
 cudaError_t launch_attn_decode(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
                                cudaStream_t s) {
   if (a.b.head_dim == 128)
-    return a.L.d_rows == 16 ? launch<128, 1>(a, tk, tv, s) : launch<128, 2>(a, tk, tv, s);
+    return launch<128, 1>(a, tk, tv, s);
   return a.L.d_rows == 16 ? launch<64, 1>(a, tk, tv, s) : launch<64, 2>(a, tk, tv, s);
 }
 

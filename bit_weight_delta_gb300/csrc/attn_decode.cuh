@@ -241,8 +241,8 @@ __device__ __forceinline__ void run(const CUtensorMap& tmap_k, const CUtensorMap
       const uint32_t kb = smem_addr(ring + stage * C::kStage);
       const uint32_t vb = kb + C::kKv;
       const int key0 = r.k0 + 16 * tile;
-      // two chains of products per score, each half as long (for 32 rows their
-      // registers would spill, and the two row tiles are two chains already)
+      // two chains of products per score, each half as long (the two row tiles of
+      // 32 rows are two chains already)
       constexpr int kChains = RT == 1 ? 2 : 1;
       float s[RT][2][4], part[kChains][RT][2][4];
 #pragma unroll

@@ -796,7 +796,7 @@ cudaError_t launch(const AttnArgs& a, const TileMaps& maps, cudaStream_t s) {
 
 cudaError_t launch_attn_tile(const AttnArgs& a, const TileMaps& maps, cudaStream_t s) {
   if (a.b.head_dim == 128)
-    return a.L.d_rows == 16 ? launch<128, 1>(a, maps, s) : launch<128, 2>(a, maps, s);
+    return launch<128, 1>(a, maps, s);
   return a.L.d_rows == 16 ? launch<64, 1>(a, maps, s) : launch<64, 2>(a, maps, s);
 }
 

@@ -171,6 +171,22 @@ def test_one_long_context(hq, hkv, dim):
     c.check(*c.run())
 
 
+@pytest.mark.parametrize("hq,hkv,dim", [(32, 1, 128), (32, 1, 64), (20, 1, 128), (9, 1, 128)])
+def test_one_long_context_of_many_heads(hq, hkv, dim):
+    """Hundreds of parts per row, whose join is cut by rows as well."""
+    c = Case([(1, 9001)], hq, hkv, dim, 64, seed=31)
+    out, lse = c.run()
+    c.check(out, lse)
+    assert torch.equal(out, c.run()[0])
+
+
+@pytest.mark.parametrize("hq,hkv,q", [(40, 2, 1), (16, 2, 4)])
+def test_about_as_many_uneven_tiles_as_ctas(hq, hkv, q):
+    """Tiles of 1 to 24 blocks, which are cut to half of a CTA's share."""
+    c = Case([(q, 4 + 41 * s) for s in range(74)], hq, hkv, 128, 32, seed=32)
+    c.check(*c.run())
+
+
 def test_many_sequences():
     rng = np.random.default_rng(3)
     lens = [(1, int(k)) for k in rng.integers(1, 700, 300)]
