@@ -16,7 +16,7 @@
 //
 // Measured (64 query and 8 key heads of 128, in the decode kernel): 64 tokens
 // over 500 to 8000 keys each, 1.12 GB of cache, 175 us, 6.4 TB/s; one token
-// over 131071 keys, 537 MB, 89.7 us, 6.0 TB/s, of which the launch, the first
+// over 131071 keys, 537 MB, 87.2 us, 6.2 TB/s, of which the launch, the first
 // pages' latency and the join are about 8; 8 tokens over 120 to 1000 keys, 10.7
 // us, bound by that latency.  Taking two tiles at a time won 2.5% on the one long
 // context and lost as much on the 8 tokens.
