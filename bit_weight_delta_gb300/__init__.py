@@ -610,13 +610,18 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream(stream, device):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+def _stream_on(stream, device):
+    """`stream`, or the device's current one; a stream of another device is refused."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the call's tensors on {device}")
+    return stream
 
 
 def _empty(n: int, device, stream):
     """n bytes that belong to the stream that will use them."""
-    with torch.cuda.stream(stream):          # None: the current one
+    with torch.cuda.stream(stream):
         return torch.empty(n, dtype=torch.uint8, device=device)
 
 
@@ -648,7 +653,7 @@ def bitdelta_add_norm(y, residual=None, pre_table=None, post_table=None, gate=No
     written.  residual: bf16 or fp32 (None: zero, h is then bf16); gate: bf16
     [d] or like y.  residual_out may be residual itself."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with torch.cuda.stream(_stream_on(stream, y.device)):
             return bitdelta_add_norm(y, residual, pre_table, post_table, gate, scale, eps,
                                      seg_offsets, seg_variant, residual_out, out)
     r = (_native or _load_native()).add_norm(y, residual, pre_table, post_table, gate, scale, eps,
@@ -667,6 +672,11 @@ class _AttentionBatch(ctypes.Structure):
                 ("seq_offsets", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
                 ("page_table", ctypes.c_void_p), ("n_group", ctypes.c_int32),
                 ("group_offsets", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p)]
+
+
+class _BatchState(ctypes.Structure):
+    """What csrc/binding.cpp reads of an AttentionBatch."""
+    _fields_ = [("c", _AttentionBatch), ("device", ctypes.c_int64)]
 
 
 class AttentionBatch:
@@ -698,22 +708,31 @@ class AttentionBatch:
             if _dev(group_offsets, torch.int32, "group_offsets").numel() != n_group + 1:
                 raise ValueError("group_offsets must have one entry more than prefix_len")
         self._keep = (seq_offsets, kv_len, page_table, group_offsets, prefix_len)
-        self._c = _AttentionBatch(
+        self._device = kv_len.device
+        if any(t is not None and t.device != self._device for t in self._keep):
+            raise ValueError("the batch's tensors must be on one device")
+        self._state = _BatchState(_AttentionBatch(
             n_tokens, n_seq, max_q_len, max_kv_len, n_q_heads, n_kv_heads, head_dim, page_size, 0,
             page_table.shape[1], seq_offsets.data_ptr(), kv_len.data_ptr(),
-            page_table.data_ptr(), n_group, _addr(group_offsets), _addr(prefix_len))
-        self._ref = ctypes.addressof(self._c)
+            page_table.data_ptr(), n_group, _addr(group_offsets), _addr(prefix_len)),
+            self._device.index)
+        self._ref = ctypes.addressof(self._state)
         lib = load()
-        self._plan = _empty(lib.bitdelta_attention_plan_bytes(self._ref), kv_len.device, stream)
-        self._ws = _empty(lib.bitdelta_attention_workspace_bytes(self._ref), kv_len.device, stream)
+        with torch.cuda.device(self._device):    # its SM count goes into the sizes
+            stream = _stream_on(stream, self._device)
+            self._plan, self._ws = (
+                _empty(size(self._ref), self._device, stream)
+                for size in (lib.bitdelta_attention_plan_bytes,
+                             lib.bitdelta_attention_workspace_bytes))
         self._args = (self._ref, self._plan.data_ptr(), self._plan.numel(), self._ws.data_ptr(),
                       self._ws.numel())
         self.plan(stream)
 
     def plan(self, stream=None) -> None:
         """Compute the plan from the lengths now in the batch's tensors."""
-        _check("bitdelta_attention_plan", load().bitdelta_attention_plan(
-            *self._args[:3], _raw_stream(stream, self._plan.device)))
+        with torch.cuda.device(self._device):
+            _check("bitdelta_attention_plan", load().bitdelta_attention_plan(
+                *self._args[:3], _stream_on(stream, self._device).cuda_stream))
 
 
 def bitdelta_kv_append(batch: AttentionBatch, qkv, rope, k_pages, v_pages,
@@ -725,7 +744,7 @@ def bitdelta_kv_append(batch: AttentionBatch, qkv, rope, k_pages, v_pages,
     rope: fp32 [positions, rot_dim], cosines then sines (None: no rotation);
     interleaved rotates neighbours (2i, 2i+1) instead of halves."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with torch.cuda.stream(_stream_on(stream, qkv.device)):
             return bitdelta_kv_append(batch, qkv, rope, k_pages, v_pages, interleaved, out)
     r = (_native or _load_native()).kv_append(batch._ref, qkv, rope, k_pages, v_pages, interleaved, out)
     if type(r) is int:
@@ -739,7 +758,7 @@ def bitdelta_attention(batch: AttentionBatch, q, k_pages, v_pages, scale: float 
     Returns (out, lse): bf16 like q, and fp32 [n_tokens, n_q_heads].  scale
     defaults to 1/sqrt(head_dim)."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with torch.cuda.stream(_stream_on(stream, q.device)):
             return bitdelta_attention(batch, q, k_pages, v_pages, scale, out, lse)
     r = (_native or _load_native()).attention(*batch._args, q, k_pages, v_pages, scale, out, lse)
     if type(r) is int:

@@ -6,7 +6,7 @@
 // made in C++ on torch's tensors, and the library's C entry points are called
 // through their addresses, which bind() receives from the loaded library.
 // Every function launches on its tensors' device, on that device's current
-// stream.
+// stream; tensors of several devices are refused.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -45,23 +45,32 @@ const char* type_name(at::ScalarType t) {
   }
 }
 
-const at::Tensor& tensor(PyObject* o, at::ScalarType type, const char* name) {
-  if (!THPVariable_Check(o)) refuse("%s must be a tensor", name);
-  const at::Tensor& t = THPVariable_Unpack(o);
-  if (!t.is_cuda()) refuse("%s must be a CUDA tensor", name);
-  if (t.scalar_type() != type) refuse("%s must be %s", name, type_name(type));
-  if (!t.is_contiguous()) refuse("%s must be contiguous", name);
-  return t;
-}
-const at::Tensor& shaped(PyObject* o, at::ScalarType type, at::IntArrayRef shape,
-                         const char* name) {
-  const at::Tensor& t = tensor(o, type, name);
-  if (t.sizes() != shape) refuse("%s does not have the shape that the call needs", name);
-  return t;
-}
-void* address(PyObject* o, at::ScalarType type, const char* name) {
-  return o == Py_None ? nullptr : tensor(o, type, name).data_ptr();
-}
+// A call's tensors, all on the device that it launches on.
+struct Tensors {
+  int64_t device;  // index; the first tensor's where it is negative
+
+  const at::Tensor& get(PyObject* o, at::ScalarType type, const char* name) {
+    if (!THPVariable_Check(o)) refuse("%s must be a tensor", name);
+    const at::Tensor& t = THPVariable_Unpack(o);
+    const c10::Device d = t.device();
+    if (!d.is_cuda()) refuse("%s must be a CUDA tensor", name);
+    if (device < 0) device = d.index();
+    if (d.index() != device) refuse("%s is on another device than the call's other tensors", name);
+    if (t.scalar_type() != type) refuse("%s must be %s", name, type_name(type));
+    if (!t.is_contiguous()) refuse("%s must be contiguous", name);
+    return t;
+  }
+  const at::Tensor& shaped(PyObject* o, at::ScalarType type, at::IntArrayRef shape,
+                           const char* name) {
+    const at::Tensor& t = get(o, type, name);
+    if (t.sizes() != shape) refuse("%s does not have the shape that the call needs", name);
+    return t;
+  }
+  const at::Tensor* maybe(PyObject* o, at::ScalarType type, const char* name) {
+    return o == Py_None ? nullptr : &get(o, type, name);
+  }
+};
+void* address(const at::Tensor* t) { return t == nullptr ? nullptr : t->data_ptr(); }
 double number(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) throw Refused{};
@@ -118,103 +127,105 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // seg_variant, residual_out, out) -> (h, x), or the status code of a refusal.
 PyObject* add_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 11, [&]() -> PyObject* {
-    const at::Tensor& y = tensor(a[0], at::kBFloat16, "y");
+    Tensors in{-1};
+    const at::Tensor& y = in.get(a[0], at::kBFloat16, "y");
     if (y.dim() < 1) refuse("%s must have at least one dimension", "y");
-    const c10::cuda::CUDAGuard guard(y.device());
     const int64_t d = y.size(-1);
     at::ScalarType rtype = at::kBFloat16;
-    const void* residual = nullptr;
+    const at::Tensor* residual = nullptr;
     if (a[1] != Py_None) {
       if (THPVariable_Check(a[1])) rtype = THPVariable_Unpack(a[1]).scalar_type();
       if (rtype != at::kBFloat16 && rtype != at::kFloat)
         refuse("%s must be bfloat16 or float32", "residual");
-      residual = shaped(a[1], rtype, y.sizes(), "residual").data_ptr();
+      residual = &in.shaped(a[1], rtype, y.sizes(), "residual");
     }
     if (a[2] == Py_None) refuse("%s is required", "pre_table");
-    const at::Tensor& pre = tensor(a[2], at::kLong, "pre_table");
-    const void* post = address(a[3], at::kLong, "post_table");
-    if (post != nullptr && THPVariable_Unpack(a[3]).numel() != pre.numel())
+    const at::Tensor& pre = in.get(a[2], at::kLong, "pre_table");
+    const at::Tensor* post = in.maybe(a[3], at::kLong, "post_table");
+    if (post != nullptr && post->numel() != pre.numel())
       refuse("pre_table and %s must have the same number of slots", "post_table");
-    const void* gate = nullptr;
+    const at::Tensor* gate = in.maybe(a[4], at::kBFloat16, "gate");
     int64_t gate_stride = 0;
-    if (a[4] != Py_None) {
-      const at::Tensor& g = tensor(a[4], at::kBFloat16, "gate");
-      if (g.dim() > 1 && g.sizes() == y.sizes())
+    if (gate != nullptr) {
+      if (gate->dim() > 1 && gate->sizes() == y.sizes())
         gate_stride = d;
-      else if (g.dim() != 1 || g.size(0) != d)
+      else if (gate->dim() != 1 || gate->size(0) != d)
         refuse("%s must be [d] or have the shape of y", "gate");
-      gate = g.data_ptr();
     }
     const double scale = number(a[5]), eps = number(a[6]);
     if ((a[7] == Py_None) != (a[8] == Py_None))
       refuse("%s and seg_variant go together", "seg_offsets");
-    const void* offsets = address(a[7], at::kInt, "seg_offsets");
-    const void* variant = address(a[8], at::kInt, "seg_variant");
-    int64_t n_seg = 0;
-    if (a[8] != Py_None) {
-      n_seg = THPVariable_Unpack(a[8]).numel();
-      if (THPVariable_Unpack(a[7]).numel() != n_seg + 1)
-        refuse("%s must have one entry more than seg_variant", "seg_offsets");
-    }
-    const at::Tensor h = a[9] != Py_None ? shaped(a[9], rtype, y.sizes(), "residual_out")
-                                         : fresh(y.sizes(), rtype, y);
-    const at::Tensor x = a[10] != Py_None ? shaped(a[10], at::kBFloat16, y.sizes(), "out")
-                                          : fresh(y.sizes(), at::kBFloat16, y);
+    const at::Tensor* offsets = in.maybe(a[7], at::kInt, "seg_offsets");
+    const at::Tensor* variant = in.maybe(a[8], at::kInt, "seg_variant");
+    const int64_t n_seg = variant != nullptr ? variant->numel() : 0;
+    if (offsets != nullptr && offsets->numel() != n_seg + 1)
+      refuse("%s must have one entry more than seg_variant", "seg_offsets");
+    const at::Tensor* h_out =
+        a[9] != Py_None ? &in.shaped(a[9], rtype, y.sizes(), "residual_out") : nullptr;
+    const at::Tensor* x_out =
+        a[10] != Py_None ? &in.shaped(a[10], at::kBFloat16, y.sizes(), "out") : nullptr;
+    const c10::cuda::CUDAGuard guard(y.device());
+    const at::Tensor h = h_out != nullptr ? *h_out : fresh(y.sizes(), rtype, y);
+    const at::Tensor x = x_out != nullptr ? *x_out : fresh(y.sizes(), at::kBFloat16, y);
     const bd_status st = g_add_norm(
-        static_cast<const uint16_t*>(y.data_ptr()), d > 0 ? y.numel() / d : 0, d, residual,
-        h.data_ptr(), rtype == at::kFloat ? BD_RESIDUAL_F32 : BD_RESIDUAL_BF16,
-        static_cast<const uint16_t*>(gate), gate_stride, static_cast<float>(scale),
+        static_cast<const uint16_t*>(y.data_ptr()), d > 0 ? y.numel() / d : 0, d,
+        address(residual), h.data_ptr(), rtype == at::kFloat ? BD_RESIDUAL_F32 : BD_RESIDUAL_BF16,
+        static_cast<const uint16_t*>(address(gate)), gate_stride, static_cast<float>(scale),
         static_cast<float>(eps), static_cast<const uint16_t* const*>(pre.data_ptr()),
-        static_cast<const uint16_t* const*>(post), static_cast<int32_t>(pre.numel()),
-        static_cast<const int32_t*>(offsets), static_cast<const int32_t*>(variant),
-        static_cast<int32_t>(n_seg), static_cast<uint16_t*>(x.data_ptr()), stream_of(y));
+        static_cast<const uint16_t* const*>(address(post)), static_cast<int32_t>(pre.numel()),
+        static_cast<const int32_t*>(address(offsets)),
+        static_cast<const int32_t*>(address(variant)), static_cast<int32_t>(n_seg),
+        static_cast<uint16_t*>(x.data_ptr()), stream_of(y));
     if (st != BD_OK) return PyLong_FromLong(st);
     return two(h, x);
   });
 }
 
-// The batch's struct with this call's cache in it.
-bd_attention_batch* batch_of(PyObject* o, PyObject* k_pages, PyObject* v_pages, uint16_t** k,
-                             uint16_t** v) {
-  auto* b = static_cast<bd_attention_batch*>(pointer(o));
-  const at::Tensor& kp = tensor(k_pages, at::kBFloat16, "k_pages");
-  const at::Tensor& vp = tensor(v_pages, at::kBFloat16, "v_pages");
-  if (kp.dim() != 4 || kp.sizes() != vp.sizes() || kp.size(1) != b->n_kv_heads ||
-      kp.size(2) != b->page_size || kp.size(3) != b->head_dim)
+// A batch as the Python class holds it: the C struct and the device of its
+// tables, plan and workspace.
+struct Batch {
+  bd_attention_batch c;
+  int64_t device;
+};
+
+// A call's cache: its shape goes into the batch's struct.
+struct Cache {
+  uint16_t *k, *v;
+};
+Cache cache_of(Tensors& in, Batch* b, PyObject* k_pages, PyObject* v_pages) {
+  const at::Tensor& kp = in.get(k_pages, at::kBFloat16, "k_pages");
+  const at::Tensor& vp = in.get(v_pages, at::kBFloat16, "v_pages");
+  if (kp.dim() != 4 || kp.sizes() != vp.sizes() || kp.size(1) != b->c.n_kv_heads ||
+      kp.size(2) != b->c.page_size || kp.size(3) != b->c.head_dim)
     refuse("k_pages and %s must be [n_pages, n_kv_heads, page_size, head_dim]", "v_pages");
-  b->n_pages = kp.size(0);
-  *k = static_cast<uint16_t*>(kp.data_ptr());
-  *v = static_cast<uint16_t*>(vp.data_ptr());
-  return b;
+  b->c.n_pages = kp.size(0);
+  return {static_cast<uint16_t*>(kp.data_ptr()), static_cast<uint16_t*>(vp.data_ptr())};
 }
 
 // kv_append(batch, qkv, rope, k_pages, v_pages, interleaved, out) -> q, or a
 // status code.
 PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 7, [&]() -> PyObject* {
-    uint16_t *k, *v;
-    const bd_attention_batch* b = batch_of(a[0], a[3], a[4], &k, &v);
-    const int64_t width = static_cast<int64_t>(b->n_q_heads + 2 * b->n_kv_heads) * b->head_dim;
-    const at::Tensor& qkv = shaped(a[1], at::kBFloat16, {b->n_tokens, width}, "qkv");
-    const c10::cuda::CUDAGuard guard(qkv.device());
-    const float* rope = nullptr;
-    int64_t rows = 0, rot = 0;
-    if (a[2] != Py_None) {
-      const at::Tensor& r = tensor(a[2], at::kFloat, "rope");
-      if (r.dim() != 2) refuse("%s must be [positions, rot_dim]", "rope");
-      rows = r.size(0);
-      rot = r.size(1);
-      rope = static_cast<const float*>(r.data_ptr());
-    }
+    Batch* batch = static_cast<Batch*>(pointer(a[0]));
+    const bd_attention_batch& b = batch->c;
+    Tensors in{batch->device};
+    const int64_t width = static_cast<int64_t>(b.n_q_heads + 2 * b.n_kv_heads) * b.head_dim;
+    const at::Tensor& qkv = in.shaped(a[1], at::kBFloat16, {b.n_tokens, width}, "qkv");
+    const at::Tensor* rope = in.maybe(a[2], at::kFloat, "rope");
+    if (rope != nullptr && rope->dim() != 2) refuse("%s must be [positions, rot_dim]", "rope");
+    const int64_t rows = rope != nullptr ? rope->size(0) : 0;
+    const int64_t rot = rope != nullptr ? rope->size(1) : 0;
     const bool pairs = PyObject_IsTrue(a[5]) == 1;
-    const int64_t shape[3] = {b->n_tokens, b->n_q_heads, b->head_dim};
-    const at::Tensor q =
-        a[6] != Py_None ? shaped(a[6], at::kBFloat16, shape, "out") : fresh(shape, at::kBFloat16, qkv);
+    const int64_t shape[3] = {b.n_tokens, b.n_q_heads, b.head_dim};
+    const at::Tensor* out = a[6] != Py_None ? &in.shaped(a[6], at::kBFloat16, shape, "out") : nullptr;
+    const Cache cache = cache_of(in, batch, a[3], a[4]);
+    const c10::cuda::CUDAGuard guard(qkv.device());
+    const at::Tensor q = out != nullptr ? *out : fresh(shape, at::kBFloat16, qkv);
     const bd_status st = g_kv_append(
-        b, static_cast<const uint16_t*>(qkv.data_ptr()), rope, rows,
-        static_cast<int32_t>(rot < INT32_MAX ? rot : INT32_MAX),
-        pairs ? BD_ROPE_PAIRS : BD_ROPE_HALVES, k, v, static_cast<uint16_t*>(q.data_ptr()),
-        stream_of(qkv));
+        &b, static_cast<const uint16_t*>(qkv.data_ptr()), static_cast<const float*>(address(rope)),
+        rows, static_cast<int32_t>(rot < INT32_MAX ? rot : INT32_MAX),
+        pairs ? BD_ROPE_PAIRS : BD_ROPE_HALVES, cache.k, cache.v,
+        static_cast<uint16_t*>(q.data_ptr()), stream_of(qkv));
     if (st != BD_OK) return PyLong_FromLong(st);
     return THPVariable_Wrap(q);
   });
@@ -224,21 +235,23 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // v_pages, scale, out, lse) -> (out, lse), or a status code.
 PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 11, [&]() -> PyObject* {
-    uint16_t *k, *v;
-    const bd_attention_batch* b = batch_of(a[0], a[6], a[7], &k, &v);
-    const int64_t shape[3] = {b->n_tokens, b->n_q_heads, b->head_dim};
-    const at::Tensor& q = shaped(a[5], at::kBFloat16, shape, "q");
-    const c10::cuda::CUDAGuard guard(q.device());
-    const double scale =
-        a[8] == Py_None ? 1.0 / std::sqrt(static_cast<double>(b->head_dim)) : number(a[8]);
-    const at::Tensor out =
-        a[9] != Py_None ? shaped(a[9], at::kBFloat16, shape, "out") : fresh(shape, at::kBFloat16, q);
+    Batch* batch = static_cast<Batch*>(pointer(a[0]));
+    const bd_attention_batch& b = batch->c;
+    Tensors in{batch->device};
+    const int64_t shape[3] = {b.n_tokens, b.n_q_heads, b.head_dim};
     const at::IntArrayRef rows(shape, 2);
-    const at::Tensor lse =
-        a[10] != Py_None ? shaped(a[10], at::kFloat, rows, "lse") : fresh(rows, at::kFloat, q);
+    const at::Tensor& q = in.shaped(a[5], at::kBFloat16, shape, "q");
+    const double scale =
+        a[8] == Py_None ? 1.0 / std::sqrt(static_cast<double>(b.head_dim)) : number(a[8]);
+    const at::Tensor* o_out = a[9] != Py_None ? &in.shaped(a[9], at::kBFloat16, shape, "out") : nullptr;
+    const at::Tensor* l_out = a[10] != Py_None ? &in.shaped(a[10], at::kFloat, rows, "lse") : nullptr;
+    const Cache cache = cache_of(in, batch, a[6], a[7]);
+    const c10::cuda::CUDAGuard guard(q.device());
+    const at::Tensor out = o_out != nullptr ? *o_out : fresh(shape, at::kBFloat16, q);
+    const at::Tensor lse = l_out != nullptr ? *l_out : fresh(rows, at::kFloat, q);
     const bd_status st = g_attention(
-        b, pointer(a[1]), PyLong_AsSize_t(a[2]), static_cast<const uint16_t*>(q.data_ptr()), k, v,
-        static_cast<float>(scale), static_cast<uint16_t*>(out.data_ptr()),
+        &b, pointer(a[1]), PyLong_AsSize_t(a[2]), static_cast<const uint16_t*>(q.data_ptr()),
+        cache.k, cache.v, static_cast<float>(scale), static_cast<uint16_t*>(out.data_ptr()),
         static_cast<float*>(lse.data_ptr()), pointer(a[3]), PyLong_AsSize_t(a[4]), stream_of(q));
     if (st != BD_OK) return PyLong_FromLong(st);
     return two(out, lse);

@@ -1,0 +1,160 @@
+"""The decoder-block calls run on their tensors' device, whichever is current,
+and refuse tensors of several devices before any launch (no GPU needed: the
+tensors, the library and the device guard are stand-ins)."""
+import contextlib
+import ctypes
+
+import pytest
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+
+import bit_weight_delta_gb300 as bd
+
+BF16, F32, I32, I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+
+
+class Tensor:
+    """An int32 CUDA tensor as AttentionBatch looks at it."""
+    is_cuda, dtype = True, torch.int32
+
+    def __init__(self, *shape, device=1):
+        self.shape, self.device = shape, torch.device("cuda", device)
+        self.recorded = []
+
+    def numel(self):
+        n = 1
+        for s in self.shape:
+            n *= s
+        return n
+
+    def dim(self):
+        return len(self.shape)
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 0x100000
+
+    def record_stream(self, stream):
+        self.recorded.append(stream.cuda_stream)
+
+
+class Stream:
+    def __init__(self, handle, device):
+        self.cuda_stream, self.device = handle, torch.device("cuda", device)
+
+
+class World:
+    """The current device, and what the library was called with under which."""
+
+    def __init__(self, monkeypatch):
+        self.current, self.calls = 0, []
+
+        @contextlib.contextmanager
+        def guard(device):
+            before, self.current = self.current, torch.device(device).index
+            yield
+            self.current = before
+
+        def call(name, result):
+            def f(*args):
+                self.calls.append((name, self.current, args[-1]))
+                return result
+            return f
+
+        self.lib = type("Lib", (), {})()
+        self.lib.bitdelta_attention_plan_bytes = call("plan_bytes", 512)
+        self.lib.bitdelta_attention_workspace_bytes = call("workspace_bytes", 1024)
+        self.lib.bitdelta_attention_plan = call("plan", 0)
+        monkeypatch.setattr(bd, "load", lambda *a: self.lib)
+        monkeypatch.setattr(bd, "_empty", lambda n, device, stream: Tensor(n, device=device.index))
+        monkeypatch.setattr(torch.cuda, "device", guard)
+        monkeypatch.setattr(torch.cuda, "current_stream",
+                            lambda device=None: Stream(0x77, torch.device(device).index))
+
+
+@pytest.fixture
+def world(monkeypatch):
+    return World(monkeypatch)
+
+
+def batch(**over):
+    a = dict(seq_offsets=Tensor(3), kv_len=Tensor(2), page_table=Tensor(2, 4), **over)
+    return bd.AttentionBatch(a.pop("seq_offsets"), a.pop("kv_len"), a.pop("page_table"), 4, 2, 64,
+                             8, 2, 128, 16, **a)
+
+
+def test_sizes_and_plan_on_the_tensors_device(world):
+    b = batch()
+    assert [(n, d) for n, d, _ in world.calls] == [("plan_bytes", 1), ("workspace_bytes", 1),
+                                                   ("plan", 1)]
+    assert world.calls[-1][2] == 0x77                # that device's current stream
+    assert b._plan.device.index == b._ws.device.index == 1
+    b.plan(Stream(0x99, 1))
+    assert world.calls[-1] == ("plan", 1, 0x99)
+    assert world.current == 0
+
+
+@pytest.mark.parametrize("name", ["group_offsets", "prefix_len"])
+def test_batch_tensors_of_two_devices(world, name):
+    groups = {"group_offsets": Tensor(2), "prefix_len": Tensor(1)}
+    batch(**groups)
+    groups[name].device = torch.device("cuda", 0)
+    with pytest.raises(ValueError, match="one device"):
+        batch(**groups)
+    with pytest.raises(ValueError, match="one device"):
+        bd.AttentionBatch(Tensor(3, device=0), Tensor(2), Tensor(2, 4), 4, 2, 64, 8, 2, 128, 16)
+
+
+def test_a_stream_of_another_device(world):
+    with pytest.raises(ValueError, match="stream"):
+        batch(stream=Stream(0x99, 0))
+    b = batch()
+    with pytest.raises(ValueError, match="stream"):
+        b.plan(Stream(0x99, 0))
+    for f in (lambda s: bd.bitdelta_add_norm(Tensor(4, 64), stream=s),
+              lambda s: bd.bitdelta_kv_append(b, Tensor(4, 64), None, None, None, stream=s),
+              lambda s: bd.bitdelta_attention(b, Tensor(4, 64), None, None, stream=s)):
+        with pytest.raises(ValueError, match="stream"):
+            f(Stream(0x99, 0))
+
+
+def fake(dtype, *shape, device=0):
+    return torch.empty(shape, dtype=dtype, device=f"cuda:{device}")
+
+
+def test_add_norm_refuses_another_device():
+    with FakeTensorMode():
+        args = dict(y=fake(BF16, 4, 64), residual=fake(F32, 4, 64), pre_table=fake(I64, 2),
+                    post_table=fake(I64, 2), gate=fake(BF16, 64), seg_offsets=fake(I32, 2),
+                    seg_variant=fake(I32, 1), residual_out=fake(F32, 4, 64), out=fake(BF16, 4, 64))
+        for name, t in args.items():
+            other = torch.empty(t.shape, dtype=t.dtype, device="cuda:1")
+            with pytest.raises(ValueError, match="another device"):
+                bd.bitdelta_add_norm(**{**args, name: other})
+
+
+class Batch:
+    """A batch whose tables, plan and workspace lie on a device."""
+
+    def __init__(self, device):
+        self._state = bd._BatchState(bd._AttentionBatch(4, 2, 2, 64, 8, 2, 128, 16, 0, 4), device)
+        self._ref = ctypes.addressof(self._state)
+        self._args = (self._ref, 0x100000, 1 << 40, 0x100000, 1 << 40)
+
+
+def test_append_and_attention_refuse_another_device():
+    with FakeTensorMode():
+        append = dict(qkv=fake(BF16, 4, 12 * 128), rope=fake(F32, 64, 128),
+                      k_pages=fake(BF16, 3, 2, 16, 128), v_pages=fake(BF16, 3, 2, 16, 128),
+                      out=fake(BF16, 4, 8, 128))
+        attention = dict(q=fake(BF16, 4, 8, 128), k_pages=append["k_pages"],
+                         v_pages=append["v_pages"], out=append["out"], lse=fake(F32, 4, 8))
+        for call, args in ((bd.bitdelta_kv_append, append), (bd.bitdelta_attention, attention)):
+            for name, t in args.items():
+                other = torch.empty(t.shape, dtype=t.dtype, device="cuda:1")
+                with pytest.raises(ValueError, match="another device"):
+                    call(Batch(0), **{**args, name: other})
+            with pytest.raises(ValueError, match="another device"):
+                call(Batch(1), **args)               # all but the batch on device 0
