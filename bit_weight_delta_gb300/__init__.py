@@ -674,9 +674,13 @@ class _AttentionBatch(ctypes.Structure):
                 ("group_offsets", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p)]
 
 
+_NO_STREAM = 2 ** 64 - 1
+
+
 class _BatchState(ctypes.Structure):
     """What csrc/binding.cpp reads of an AttentionBatch."""
-    _fields_ = [("c", _AttentionBatch), ("device", ctypes.c_int64)]
+    _fields_ = [("c", _AttentionBatch), ("device", ctypes.c_int64),
+                ("stream", ctypes.c_uint64)]      # that last used the tensors
 
 
 class AttentionBatch:
@@ -689,7 +693,9 @@ class AttentionBatch:
     constructor computes the plan (stream-ordered, on the device); it holds for
     every layer of the step.  After writing new lengths into the same tensors,
     call plan() again.  The batch owns one plan and workspace: attention calls
-    that can overlap on the GPU need batches of their own."""
+    that can overlap on the GPU need batches of their own.  Calls on another
+    stream than the plan's must be ordered after it; the batch may be dropped
+    while they are in flight (a graph that holds them needs it kept)."""
 
     def __init__(self, seq_offsets, kv_len, page_table, n_tokens: int, max_q_len: int,
                  max_kv_len: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
@@ -715,7 +721,7 @@ class AttentionBatch:
             n_tokens, n_seq, max_q_len, max_kv_len, n_q_heads, n_kv_heads, head_dim, page_size, 0,
             page_table.shape[1], seq_offsets.data_ptr(), kv_len.data_ptr(),
             page_table.data_ptr(), n_group, _addr(group_offsets), _addr(prefix_len)),
-            self._device.index)
+            self._device.index, _NO_STREAM)    # the lengths may be another stream's tensors
         self._ref = ctypes.addressof(self._state)
         lib = load()
         with torch.cuda.device(self._device):    # its SM count goes into the sizes
@@ -724,15 +730,21 @@ class AttentionBatch:
                 _empty(size(self._ref), self._device, stream)
                 for size in (lib.bitdelta_attention_plan_bytes,
                              lib.bitdelta_attention_workspace_bytes))
-        self._args = (self._ref, self._plan.data_ptr(), self._plan.numel(), self._ws.data_ptr(),
-                      self._ws.numel())
+        self._tensors = (self._plan, self._ws, *(t for t in self._keep if t is not None))
+        self._args = (self._ref, self._tensors, self._plan.data_ptr(), self._plan.numel(),
+                      self._ws.data_ptr(), self._ws.numel())
         self.plan(stream)
 
     def plan(self, stream=None) -> None:
         """Compute the plan from the lengths now in the batch's tensors."""
         with torch.cuda.device(self._device):
+            stream = _stream_on(stream, self._device)
             _check("bitdelta_attention_plan", load().bitdelta_attention_plan(
-                *self._args[:3], _stream_on(stream, self._device).cuda_stream))
+                self._ref, *self._args[2:4], stream.cuda_stream))
+        if self._state.stream != stream.cuda_stream:
+            for t in self._tensors:
+                t.record_stream(stream)
+            self._state.stream = stream.cuda_stream
 
 
 def bitdelta_kv_append(batch: AttentionBatch, qkv, rope, k_pages, v_pages,
@@ -746,7 +758,8 @@ def bitdelta_kv_append(batch: AttentionBatch, qkv, rope, k_pages, v_pages,
     if stream is not None:
         with torch.cuda.stream(_stream_on(stream, qkv.device)):
             return bitdelta_kv_append(batch, qkv, rope, k_pages, v_pages, interleaved, out)
-    r = (_native or _load_native()).kv_append(batch._ref, qkv, rope, k_pages, v_pages, interleaved, out)
+    r = (_native or _load_native()).kv_append(batch._ref, batch._tensors, qkv, rope, k_pages, v_pages,
+                                              interleaved, out)
     if type(r) is int:
         _check("bitdelta_kv_append", r)
     return r

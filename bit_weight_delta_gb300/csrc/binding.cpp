@@ -181,12 +181,27 @@ PyObject* add_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// A batch as the Python class holds it: the C struct and the device of its
-// tables, plan and workspace.
+// A batch as the Python class holds it: the C struct, the device of its tables,
+// plan and workspace, and the stream that last used them.
 struct Batch {
   bd_attention_batch c;
   int64_t device;
+  uint64_t stream;
 };
+
+// Tells the allocator that `stream` uses the batch's tensors too, so that their
+// memory is not handed out while work there is in flight, even where the batch
+// is dropped at once.  The caller cannot: plan and workspace are the batch's own.
+bd_stream_t used_by(Batch* b, PyObject* tensors, const at::Tensor& on) {
+  const c10::cuda::CUDAStream s = c10::cuda::getCurrentCUDAStream(on.device().index());
+  const uint64_t handle = reinterpret_cast<uint64_t>(s.stream());
+  if (b->stream != handle) {
+    for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(tensors); ++i)
+      THPVariable_Unpack(PyTuple_GET_ITEM(tensors, i)).record_stream(s);
+    b->stream = handle;
+  }
+  return reinterpret_cast<bd_stream_t>(s.stream());
+}
 
 // A call's cache: its shape goes into the batch's struct.
 struct Cache {
@@ -202,57 +217,61 @@ Cache cache_of(Tensors& in, Batch* b, PyObject* k_pages, PyObject* v_pages) {
   return {static_cast<uint16_t*>(kp.data_ptr()), static_cast<uint16_t*>(vp.data_ptr())};
 }
 
-// kv_append(batch, qkv, rope, k_pages, v_pages, interleaved, out) -> q, or a
-// status code.
+// kv_append(batch, its tensors, qkv, rope, k_pages, v_pages, interleaved, out) ->
+// q, or a status code.
 PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 7, [&]() -> PyObject* {
+  return guarded(n, 8, [&]() -> PyObject* {
     Batch* batch = static_cast<Batch*>(pointer(a[0]));
     const bd_attention_batch& b = batch->c;
     Tensors in{batch->device};
     const int64_t width = static_cast<int64_t>(b.n_q_heads + 2 * b.n_kv_heads) * b.head_dim;
-    const at::Tensor& qkv = in.shaped(a[1], at::kBFloat16, {b.n_tokens, width}, "qkv");
-    const at::Tensor* rope = in.maybe(a[2], at::kFloat, "rope");
+    const at::Tensor& qkv = in.shaped(a[2], at::kBFloat16, {b.n_tokens, width}, "qkv");
+    const at::Tensor* rope = in.maybe(a[3], at::kFloat, "rope");
     if (rope != nullptr && rope->dim() != 2) refuse("%s must be [positions, rot_dim]", "rope");
     const int64_t rows = rope != nullptr ? rope->size(0) : 0;
     const int64_t rot = rope != nullptr ? rope->size(1) : 0;
-    const bool pairs = PyObject_IsTrue(a[5]) == 1;
+    const bool pairs = PyObject_IsTrue(a[6]) == 1;
     const int64_t shape[3] = {b.n_tokens, b.n_q_heads, b.head_dim};
-    const at::Tensor* out = a[6] != Py_None ? &in.shaped(a[6], at::kBFloat16, shape, "out") : nullptr;
-    const Cache cache = cache_of(in, batch, a[3], a[4]);
+    const at::Tensor* out =
+        a[7] != Py_None ? &in.shaped(a[7], at::kBFloat16, shape, "out") : nullptr;
+    const Cache cache = cache_of(in, batch, a[4], a[5]);
     const c10::cuda::CUDAGuard guard(qkv.device());
     const at::Tensor q = out != nullptr ? *out : fresh(shape, at::kBFloat16, qkv);
     const bd_status st = g_kv_append(
         &b, static_cast<const uint16_t*>(qkv.data_ptr()), static_cast<const float*>(address(rope)),
         rows, static_cast<int32_t>(rot < INT32_MAX ? rot : INT32_MAX),
         pairs ? BD_ROPE_PAIRS : BD_ROPE_HALVES, cache.k, cache.v,
-        static_cast<uint16_t*>(q.data_ptr()), stream_of(qkv));
+        static_cast<uint16_t*>(q.data_ptr()), used_by(batch, a[1], qkv));
     if (st != BD_OK) return PyLong_FromLong(st);
     return THPVariable_Wrap(q);
   });
 }
 
-// attention(batch, plan, plan_bytes, workspace, workspace_bytes, q, k_pages,
-// v_pages, scale, out, lse) -> (out, lse), or a status code.
+// attention(batch, its tensors, plan, plan_bytes, workspace, workspace_bytes, q,
+// k_pages, v_pages, scale, out, lse) -> (out, lse), or a status code.
 PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 11, [&]() -> PyObject* {
+  return guarded(n, 12, [&]() -> PyObject* {
     Batch* batch = static_cast<Batch*>(pointer(a[0]));
     const bd_attention_batch& b = batch->c;
     Tensors in{batch->device};
     const int64_t shape[3] = {b.n_tokens, b.n_q_heads, b.head_dim};
     const at::IntArrayRef rows(shape, 2);
-    const at::Tensor& q = in.shaped(a[5], at::kBFloat16, shape, "q");
+    const at::Tensor& q = in.shaped(a[6], at::kBFloat16, shape, "q");
     const double scale =
-        a[8] == Py_None ? 1.0 / std::sqrt(static_cast<double>(b.head_dim)) : number(a[8]);
-    const at::Tensor* o_out = a[9] != Py_None ? &in.shaped(a[9], at::kBFloat16, shape, "out") : nullptr;
-    const at::Tensor* l_out = a[10] != Py_None ? &in.shaped(a[10], at::kFloat, rows, "lse") : nullptr;
-    const Cache cache = cache_of(in, batch, a[6], a[7]);
+        a[9] == Py_None ? 1.0 / std::sqrt(static_cast<double>(b.head_dim)) : number(a[9]);
+    const at::Tensor* o_out =
+        a[10] != Py_None ? &in.shaped(a[10], at::kBFloat16, shape, "out") : nullptr;
+    const at::Tensor* l_out =
+        a[11] != Py_None ? &in.shaped(a[11], at::kFloat, rows, "lse") : nullptr;
+    const Cache cache = cache_of(in, batch, a[7], a[8]);
     const c10::cuda::CUDAGuard guard(q.device());
     const at::Tensor out = o_out != nullptr ? *o_out : fresh(shape, at::kBFloat16, q);
     const at::Tensor lse = l_out != nullptr ? *l_out : fresh(rows, at::kFloat, q);
     const bd_status st = g_attention(
-        &b, pointer(a[1]), PyLong_AsSize_t(a[2]), static_cast<const uint16_t*>(q.data_ptr()),
+        &b, pointer(a[2]), PyLong_AsSize_t(a[3]), static_cast<const uint16_t*>(q.data_ptr()),
         cache.k, cache.v, static_cast<float>(scale), static_cast<uint16_t*>(out.data_ptr()),
-        static_cast<float*>(lse.data_ptr()), pointer(a[3]), PyLong_AsSize_t(a[4]), stream_of(q));
+        static_cast<float*>(lse.data_ptr()), pointer(a[4]), PyLong_AsSize_t(a[5]),
+        used_by(batch, a[1], q));
     if (st != BD_OK) return PyLong_FromLong(st);
     return two(out, lse);
   });

@@ -120,6 +120,19 @@ def test_a_stream_of_another_device(world):
             f(Stream(0x99, 0))
 
 
+def test_the_plans_stream_is_recorded(world):
+    """On every tensor of the batch: its memory outlives the work on that stream."""
+    lengths = dict(seq_offsets=Tensor(3), kv_len=Tensor(2), page_table=Tensor(2, 4),
+                   group_offsets=Tensor(2), prefix_len=Tensor(1))
+    b = bd.AttentionBatch(**lengths, n_tokens=4, max_q_len=2, max_kv_len=64, n_q_heads=8,
+                          n_kv_heads=2, head_dim=128, page_size=16)
+    every = [b._plan, b._ws, *lengths.values()]
+    assert len(b._tensors) == len(every) and all(x is y for x, y in zip(b._tensors, every))
+    assert all(t.recorded == [0x77] for t in every) and b._state.stream == 0x77
+    b.plan(Stream(0x99, 1))
+    assert all(t.recorded == [0x77, 0x99] for t in every) and b._state.stream == 0x99
+
+
 def fake(dtype, *shape, device=0):
     return torch.empty(shape, dtype=dtype, device=f"cuda:{device}")
 
@@ -141,7 +154,8 @@ class Batch:
     def __init__(self, device):
         self._state = bd._BatchState(bd._AttentionBatch(4, 2, 2, 64, 8, 2, 128, 16, 0, 4), device)
         self._ref = ctypes.addressof(self._state)
-        self._args = (self._ref, 0x100000, 1 << 40, 0x100000, 1 << 40)
+        self._tensors = ()
+        self._args = (self._ref, (), 0x100000, 1 << 40, 0x100000, 1 << 40)
 
 
 def test_append_and_attention_refuse_another_device():

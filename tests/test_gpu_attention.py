@@ -400,3 +400,41 @@ def test_one_token_everywhere():
         c.check(out, lse)
         want = c.vp[c.table[0, 0], 0, 0]
         assert torch.equal(out[0, 0], want)          # its own value, weight one
+
+
+def test_a_dropped_batch_keeps_its_memory_while_another_stream_works():
+    """The plan, the workspace and the tables belong to the stream that made them; a
+    batch that another stream uses is dropped while that stream still works, and the
+    first stream is not given their memory before it is done."""
+    c = Case([(1, 900), (100, 500)], 16, 2, 128, 16, seed=40)
+    want = c.run()
+    kv = torch.from_numpy(c.kv).cuda()
+    qkv = torch.zeros((c.t, 20 * 128), dtype=torch.bfloat16, device="cuda")
+    k2, v2 = c.kp.clone(), c.vp.clone()
+    # kernels loaded and outputs in hand: either would wait for the stream's work
+    out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+    q2 = bd.bitdelta_kv_append(c.batch, qkv, None, k2, v2)
+    side = torch.cuda.Stream()
+    for call in ("attention", "append"):
+        batch = bd.AttentionBatch(
+            torch.from_numpy(c.off).cuda(), kv.clone(), torch.from_numpy(c.table).cuda(),
+            n_tokens=c.t, max_q_len=100, max_kv_len=900, n_q_heads=16, n_kv_heads=2, head_dim=128,
+            page_size=16)
+        used = {t.data_ptr() for t in batch._tensors}
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(1_000_000_000)               # about half a second
+        if call == "attention":
+            bd.bitdelta_attention(batch, c.q, c.kp, c.vp, out=out, lse=lse, stream=side)
+        else:
+            bd.bitdelta_kv_append(batch, qkv, None, k2, v2, out=q2, stream=side)
+        done = side.record_event()
+        del batch
+        free = {b["address"] for seg in torch.cuda.memory_snapshot() for b in seg["blocks"]
+                if b["state"] == "inactive"}
+        assert not done.query(), "the stream was done too early to tell"
+        assert not used & free
+        side.synchronize()
+        if call == "attention":
+            assert torch.equal(want[0], out) and torch.equal(want[1], lse)
+    assert bd.bitdelta_check_error() == 0
