@@ -598,11 +598,16 @@ class KMergePool:
 def norm_table(weights):
     """Device array of pointers to bf16 [d] norm weights: slot 0 the base
     model's, slot v variant v's.  The returned tensor object keeps the weights
-    alive."""
+    alive and carries their length, which bitdelta_add_norm compares with its
+    rows' (pointers in a tensor of the caller's own are not checked)."""
     weights = [_dev(w, torch.bfloat16, "norm weight") for w in weights]
+    if not weights or any(w.numel() != weights[0].numel() or w.device != weights[0].device
+                          for w in weights):
+        raise ValueError("norm weights must be one or more, of one length and on one device")
     table = torch.tensor([w.data_ptr() for w in weights], dtype=torch.int64,
                          device=weights[0].device)
     table.weights = weights
+    table.norm_width = weights[0].numel()
     return table
 
 

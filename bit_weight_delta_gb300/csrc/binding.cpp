@@ -123,6 +123,22 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// Refuses a table of norm_table() whose weights are shorter than the rows: the
+// kernel would read past them.
+void check_width(PyObject* table, int64_t d, const char* name) {
+  static PyObject* const attribute = PyUnicode_InternFromString("norm_width");
+  PyObject* const width = PyObject_GetAttr(table, attribute);
+  if (width == nullptr) {  // pointers that the caller made
+    if (!PyErr_ExceptionMatches(PyExc_AttributeError)) throw Refused{};
+    PyErr_Clear();
+    return;
+  }
+  const int64_t have = PyLong_AsLongLong(width);
+  Py_DECREF(width);
+  if (have == -1 && PyErr_Occurred()) throw Refused{};
+  if (have < d) refuse("%s's weights are shorter than y's rows", name);
+}
+
 // add_norm(y, residual, pre_table, post_table, gate, scale, eps, seg_offsets,
 // seg_variant, residual_out, out) -> (h, x), or the status code of a refusal.
 PyObject* add_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -141,7 +157,9 @@ PyObject* add_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     if (a[2] == Py_None) refuse("%s is required", "pre_table");
     const at::Tensor& pre = in.get(a[2], at::kLong, "pre_table");
+    check_width(a[2], d, "pre_table");
     const at::Tensor* post = in.maybe(a[3], at::kLong, "post_table");
+    if (post != nullptr) check_width(a[3], d, "post_table");
     if (post != nullptr && post->numel() != pre.numel())
       refuse("pre_table and %s must have the same number of slots", "post_table");
     const at::Tensor* gate = in.maybe(a[4], at::kBFloat16, "gate");

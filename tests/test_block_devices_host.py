@@ -172,3 +172,20 @@ def test_append_and_attention_refuse_another_device():
                     call(Batch(0), **{**args, name: other})
             with pytest.raises(ValueError, match="another device"):
                 call(Batch(1), **args)               # all but the batch on device 0
+
+
+def test_norm_weights_shorter_than_a_row_are_refused():
+    """norm_table's length travels with the table; weights shorter than a row would be
+    read past their end."""
+    class Weight(Tensor):
+        dtype = torch.bfloat16
+
+    for weights in ([], [Weight(64), Weight(32)], [Weight(64), Weight(64, device=0)]):
+        with pytest.raises(ValueError):
+            bd.norm_table(weights)
+    with FakeTensorMode():
+        y, short, right = fake(BF16, 4, 64), fake(I64, 2), fake(I64, 2)
+        short.norm_width, right.norm_width = 32, 64
+        for kw in (dict(pre_table=short), dict(pre_table=right, post_table=short)):
+            with pytest.raises(ValueError, match="shorter"):
+                bd.bitdelta_add_norm(y, **kw)

@@ -175,3 +175,20 @@ def test_refusals():
         bd.bitdelta_add_norm(y, None, table, seg_variant=torch.zeros(1, dtype=torch.int32).cuda())
     with pytest.raises(bd.BitDeltaError):
         bd.bitdelta_add_norm(torch.ones((2, 12), dtype=torch.bfloat16, device="cuda"), None, table)
+
+
+def test_weights_shorter_than_a_row_are_refused():
+    ones = torch.ones(256, dtype=torch.bfloat16, device="cuda")
+    y = torch.ones((2, 256), dtype=torch.bfloat16, device="cuda")
+    right, short, long = (bd.norm_table([w, w]) for w in (ones, ones[:128], torch.cat([ones, ones])))
+    for pre, post in ((short, None), (right, short)):
+        with pytest.raises(ValueError):
+            bd.bitdelta_add_norm(y, None, pre, post_table=post)
+    with pytest.raises(ValueError):
+        bd.norm_table([ones, ones[:128]])
+    with pytest.raises(ValueError):
+        bd.norm_table([])
+    for table in (long, right.clone()):      # their first 256 elements; the caller's own pointers
+        h, x = bd.bitdelta_add_norm(y, None, table)
+        assert (h == 1).all()
+    assert bd.bitdelta_check_error() == 0
