@@ -650,12 +650,12 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtas) combine_kernel(const 
       o.z = fmaf(v.z, s, o.z);
       o.w = fmaf(v.w, s, o.w);
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l != 0.f ? 1.f / l : 0.f;  // (a NaN goes through)
     const int64_t at = static_cast<int64_t>(it.tok) * b.n_q_heads + kvh * g + row;
     reinterpret_cast<uint2*>(p.out + at * D)[d4] =
         make_uint2(pack_bf16x2_rn(o.x * inv, o.y * inv), pack_bf16x2_rn(o.z * inv, o.w * inv));
     if (d4 == 0 && p.lse != nullptr)
-      p.lse[at] = l > 0.f ? (ref + log2f(l)) * kLn2 : -INFINITY;
+      p.lse[at] = l != 0.f ? (ref + log2f(l)) * kLn2 : -INFINITY;
   }
 }
 

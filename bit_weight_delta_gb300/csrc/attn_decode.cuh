@@ -464,13 +464,13 @@ __device__ __forceinline__ void run(const CUtensorMap& tmap_k, const CUtensorMap
         const int64_t tok = r.tok0 + row / g;
         const int64_t at = tok * b.n_q_heads + cons.h * g + row % g;
         if (last) {
-          const float inv = l[m][e] > 0.f ? 1.f / l[m][e] : 0.f;
+          const float inv = l[m][e] != 0.f ? 1.f / l[m][e] : 0.f;  // (a NaN goes through)
           uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + at * D) + t4;
 #pragma unroll
           for (int n = 0; n < D / 8; ++n)
             dst[4 * n] = pack_bf16x2_rn(o[m][n][2 * e] * inv, o[m][n][2 * e + 1] * inv);
           if (t4 == 0 && p.lse != nullptr)
-            p.lse[at] = l[m][e] > 0.f ? (mref[m][e] + log2f(l[m][e])) * kLn2 : -INFINITY;
+            p.lse[at] = l[m][e] != 0.f ? (mref[m][e] + log2f(l[m][e])) * kLn2 : -INFINITY;
           continue;
         }
         int part_row = row;

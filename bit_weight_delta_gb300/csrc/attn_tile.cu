@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         o_phase ^= 1u;
         tc_fence_after();
       }
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = l != 0.f ? 1.f / l : 0.f;  // (a NaN goes through)
       const uint64_t inv2 = pack2(inv, inv);
       const int row_at = i * b.n_q_heads + row_head;  // the row's head in the tile's tokens
       const int64_t tile_at = static_cast<int64_t>(e.tok0) * b.n_q_heads + kvh * g;
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (e.slot >= 0)
           part_ml(p.ws + p.L.w_t_ml, slot, 2 * kHalfRows)[h * kHalfRows + r] = make_float2(mref, l);
         else if (p.lse != nullptr)
-          p.lse[tile_at + row_at] = l > 0.f ? (mref + log2f(l)) * kLn2 : -INFINITY;
+          p.lse[tile_at + row_at] = l != 0.f ? (mref + log2f(l)) * kLn2 : -INFINITY;
       }
       tc_fence_before();  // O has been read before the next piece's first P is signalled
     }

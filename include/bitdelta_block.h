@@ -151,7 +151,8 @@ bd_status bitdelta_attention_plan(const bd_attention_batch* batch, void* plan, s
  * (the logarithm of the softmax's denominator) or NULL.  Scores, softmax
  * statistics and sums in fp32; the softmax weights are rounded to bf16 for
  * the product with the values.  A row with no key (a negative position)
- * gives zeros and an lse of −inf.  Positions past a sequence's kv_len are
+ * gives zeros and an lse of −inf, a row whose query holds a NaN gives NaN in
+ * both.  Positions past a sequence's kv_len are
  * never read as values, whatever the page holds there; within kv_len, keys
  * and values are expected finite, and values below 2^57 (a row's sums are kept
  * relative to a score that may lie 2^40 below its largest).

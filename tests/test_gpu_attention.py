@@ -438,3 +438,28 @@ def test_a_dropped_batch_keeps_its_memory_while_another_stream_works():
         if call == "attention":
             assert torch.equal(want[0], out) and torch.equal(want[1], lse)
     assert bd.bitdelta_check_error() == 0
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_a_nan_query_gives_nan(dim):
+    """Output and lse of its rows alone; an lse of minus infinity is for rows without a
+    key.  Single tokens alone and in parts, prompts whole and cut, shared prefixes."""
+    batches = [([(1, 40), (1, 20011), (1, 300)], ()), ([(100, 300), (1, 50), (40, 9000)], ()),
+               ([(1, 512 + i) for i in range(1, 31)] + [(40, 600)], [(30, 512)])]
+    for lens, groups in batches:
+        c = Case(lens, 8, 2, dim, 16, groups=groups, seed=41)
+        want, want_l = c.run()
+        rows = [(int(c.off[s + 1]) - 1, 3 * s % 8) for s in range(len(lens))]
+        hit = torch.zeros((c.t, 8), dtype=torch.bool, device="cuda")
+        for t, h in rows:
+            c.q[t, h, 5] = NAN
+            hit[t, h] = True
+        out, lse = c.run()
+        assert out[hit].isnan().all() and lse[hit].isnan().all()
+        # a row's neighbours share its exchanges but not its values
+        ok = ~hit
+        assert torch.isfinite(out[ok].float()).all()
+        assert ((out[ok].float() - want[ok].float()).abs() <= 2.0 ** -7 * c.vp.float().nan_to_num(
+            0.0).abs().max()).all()
+        assert ((lse[ok] - want_l[ok]).abs() <= 2.0 ** -14 * (1 + want_l[ok].abs())).all()
+        assert bd.bitdelta_check_error() == 0
