@@ -3,8 +3,8 @@
 //
 // One CTA per token.  Every element moves once (QKV in, q and the cache rows
 // out), so the floor is those bytes over the HBM bandwidth; a decode step's
-// few tokens are bound by the chain of dependent loads token -> sequence ->
-// page -> store instead.  A thread owns one 16-element unit of a head (the
+// few tokens are bound by the chain of dependent loads lengths -> page ->
+// store instead.  A thread owns one 16-element unit of a head (the
 // two 8-element halves that rotate together, or 16 neighbours), keeps its
 // angle's cosines and sines in registers and walks over the heads with it.
 //
@@ -71,7 +71,7 @@ __device__ __forceinline__ void rotate_unit(uint4& lo, uint4& hi, const float (&
 // CTAs will take.
 template <bool kPairs, bool kAhead>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs p) {
-  __shared__ int s_seq;
+  __shared__ int s_seq, s_pos;
   const bd_attention_batch& b = p.b;
   const int64_t t = blockIdx.x;
   const int tid = threadIdx.x;
@@ -92,12 +92,23 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
       prefetch_l2(p.qkv + (t + p.ahead) * n_heads * b.head_dim, 2 * n_heads * b.head_dim);
   }
   __syncthreads();
-  for (int s = tid; s < b.n_seq; s += kAppendThreads)
-    if (b.seq_offsets[s] <= t && t < b.seq_offsets[s + 1]) s_seq = s;
-  __syncthreads();
+  // The token's sequence, by the thread that holds its offset, and the table's
+  // bounds: a table that breaks them appends nothing (in the same round of
+  // loads, which has the position as well).
+  int bad = 0;
+  for (int s = tid; s < b.n_seq; s += kAppendThreads) {
+    const int lo = b.seq_offsets[s], hi = b.seq_offsets[s + 1], kv = b.kv_len[s];
+    bad |= lo < 0 || hi < lo || hi > b.n_tokens || hi - lo > b.max_q_len || kv < 0 ||
+           kv > b.max_kv_len;
+    if (lo <= t && t < hi) {
+      s_seq = s;
+      s_pos = kv - (hi - static_cast<int>(t));
+    }
+  }
+  bad = __syncthreads_or(bad);
+  if (bad && tid == 0) record_error(p.ctx, kErrBounds);
   const int seq = s_seq;
-  int64_t pos = -1;
-  if (seq >= 0) pos = static_cast<int64_t>(b.kv_len[seq]) - (b.seq_offsets[seq + 1] - t);
+  const int64_t pos = seq >= 0 && !bad ? s_pos : -1;
   bool ok = pos >= 0;
   int64_t row0 = 0;  // the token's first cache row (head 0) in rows of head_dim
   if (ok) {

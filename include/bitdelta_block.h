@@ -124,7 +124,8 @@ typedef struct {
  * A token at a negative position (kv_len < q_len), or of no sequence, is
  * padding: its query is zero and nothing is appended.  A position past rope_rows or past the page
  * table's row, or a page outside [0, n_pages), sets BD_ERR_DEVICE_BOUNDS; the
- * query is then zero and nothing is appended for that token.
+ * query is then zero and nothing is appended for that token; a batch whose
+ * lengths break its bounds or are not sorted has zero queries and appends nothing.
  * rot_dim: a multiple of 16, 0 .. head_dim.
  */
 bd_status bitdelta_kv_append(const bd_attention_batch* batch, const uint16_t* qkv,

@@ -178,3 +178,31 @@ def test_refusals():
         bd.bitdelta_kv_append(batch, qkv, rope[:, :24].contiguous(), kp, vp)
     with pytest.raises(bd.BitDeltaError):     # rot_dim above head_dim
         bd.bitdelta_kv_append(batch, qkv, torch.cat([rope, rope], 1), kp, vp)
+
+
+@pytest.mark.parametrize("what", ["not sorted", "past the tokens", "negative offset", "max_q_len",
+                                  "max_kv_len", "negative length"])
+def test_lengths_that_break_the_batch_are_reported(what):
+    """As the batch says of all its calls: queries of zeros, nothing appended."""
+    batch, off, kv, table, qkv, rope, kp, vp = make([(2, 20), (1, 5), (4, 9)], 4, 2, 64, 16)
+    k0, v0 = kp.clone(), vp.clone()
+    offs, lens, most_q, most_kv = off.copy(), kv.copy(), 4, 20
+    if what == "not sorted":
+        offs[1:3] = [5, 3]                       # tokens 3 and 4 in two sequences
+    elif what == "past the tokens":
+        offs[3] = 8
+    elif what == "negative offset":
+        offs[0] = -1
+    elif what == "max_q_len":
+        most_q = 3
+    elif what == "max_kv_len":
+        most_kv = 19
+    else:
+        lens[1] = -5
+    b = bd.AttentionBatch(torch.from_numpy(offs).cuda(), torch.from_numpy(lens).cuda(),
+                          torch.from_numpy(table).cuda(), 7, most_q, most_kv, 4, 2, 64, 16)
+    assert bd.bitdelta_check_error() == 7        # of the plan
+    q = torch.full((7, 4, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    bd.bitdelta_kv_append(b, qkv, rope, kp, vp, out=q)
+    assert bd.bitdelta_check_error() == 7
+    assert (q == 0).all() and torch.equal(kp, k0) and torch.equal(vp, v0)
