@@ -655,7 +655,7 @@ def bitdelta_add_norm(y, residual=None, pre_table=None, post_table=None, gate=No
     pre_table / post_table come from norm_table(); with seg_offsets and
     seg_variant (int32, as in bitdelta_linear_grouped) a row takes its
     segment's variant's weights, else slot 0.  Rows of no segment are not
-    written.  residual: bf16 or fp32 (None: zero, h is then bf16); gate: bf16
+    written, nor any where the offsets are unsorted or past the rows.  residual: bf16 or fp32 (None: zero, h is then bf16); gate: bf16
     [d] or like y.  residual_out may be residual itself."""
     if stream is not None:
         with torch.cuda.stream(_stream_on(stream, y.device)):

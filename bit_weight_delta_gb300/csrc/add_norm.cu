@@ -92,7 +92,7 @@ __device__ __forceinline__ const uint16_t* weights_of(const uint16_t* const* tab
 template <int C, bool kF32, bool kAhead>
 __global__ void __launch_bounds__(1024, C == 1 ? 2 : 1) add_norm_kernel(const NormArgs p) {
   __shared__ float s_post[32], s_pre[32];
-  __shared__ int s_seg;
+  __shared__ int s_seg, s_bad;
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x;
   const int n8 = p.d >> 3;
@@ -137,11 +137,22 @@ __global__ void __launch_bounds__(1024, C == 1 ? 2 : 1) add_norm_kernel(const No
   // loads instead of a search of dependent ones.
   int slot = 0;
   if (p.seg_offsets != nullptr) {
-    if (tid == 0) s_seg = -1;
+    if (tid == 0) {
+      s_seg = -1;
+      s_bad = 0;
+    }
     __syncthreads();
-    for (int s = tid; s < p.n_seg; s += blockDim.x)
-      if (p.seg_offsets[s] <= row && row < p.seg_offsets[s + 1]) s_seg = s;
+    const int at = static_cast<int>(row), rows = static_cast<int>(p.M);
+    for (int s = tid; s < p.n_seg; s += blockDim.x) {
+      const int lo = p.seg_offsets[s], hi = p.seg_offsets[s + 1];
+      if (lo <= at && at < hi) s_seg = s;
+      if (lo < 0 || hi < lo || hi > rows) s_bad = 1;  // overlapping ones have no one variant
+    }
     __syncthreads();
+    if (s_bad != 0) {
+      if (tid == 0) record_error(p.ctx, kErrBounds);
+      return;
+    }
     if (s_seg < 0) return;  // a row of no segment
     slot = p.seg_variant[s_seg];
     if (slot < 0 || slot >= p.n_tab) {

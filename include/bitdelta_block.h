@@ -58,7 +58,9 @@ typedef enum { BD_ROPE_HALVES = 0, BD_ROPE_PAIRS = 1 } bd_rope_style;
  *                BD_ERR_DEVICE_BOUNDS and reads as ones.
  *   seg_offsets [n_seg+1], seg_variant [n_seg]   device int32, as in
  *                bitdelta_linear_grouped; both NULL with n_seg = 0: every row
- *                takes slot 0.  Rows of no segment are left alone.  A variant
+ *                takes slot 0.  Rows of no segment are left alone, and all rows
+ *                where the offsets decrease or leave [0, M], which sets
+ *                BD_ERR_DEVICE_BOUNDS.  A variant
  *                id outside [0, n_tab) sets BD_ERR_DEVICE_BOUNDS and reads as
  *                slot 0.
  *   x_out        bf16 [M, d], or NULL (then pre_table may be NULL).

@@ -192,3 +192,18 @@ def test_weights_shorter_than_a_row_are_refused():
         h, x = bd.bitdelta_add_norm(y, None, table)
         assert (h == 1).all()
     assert bd.bitdelta_check_error() == 0
+
+
+@pytest.mark.parametrize("cuts", [[0, 4, 2, 6], [0, 2, 4, 7], [-1, 2, 4, 6], [3, 2, 1, 0]])
+def test_malformed_segments_are_reported_and_write_nothing(cuts):
+    """Overlapping segments, one past the rows, one before them."""
+    table = bd.norm_table([torch.full((256,), i + 1.0, dtype=torch.bfloat16, device="cuda")
+                           for i in range(3)])
+    y = torch.ones((6, 256), dtype=torch.bfloat16, device="cuda")
+    h = torch.full((6, 256), 7.0, dtype=torch.bfloat16, device="cuda")
+    x = h.clone()
+    bd.bitdelta_add_norm(y, None, table, residual_out=h, out=x,
+                         seg_offsets=torch.tensor(cuts, dtype=torch.int32).cuda(),
+                         seg_variant=torch.tensor([0, 1, 2], dtype=torch.int32).cuda())
+    assert bd.bitdelta_check_error() == 7
+    assert (h == 7).all() and (x == 7).all()
