@@ -178,6 +178,7 @@ PyObject* add_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t n_seg = variant != nullptr ? variant->numel() : 0;
     if (offsets != nullptr && offsets->numel() != n_seg + 1)
       refuse("%s must have one entry more than seg_variant", "seg_offsets");
+    if (n_seg == 0) variant = offsets;  // no segments: an address that is not read
     const at::Tensor* h_out =
         a[9] != Py_None ? &in.shaped(a[9], rtype, y.sizes(), "residual_out") : nullptr;
     const at::Tensor* x_out =

@@ -207,3 +207,16 @@ def test_malformed_segments_are_reported_and_write_nothing(cuts):
                          seg_variant=torch.tensor([0, 1, 2], dtype=torch.int32).cuda())
     assert bd.bitdelta_check_error() == 7
     assert (h == 7).all() and (x == 7).all()
+
+
+def test_a_table_of_no_segments_writes_nothing():
+    """As in the grouped linear: not a refusal, and not the whole batch on slot 0."""
+    table = bd.norm_table([torch.ones(256, dtype=torch.bfloat16, device="cuda")])
+    y = torch.ones((6, 256), dtype=torch.bfloat16, device="cuda")
+    h = torch.full((6, 256), 7.0, dtype=torch.bfloat16, device="cuda")
+    x = h.clone()
+    bd.bitdelta_add_norm(y, None, table, residual_out=h, out=x,
+                         seg_offsets=torch.zeros(1, dtype=torch.int32).cuda(),
+                         seg_variant=torch.zeros(0, dtype=torch.int32).cuda())
+    assert (h == 7).all() and (x == 7).all()
+    assert bd.bitdelta_check_error() == 0
