@@ -747,7 +747,8 @@ bd_status bitdelta_attention(const bd_attention_batch* batch, void* plan, size_t
                              size_t workspace_bytes, bd_stream_t stream) {
   int st = bd::check_attention_batch(batch);
   if (st != BD_OK) return static_cast<bd_status>(st);
-  if (!(scale > 0.f) || std::isinf(scale)) return BD_ERR_INVALID_ARG;
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!(scale > 0.f) || std::isinf(scale_log2)) return BD_ERR_INVALID_ARG;
   if (batch->n_tokens == 0) return BD_OK;
   if (!q || !k_pages || !v_pages || !out || batch->n_pages < 1) return BD_ERR_INVALID_ARG;
   if (!plan || !workspace) return BD_ERR_WORKSPACE;
@@ -764,7 +765,7 @@ bd_status bitdelta_attention(const bd_attention_batch* batch, void* plan, size_t
   p.q = q;
   p.k_pages = k_pages;
   p.v_pages = v_pages;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale_log2 = scale_log2;
   p.out = out;
   p.lse = lse;
   return bd::run_attention(p, reinterpret_cast<cudaStream_t>(stream));

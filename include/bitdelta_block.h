@@ -164,7 +164,7 @@ bd_status bitdelta_attention_plan(const bd_attention_batch* batch, void* plan, s
  *   workspace    device memory of bitdelta_attention_workspace_bytes(batch)
  *                bytes on a 256-byte boundary.
  *   Calls that can overlap on the GPU need plans and workspaces of their own.
- * scale must be positive and finite.
+ * scale must be positive and at most 2^127 (times log2 e it has to be finite).
  */
 size_t bitdelta_attention_workspace_bytes(const bd_attention_batch* batch);
 bd_status bitdelta_attention(const bd_attention_batch* batch, void* plan, size_t plan_bytes,

@@ -147,3 +147,12 @@ def test_attention(lib):
     assert call(ws=0x100010) == MISALIGNED
     assert lib.bitdelta_attention_plan(base["b"], None, HUGE, None) == WORKSPACE
     assert lib.bitdelta_attention_plan(base["b"], 0x100010, HUGE, None) == MISALIGNED
+
+
+def test_attention_refuses_a_scale_that_overflows_in_base_2(lib):
+    """Scores are scaled by scale·log2(e) in fp32: infinite times a zero score is no number."""
+    b = batch()
+    for scale, status in ((2.0 ** 127, None), (3e38, INVALID), (2.5e38, INVALID)):
+        st = lib.bitdelta_attention(ctypes.addressof(b), GOOD, 16, GOOD, GOOD, GOOD, scale, GOOD,
+                                    None, GOOD, HUGE, None)
+        assert st == (WORKSPACE if status is None else status)    # 16 bytes hold no plan
