@@ -13,6 +13,7 @@ bf16 tensors are torch.bfloat16; the packed sign matrix is torch.uint8
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 
 import torch
@@ -639,6 +640,8 @@ def _load_native():
     global _native
     if _native is None:
         lib = load()
+        _build.build_binding()       # where it is missing or stale
+        importlib.invalidate_caches()
         from . import _binding as native
         native.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
             "bitdelta_add_norm", "bitdelta_kv_append", "bitdelta_attention")))

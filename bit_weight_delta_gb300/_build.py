@@ -1,5 +1,6 @@
 """In-tree build of libbitdelta.so (sm_103a) with nvcc, and of the Python binding
-of the decoder-block operators (_binding.so) with g++ on torch's headers.
+of the decoder-block operators (_binding.so) with g++ on torch's headers.  The
+library needs neither g++ nor torch's headers, and is built without them.
 
 Each .cu file compiles to an object in parallel, then nvcc links the shared
 library next to this file.  The CUDA runtime is linked statically; the driver
@@ -36,18 +37,17 @@ def _nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
-def _inputs_mtime() -> float:
-    paths = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + [BINDING_SOURCE]]
-    paths.append(os.path.join(INCLUDE, "bitdelta.h"))
-    paths.append(os.path.join(INCLUDE, "bitdelta_cache.h"))
-    paths.append(os.path.join(INCLUDE, "bitdelta_kmerge.h"))
-    paths.append(os.path.join(INCLUDE, "bitdelta_block.h"))
+def _current(out: str, sources, headers) -> bool:
+    """Whether `out` is newer than these files and this one."""
+    paths = [os.path.join(CSRC, f) for f in sources] + [os.path.join(INCLUDE, f) for f in headers]
     paths.append(os.path.abspath(__file__))
-    return max(os.path.getmtime(p) for p in paths)
+    return os.path.exists(out) and os.path.getmtime(out) >= max(map(os.path.getmtime, paths))
 
 
-def _build_binding() -> None:
+def build_binding(force: bool = False) -> str:
     import torch
+    if not force and _current(BINDING_PATH, [BINDING_SOURCE], ["bitdelta.h", "bitdelta_block.h"]):
+        return BINDING_PATH
     base = os.path.dirname(torch.__file__)
     lib = os.path.join(base, "lib")
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
@@ -59,16 +59,21 @@ def _build_binding() -> None:
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            os.path.join(CSRC, BINDING_SOURCE), "-o", tmp, "-L", lib, "-lc10", "-ltorch_cpu",
            "-ltorch_python", "-ltorch_cuda", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        raise RuntimeError(f"g++ is needed for {BINDING_SOURCE}: {e}") from e
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {BINDING_SOURCE}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    newest = _inputs_mtime()
-    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= newest
-                         for p in (LIB_PATH, BINDING_PATH)):
+    """The C library."""
+    if not force and _current(LIB_PATH, SOURCES + HEADERS,
+                              ["bitdelta.h", "bitdelta_cache.h", "bitdelta_kmerge.h",
+                               "bitdelta_block.h"]):
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     nvcc = _nvcc()
@@ -84,10 +89,8 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             print(r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(_build_binding)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
-        binding.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -97,6 +100,15 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     return LIB_PATH
 
 
+def build_all(force: bool = False, verbose_ptxas: bool = False) -> str:
+    """The library and the binding, side by side."""
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        binding = ex.submit(build_binding, force)
+        path = build(force, verbose_ptxas)
+        binding.result()
+    return path
+
+
 if __name__ == "__main__":
     import sys
-    print(build(force=True, verbose_ptxas="-v" in sys.argv))
+    print(build_all(force=True, verbose_ptxas="-v" in sys.argv))
