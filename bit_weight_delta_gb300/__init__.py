@@ -640,7 +640,7 @@ def _load_native():
     global _native
     if _native is None:
         lib = load()
-        _build.build_binding()       # where it is missing or stale
+        _build.build_binding()       # where it is missing, or not this torch's
         importlib.invalidate_caches()
         from . import _binding as native
         native.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (

@@ -22,6 +22,7 @@ BUILD_DIR = os.path.join(ROOT, "_build", "bitdelta")
 LIB_PATH = os.path.join(HERE, "libbitdelta.so")
 BINDING_PATH = os.path.join(HERE, "_binding.so")
 BINDING_SOURCE = "binding.cpp"
+BINDING_STAMP = os.path.join(BUILD_DIR, "binding.txt")  # what _binding.so was built for
 
 SOURCES = ["abi.cu", "compress.cu", "reconstruct.cu", "gemv.cu", "gemm_pair.cu", "cache.cu",
            "kmerge.cu", "similarity.cu", "monosoup.cu", "add_norm.cu", "kv_append.cu",
@@ -44,10 +45,26 @@ def _current(out: str, sources, headers) -> bool:
     return os.path.exists(out) and os.path.getmtime(out) >= max(map(os.path.getmtime, paths))
 
 
+def _binding_for() -> str:
+    """What a binary on torch's C++ classes is bound to."""
+    import torch
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+
+
+def _stamp() -> str:
+    try:
+        with open(BINDING_STAMP) as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
 def build_binding(force: bool = False) -> str:
     import torch
-    if not force and _current(BINDING_PATH, [BINDING_SOURCE], ["bitdelta.h", "bitdelta_block.h"]):
+    if not force and _stamp() == _binding_for() and _current(
+            BINDING_PATH, [BINDING_SOURCE], ["bitdelta.h", "bitdelta_block.h"]):
         return BINDING_PATH
+    os.makedirs(BUILD_DIR, exist_ok=True)
     base = os.path.dirname(torch.__file__)
     lib = os.path.join(base, "lib")
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
@@ -66,6 +83,8 @@ def build_binding(force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {BINDING_SOURCE}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING_PATH)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(_binding_for())
     return BINDING_PATH
 
 

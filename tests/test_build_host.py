@@ -1,10 +1,12 @@
 """What a build does without: the C library is built and loaded without g++ and
-torch's headers.  The compilers are stand-ins (no GPU needed)."""
+torch's headers; the binding is built again for another torch.  The compilers are
+stand-ins (no GPU needed)."""
 import os
 import subprocess
 import types
 
 import pytest
+import torch
 
 from bit_weight_delta_gb300 import _build
 
@@ -26,7 +28,8 @@ def compilers(tmp_path, monkeypatch):
     run.missing = set()
     monkeypatch.setattr(subprocess, "run", run)
     for name, value in (("BUILD_DIR", tmp_path / "objects"), ("LIB_PATH", tmp_path / "lib.so"),
-                        ("BINDING_PATH", tmp_path / "binding.so")):
+                        ("BINDING_PATH", tmp_path / "binding.so"),
+                        ("BINDING_STAMP", tmp_path / "objects" / "binding.txt")):
         monkeypatch.setattr(_build, name, str(value), raising=False)
     return types.SimpleNamespace(ran=ran, missing=run.missing)
 
@@ -46,3 +49,12 @@ def test_a_current_library_is_not_built_for_want_of_the_binding(compilers):
     assert compilers.ran == []
     _build.build_binding()
     assert compilers.ran == ["g++"]
+
+
+def test_the_binding_is_built_once_and_again_for_another_torch(compilers, monkeypatch):
+    for _ in range(2):
+        _build.build_all()
+    assert compilers.ran.count("g++") == 1
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    _build.build_all()
+    assert compilers.ran.count("g++") == 2 and compilers.ran.count("nvcc") == len(_build.SOURCES) + 1
