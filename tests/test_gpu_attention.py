@@ -463,3 +463,59 @@ def test_a_nan_query_gives_nan(dim):
             0.0).abs().max()).all()
         assert ((lse[ok] - want_l[ok]).abs() <= 2.0 ** -14 * (1 + want_l[ok].abs())).all()
         assert bd.bitdelta_check_error() == 0
+
+
+@pytest.mark.parametrize("what", ["single", "groups", "prompts", "tiles"])
+def test_more_sequences_and_tiles_than_the_plan_takes_at_once(what):
+    """The plan walks sequences and tiles 1024 at a time and carries its sums over."""
+    rng = np.random.default_rng(42)
+    groups = []
+    if what == "single":
+        lens = [(1, int(k)) for k in rng.integers(0, 40, 2500)]
+    elif what == "groups":
+        groups = [(9, 32)] * 150
+        lens = [(1, 33 + int(k)) for k in rng.integers(0, 40, 1350)]
+        lens += [(1, int(k)) for k in rng.integers(0, 40, 200)]
+    elif what == "prompts":
+        lens = [(1, int(k)) for k in rng.integers(1, 40, 2100)]
+        for s in (0, 1023, 1024, 1500, 2047, 2048, 2099):
+            lens[s] = (int(rng.integers(20, 200)), 200)
+    else:
+        lens = [(int(q), 30 + int(q)) for q in rng.integers(5, 9, 2200)]    # a tile each
+    n = len(lens)
+    c = Case(lens, 4, 1 if what == "tiles" else 2, 64, 16, groups=groups, seed=43, extra_tokens=2)
+    out, lse = c.run()
+    near = {s for k in (0, 1024, 2048, n) for s in range(k - 5, k + 5) if 0 <= s < n}
+    c.check(out, lse, seqs=sorted(near | set(range(0, n, 11))))
+    again, lse2 = c.run()
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("lens", [[(1, 100), (1, 64)], [(1, 100), (40, 64)]])
+@pytest.mark.parametrize("what", ["max_q_len", "max_kv_len", "not sorted", "past the tokens",
+                                  "narrow table", "groups"])
+def test_a_refused_table_writes_rows_without_keys(lens, what):
+    """Every row, in either kernel: nothing of the outputs is left as it was."""
+    groups = [(2, 16)] if what == "groups" else ()
+    c = Case(lens, 8, 2, 128, 16, groups=groups, seed=44)
+    over = {}
+    if what == "max_q_len":
+        over["max_q_len"] = max(q for q, _ in lens) - 1
+    elif what == "max_kv_len":
+        over["max_kv_len"] = 99
+    elif what == "not sorted":
+        c.off[1] = c.t + 1
+    elif what == "past the tokens":
+        c.off[2] += 1
+        over["max_q_len"] = 64
+    elif what == "narrow table":
+        c.table = np.ascontiguousarray(c.table[:, :6])
+    else:
+        over["group_offsets"] = torch.tensor([2, 0], dtype=torch.int32).cuda()
+    batch = c.make(**over)
+    assert bd.bitdelta_check_error() == 7
+    out = torch.full((c.t, 8, 128), NAN, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((c.t, 8), NAN, device="cuda")
+    bd.bitdelta_attention(batch, c.q, c.kp, c.vp, out=out, lse=lse)
+    assert (out == 0).all() and torch.isneginf(lse).all()
+    assert bd.bitdelta_check_error() == 0
