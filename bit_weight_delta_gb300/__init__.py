@@ -721,6 +721,8 @@ class AttentionBatch:
             n_group = _dev(prefix_len, torch.int32, "prefix_len").numel()
             if _dev(group_offsets, torch.int32, "group_offsets").numel() != n_group + 1:
                 raise ValueError("group_offsets must have one entry more than prefix_len")
+        if max(max_q_len, max_kv_len, n_q_heads, n_kv_heads, head_dim, page_size) >= 2 ** 31:
+            raise ValueError("the batch's bounds and head counts must fit 32 bits")
         self._keep = (seq_offsets, kv_len, page_table, group_offsets, prefix_len)
         self._device = kv_len.device
         if any(t is not None and t.device != self._device for t in self._keep):

@@ -133,6 +133,16 @@ def test_the_plans_stream_is_recorded(world):
     assert all(t.recorded == [0x77, 0x99] for t in every) and b._state.stream == 0x99
 
 
+def test_bounds_that_do_not_fit_the_struct(world):
+    """2^32 + 64 keys would be 64 of them to the library."""
+    sizes = [4, 2, 64, 8, 2, 128, 16]
+    for i in range(1, len(sizes)):
+        wrapped = sizes[:i] + [sizes[i] + 2 ** 32] + sizes[i + 1:]
+        with pytest.raises(ValueError, match="32 bits"):
+            bd.AttentionBatch(Tensor(3), Tensor(2), Tensor(2, 4), *wrapped)
+    assert world.calls == []
+
+
 def fake(dtype, *shape, device=0):
     return torch.empty(shape, dtype=dtype, device=f"cuda:{device}")
 
