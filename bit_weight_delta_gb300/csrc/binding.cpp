@@ -249,7 +249,8 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (rope != nullptr && rope->dim() != 2) refuse("%s must be [positions, rot_dim]", "rope");
     const int64_t rows = rope != nullptr ? rope->size(0) : 0;
     const int64_t rot = rope != nullptr ? rope->size(1) : 0;
-    const bool pairs = PyObject_IsTrue(a[6]) == 1;
+    const int pairs = PyObject_IsTrue(a[6]);
+    if (pairs < 0) throw Refused{};
     const int64_t shape[3] = {b.n_tokens, b.n_q_heads, b.head_dim};
     const at::Tensor* out =
         a[7] != Py_None ? &in.shaped(a[7], at::kBFloat16, shape, "out") : nullptr;
@@ -259,7 +260,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const bd_status st = g_kv_append(
         &b, static_cast<const uint16_t*>(qkv.data_ptr()), static_cast<const float*>(address(rope)),
         rows, static_cast<int32_t>(rot < INT32_MAX ? rot : INT32_MAX),
-        pairs ? BD_ROPE_PAIRS : BD_ROPE_HALVES, cache.k, cache.v,
+        pairs != 0 ? BD_ROPE_PAIRS : BD_ROPE_HALVES, cache.k, cache.v,
         static_cast<uint16_t*>(q.data_ptr()), used_by(batch, a[1], qkv));
     if (st != BD_OK) return PyLong_FromLong(st);
     return THPVariable_Wrap(q);

@@ -4,6 +4,7 @@ tensors, the library and the device guard are stand-ins)."""
 import contextlib
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 from torch._subclasses.fake_tensor import FakeTensorMode
@@ -199,3 +200,12 @@ def test_norm_weights_shorter_than_a_row_are_refused():
         for kw in (dict(pre_table=short), dict(pre_table=right, post_table=short)):
             with pytest.raises(ValueError, match="shorter"):
                 bd.bitdelta_add_norm(y, **kw)
+
+
+def test_an_argument_without_a_truth_value():
+    """Its own error, not a call that succeeds with an error set."""
+    with FakeTensorMode():
+        cache = fake(BF16, 3, 2, 16, 128)
+        with pytest.raises(ValueError, match="truth value"):
+            bd.bitdelta_kv_append(Batch(0), fake(BF16, 4, 12 * 128), None, cache, cache,
+                                  interleaved=np.zeros(2))
