@@ -616,19 +616,11 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream_on(stream, device):
-    """`stream`, or the device's current one; a stream of another device is refused."""
-    if stream is None:
-        return torch.cuda.current_stream(device)
+def _on(stream, device):
+    """`stream` as the current one; a stream of another device is refused."""
     if stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the call's tensors on {device}")
-    return stream
-
-
-def _empty(n: int, device, stream):
-    """n bytes that belong to the stream that will use them."""
-    with torch.cuda.stream(stream):
-        return torch.empty(n, dtype=torch.uint8, device=device)
+    return torch.cuda.stream(stream)
 
 
 _native = None
@@ -661,7 +653,7 @@ def bitdelta_add_norm(y, residual=None, pre_table=None, post_table=None, gate=No
     written, nor any where the offsets are unsorted or past the rows.  residual: bf16 or fp32 (None: zero, h is then bf16); gate: bf16
     [d] or like y.  residual_out may be residual itself."""
     if stream is not None:
-        with torch.cuda.stream(_stream_on(stream, y.device)):
+        with _on(stream, y.device):
             return bitdelta_add_norm(y, residual, pre_table, post_table, gate, scale, eps,
                                      seg_offsets, seg_variant, residual_out, out)
     r = (_native or _load_native()).add_norm(y, residual, pre_table, post_table, gate, scale, eps,
@@ -733,28 +725,33 @@ class AttentionBatch:
             page_table.data_ptr(), n_group, _addr(group_offsets), _addr(prefix_len)),
             self._device.index, _NO_STREAM)    # the lengths may be another stream's tensors
         self._ref = ctypes.addressof(self._state)
+        if stream is None:
+            self._make()
+        else:
+            with _on(stream, self._device):
+                self._make()
+
+    def _make(self) -> None:
         lib = load()
         with torch.cuda.device(self._device):    # its SM count goes into the sizes
-            stream = _stream_on(stream, self._device)
             self._plan, self._ws = (
-                _empty(size(self._ref), self._device, stream)
+                torch.empty(size(self._ref), dtype=torch.uint8, device=self._device)
                 for size in (lib.bitdelta_attention_plan_bytes,
                              lib.bitdelta_attention_workspace_bytes))
         self._tensors = (self._plan, self._ws, *(t for t in self._keep if t is not None))
         self._args = (self._ref, self._tensors, self._plan.data_ptr(), self._plan.numel(),
                       self._ws.data_ptr(), self._ws.numel())
-        self.plan(stream)
+        self.plan()
 
     def plan(self, stream=None) -> None:
         """Compute the plan from the lengths now in the batch's tensors."""
+        if stream is not None:
+            with _on(stream, self._device):
+                return self.plan()
+        handle = (_native or _load_native()).used_by_current_stream(self._ref, self._tensors)
         with torch.cuda.device(self._device):
-            stream = _stream_on(stream, self._device)
             _check("bitdelta_attention_plan", load().bitdelta_attention_plan(
-                self._ref, *self._args[2:4], stream.cuda_stream))
-        if self._state.stream != stream.cuda_stream:
-            for t in self._tensors:
-                t.record_stream(stream)
-            self._state.stream = stream.cuda_stream
+                self._ref, *self._args[2:4], handle))
 
 
 def bitdelta_kv_append(batch: AttentionBatch, qkv, rope, k_pages, v_pages,
@@ -766,7 +763,7 @@ def bitdelta_kv_append(batch: AttentionBatch, qkv, rope, k_pages, v_pages,
     rope: fp32 [positions, rot_dim], cosines then sines (None: no rotation);
     interleaved rotates neighbours (2i, 2i+1) instead of halves."""
     if stream is not None:
-        with torch.cuda.stream(_stream_on(stream, qkv.device)):
+        with _on(stream, qkv.device):
             return bitdelta_kv_append(batch, qkv, rope, k_pages, v_pages, interleaved, out)
     r = (_native or _load_native()).kv_append(batch._ref, batch._tensors, qkv, rope, k_pages, v_pages,
                                               interleaved, out)
@@ -781,7 +778,7 @@ def bitdelta_attention(batch: AttentionBatch, q, k_pages, v_pages, scale: float 
     Returns (out, lse): bf16 like q, and fp32 [n_tokens, n_q_heads].  scale
     defaults to 1/sqrt(head_dim)."""
     if stream is not None:
-        with torch.cuda.stream(_stream_on(stream, q.device)):
+        with _on(stream, q.device):
             return bitdelta_attention(batch, q, k_pages, v_pages, scale, out, lse)
     r = (_native or _load_native()).attention(*batch._args, q, k_pages, v_pages, scale, out, lse)
     if type(r) is int:

@@ -15,6 +15,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -211,15 +212,24 @@ struct Batch {
 // Tells the allocator that `stream` uses the batch's tensors too, so that their
 // memory is not handed out while work there is in flight, even where the batch
 // is dropped at once.  The caller cannot: plan and workspace are the batch's own.
-bd_stream_t used_by(Batch* b, PyObject* tensors, const at::Tensor& on) {
-  const c10::cuda::CUDAStream s = c10::cuda::getCurrentCUDAStream(on.device().index());
+bd_stream_t used_by_current_stream(Batch* b, PyObject* tensors) {
+  const c10::cuda::CUDAStream s =
+      c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(b->device));
   const uint64_t handle = reinterpret_cast<uint64_t>(s.stream());
   if (b->stream != handle) {
     for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(tensors); ++i)
-      THPVariable_Unpack(PyTuple_GET_ITEM(tensors, i)).record_stream(s);
+      c10::cuda::CUDACachingAllocator::recordStream(
+          THPVariable_Unpack(PyTuple_GET_ITEM(tensors, i)).storage().data_ptr(), s);
     b->stream = handle;
   }
   return reinterpret_cast<bd_stream_t>(s.stream());
+}
+
+// used_by_current_stream(batch, its tensors) -> the handle of that stream.
+PyObject* used(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 2, [&]() -> PyObject* {
+    return PyLong_FromVoidPtr(used_by_current_stream(static_cast<Batch*>(pointer(a[0])), a[1]));
+  });
 }
 
 // A call's cache: its shape goes into the batch's struct.
@@ -261,7 +271,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         &b, static_cast<const uint16_t*>(qkv.data_ptr()), static_cast<const float*>(address(rope)),
         rows, static_cast<int32_t>(rot < INT32_MAX ? rot : INT32_MAX),
         pairs != 0 ? BD_ROPE_PAIRS : BD_ROPE_HALVES, cache.k, cache.v,
-        static_cast<uint16_t*>(q.data_ptr()), used_by(batch, a[1], qkv));
+        static_cast<uint16_t*>(q.data_ptr()), used_by_current_stream(batch, a[1]));
     if (st != BD_OK) return PyLong_FromLong(st);
     return THPVariable_Wrap(q);
   });
@@ -291,7 +301,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         &b, pointer(a[2]), PyLong_AsSize_t(a[3]), static_cast<const uint16_t*>(q.data_ptr()),
         cache.k, cache.v, static_cast<float>(scale), static_cast<uint16_t*>(out.data_ptr()),
         static_cast<float*>(lse.data_ptr()), pointer(a[4]), PyLong_AsSize_t(a[5]),
-        used_by(batch, a[1], q));
+        used_by_current_stream(batch, a[1]));
     if (st != BD_OK) return PyLong_FromLong(st);
     return two(out, lse);
   });
@@ -305,6 +315,7 @@ constexpr PyCFunction as_function() {
 PyMethodDef methods[] = {
     {"bind", as_function<bind>(), METH_FASTCALL, nullptr},
     {"add_norm", as_function<add_norm>(), METH_FASTCALL, nullptr},
+    {"used_by_current_stream", as_function<used>(), METH_FASTCALL, nullptr},
     {"kv_append", as_function<kv_append>(), METH_FASTCALL, nullptr},
     {"attention", as_function<attention>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},

@@ -20,7 +20,7 @@ class Tensor:
 
     def __init__(self, *shape, device=1):
         self.shape, self.device = shape, torch.device("cuda", device)
-        self.recorded = []
+        self.recorded = []         # streams
 
     def numel(self):
         n = 1
@@ -37,9 +37,6 @@ class Tensor:
     def data_ptr(self):
         return 0x100000
 
-    def record_stream(self, stream):
-        self.recorded.append(stream.cuda_stream)
-
 
 class Stream:
     def __init__(self, handle, device):
@@ -47,10 +44,10 @@ class Stream:
 
 
 class World:
-    """The current device, and what the library was called with under which."""
+    """The current device and streams, and what the library was called with under which."""
 
     def __init__(self, monkeypatch):
-        self.current, self.calls = 0, []
+        self.current, self.streams, self.calls = 0, {0: 0x66, 1: 0x77}, []
 
         @contextlib.contextmanager
         def guard(device):
@@ -58,21 +55,38 @@ class World:
             yield
             self.current = before
 
+        @contextlib.contextmanager
+        def on(stream):
+            with guard(stream.device):
+                before = self.streams[self.current]
+                self.streams[self.current] = stream.cuda_stream
+                yield
+                self.streams[self.current] = before
+
         def call(name, result):
             def f(*args):
                 self.calls.append((name, self.current, args[-1]))
                 return result
             return f
 
+        def used_by_current_stream(ref, tensors):
+            stream = self.streams[bd._BatchState.from_address(ref).device]
+            for t in tensors:
+                t.recorded.append(stream)
+            return stream
+
         self.lib = type("Lib", (), {})()
         self.lib.bitdelta_attention_plan_bytes = call("plan_bytes", 512)
         self.lib.bitdelta_attention_workspace_bytes = call("workspace_bytes", 1024)
         self.lib.bitdelta_attention_plan = call("plan", 0)
+        native = type("Native", (), {})()
+        native.used_by_current_stream = used_by_current_stream
         monkeypatch.setattr(bd, "load", lambda *a: self.lib)
-        monkeypatch.setattr(bd, "_empty", lambda n, device, stream: Tensor(n, device=device.index))
+        monkeypatch.setattr(bd, "_native", native)
+        monkeypatch.setattr(torch, "empty",
+                            lambda n, dtype, device: Tensor(n, device=device.index))
         monkeypatch.setattr(torch.cuda, "device", guard)
-        monkeypatch.setattr(torch.cuda, "current_stream",
-                            lambda device=None: Stream(0x77, torch.device(device).index))
+        monkeypatch.setattr(torch.cuda, "stream", on)
 
 
 @pytest.fixture
@@ -129,9 +143,11 @@ def test_the_plans_stream_is_recorded(world):
                           n_kv_heads=2, head_dim=128, page_size=16)
     every = [b._plan, b._ws, *lengths.values()]
     assert len(b._tensors) == len(every) and all(x is y for x, y in zip(b._tensors, every))
-    assert all(t.recorded == [0x77] for t in every) and b._state.stream == 0x77
+    assert all(t.recorded == [0x77] for t in every)
     b.plan(Stream(0x99, 1))
-    assert all(t.recorded == [0x77, 0x99] for t in every) and b._state.stream == 0x99
+    assert all(t.recorded == [0x77, 0x99] for t in every)
+    b = batch(stream=Stream(0x55, 1))
+    assert all(t.recorded == [0x55] for t in b._tensors)
 
 
 def test_bounds_that_do_not_fit_the_struct(world):
