@@ -6,15 +6,22 @@
 //
 // One CTA per row, the row in registers as fp32 from the first load to the
 // last store, so every input is read once and every output written once:
-// the floor is those bytes over the HBM bandwidth.  The two sums of squares
-// are each one warp-shuffle reduction and one exchange through shared memory.
+// the floor is those bytes over the HBM bandwidth.  (Above 16384 elements a
+// little of the row, above 32768 about half of it, goes through local memory: a
+// thread has 64 registers.)  The two sums of squares are each one warp-shuffle
+// reduction and one exchange through shared memory.
 //
 // Measured: 2112 rows x 4096 with both norms, a gate and an fp32 residual (104
-// MB, 15.6 us at the copy rate) 18.2 us on repeated inputs and 22.1 us on
-// inputs that change (4.7 TB/s): each row's chain of load, sum, exchange, sum
-// and store leaves loads in flight for only part of a CTA's life.  8 rows x
-// 8192: 3.0 us on the GPU, bound by that chain.  Rows streamed through a ring
-// in shared memory by one persistent CTA per SM were slower at every size.
+// MB, 15.6 us at the copy rate) 17.7 us on repeated inputs and 22.2 us on
+// inputs that change (4.7 TB/s): behind its loads a row waits for its segment, the
+// segment's variant, that one's two table entries and, after the first sum, the
+// weights, with no other loads in flight, and 2112 rows are 3.5 rounds of CTAs.
+// 2048 bf16 rows of 8192 22.1 us (6.1 TB/s); 512 of 16384, 32768 and 65536 14.4,
+// 26.7 and 98.7 us (4.7, 5.0 and 2.7 TB/s; the last stores and loads another
+// 0.8 MB of local memory a row, more than the row's own 0.5).
+// 8 rows x 8192: 2.9 us on the GPU, bound by a row's chain.  Rows streamed
+// through a ring in shared memory by one persistent CTA per SM were slower at
+// every size.
 #include <cstdint>
 
 #include "bitdelta_block.h"

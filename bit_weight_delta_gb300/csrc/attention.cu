@@ -45,11 +45,12 @@ AttnLayout attn_layout(const bd_attention_batch& b, int num_sms) {
   if (max_rows > L.d_rows) L.max_tiles += T / tile_tok + long_seqs;
   const int64_t prefix_tiles = b.n_group > 0 ? T / tile_tok + b.n_group : 0;
   L.max_tiles += prefix_tiles;
-  // pieces: at most one per tile plus one per CTA of the launch (the plan cuts
-  // tiles longer than the CTAs' even share)
+  // pieces: at most one per tile plus two per CTA of the launch (the plan cuts
+  // tiles longer than the CTAs' even share, into shares or half shares)
   L.max_entries = L.use_tile ? L.max_tiles + 2 * L.t_ctas : 0;
-  // slots: the pieces of cut tiles (at most two per CTA), with groups every
-  // prefix piece and every own piece of a member
+  // slots: the pieces of cut tiles (a tile of more than one piece has at most
+  // twice its blocks' worth of them, so four per CTA), with groups every prefix
+  // piece and every own piece of a member
   L.t_slots = L.use_tile ? 4 * L.t_ctas + (b.n_group > 0 ? L.max_tiles * b.n_kv_heads : 0) : 0;
   size_t o = pad256(sizeof(PlanHeader));
   const auto take = [&](size_t bytes) {

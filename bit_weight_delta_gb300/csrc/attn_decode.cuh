@@ -3,11 +3,12 @@
 //
 // A run has at most 16·RT rows per key head (query tokens x query heads per
 // key head), so each key and value byte feeds few products and the kernel's
-// floor is reading the cache once.  The batch's keys, in units of 64, key head
-// by key head and sequence by sequence, are cut evenly over the CTAs; a run
-// cut between CTAs leaves partial results that the combine kernel joins.
+// floor is reading the cache once.  The batch's keys, in units of 16, key head
+// by key head and sequence by sequence, are cut evenly over the warps; a run
+// cut between them leaves partial results that the combine kernel joins.
 //
-// Within a CTA the warps (W of them) take 16-key tiles in turn, each from its own
+// Where a CTA's whole range lies in one run its warps (W of them) take the
+// run's 16-key tiles in turn; elsewhere each walks its own range.  A warp has its own
 // ring of stages that it fills itself by TMA (one box of 16 keys for K, one
 // for V, in the 128-byte swizzle), so warps never wait for one another but at
 // the end of a run.  Scores are mma.sync m16n8k16 products of the rows with 16

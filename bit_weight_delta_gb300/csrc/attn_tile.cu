@@ -26,8 +26,8 @@
 //
 // Measured (64 query and 8 key heads of 128): a prompt of 8192 tokens 690 us,
 // 1.59 PFLOP/s of the products that the mask leaves, with the tensor pipe busy
-// 74% of the time and the SM clock held down by power; one of 2048 tokens 55
-// to 60 us, 1.15 to 1.26 PFLOP/s: 512 pieces of 1 to 16 blocks leave a CTA three
+// 74% of the time and the SM clock held down by power; one of 2048 tokens 54.7
+// us on repeated inputs, 59.7 on inputs that change, 1.26 and 1.15 PFLOP/s: 512 pieces of 1 to 16 blocks leave a CTA three
 // or four changes of piece, a start of about 5 us and an uneven end.  A half's
 // 128·128 powers take the multifunction units half as long as its products take
 // the tensor core; the maximum, the scaling, the rounding and the moves to and

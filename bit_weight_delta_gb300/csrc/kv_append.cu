@@ -9,8 +9,9 @@
 // angle's cosines and sines in registers and walks over the heads with it.
 //
 // Measured: 4 prompts of 2048 tokens, 64 query and 8 key heads of 128 (340 MB)
-// 52.6 us, 6.45 TB/s; 64 single tokens and four chunks of 512, 32 query heads
-// (52 MB) 12.3 us; 8 single tokens 3.2 us (3.7 a call from the host).
+// 51.8 us, 6.57 TB/s; 64 single tokens and four chunks of 512, 32 query heads
+// (52 MB) 11.9 us: 2.8 rounds of CTAs, whose QKV loads come behind that chain;
+// 8 single tokens 2.7 us (3.6 a call from the host).
 #include <cstdint>
 
 #include "bitdelta_block.h"
@@ -214,10 +215,11 @@ extern "C" bd_status bitdelta_kv_append(const bd_attention_batch* batch, const u
   p.v_pages = v_pages;
   p.q_out = q_out;
   // Five CTAs of 48 registers a thread per SM.  From two rounds of them on, the
-  // fetch ahead keeps reads in flight while CTAs search, wait and store (4 x 2048
-  // tokens of 80 heads 58.9 -> 52.4 us, 2 x 1024 of 48 heads 12.3 -> 11.4); below
-  // it costs its instructions (512 tokens 5.6 -> 5.8 us, 8 tokens 3.2 -> 3.3).
-  // Distances of one, three and five CTAs per SM: 52.5, 52.7 and 53.6 us.
+  // fetch ahead keeps reads in flight while CTAs search, wait and store (in a
+  // graph, 4 x 2048 tokens of 80 heads 57.6 -> 51.5 us, 2 x 1024 of 48 heads 10.4
+  // -> 9.9); below it gives little (512 tokens 5.90 -> 5.84 us) or costs its
+  // instructions (8 tokens 2.65 -> 2.74).  Distances of one, three and five CTAs
+  // per SM: 51.6, 51.5 and 52.3 us.
   p.ahead = sms * 2;
   const bool ahead = batch->n_tokens >= 2 * 5 * static_cast<int64_t>(sms);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -2,8 +2,8 @@
  * bitdelta_block.h — the operators between a decoder block's delta linears
  * (include/bitdelta.h): the norms around a sub-block with its residual, the
  * rotary append of new keys and values to a paged cache, and the attention
- * that reads that cache.  With the linears they make a whole block of a
- * served model run in this library:
+ * that reads that cache.  With the linears they are all of a served model's
+ * block but the gated activation between its last two projections:
  *
  *   x            = bitdelta_add_norm                 (input norm)
  *   qkv          = bitdelta_linear_grouped(x)        (QKV projection)
@@ -162,7 +162,11 @@ bd_status bitdelta_attention_plan(const bd_attention_batch* batch, void* plan, s
  *   plan         as made by bitdelta_attention_plan for the same batch.  A call
  *                uses a counter in it and leaves it as it was.
  *   workspace    device memory of bitdelta_attention_workspace_bytes(batch)
- *                bytes on a 256-byte boundary.
+ *                bytes on a 256-byte boundary.  The host knows no lengths: with
+ *                groups, every 256-row tile that the batch may hold has an fp32
+ *                part per key head, and every token one (a group of 16 chunks of
+ *                512 tokens, 64 and 8 heads of 128, 937 MB; 64 single tokens in
+ *                two groups 108 MB; without groups 101 and 20 MB).
  *   Calls that can overlap on the GPU need plans and workspaces of their own.
  * scale must be positive and at most 2^127 (times log2 e it has to be finite).
  */
