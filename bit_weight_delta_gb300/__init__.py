@@ -53,6 +53,10 @@ BLOCK_EXPORTED = (
     "bitdelta_add_norm", "bitdelta_kv_append", "bitdelta_attention_plan_bytes",
     "bitdelta_attention_plan", "bitdelta_attention_workspace_bytes", "bitdelta_attention",
 )
+DECODE_EXPORTED = (
+    "bitdelta_sample", "bitdelta_kv_append_at", "bitdelta_kv_weigh", "bitdelta_kv_evict",
+    "bitdelta_kv_evict_lengths",
+)
 
 
 class BitDeltaError(RuntimeError):
@@ -147,7 +151,12 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.bitdelta_kv_append.argtypes = [p, p, p, i64, i32, st, p, p, p, p]
     lib.bitdelta_attention_plan.argtypes = [p, p, sz, p]
     lib.bitdelta_attention.argtypes = [p, p, sz, p, p, p, f32, p, p, p, sz, p]
-    for name in BLOCK_EXPORTED:
+    lib.bitdelta_sample.argtypes = [p, i64, i64, i64, p, p, p, p, p, p, p, p]
+    lib.bitdelta_kv_append_at.argtypes = [p, p, p, p, i64, i32, st, p, p, p, p]
+    lib.bitdelta_kv_weigh.argtypes = [p, p, p, p, f32, i32, p, p, p, p]
+    lib.bitdelta_kv_evict.argtypes = [p, p, i32, i32, p, p, p, p, p, p, p, p]
+    lib.bitdelta_kv_evict_lengths.argtypes = [p, p, p, p, p]
+    for name in BLOCK_EXPORTED + DECODE_EXPORTED:
         getattr(lib, name).restype = st
     for name in ("bitdelta_attention_plan_bytes", "bitdelta_attention_workspace_bytes"):
         getattr(lib, name).argtypes = [p]
@@ -636,7 +645,9 @@ def _load_native():
         importlib.invalidate_caches()
         from . import _binding as native
         native.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
-            "bitdelta_add_norm", "bitdelta_kv_append", "bitdelta_attention")))
+            "bitdelta_add_norm", "bitdelta_kv_append_at", "bitdelta_attention",
+            "bitdelta_kv_weigh", "bitdelta_kv_evict", "bitdelta_kv_evict_lengths",
+            "bitdelta_sample")))
         _native = native
     return _native
 
@@ -755,18 +766,21 @@ class AttentionBatch:
 
 
 def bitdelta_kv_append(batch: AttentionBatch, qkv, rope, k_pages, v_pages,
-                       interleaved: bool = False, out=None, stream=None):
+                       interleaved: bool = False, out=None, stream=None, pos_offset=None):
     """Rotates the query and key heads of qkv [n_tokens, (n_q_heads +
     2·n_kv_heads)·head_dim] by their tokens' positions, appends keys and values
     to the cache and returns the queries [n_tokens, n_q_heads, head_dim].
 
     rope: fp32 [positions, rot_dim], cosines then sines (None: no rotation);
-    interleaved rotates neighbours (2i, 2i+1) instead of halves."""
+    interleaved rotates neighbours (2i, 2i+1) instead of halves.  pos_offset: int32
+    [n_seq], what evictions took from the sequences: slot p's angle is that of
+    position p + pos_offset."""
     if stream is not None:
         with _on(stream, qkv.device):
-            return bitdelta_kv_append(batch, qkv, rope, k_pages, v_pages, interleaved, out)
+            return bitdelta_kv_append(batch, qkv, rope, k_pages, v_pages, interleaved, out,
+                                      pos_offset=pos_offset)
     r = (_native or _load_native()).kv_append(batch._ref, batch._tensors, qkv, rope, k_pages, v_pages,
-                                              interleaved, out)
+                                              interleaved, out, pos_offset)
     if type(r) is int:
         _check("bitdelta_kv_append", r)
     return r
@@ -783,4 +797,79 @@ def bitdelta_attention(batch: AttentionBatch, q, k_pages, v_pages, scale: float 
     r = (_native or _load_native()).attention(*batch._args, q, k_pages, v_pages, scale, out, lse)
     if type(r) is int:
         _check("bitdelta_attention", r)
+    return r
+
+
+# ------------------------------------------------------------------ end of a step
+
+
+def bitdelta_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None,
+                    prob=None, stream=None):
+    """A token per row of logits [M, V] (bf16; rows may be padded apart) from the
+    random numbers u (fp32 [M], in [0, 1)).  Returns (tokens int32 [M], prob fp32
+    [M]): prob is the token's probability among those that the cuts keep.
+
+    temperature (fp32, 0 takes the largest), top_k (int32, <= 0 off), top_p (fp32, >= 1
+    off) and min_p (fp32, <= 0 off) are per row, None for all rows without.  Tokens are
+    taken in the order of their logits, the largest first, equal ones by index."""
+    if stream is not None:
+        with _on(stream, logits.device):
+            return bitdelta_sample(logits, u, temperature, top_k, top_p, min_p, tokens, prob)
+    r = (_native or _load_native()).sample(logits, u, temperature, top_k, top_p, min_p, tokens,
+                                           prob)
+    if type(r) is int:
+        _check("bitdelta_sample", r)
+    return r
+
+
+def bitdelta_kv_weigh(batch: AttentionBatch, q, lse, k_pages, weights, positions, window: int = 0,
+                      pos_offset=None, scale: float | None = None, stream=None):
+    """Adds to weights (fp32 [n_pages, n_kv_heads, page_size]) what attention weight
+    each cached key got from the batch's queries, given the lse of bitdelta_attention;
+    the slots of the step's own tokens begin with it, and positions (int32, like
+    weights) gets theirs.  window: only each sequence's last so many query tokens count
+    (0: all).  pos_offset as in bitdelta_kv_append.  Returns (weights, positions)."""
+    if stream is not None:
+        with _on(stream, q.device):
+            return bitdelta_kv_weigh(batch, q, lse, k_pages, weights, positions, window, pos_offset,
+                                     scale)
+    r = (_native or _load_native()).kv_weigh(batch._ref, batch._tensors, q, lse, k_pages, weights,
+                                             positions, window, pos_offset, scale)
+    if type(r) is int:
+        _check("bitdelta_kv_weigh", r)
+    return r
+
+
+def bitdelta_kv_evict(batch: AttentionBatch, keep, k_pages, v_pages, weights, positions,
+                      recent: int = 0, sink: int = 0, pos_offset=None, weights_out=None,
+                      positions_out=None, stream=None):
+    """Cuts a layer's cache to keep (int32 [n_seq], negative: as it is) keys per
+    sequence and key head: the last `recent` positions, the first `sink` ones and the
+    heaviest others stay, and those in slots past the new length move into the freed
+    ones.  weights_out and positions_out default to the tables themselves; others get
+    all slots of the new lengths.  Once every layer is cut,
+    bitdelta_kv_evict_lengths sets the lengths.  Returns (weights_out, positions_out)."""
+    if stream is not None:
+        with _on(stream, k_pages.device):
+            return bitdelta_kv_evict(batch, keep, k_pages, v_pages, weights, positions, recent,
+                                     sink, pos_offset, weights_out, positions_out)
+    r = (_native or _load_native()).kv_evict(batch._ref, batch._tensors, keep, k_pages, v_pages,
+                                             weights, positions, recent, sink, pos_offset,
+                                             weights_out, positions_out)
+    if type(r) is int:
+        _check("bitdelta_kv_evict", r)
+    return r
+
+
+def bitdelta_kv_evict_lengths(batch: AttentionBatch, keep, kv_len, pos_offset, stream=None):
+    """The lengths after bitdelta_kv_evict: kv_len (int32 [n_seq], the batch's own tensor
+    or another) gets the new ones, pos_offset grows by what was dropped.  Call
+    batch.plan() before the next attention.  Returns (kv_len, pos_offset)."""
+    if stream is not None:
+        with _on(stream, kv_len.device):
+            return bitdelta_kv_evict_lengths(batch, keep, kv_len, pos_offset)
+    r = (_native or _load_native()).kv_evict_lengths(batch._ref, batch._tensors, keep, kv_len,
+                                                     pos_offset)
+    if type(r) is int:
+        _check("bitdelta_kv_evict_lengths", r)
     return r

@@ -26,7 +26,8 @@ BINDING_STAMP = os.path.join(BUILD_DIR, "binding.txt")  # what _binding.so was b
 
 SOURCES = ["abi.cu", "compress.cu", "reconstruct.cu", "gemv.cu", "gemm_pair.cu", "cache.cu",
            "kmerge.cu", "similarity.cu", "monosoup.cu", "add_norm.cu", "kv_append.cu",
-           "attention.cu", "attn_decode.cu", "attn_tile.cu"]
+           "attention.cu", "attn_decode.cu", "attn_tile.cu", "kv_weigh.cu", "kv_evict.cu",
+           "sample.cu"]
 HEADERS = ["common.cuh", "kernels.h", "gemm_common.cuh", "split_schedule.h", "attention.cuh", "attn_decode.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
@@ -62,7 +63,7 @@ def _stamp() -> str:
 def build_binding(force: bool = False) -> str:
     import torch
     if not force and _stamp() == _binding_for() and _current(
-            BINDING_PATH, [BINDING_SOURCE], ["bitdelta.h", "bitdelta_block.h"]):
+            BINDING_PATH, [BINDING_SOURCE], ["bitdelta.h", "bitdelta_block.h", "bitdelta_decode.h"]):
         return BINDING_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     base = os.path.dirname(torch.__file__)
@@ -92,7 +93,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     """The C library."""
     if not force and _current(LIB_PATH, SOURCES + HEADERS,
                               ["bitdelta.h", "bitdelta_cache.h", "bitdelta_kmerge.h",
-                               "bitdelta_block.h"]):
+                               "bitdelta_block.h", "bitdelta_decode.h"]):
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     nvcc = _nvcc()

@@ -1,4 +1,5 @@
-// binding.cpp — the Python calls of the decoder-block operators.
+// binding.cpp — the Python calls of the decoder-block operators and of those at the
+// end of a serving step.
 //
 // A decode step's calls take the GPU two to ten microseconds, less than their
 // argument checks, output allocations and ctypes marshalling took in Python
@@ -21,13 +22,17 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include "bitdelta_block.h"
+#include "bitdelta_decode.h"
 
 namespace {
 
 decltype(&bitdelta_add_norm) g_add_norm = nullptr;
-decltype(&bitdelta_kv_append) g_kv_append = nullptr;
+decltype(&bitdelta_kv_append_at) g_kv_append = nullptr;
 decltype(&bitdelta_attention) g_attention = nullptr;
+decltype(&bitdelta_kv_weigh) g_kv_weigh = nullptr;
+decltype(&bitdelta_kv_evict) g_kv_evict = nullptr;
+decltype(&bitdelta_kv_evict_lengths) g_kv_evict_lengths = nullptr;
+decltype(&bitdelta_sample) g_sample = nullptr;
 
 struct Refused {};  // a Python error has been set
 
@@ -77,6 +82,13 @@ double number(PyObject* o) {
   if (v == -1.0 && PyErr_Occurred()) throw Refused{};
   return v;
 }
+int32_t count(PyObject* o, const char* name) {
+  int over = 0;
+  const int64_t v = PyLong_AsLongLongAndOverflow(o, &over);
+  if (v == -1 && PyErr_Occurred()) throw Refused{};
+  if (over != 0 || v < 0 || v > INT32_MAX) refuse("%s must be 0 or more and fit 32 bits", name);
+  return static_cast<int32_t>(v);
+}
 void* pointer(PyObject* o) {
   void* p = PyLong_AsVoidPtr(o);
   if (p == nullptr && PyErr_Occurred()) throw Refused{};
@@ -114,12 +126,17 @@ PyObject* guarded(Py_ssize_t have, Py_ssize_t want, F f) {
   END_HANDLE_TH_ERRORS
 }
 
-// bind(add_norm, kv_append, attention): the entry points' addresses.
+// bind(add_norm, kv_append_at, attention, kv_weigh, kv_evict, kv_evict_lengths,
+// sample): the entry points' addresses.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 3, [&]() -> PyObject* {
+  return guarded(n, 7, [&]() -> PyObject* {
     g_add_norm = reinterpret_cast<decltype(g_add_norm)>(pointer(a[0]));
     g_kv_append = reinterpret_cast<decltype(g_kv_append)>(pointer(a[1]));
     g_attention = reinterpret_cast<decltype(g_attention)>(pointer(a[2]));
+    g_kv_weigh = reinterpret_cast<decltype(g_kv_weigh)>(pointer(a[3]));
+    g_kv_evict = reinterpret_cast<decltype(g_kv_evict)>(pointer(a[4]));
+    g_kv_evict_lengths = reinterpret_cast<decltype(g_kv_evict_lengths)>(pointer(a[5]));
+    g_sample = reinterpret_cast<decltype(g_sample)>(pointer(a[6]));
     Py_RETURN_NONE;
   });
 }
@@ -246,10 +263,15 @@ Cache cache_of(Tensors& in, Batch* b, PyObject* k_pages, PyObject* v_pages) {
   return {static_cast<uint16_t*>(kp.data_ptr()), static_cast<uint16_t*>(vp.data_ptr())};
 }
 
-// kv_append(batch, its tensors, qkv, rope, k_pages, v_pages, interleaved, out) ->
-// q, or a status code.
+// A tensor with an int32 for each of the batch's sequences.
+const int32_t* per_sequence(Tensors& in, const Batch* b, PyObject* o, const char* name) {
+  return static_cast<const int32_t*>(in.shaped(o, at::kInt, {b->c.n_seq}, name).data_ptr());
+}
+
+// kv_append(batch, its tensors, qkv, rope, k_pages, v_pages, interleaved, out,
+// pos_offset) -> q, or a status code.
 PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 8, [&]() -> PyObject* {
+  return guarded(n, 9, [&]() -> PyObject* {
     Batch* batch = static_cast<Batch*>(pointer(a[0]));
     const bd_attention_batch& b = batch->c;
     Tensors in{batch->device};
@@ -264,12 +286,14 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t shape[3] = {b.n_tokens, b.n_q_heads, b.head_dim};
     const at::Tensor* out =
         a[7] != Py_None ? &in.shaped(a[7], at::kBFloat16, shape, "out") : nullptr;
+    const int32_t* shift =
+        a[8] != Py_None ? per_sequence(in, batch, a[8], "pos_offset") : nullptr;
     const Cache cache = cache_of(in, batch, a[4], a[5]);
     const c10::cuda::CUDAGuard guard(qkv.device());
     const at::Tensor q = out != nullptr ? *out : fresh(shape, at::kBFloat16, qkv);
     const bd_status st = g_kv_append(
-        &b, static_cast<const uint16_t*>(qkv.data_ptr()), static_cast<const float*>(address(rope)),
-        rows, static_cast<int32_t>(rot < INT32_MAX ? rot : INT32_MAX),
+        &b, shift, static_cast<const uint16_t*>(qkv.data_ptr()),
+        static_cast<const float*>(address(rope)), rows, static_cast<int32_t>(rot < INT32_MAX ? rot : INT32_MAX),
         pairs != 0 ? BD_ROPE_PAIRS : BD_ROPE_HALVES, cache.k, cache.v,
         static_cast<uint16_t*>(q.data_ptr()), used_by_current_stream(batch, a[1]));
     if (st != BD_OK) return PyLong_FromLong(st);
@@ -307,6 +331,128 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// A tensor beside the cache's slots.
+void* beside(Tensors& in, const Batch* b, PyObject* o, at::ScalarType type, const char* name) {
+  return in.shaped(o, type, {b->c.n_pages, b->c.n_kv_heads, b->c.page_size}, name).data_ptr();
+}
+
+PyObject* pair_of(PyObject* a, PyObject* b) { return PyTuple_Pack(2, a, b); }
+
+// kv_weigh(batch, its tensors, q, lse, k_pages, weights, positions, window,
+// pos_offset, scale) -> (weights, positions), or a status code.
+PyObject* kv_weigh(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 10, [&]() -> PyObject* {
+    Batch* batch = static_cast<Batch*>(pointer(a[0]));
+    const bd_attention_batch& b = batch->c;
+    Tensors in{batch->device};
+    const int64_t shape[3] = {b.n_tokens, b.n_q_heads, b.head_dim};
+    const at::Tensor& q = in.shaped(a[2], at::kBFloat16, shape, "q");
+    const at::Tensor& lse = in.shaped(a[3], at::kFloat, at::IntArrayRef(shape, 2), "lse");
+    const Cache cache = cache_of(in, batch, a[4], a[4]);
+    void* weights = beside(in, batch, a[5], at::kFloat, "weights");
+    void* positions = beside(in, batch, a[6], at::kInt, "positions");
+    const int32_t window = count(a[7], "window");
+    const int32_t* shift =
+        a[8] != Py_None ? per_sequence(in, batch, a[8], "pos_offset") : nullptr;
+    const double scale =
+        a[9] == Py_None ? 1.0 / std::sqrt(static_cast<double>(b.head_dim)) : number(a[9]);
+    const c10::cuda::CUDAGuard guard(q.device());
+    const bd_status st = g_kv_weigh(
+        &b, static_cast<const uint16_t*>(q.data_ptr()), static_cast<const float*>(lse.data_ptr()),
+        cache.k, static_cast<float>(scale), window, shift, static_cast<float*>(weights),
+        static_cast<int32_t*>(positions), used_by_current_stream(batch, a[1]));
+    if (st != BD_OK) return PyLong_FromLong(st);
+    return pair_of(a[5], a[6]);
+  });
+}
+
+// kv_evict(batch, its tensors, keep, k_pages, v_pages, weights, positions, recent,
+// sink, pos_offset, weights_out, positions_out) -> (weights_out, positions_out), or a
+// status code.
+PyObject* kv_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 12, [&]() -> PyObject* {
+    Batch* batch = static_cast<Batch*>(pointer(a[0]));
+    Tensors in{batch->device};
+    const int32_t* keep = per_sequence(in, batch, a[2], "keep");
+    const Cache cache = cache_of(in, batch, a[3], a[4]);
+    const void* weights = beside(in, batch, a[5], at::kFloat, "weights");
+    const void* positions = beside(in, batch, a[6], at::kInt, "positions");
+    const int32_t recent = count(a[7], "recent"), sink = count(a[8], "sink");
+    const int32_t* shift =
+        a[9] != Py_None ? per_sequence(in, batch, a[9], "pos_offset") : nullptr;
+    PyObject* const w_out = a[10] != Py_None ? a[10] : a[5];
+    PyObject* const p_out = a[11] != Py_None ? a[11] : a[6];
+    void* weights_out = beside(in, batch, w_out, at::kFloat, "weights_out");
+    void* positions_out = beside(in, batch, p_out, at::kInt, "positions_out");
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(batch->device));
+    const bd_status st = g_kv_evict(
+        &batch->c, keep, recent, sink, shift, cache.k, cache.v, static_cast<const float*>(weights),
+        static_cast<const int32_t*>(positions), static_cast<float*>(weights_out),
+        static_cast<int32_t*>(positions_out), used_by_current_stream(batch, a[1]));
+    if (st != BD_OK) return PyLong_FromLong(st);
+    return pair_of(w_out, p_out);
+  });
+}
+
+// kv_evict_lengths(batch, its tensors, keep, kv_len, pos_offset) -> (kv_len,
+// pos_offset), or a status code.
+PyObject* kv_evict_lengths(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 5, [&]() -> PyObject* {
+    Batch* batch = static_cast<Batch*>(pointer(a[0]));
+    Tensors in{batch->device};
+    const int32_t* keep = per_sequence(in, batch, a[2], "keep");
+    const int32_t* len = per_sequence(in, batch, a[3], "kv_len");
+    const int32_t* shift = per_sequence(in, batch, a[4], "pos_offset");
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(batch->device));
+    const bd_status st = g_kv_evict_lengths(&batch->c, keep, const_cast<int32_t*>(len),
+                                            const_cast<int32_t*>(shift),
+                                            used_by_current_stream(batch, a[1]));
+    if (st != BD_OK) return PyLong_FromLong(st);
+    return pair_of(a[3], a[4]);
+  });
+}
+
+// sample(logits, u, temperature, top_k, top_p, min_p, tokens, prob) -> (tokens, prob),
+// or a status code.
+PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 8, [&]() -> PyObject* {
+    // (rows may be apart: a head's output padded to whole tiles)
+    if (!THPVariable_Check(a[0])) refuse("%s must be a tensor", "logits");
+    const at::Tensor& logits = THPVariable_Unpack(a[0]);
+    if (!logits.device().is_cuda()) refuse("%s must be a CUDA tensor", "logits");
+    if (logits.scalar_type() != at::kBFloat16) refuse("%s must be %s", "logits", "torch.bfloat16");
+    if (logits.dim() != 2 || logits.size(1) < 1) refuse("%s must be [rows, vocabulary]", "logits");
+    const int64_t rows = logits.size(0), vocab = logits.size(1);
+    if ((vocab > 1 && logits.stride(1) != 1) || (rows > 1 && logits.stride(0) < vocab))
+      refuse("%s must have neighbouring elements in a row, and rows apart", "logits");
+    Tensors in{logits.device().index()};
+    const auto setting = [&](PyObject* o, at::ScalarType type, const char* name) -> const void* {
+      return o == Py_None ? nullptr : in.shaped(o, type, {rows}, name).data_ptr();
+    };
+    const void* u = in.shaped(a[1], at::kFloat, {rows}, "u").data_ptr();
+    const void* temperature = setting(a[2], at::kFloat, "temperature");
+    const void* top_k = setting(a[3], at::kInt, "top_k");
+    const void* top_p = setting(a[4], at::kFloat, "top_p");
+    const void* min_p = setting(a[5], at::kFloat, "min_p");
+    const at::Tensor* t_out =
+        a[6] != Py_None ? &in.shaped(a[6], at::kInt, {rows}, "tokens") : nullptr;
+    const at::Tensor* p_out =
+        a[7] != Py_None ? &in.shaped(a[7], at::kFloat, {rows}, "prob") : nullptr;
+    const c10::cuda::CUDAGuard guard(logits.device());
+    const at::Tensor tokens = t_out != nullptr ? *t_out : fresh({rows}, at::kInt, logits);
+    const at::Tensor prob = p_out != nullptr ? *p_out : fresh({rows}, at::kFloat, logits);
+    const bd_status st = g_sample(
+        static_cast<const uint16_t*>(logits.data_ptr()), rows, vocab,
+        rows > 1 ? logits.stride(0) : vocab, static_cast<const float*>(u),
+        static_cast<const float*>(temperature), static_cast<const int32_t*>(top_k),
+        static_cast<const float*>(top_p), static_cast<const float*>(min_p),
+        static_cast<int32_t*>(tokens.data_ptr()), static_cast<float*>(prob.data_ptr()),
+        stream_of(logits));
+    if (st != BD_OK) return PyLong_FromLong(st);
+    return two(tokens, prob);
+  });
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 constexpr PyCFunction as_function() {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F));
@@ -318,6 +464,10 @@ PyMethodDef methods[] = {
     {"used_by_current_stream", as_function<used>(), METH_FASTCALL, nullptr},
     {"kv_append", as_function<kv_append>(), METH_FASTCALL, nullptr},
     {"attention", as_function<attention>(), METH_FASTCALL, nullptr},
+    {"kv_weigh", as_function<kv_weigh>(), METH_FASTCALL, nullptr},
+    {"kv_evict", as_function<kv_evict>(), METH_FASTCALL, nullptr},
+    {"kv_evict_lengths", as_function<kv_evict_lengths>(), METH_FASTCALL, nullptr},
+    {"sample", as_function<sample>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods,

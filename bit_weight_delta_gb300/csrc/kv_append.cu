@@ -1,5 +1,5 @@
 // kv_append.cu — rotary positions on a QKV row and the append of its keys and
-// values to the paged cache (bitdelta_kv_append).
+// values to the paged cache (bitdelta_kv_append, bitdelta_kv_append_at).
 //
 // One CTA per token.  Every element moves once (QKV in, q and the cache rows
 // out), so the floor is those bytes over the HBM bandwidth; a decode step's
@@ -14,7 +14,7 @@
 // 8 single tokens 2.7 us (3.6 a call from the host).
 #include <cstdint>
 
-#include "bitdelta_block.h"
+#include "bitdelta_decode.h"
 #include "kernels.h"
 
 namespace bd {
@@ -27,6 +27,7 @@ struct AppendArgs {
   int64_t rope_rows;
   int32_t rot_dim;
   uint16_t *k_pages, *v_pages, *q_out;
+  const int32_t* pos_offset;  // or null
   int32_t ahead;  // tokens
   DevCtx ctx;
 };
@@ -111,11 +112,13 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
   const int seq = s_seq;
   const int64_t pos = seq >= 0 && !bad ? s_pos : -1;
   bool ok = pos >= 0;
+  // the position that the angle goes by
+  const int64_t at = pos + (ok && p.pos_offset != nullptr ? p.pos_offset[seq] : 0);
   int64_t row0 = 0;  // the token's first cache row (head 0) in rows of head_dim
   if (ok) {
     const int64_t pg = pos / b.page_size;
     int64_t page = -1;
-    if (pg < b.table_stride && pos < p.rope_rows)
+    if (pg < b.table_stride && (p.rot_dim == 0 || (at >= 0 && at < p.rope_rows)))
       page = b.page_table[static_cast<int64_t>(seq) * b.table_stride + pg];
     if (page < 0 || page >= b.n_pages) {
       if (tid == 0) record_error(p.ctx, kErrBounds);
@@ -126,7 +129,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
   }
   float cs[8], sn[8];
   if (ok && u < rot_units) {
-    const float* r = p.rope + pos * p.rot_dim + 8 * u;
+    const float* r = p.rope + at * p.rot_dim + 8 * u;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const float4 c = reinterpret_cast<const float4*>(r)[j];
@@ -193,6 +196,16 @@ extern "C" bd_status bitdelta_kv_append(const bd_attention_batch* batch, const u
                                         const float* rope, int64_t rope_rows, int32_t rot_dim,
                                         bd_rope_style style, uint16_t* k_pages,
                                         uint16_t* v_pages, uint16_t* q_out, bd_stream_t stream) {
+  return bitdelta_kv_append_at(batch, nullptr, qkv, rope, rope_rows, rot_dim, style, k_pages,
+                               v_pages, q_out, stream);
+}
+
+extern "C" bd_status bitdelta_kv_append_at(const bd_attention_batch* batch,
+                                           const int32_t* pos_offset, const uint16_t* qkv,
+                                           const float* rope, int64_t rope_rows, int32_t rot_dim,
+                                           bd_rope_style style, uint16_t* k_pages,
+                                           uint16_t* v_pages, uint16_t* q_out,
+                                           bd_stream_t stream) {
   int st = bd::check_attention_batch(batch);
   if (st != BD_OK) return static_cast<bd_status>(st);
   if (style != BD_ROPE_HALVES && style != BD_ROPE_PAIRS) return BD_ERR_INVALID_ARG;
@@ -201,15 +214,16 @@ extern "C" bd_status bitdelta_kv_append(const bd_attention_batch* batch, const u
   if (batch->n_tokens == 0) return BD_OK;
   if (!qkv || !q_out || !k_pages || !v_pages || (rot_dim > 0 && !rope)) return BD_ERR_INVALID_ARG;
   if (bd::off(qkv, 16) || bd::off(q_out, 16) || bd::off(k_pages, 16) || bd::off(v_pages, 16) ||
-      bd::off(rope, 16))
+      bd::off(rope, 16) || bd::off(pos_offset, 4))
     return BD_ERR_MISALIGNED;
   bd::AppendArgs p{};
   int sms = 0;
   if ((st = bd::current_device_context(&p.ctx, &sms)) != BD_OK) return static_cast<bd_status>(st);
   p.b = *batch;
+  p.pos_offset = pos_offset;
   p.qkv = qkv;
   p.rope = rope;
-  p.rope_rows = rot_dim > 0 ? rope_rows : INT64_MAX;
+  p.rope_rows = rope_rows;
   p.rot_dim = rot_dim;
   p.k_pages = k_pages;
   p.v_pages = v_pages;
