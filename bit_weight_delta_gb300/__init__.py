@@ -54,8 +54,8 @@ BLOCK_EXPORTED = (
     "bitdelta_attention_plan", "bitdelta_attention_workspace_bytes", "bitdelta_attention",
 )
 DECODE_EXPORTED = (
-    "bitdelta_sample", "bitdelta_kv_append_at", "bitdelta_kv_weigh", "bitdelta_kv_evict",
-    "bitdelta_kv_evict_lengths",
+    "bitdelta_sample", "bitdelta_kv_append_at", "bitdelta_kv_weigh_workspace_bytes", "bitdelta_kv_weigh",
+    "bitdelta_kv_evict", "bitdelta_kv_evict_lengths",
 )
 
 
@@ -153,12 +153,13 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.bitdelta_attention.argtypes = [p, p, sz, p, p, p, f32, p, p, p, sz, p]
     lib.bitdelta_sample.argtypes = [p, i64, i64, i64, p, p, p, p, p, p, p, p]
     lib.bitdelta_kv_append_at.argtypes = [p, p, p, p, i64, i32, st, p, p, p, p]
-    lib.bitdelta_kv_weigh.argtypes = [p, p, p, p, f32, i32, p, p, p, p]
+    lib.bitdelta_kv_weigh.argtypes = [p, p, p, p, f32, i32, p, p, p, p, sz, p]
     lib.bitdelta_kv_evict.argtypes = [p, p, i32, i32, p, p, p, p, p, p, p, p]
     lib.bitdelta_kv_evict_lengths.argtypes = [p, p, p, p, p]
     for name in BLOCK_EXPORTED + DECODE_EXPORTED:
         getattr(lib, name).restype = st
-    for name in ("bitdelta_attention_plan_bytes", "bitdelta_attention_workspace_bytes"):
+    for name in ("bitdelta_attention_plan_bytes", "bitdelta_attention_workspace_bytes",
+                 "bitdelta_kv_weigh_workspace_bytes"):
         getattr(lib, name).argtypes = [p]
         getattr(lib, name).restype = sz
     _lib = lib
@@ -703,8 +704,8 @@ class AttentionBatch:
     consecutive sequences that share their first positions' pages.  The
     constructor computes the plan (stream-ordered, on the device); it holds for
     every layer of the step.  After writing new lengths into the same tensors,
-    call plan() again.  The batch owns one plan and workspace: attention calls
-    that can overlap on the GPU need batches of their own.  Calls on another
+    call plan() again.  The batch owns one plan and workspace: calls of bitdelta_attention
+    and bitdelta_kv_weigh that can overlap on the GPU need batches of their own.  Calls on another
     stream than the plan's must be ordered after it; the batch may be dropped
     while they are in flight (a graph that holds them needs it kept)."""
 
@@ -833,8 +834,8 @@ def bitdelta_kv_weigh(batch: AttentionBatch, q, lse, k_pages, weights, positions
         with _on(stream, q.device):
             return bitdelta_kv_weigh(batch, q, lse, k_pages, weights, positions, window, pos_offset,
                                      scale)
-    r = (_native or _load_native()).kv_weigh(batch._ref, batch._tensors, q, lse, k_pages, weights,
-                                             positions, window, pos_offset, scale)
+    r = (_native or _load_native()).kv_weigh(*batch._args, q, lse, k_pages, weights, positions,
+                                             window, pos_offset, scale)
     if type(r) is int:
         _check("bitdelta_kv_weigh", r)
     return r

@@ -26,9 +26,10 @@ BINDING_STAMP = os.path.join(BUILD_DIR, "binding.txt")  # what _binding.so was b
 
 SOURCES = ["abi.cu", "compress.cu", "reconstruct.cu", "gemv.cu", "gemm_pair.cu", "cache.cu",
            "kmerge.cu", "similarity.cu", "monosoup.cu", "add_norm.cu", "kv_append.cu",
-           "attention.cu", "attn_decode.cu", "attn_tile.cu", "kv_weigh.cu", "kv_evict.cu",
-           "sample.cu"]
-HEADERS = ["common.cuh", "kernels.h", "gemm_common.cuh", "split_schedule.h", "attention.cuh", "attn_decode.cuh"]
+           "attention.cu", "attn_decode.cu", "attn_tile.cu", "kv_weigh.cu",
+           "kv_weigh_tile.cu", "kv_evict.cu", "sample.cu"]
+HEADERS = ["common.cuh", "kernels.h", "gemm_common.cuh", "split_schedule.h", "attention.cuh", "attn_decode.cuh",
+           "tc_tile.cuh", "kv_weigh.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
               "-I", CSRC]

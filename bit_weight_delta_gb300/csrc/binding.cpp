@@ -338,31 +338,33 @@ void* beside(Tensors& in, const Batch* b, PyObject* o, at::ScalarType type, cons
 
 PyObject* pair_of(PyObject* a, PyObject* b) { return PyTuple_Pack(2, a, b); }
 
-// kv_weigh(batch, its tensors, q, lse, k_pages, weights, positions, window,
-// pos_offset, scale) -> (weights, positions), or a status code.
+// kv_weigh(batch, its tensors, plan, plan_bytes, workspace, workspace_bytes, q, lse,
+// k_pages, weights, positions, window, pos_offset, scale) -> (weights, positions), or
+// a status code.
 PyObject* kv_weigh(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 10, [&]() -> PyObject* {
+  return guarded(n, 14, [&]() -> PyObject* {
     Batch* batch = static_cast<Batch*>(pointer(a[0]));
     const bd_attention_batch& b = batch->c;
     Tensors in{batch->device};
     const int64_t shape[3] = {b.n_tokens, b.n_q_heads, b.head_dim};
-    const at::Tensor& q = in.shaped(a[2], at::kBFloat16, shape, "q");
-    const at::Tensor& lse = in.shaped(a[3], at::kFloat, at::IntArrayRef(shape, 2), "lse");
-    const Cache cache = cache_of(in, batch, a[4], a[4]);
-    void* weights = beside(in, batch, a[5], at::kFloat, "weights");
-    void* positions = beside(in, batch, a[6], at::kInt, "positions");
-    const int32_t window = count(a[7], "window");
+    const at::Tensor& q = in.shaped(a[6], at::kBFloat16, shape, "q");
+    const at::Tensor& lse = in.shaped(a[7], at::kFloat, at::IntArrayRef(shape, 2), "lse");
+    const Cache cache = cache_of(in, batch, a[8], a[8]);
+    void* weights = beside(in, batch, a[9], at::kFloat, "weights");
+    void* positions = beside(in, batch, a[10], at::kInt, "positions");
+    const int32_t window = count(a[11], "window");
     const int32_t* shift =
-        a[8] != Py_None ? per_sequence(in, batch, a[8], "pos_offset") : nullptr;
+        a[12] != Py_None ? per_sequence(in, batch, a[12], "pos_offset") : nullptr;
     const double scale =
-        a[9] == Py_None ? 1.0 / std::sqrt(static_cast<double>(b.head_dim)) : number(a[9]);
+        a[13] == Py_None ? 1.0 / std::sqrt(static_cast<double>(b.head_dim)) : number(a[13]);
     const c10::cuda::CUDAGuard guard(q.device());
     const bd_status st = g_kv_weigh(
         &b, static_cast<const uint16_t*>(q.data_ptr()), static_cast<const float*>(lse.data_ptr()),
         cache.k, static_cast<float>(scale), window, shift, static_cast<float*>(weights),
-        static_cast<int32_t*>(positions), used_by_current_stream(batch, a[1]));
+        static_cast<int32_t*>(positions), pointer(a[4]), PyLong_AsSize_t(a[5]),
+        used_by_current_stream(batch, a[1]));
     if (st != BD_OK) return PyLong_FromLong(st);
-    return pair_of(a[5], a[6]);
+    return pair_of(a[9], a[10]);
   });
 }
 

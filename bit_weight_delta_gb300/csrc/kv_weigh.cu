@@ -6,8 +6,10 @@
 // The attention has left each row's lse, so a weight needs no second pass: the
 // keys are read once and the values not at all.
 //
-// A run is a set of rows with the keys that they look at: a sequence's window of
-// query tokens over its own keys, or all of a group's over their shared prefix.
+// Runs of at most 16 rows (single tokens, as a rule) are this file's, whose time is
+// reading the keys; longer ones are kv_weigh_tile.cu's, on the tensor cores, whose
+// parts of blocks are joined here.
+//
 // A unit is 32 keys of a run and key head, worked on by one warp: the keys are the
 // rows of mma.sync tiles (16 keys by 8 query rows by 16 elements) and stay in
 // registers while the query rows pass, 8 at a time, so that a key's sum stays
@@ -17,37 +19,18 @@
 #include <cmath>
 #include <cstdint>
 
-#include "bitdelta_decode.h"
-#include "kernels.h"
+#include "attention.cuh"
+#include "kv_weigh.cuh"
 
 namespace bd {
 int check_attention_batch(const bd_attention_batch* b);
 
 namespace {
 
-struct WeighArgs {
-  bd_attention_batch b;
-  const uint16_t* q;
-  const float* lse;
-  const uint16_t* k_pages;
-  float scale_log2;
-  int32_t window;
-  const int32_t* pos_offset;
-  float* weights;
-  int32_t* positions;
-  DevCtx ctx;
-};
-
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnitKeys = 32;
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
+static_assert(kThreads == kWeighBlockKeys, "the join takes a key per thread");
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -58,82 +41,41 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-struct Run {
-  int seq;       // whose page-table row is read
-  int k0, k1;    // slots
-  int tok0, tok1;  // query tokens whose rows look at them
-  int causal;    // token t sees slots up to t + causal
-  int fresh;     // first slot of the step's own tokens
-  int units;     // per key head
+// A run with its units per key head: none where the tile kernel has it.
+struct Run : WeighRun {
+  int units;
 };
-
-// The prefix of sequence s (0 outside of every group); the groups are sorted.
-__device__ __forceinline__ int prefix_of(const bd_attention_batch& b, int s) {
-  int lo = 0, hi = b.n_group;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (b.group_offsets[mid + 1] <= s)
-      lo = mid + 1;
-    else
-      hi = mid;
-  }
-  return lo < b.n_group && b.group_offsets[lo] <= s ? b.prefix_len[lo] : 0;
-}
-
-// Run r: the sequences' own, then the groups'.
-__device__ Run run_of(const WeighArgs& p, int r) {
-  const bd_attention_batch& b = p.b;
+__device__ __forceinline__ Run run_of(const WeighArgs& p, int r) {
   Run x{};
-  if (r < b.n_seq) {
-    const int lo = b.seq_offsets[r], hi = b.seq_offsets[r + 1], kv = b.kv_len[r];
-    x.seq = r;
-    x.k0 = b.n_group > 0 ? prefix_of(b, r) : 0;
-    x.k1 = kv;
-    x.tok0 = p.window > 0 && hi - lo > p.window ? hi - p.window : lo;
-    x.tok1 = hi;
-    x.causal = kv - hi;
-    x.fresh = kv - (hi - lo);
-  } else {
-    const int g = r - b.n_seq, a = b.group_offsets[g], e = b.group_offsets[g + 1];
-    x.seq = a;
-    x.k1 = e > a ? b.prefix_len[g] : 0;
-    x.tok0 = e > a ? b.seq_offsets[a] : 0;
-    x.tok1 = e > a ? b.seq_offsets[e] : 0;
-    x.causal = 1 << 30;
-    x.fresh = INT32_MAX;
-  }
-  x.units = x.tok1 > x.tok0 && x.k1 > x.k0 ? (x.k1 - x.k0 + kUnitKeys - 1) / kUnitKeys : 0;
+  static_cast<WeighRun&>(x) = weigh_run(p, r);
+  const int64_t rows =
+      static_cast<int64_t>(x.tok1 - x.tok0) * (p.b.n_q_heads / p.b.n_kv_heads);
+  x.units = rows <= kWeighShortRows && x.k1 > x.k0 ? (x.k1 - x.k0 + kUnitKeys - 1) / kUnitKeys : 0;
   return x;
 }
 
-// Whether the batch's tables break their bounds (this thread's share of them).
-__device__ bool breaks_bounds(const WeighArgs& p) {
-  const bd_attention_batch& b = p.b;
-  bool bad = false;
-  for (int g = threadIdx.x; g < b.n_group; g += kThreads) {
-    const int a = b.group_offsets[g], e = b.group_offsets[g + 1], len = b.prefix_len[g];
-    bad |= a < 0 || e < a || e > b.n_seq || len < 0 || len % b.page_size != 0;
+// The blocks that several CTAs of the tile kernel share: their parts in their
+// order.
+__device__ void join_parts(const WeighArgs& p) {
+  const int n = 2 * p.tile_ctas;
+  for (int i = blockIdx.x; i < n; i += gridDim.x) {
+    const WeighRecord r = p.records[i];
+    if (!r.used || !r.begins) continue;
+    float a = p.parts[static_cast<int64_t>(i) * kWeighBlockKeys + threadIdx.x];
+    bool more = !r.ends;
+    for (int j = i + 1; more && j < n; ++j) {
+      const WeighRecord o = p.records[j];
+      if (!o.used) continue;
+      a += p.parts[static_cast<int64_t>(j) * kWeighBlockKeys + threadIdx.x];
+      more = !o.ends;
+    }
+    const WeighRun x = weigh_run(p, r.run);
+    const int key = x.k0 + r.block * kWeighBlockKeys + static_cast<int>(threadIdx.x);
+    if (key < x.k1) {
+      const int64_t row = weigh_row(p.b, x.seq, key, r.head);
+      if (row >= 0) weigh_add(p, x, key, row, a);
+    }
   }
-  for (int s = threadIdx.x; s < b.n_seq; s += kThreads) {
-    const int lo = b.seq_offsets[s], hi = b.seq_offsets[s + 1], kv = b.kv_len[s];
-    bad |= lo < 0 || hi < lo || hi > b.n_tokens || hi - lo > b.max_q_len || kv < 0 ||
-           kv > b.max_kv_len || kv > b.table_stride * b.page_size ||
-           (b.n_group > 0 && static_cast<int64_t>(kv) - (hi - lo) < prefix_of(b, s) &&
-            prefix_of(b, s) > 0);
-  }
-  return bad;
-}
-
-// Whether token t counts in the window of its sequence, one of [s0, s1).
-__device__ bool in_window(const WeighArgs& p, int t, int s0, int s1) {
-  while (s1 - s0 > 1) {
-    const int mid = (s0 + s1) >> 1;
-    if (p.b.seq_offsets[mid] <= t)
-      s0 = mid;
-    else
-      s1 = mid;
-  }
-  return p.b.seq_offsets[s0 + 1] - t <= p.window;
 }
 
 template <int D>
@@ -146,10 +88,11 @@ __global__ void __launch_bounds__(kThreads) kv_weigh_kernel(const WeighArgs p) {
   const int n_run = b.n_seq + b.n_group;
   griddep_wait();
   griddep_launch_dependents();
-  if (__syncthreads_or(breaks_bounds(p))) {
+  if (__syncthreads_or(weigh_breaks_bounds(p))) {
     if (tid == 0 && blockIdx.x == 0) record_error(p.ctx, kErrBounds);
     return;
   }
+  if (p.tile_ctas > 0) join_parts(p);
   // ---- an even share of all units for each warp
   int64_t mine = 0;
   for (int r = tid; r < n_run; r += kThreads) mine += run_of(p, r).units;
@@ -250,9 +193,9 @@ __global__ void __launch_bounds__(kThreads) kv_weigh_kernel(const WeighArgs p) {
             const float l = p.lse[static_cast<int64_t>(t) * b.n_q_heads + h * G + row % G];
             const bool counts =
                 !group || !windowed ||
-                in_window(p, t, x.seq, b.group_offsets[r0 + src - b.n_seq + 1]);
+                weigh_in_window(p, t, x.seq, b.group_offsets[r0 + src - b.n_seq + 1]);
             if (isfinite(l) && counts) {
-              lse[y] = l * kLog2e;
+              lse[y] = l * kWeighLog2e;
               sees[y] = group ? INT32_MAX : t + x.causal;
             }
           }
@@ -286,13 +229,7 @@ __global__ void __launch_bounds__(kThreads) kv_weigh_kernel(const WeighArgs p) {
       const int key = key0 + 16 * i + 8 * y + g8;
       const int64_t tile = i == 0 ? tile_row[0] : tile_row[1];
       if (key < x.k1 && tile >= 0) {
-        const int64_t row = tile + 8 * y + g8;
-        if (key >= x.fresh) {
-          p.weights[row] = a;
-          p.positions[row] = key + (p.pos_offset != nullptr ? p.pos_offset[x.seq] : 0);
-        } else {
-          p.weights[row] += a;
-        }
+        weigh_add(p, x, key, tile + 8 * y + g8, a);
       }
     }
     before = end;
@@ -301,25 +238,77 @@ __global__ void __launch_bounds__(kThreads) kv_weigh_kernel(const WeighArgs p) {
 
 bool off(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) != 0; }
 
+// Whether a batch may hold runs of the tile kernel.
+bool may_tile(const bd_attention_batch& b) {
+  return b.n_group > 0 ||
+         static_cast<int64_t>(b.max_q_len) * (b.n_q_heads / b.n_kv_heads) > kWeighShortRows;
+}
+size_t records_bytes(int ctas) {
+  return (sizeof(WeighRecord) * 2 * static_cast<size_t>(ctas) + 255) / 256 * 256;
+}
+size_t workspace_bytes(int ctas) {
+  return records_bytes(ctas) + sizeof(float) * 2 * static_cast<size_t>(ctas) * kWeighBlockKeys;
+}
+
+bd_status run_weigh(WeighArgs& p, int sms, cudaStream_t s) {
+  const bd_attention_batch& b = p.b;
+  if (p.tile_ctas > 0) {
+    const uint64_t D = static_cast<uint64_t>(b.head_dim), H = static_cast<uint64_t>(b.n_q_heads);
+    const int g = b.n_q_heads / b.n_kv_heads;
+    const uint64_t rows =
+        static_cast<uint64_t>(b.n_pages) * b.n_kv_heads * static_cast<uint64_t>(b.page_size);
+    const uint64_t kdims[3] = {64, rows, D / 64}, kstr[2] = {2 * D, 128};
+    const uint32_t kbox[3] = {64, static_cast<uint32_t>(b.page_size), 1};
+    const uint64_t qdims[3] = {D, H, static_cast<uint64_t>(b.n_tokens)};
+    const uint64_t qstr[2] = {2 * D, 2 * D * H};
+    const uint32_t qbox[3] = {64, static_cast<uint32_t>(g),
+                              static_cast<uint32_t>(weigh_tile_tokens(g))};
+    WeighMaps m;
+    if (!encode_tmap_bf16_3d(&m.k, p.k_pages, kdims, kstr, kbox) ||
+        !encode_tmap_bf16_3d(&m.q, p.q, qdims, qstr, qbox))
+      return BD_ERR_CUDA;
+    if (launch_weigh_tile(p, m, s) != cudaSuccess) return BD_ERR_CUDA;
+  }
+  const dim3 grid(2 * sms), block(kThreads);
+  const cudaError_t e = b.head_dim == 128
+                            ? launch_pdl(kv_weigh_kernel<128>, grid, block, 0, s, p)
+                            : launch_pdl(kv_weigh_kernel<64>, grid, block, 0, s, p);
+  return e == cudaSuccess ? BD_OK : BD_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace bd
 
-extern "C" bd_status bitdelta_kv_weigh(const bd_attention_batch* batch, const uint16_t* q,
-                                       const float* lse, const uint16_t* k_pages, float scale,
-                                       int32_t window, const int32_t* pos_offset, float* weights,
-                                       int32_t* positions, bd_stream_t stream) {
+extern "C" {
+
+size_t bitdelta_kv_weigh_workspace_bytes(const bd_attention_batch* batch) {
+  if (bd::check_attention_batch(batch) != BD_OK) return 0;
+  bd::DevCtx ctx;
+  int sms = 0;
+  if (bd::current_device_context(&ctx, &sms) != BD_OK) sms = 152;
+  return bd::workspace_bytes(sms);
+}
+
+bd_status bitdelta_kv_weigh(const bd_attention_batch* batch, const uint16_t* q, const float* lse,
+                            const uint16_t* k_pages, float scale, int32_t window,
+                            const int32_t* pos_offset, float* weights, int32_t* positions,
+                            void* workspace, size_t workspace_bytes, bd_stream_t stream) {
   int st = bd::check_attention_batch(batch);
   if (st != BD_OK) return static_cast<bd_status>(st);
-  const float scale_log2 = scale * bd::kLog2e;
+  const float scale_log2 = scale * bd::kWeighLog2e;
   if (!(scale > 0.f) || std::isinf(scale_log2) || window < 0) return BD_ERR_INVALID_ARG;
   if (batch->n_tokens == 0 || batch->n_seq == 0) return BD_OK;
-  if (!q || !lse || !k_pages || !weights || !positions) return BD_ERR_INVALID_ARG;
+  if (!q || !lse || !k_pages || !weights || !positions || batch->n_pages < 1)
+    return BD_ERR_INVALID_ARG;
+  if (!workspace) return BD_ERR_WORKSPACE;
   if (bd::off(q, 16) || bd::off(lse, 4) || bd::off(k_pages, 16) || bd::off(pos_offset, 4) ||
-      bd::off(weights, 4) || bd::off(positions, 4))
+      bd::off(weights, 4) || bd::off(positions, 4) || bd::off(workspace, 256))
     return BD_ERR_MISALIGNED;
+  if (workspace_bytes < 256) return BD_ERR_WORKSPACE;  // no workspace is smaller
   bd::WeighArgs p{};
   int sms = 0;
   if ((st = bd::current_device_context(&p.ctx, &sms)) != BD_OK) return static_cast<bd_status>(st);
+  if (workspace_bytes < bd::workspace_bytes(sms)) return BD_ERR_WORKSPACE;
   p.b = *batch;
   p.q = q;
   p.lse = lse;
@@ -329,10 +318,10 @@ extern "C" bd_status bitdelta_kv_weigh(const bd_attention_batch* batch, const ui
   p.pos_offset = pos_offset;
   p.weights = weights;
   p.positions = positions;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const dim3 grid(2 * sms), block(bd::kThreads);
-  const cudaError_t e = batch->head_dim == 128
-                            ? bd::launch_pdl(bd::kv_weigh_kernel<128>, grid, block, 0, s, p)
-                            : bd::launch_pdl(bd::kv_weigh_kernel<64>, grid, block, 0, s, p);
-  return e == cudaSuccess ? BD_OK : BD_ERR_CUDA;
+  p.tile_ctas = bd::may_tile(*batch) ? sms : 0;
+  p.records = static_cast<bd::WeighRecord*>(workspace);
+  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + bd::records_bytes(sms));
+  return bd::run_weigh(p, sms, reinterpret_cast<cudaStream_t>(stream));
 }
+
+}  // extern "C"

@@ -85,16 +85,20 @@ bd_status bitdelta_kv_append_at(const bd_attention_batch* batch, const int32_t* 
  * that the batch alone decides.
  *   pos_offset   device int32 [n_seq]: tokens that evictions took from the
  *                sequence; NULL: 0.
+ *   workspace    device memory of bitdelta_kv_weigh_workspace_bytes(batch) bytes
+ *                (0.3 MB) on a 256-byte boundary.  Calls that can overlap on the
+ *                GPU need workspaces of their own.
  * A batch whose tables break its bounds, or a group with a prefix_len that is
  * not a multiple of page_size or reaches into a member's query tokens, sets
  * BD_ERR_DEVICE_BOUNDS and changes nothing; a page outside [0, n_pages) sets it and
  * is skipped.  Two sequences that share a page outside of a group are not
  * supported (the page would have two writers).
  */
+size_t bitdelta_kv_weigh_workspace_bytes(const bd_attention_batch* batch);
 bd_status bitdelta_kv_weigh(const bd_attention_batch* batch, const uint16_t* q, const float* lse,
                             const uint16_t* k_pages, float scale, int32_t window,
                             const int32_t* pos_offset, float* weights, int32_t* positions,
-                            bd_stream_t stream);
+                            void* workspace, size_t workspace_bytes, bd_stream_t stream);
 
 /*
  * Eviction: a sequence of more than keep[s] keys goes down to
