@@ -45,9 +45,9 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
 struct Run : WeighRun {
   int units;
 };
-__device__ __forceinline__ Run run_of(const WeighArgs& p, int r) {
+__device__ __forceinline__ Run run_of(const WeighArgs& p, int r, bool* bad) {
   Run x{};
-  static_cast<WeighRun&>(x) = weigh_run(p, r);
+  static_cast<WeighRun&>(x) = weigh_run(p, r, bad);
   const int64_t rows =
       static_cast<int64_t>(x.tok1 - x.tok0) * (p.b.n_q_heads / p.b.n_kv_heads);
   x.units = rows <= kWeighShortRows && x.k1 > x.k0 ? (x.k1 - x.k0 + kUnitKeys - 1) / kUnitKeys : 0;
@@ -69,11 +69,12 @@ __device__ void join_parts(const WeighArgs& p) {
       a += p.parts[static_cast<int64_t>(j) * kWeighBlockKeys + threadIdx.x];
       more = !o.ends;
     }
-    const WeighRun x = weigh_run(p, r.run);
+    bool bad = false;  // (the kernel that left the parts has looked)
+    const WeighRun x = weigh_run(p, r.run, &bad);
     const int key = x.k0 + r.block * kWeighBlockKeys + static_cast<int>(threadIdx.x);
     if (key < x.k1) {
       const int64_t row = weigh_row(p.b, x.seq, key, r.head);
-      if (row >= 0) weigh_add(p, x, key, row, a);
+      if (row >= 0) weigh_add(p, x.seq, x.fresh, key, row, a);
     }
   }
 }
@@ -86,23 +87,23 @@ __global__ void __launch_bounds__(kThreads) kv_weigh_kernel(const WeighArgs p) {
   const int H = b.n_kv_heads;
   const uint32_t G = b.n_q_heads / H;
   const int n_run = b.n_seq + b.n_group;
-  griddep_wait();
+  // The tile kernel ahead, where there is one, lets this one start only when it has
+  // seen all before it complete: the units here need nothing of it, and run while
+  // its last CTAs do.
+  if (p.tile_ctas == 0) griddep_wait();
   griddep_launch_dependents();
-  if (__syncthreads_or(weigh_breaks_bounds(p))) {
-    if (tid == 0 && blockIdx.x == 0) record_error(p.ctx, kErrBounds);
-    return;
-  }
-  if (p.tile_ctas > 0) join_parts(p);
   // ---- an even share of all units for each warp
+  bool bad = false;
   int64_t mine = 0;
-  for (int r = tid; r < n_run; r += kThreads) mine += run_of(p, r).units;
+  for (int r = tid; r < n_run; r += kThreads) mine += run_of(p, r, &bad).units;
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, off);
   if (lane == 0) s_sum[warp] = mine;
-  __syncthreads();
+  bad = __syncthreads_or(bad);
   int64_t total = 0;
   for (int i = 0; i < kWarps; ++i) total += s_sum[i];
-  total *= H;
+  total = bad ? 0 : total * H;
+  if (bad && tid == 0 && blockIdx.x == 0) record_error(p.ctx, kErrBounds);
   const int64_t gw = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
   const int64_t n_warps = static_cast<int64_t>(gridDim.x) * kWarps;
   const int64_t u0 = total * gw / n_warps, u1 = total * (gw + 1) / n_warps;
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(kThreads) kv_weigh_kernel(const WeighArgs p) {
   int64_t u = u0;
   for (int r0 = 0; r0 < n_run && u < u1; r0 += 32) {
     Run own{};
-    if (r0 + lane < n_run) own = run_of(p, r0 + lane);
+    if (r0 + lane < n_run) own = run_of(p, r0 + lane, &bad);
     int64_t inc = static_cast<int64_t>(own.units) * H;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -229,10 +230,14 @@ __global__ void __launch_bounds__(kThreads) kv_weigh_kernel(const WeighArgs p) {
       const int key = key0 + 16 * i + 8 * y + g8;
       const int64_t tile = i == 0 ? tile_row[0] : tile_row[1];
       if (key < x.k1 && tile >= 0) {
-        weigh_add(p, x, key, tile + 8 * y + g8, a);
+        weigh_add(p, x.seq, x.fresh, key, tile + 8 * y + g8, a);
       }
     }
     before = end;
+  }
+  if (p.tile_ctas > 0) {
+    griddep_wait();
+    join_parts(p);
   }
 }
 

@@ -73,14 +73,22 @@ __device__ __forceinline__ int weigh_prefix(const bd_attention_batch& b, int s) 
   return lo < b.n_group && b.group_offsets[lo] <= s ? b.prefix_len[lo] : 0;
 }
 
-// Run r: the sequences' own, then the groups'.
-__device__ __forceinline__ WeighRun weigh_run(const WeighArgs& p, int r) {
+// Run r: the sequences' own, then the groups'.  A run whose entries break the batch's
+// bounds is empty and sets *bad.
+__device__ __forceinline__ WeighRun weigh_run(const WeighArgs& p, int r, bool* bad) {
   const bd_attention_batch& b = p.b;
   WeighRun x{};
   if (r < b.n_seq) {
     const int lo = b.seq_offsets[r], hi = b.seq_offsets[r + 1], kv = b.kv_len[r];
+    const int prefix = b.n_group > 0 ? weigh_prefix(b, r) : 0;
+    if (lo < 0 || hi < lo || hi > b.n_tokens || hi - lo > b.max_q_len || kv < 0 ||
+        kv > b.max_kv_len || kv > b.table_stride * b.page_size ||
+        (prefix > 0 && kv - (hi - lo) < prefix)) {
+      *bad = true;
+      return x;
+    }
     x.seq = r;
-    x.k0 = b.n_group > 0 ? weigh_prefix(b, r) : 0;
+    x.k0 = prefix;
     x.k1 = kv;
     x.tok0 = p.window > 0 && hi - lo > p.window ? hi - p.window : lo;
     x.tok1 = hi;
@@ -88,36 +96,27 @@ __device__ __forceinline__ WeighRun weigh_run(const WeighArgs& p, int r) {
     x.fresh = kv - (hi - lo);
   } else {
     const int g = r - b.n_seq, a = b.group_offsets[g], e = b.group_offsets[g + 1];
+    const int len = b.prefix_len[g];
+    if (a < 0 || e < a || e > b.n_seq || len < 0 || len > b.max_kv_len ||
+        len % b.page_size != 0) {
+      *bad = true;
+      return x;
+    }
+    if (e == a) return x;
     x.seq = a;
-    x.k1 = e > a ? b.prefix_len[g] : 0;
-    x.tok0 = e > a ? b.seq_offsets[a] : 0;
-    x.tok1 = e > a ? b.seq_offsets[e] : 0;
+    x.k1 = len;
+    x.tok0 = b.seq_offsets[a];
+    x.tok1 = b.seq_offsets[e];
     x.causal = kWeighSeesAll;
     x.fresh = INT32_MAX;
+    // (the sequences check their own offsets; here only what the group's work is cut by)
+    if (x.tok0 < 0 || x.tok1 < x.tok0 || x.tok1 > b.n_tokens) {
+      *bad = true;
+      return WeighRun{};
+    }
   }
   if (x.tok1 <= x.tok0) x.k1 = x.k0;
   return x;
-}
-
-// Whether the batch's tables break their bounds (this thread's share of them).
-__device__ __forceinline__ bool weigh_breaks_bounds(const WeighArgs& p) {
-  const bd_attention_batch& b = p.b;
-  const int step = static_cast<int>(blockDim.x);
-  bool bad = false;
-  for (int g = threadIdx.x; g < b.n_group; g += step) {
-    const int a = b.group_offsets[g], e = b.group_offsets[g + 1], len = b.prefix_len[g];
-    bad |= a < 0 || e < a || e > b.n_seq || len < 0 || len % b.page_size != 0;
-  }
-  for (int s = threadIdx.x; s < b.n_seq; s += step) {
-    const int lo = b.seq_offsets[s], hi = b.seq_offsets[s + 1], kv = b.kv_len[s];
-    bad |= lo < 0 || hi < lo || hi > b.n_tokens || hi - lo > b.max_q_len || kv < 0 ||
-           kv > b.max_kv_len || kv > b.table_stride * b.page_size;
-    if (b.n_group > 0) {
-      const int prefix = weigh_prefix(b, s);
-      bad |= prefix > 0 && static_cast<int64_t>(kv) - (hi - lo) < prefix;
-    }
-  }
-  return bad;
 }
 
 // Whether token t counts in the window of its sequence, one of [s0, s1).
@@ -140,11 +139,11 @@ __device__ __forceinline__ int64_t weigh_row(const bd_attention_batch& b, int se
 }
 
 // A key's sum to the table.
-__device__ __forceinline__ void weigh_add(const WeighArgs& p, const WeighRun& x, int key,
+__device__ __forceinline__ void weigh_add(const WeighArgs& p, int seq, int fresh, int key,
                                           int64_t row, float a) {
-  if (key >= x.fresh) {
+  if (key >= fresh) {
     p.weights[row] = a;
-    p.positions[row] = key + (p.pos_offset != nullptr ? p.pos_offset[x.seq] : 0);
+    p.positions[row] = key + (p.pos_offset != nullptr ? p.pos_offset[seq] : 0);
   } else {
     p.weights[row] += a;
   }

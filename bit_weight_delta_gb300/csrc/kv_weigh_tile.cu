@@ -12,9 +12,19 @@
 // several CTAs' shares is summed from their parts, in their order, by the kernel
 // that follows.
 //
-// Warps: 0-3 and 4-7 the epilogues of the block's halves, 8 the MMA issuer, 9 the
-// TMA producer of K and Q, 10 loads the rows' lse.  Tensor memory: tile buffer b,
-// half h at column 256·b + 128·h.
+// The subtraction of lse is a product as well: three more columns, ones in K and
+// −lse/scale in three bf16 parts in Q.  (Read by the epilogue from shared memory it
+// took a quarter of a tile's time.)
+//
+// The keys are the product's A operand from tensor memory, where the epilogue's warps
+// put a block once: with both operands in shared memory the two halves' products read
+// it at its full rate (128 bytes a clock), and the loads of Q and the epilogue's of
+// lse came on top (1650 cycles a tile).
+//
+// Warps: 0-3 and 4-7 the epilogues of the block's halves, 8 and 9 their MMA
+// issuers (a warp per half: one's waits are then the time of the other's products),
+// 10 the TMA producer of K and Q, 11 loads the rows' lse.  Tensor memory: the block's halves in columns 0-127, three buffers of 128
+// columns behind them that the halves' products go to in turn.
 #include <cstdint>
 
 #include "attention.cuh"
@@ -26,35 +36,66 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMmaWarp = 8, kTmaWarp = 9, kLseWarp = 10;
+constexpr int kSumWarps = 8;
+constexpr int kMmaWarp = 8, kTmaWarp = 10, kLseWarp = 11;  // MMA: 8 and 9, a half each
+// 384 threads launch with 168 registers each; the two epilogue warpgroups take 208 and
+// leave 88 for the third: 2·208 + 88 = 3·168.
+constexpr int kSumRegs = 208;
+constexpr int kOtherRegs = 88;
 constexpr int kRows = 128;          // query rows of a tile
 constexpr int kPanel = 128 * 128;   // 128 rows x 128 bytes
 constexpr int kLseStages = 4;
+constexpr int kBuffers = 3;  // of a half's product
+// The products ("units") are numbered in the order of tiles and halves; unit u goes to
+// buffer u % 3.  It has barriers u % 6 of its own: one that two units of different
+// halves took in turn would let a half that is ahead pass for a phase too early.
+constexpr int kUnits = 2 * kBuffers;
+struct Unit {
+  int u = 0;  // modulo 12
+  __device__ __forceinline__ void skip(int n) { u = u + n >= 2 * kUnits ? u + n - 2 * kUnits : u + n; }
+  __device__ __forceinline__ int bar() const { return u >= kUnits ? u - kUnits : u; }
+  __device__ __forceinline__ uint32_t phase() const { return u >= kUnits ? 1u : 0u; }
+  __device__ __forceinline__ uint32_t column() const {
+    return 128u + 128u * (bar() >= kBuffers ? bar() - kBuffers : bar());
+  }
+  __device__ __forceinline__ Unit plus(int n) const {
+    Unit x = *this;
+    x.skip(n);
+    return x;
+  }
+};
 constexpr uint32_t kTmemCols = 512;
 
-// The rows of a tile: what is subtracted from a score (−lse in log2 units) and the
-// last slot that a row sees (−1: a row that does not count), with the least and the
-// largest of each 32 of them.
+// The last slot that each row of a tile sees (−1: a row that does not count), with
+// the least and the largest of each 32 of them.
 struct Rows {
-  float minus[kRows];
   int sees[kRows];
   int least[4], most[4];
 };
+constexpr int kLseBytes = kRows * 64;  // the rows' −lse/scale as operand columns
 
 template <int D>
 struct Cfg {
   static constexpr int kPanels = D / 64;
   static constexpr int kHalfBytes = kPanels * kPanel;  // 128 rows
-  static constexpr int kQStages = D == 128 ? 2 : 4;
-  static constexpr int kOffQ = 4 * kHalfBytes;  // two blocks of keys before it
-  static constexpr int kOffRows = kOffQ + kQStages * kHalfBytes;
-  static constexpr int kOffBar = kOffRows + kLseStages * static_cast<int>(sizeof(Rows));
-  // k_full[2], k_empty[2], s_full[2], s_empty[2], lse_full[], lse_empty[], q_full[],
-  // q_empty[], drain
-  static constexpr int kBars = 8 + 2 * kLseStages + 2 * kQStages + 1;
+  static constexpr int kQStages = D == 128 ? 3 : 4;
+  static constexpr int kOffQ = 2 * kHalfBytes;  // a block of keys before it
+  static constexpr int kOffLse = kOffQ + kQStages * kHalfBytes;
+  static constexpr int kOffOnes = kOffLse + kLseStages * kLseBytes;
+  static constexpr int kOffRows = kOffOnes + kLseBytes;
+  static constexpr int kOffItem = kOffRows + kLseStages * static_cast<int>(sizeof(Rows));
+  static constexpr int kOffBar = kOffItem + 4 * 64;  // items
+  // k_full, k_empty, k_ready[2], s_full[], s_empty[], lse_full[], lse_empty[], q_full[],
+  // q_empty[], item_full[], item_empty[], drain[2]
+  static constexpr int kBars = 4 + 4 * kBuffers + 2 * kLseStages + 2 * kQStages + 2 * 4 + 2;
   static constexpr int kOffMisc = (kOffBar + 8 * kBars + 15) / 16 * 16;
   static constexpr int kSmem = kOffMisc + 16 + 1024;  // with slack for alignment
 };
+
+// a / b of numbers that are not negative, in 32 bits where they fit.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return (a | b) >> 32 == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
 
 // A run as this kernel's work: its blocks, and the tiles of each.
 struct TileRun {
@@ -72,9 +113,9 @@ struct TileRun {
   }
 };
 
-__device__ TileRun tile_run(const WeighArgs& p, int r, int tok) {
+__device__ TileRun tile_run(const WeighArgs& p, int r, int tok, bool* bad) {
   TileRun t{};
-  t.x = weigh_run(p, r);
+  t.x = weigh_run(p, r, bad);
   t.group = r >= p.b.n_seq;
   const int g = p.b.n_q_heads / p.b.n_kv_heads;
   const int n_tok = t.x.tok1 - t.x.tok0;
@@ -90,24 +131,50 @@ __device__ TileRun tile_run(const WeighArgs& p, int r, int tok) {
   return t;
 }
 
-// Tiles [j0, j1) of a block.
+// Tiles [j0, j1) of a block, as the roles read it from shared memory; h < 0 ends the
+// work.
 struct Item {
   int h, i;
   int key0;       // the block's first slot
   int first;      // token of tile 0
   int j0, j1, n;  // n: tiles of the block
+  int run, seq;
+  int k1, tok1;   // the run's
+  int causal, fresh;
+  int s1;         // a group's end, 0 for a sequence
+  int pad[2];
 };
+static_assert(sizeof(Item) == 64, "four 16-byte words");
+constexpr int kItemStages = 4;
+constexpr int kItemReaders = kSumWarps + 3;  // the MMA issuers and the loader of lse
 
-// A CTA's share, item after item; every role walks it for itself.
+// A CTA's share, item after item.
 struct Walk {
   TileRun t;
   int64_t left;
   int run, h, i, j;
 
-  __device__ __forceinline__ bool next(const WeighArgs& p, int tok, Item& it) {
-    if (left <= 0) return false;
+  // To tile `at` of the run.
+  __device__ __forceinline__ void seek(int64_t at, int tok) {
+    h = static_cast<int>(quotient(at, t.per_head));
+    at -= h * t.per_head;
+    const int64_t full = static_cast<int64_t>(t.m_full) * t.n_full;
+    if (at < full) {
+      i = static_cast<int>(quotient(at, t.n_full));
+      at -= static_cast<int64_t>(i) * t.n_full;
+    } else {
+      at -= full;
+      for (i = t.m_full; at >= t.tiles(i, tok); ++i) at -= t.tiles(i, tok);
+    }
+    j = static_cast<int>(at);
+  }
+
+  __device__ __forceinline__ void next(const WeighArgs& p, int tok, Item& it) {
+    it.h = -1;
+    if (left <= 0) return;
     while (h == p.b.n_kv_heads) {  // (there is a further run: left counts its tiles)
-      t = tile_run(p, ++run, tok);
+      bool bad = false;
+      t = tile_run(p, ++run, tok, &bad);
       if (t.per_head > 0) h = 0;
     }
     it.h = h;
@@ -117,9 +184,15 @@ struct Walk {
     it.n = t.tiles(i, tok);
     it.j0 = j;
     it.j1 = left < it.n - j ? j + static_cast<int>(left) : it.n;
+    it.run = run;
+    it.seq = t.x.seq;
+    it.k1 = t.x.k1;
+    it.tok1 = t.x.tok1;
+    it.causal = t.x.causal;
+    it.fresh = t.x.fresh;
+    it.s1 = t.group ? p.b.group_offsets[run - p.b.n_seq + 1] : 0;
     left -= it.j1 - it.j0;
     j = it.j1;
-    // `t` stays this item's run until the next call
     if (j == it.n) {
       j = 0;
       if (++i == t.blocks) {
@@ -127,7 +200,30 @@ struct Walk {
         ++h;
       }
     }
-    return true;
+  }
+};
+
+// The CTA's items in turn, which the TMA producer puts and the other roles take.
+struct Items {
+  const Item* slots;
+  uint64_t *full, *empty;
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ bool take(Item& it, const DevCtx& ctx, volatile int* abort) {
+    if (!warp_wait(&full[at], phase, ctx, abort)) return false;
+    it = slots[at];
+    // (a value from lane 0 is known to be the same in all lanes: what it decides stays
+    // in uniform registers, which the tensor instructions take)
+    for (int* f : {&it.h, &it.i, &it.key0, &it.first, &it.j0, &it.j1, &it.n, &it.run, &it.seq,
+                   &it.k1, &it.tok1, &it.causal, &it.fresh, &it.s1})
+      *f = __shfl_sync(0xFFFFFFFFu, *f, 0);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[at]);
+    if (++at == kItemStages) {
+      at = 0;
+      phase ^= 1u;
+    }
+    return it.h >= 0;
   }
 };
 
@@ -136,19 +232,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     weigh_tile_kernel(const __grid_constant__ WeighMaps maps, const WeighArgs p) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int64_t s_sum[kWarps], s_at;
-  __shared__ int s_run;
+  __shared__ int64_t s_sum[kWarps], s_more[kWarps];
+  __shared__ Walk s_walk;
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  uint64_t* k_empty = k_full + 2;
+  uint64_t* k_empty = k_full + 1;
+  uint64_t* k_ready = k_full + 2;
   uint64_t* s_full = k_full + 4;
-  uint64_t* s_empty = k_full + 6;
-  uint64_t* lse_full = k_full + 8;
+  uint64_t* s_empty = s_full + kUnits;
+  uint64_t* lse_full = s_empty + kUnits;
   uint64_t* lse_empty = lse_full + kLseStages;
   uint64_t* q_full = lse_empty + kLseStages;
   uint64_t* q_empty = q_full + C::kQStages;
-  uint64_t* drain = q_empty + C::kQStages;
+  uint64_t* item_full = q_empty + C::kQStages;
+  uint64_t* item_empty = item_full + kItemStages;
+  uint64_t* drain = item_empty + kItemStages;
+  Item* item_slots = reinterpret_cast<Item*>(smem + C::kOffItem);
   Rows* rows = reinterpret_cast<Rows*>(smem + C::kOffRows);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
@@ -159,26 +259,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_run = b.n_seq + b.n_group;
 
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 1);
+    mbar_init(k_full, 1);
+    mbar_init(k_empty, kSumWarps);
+    for (int i = 0; i < 2; ++i) mbar_init(&k_ready[i], kSumWarps / 2);
+    for (int i = 0; i < kUnits; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 8);
+      mbar_init(&s_empty[i], kSumWarps / 2);
     }
     for (int i = 0; i < kLseStages; ++i) {
       mbar_init(&lse_full[i], 1);
-      mbar_init(&lse_empty[i], 8);
+      mbar_init(&lse_empty[i], kSumWarps);
     }
     for (int i = 0; i < C::kQStages; ++i) {
       mbar_init(&q_full[i], 1);
-      mbar_init(&q_empty[i], 1);
+      mbar_init(&q_empty[i], 2);
     }
-    mbar_init(drain, 1);
+    for (int i = 0; i < kItemStages; ++i) {
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_empty[i], kItemReaders);
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(&drain[i], 1);
     *abort = 0;
-    s_run = 0;
-    s_at = 0;
     fence_mbar_init();
   }
+  // Rows of 64 bytes in the 64-byte swizzle, of which a product step reads the first
+  // 16 columns: three ones, and three places for a row's −lse/scale.
+  for (int i = tid; i < (kLseStages + 1) * kLseBytes / 16; i += kThreads) {
+    const int row = i >> 2 & (kRows - 1), chunk = i & 3 ^ (row >> 1 & 3);
+    const bool ones = i >= kLseStages * kLseBytes / 16 && chunk == 0;
+    *reinterpret_cast<uint4*>(smem + C::kOffLse + 16 * i) =
+        make_uint4(ones ? 0x3F803F80u : 0u, ones ? 0x3F80u : 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
   if (warp == kMmaWarp) tmem_alloc(tmem_slot, kTmemCols);
   if (warp == kTmaWarp && lane == 0) {
     prefetch_tmap(&maps.q);
@@ -191,46 +303,70 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_wait();
   griddep_launch_dependents();
 
-  // ---- this CTA's share of all tiles, and where it begins
-  const bool bad = __syncthreads_or(weigh_breaks_bounds(p));
-  int64_t total = 0;
-  if (!bad) {
-    int64_t mine = 0;
-    for (int r = tid; r < n_run; r += kThreads) mine += tile_run(p, r, tok).per_head;
+  // ---- this CTA's share of all tiles, and where it begins: a run per thread, and
+  // further rounds of them where there are more runs
+  bool bad = false;
+  TileRun mine{};
+  if (tid < n_run) mine = tile_run(p, tid, tok, &bad);
+  int64_t more = 0;
+  for (int r = tid + kThreads; r < n_run; r += kThreads)
+    more += tile_run(p, r, tok, &bad).per_head;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, off);
-    if (lane == 0) s_sum[warp] = mine;
-    __syncthreads();
-    for (int i = 0; i < kWarps; ++i) total += s_sum[i];
-    total *= b.n_kv_heads;
-  } else if (tid == 0 && blockIdx.x == 0) {
-    record_error(p.ctx, kErrBounds);
+  for (int off = 16; off > 0 && n_run > kThreads; off >>= 1)
+    more += __shfl_xor_sync(0xFFFFFFFFu, more, off);
+  // inclusive sums over the round's runs
+  const auto scan = [&](int64_t n) {
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t o = __shfl_up_sync(0xFFFFFFFFu, n, off);
+      if (lane >= off) n += o;
+    }
+    return n;
+  };
+  int64_t inc = scan(mine.per_head);
+  if (lane == 31) {
+    s_sum[warp] = inc;
+    s_more[warp] = more;
   }
-  const int64_t lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
+  bad = __syncthreads_or(bad);
+  int64_t round = 0, total = 0;
+#pragma unroll 1
+  for (int i = 0; i < kWarps; ++i) {
+    if (i == warp) inc += round;
+    round += s_sum[i];
+    total += s_more[i];
+  }
+  total = bad ? 0 : (total + round) * b.n_kv_heads;
+  if (bad && tid == 0 && blockIdx.x == 0) record_error(p.ctx, kErrBounds);
+  const int64_t each = quotient(total, gridDim.x), extra = total - each * gridDim.x;
+  const int64_t lo = each * blockIdx.x + (blockIdx.x < extra ? blockIdx.x : extra);
+  const int64_t hi = lo + each + (blockIdx.x < extra ? 1 : 0);
   if (hi > lo) {
     int64_t before = 0;
     for (int base = 0; base < n_run && before <= lo; base += kThreads) {
-      const int64_t n =
-          base + tid < n_run ? tile_run(p, base + tid, tok).per_head * b.n_kv_heads : 0;
-      int64_t inc = n;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int64_t o = __shfl_up_sync(0xFFFFFFFFu, inc, off);
-        if (lane >= off) inc += o;
+      if (base > 0) {
+        mine = TileRun{};
+        if (base + tid < n_run) mine = tile_run(p, base + tid, tok, &bad);
+        inc = scan(mine.per_head);
+        __syncthreads();  // the sums before have been read
+        if (lane == 31) s_sum[warp] = inc;
+        __syncthreads();
+        round = 0;
+        for (int i = 0; i < kWarps; ++i) {
+          if (i == warp) inc += round;
+          round += s_sum[i];
+        }
       }
-      __syncthreads();  // the sums before have been read
-      if (lane == 31) s_sum[warp] = inc;
-      __syncthreads();
-      int64_t at = before;
-      for (int i = 0; i < kWarps; ++i) {
-        if (i == warp) inc += at;
-        at += s_sum[i];
+      const int64_t first = before + (inc - mine.per_head) * b.n_kv_heads;
+      if (first <= lo && lo < before + inc * b.n_kv_heads) {
+        Walk w{};
+        w.t = mine;
+        w.left = hi - lo;
+        w.run = base + tid;
+        w.seek(lo - first, tok);
+        s_walk = w;
       }
-      if (inc - n <= lo && lo < inc) {
-        s_run = base + tid;
-        s_at = lo - (inc - n);
-      }
-      before = at;
+      before += round * b.n_kv_heads;
     }
   }
   if (tid < 2) {
@@ -238,91 +374,113 @@ __global__ void __launch_bounds__(kThreads, 1)
     p.records[2 * blockIdx.x + tid] = none;
   }
   __syncthreads();
-  Walk walk{};
-  walk.left = hi - lo;
-  walk.run = s_run;
-  if (walk.left > 0) {
-    walk.t = tile_run(p, walk.run, tok);
-    walk.h = static_cast<int>(s_at / walk.t.per_head);
-    int64_t at = s_at - walk.h * walk.t.per_head;
-    const int64_t full = static_cast<int64_t>(walk.t.m_full) * walk.t.n_full;
-    if (at < full) {
-      walk.i = static_cast<int>(at / walk.t.n_full);
-      at -= static_cast<int64_t>(walk.i) * walk.t.n_full;
-    } else {
-      at -= full;
-      for (walk.i = walk.t.m_full; at >= walk.t.tiles(walk.i, tok); ++walk.i)
-        at -= walk.t.tiles(walk.i, tok);
-    }
-    walk.j = static_cast<int>(at);
-  }
+  Items items{item_slots, item_full, item_empty};
   Item it;
   bool ok = true;
 
-  if (warp < 8) {
+  if (warp < kSumWarps) {
     // ============================================================ sums
+    reg_inc<kSumRegs>();
     const int half = warp >> 2;
-    const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 128u * half;
-    const int mine = 128 * half + 32 * (warp & 3) + lane;  // key of the block
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const int row_of_half = 32 * (warp & 3) + lane;
+    const int mine = 128 * half + row_of_half;  // key of the block
     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
-    uint32_t s_phase = 0, l_phase = 0;
-    int buf = 0, ls = 0;
+    uint32_t l_phase = 0, k_phase = 0;
+    int ls = 0;
+    Unit unit;  // the tile's first
     bool started = false;  // an item before this one
-    while (ok && walk.next(p, tok, it)) {
-      const WeighRun& x = walk.t.x;
+    while (ok && items.take(it, p.ctx, abort)) {
       const int key = it.key0 + mine;
       const int key_lo = it.key0 + 128 * half;  // the half's
-      const int key_hi = key_lo + 127 < x.k1 - 1 ? key_lo + 127 : x.k1 - 1;
+      const int key_hi = key_lo + 127 < it.k1 - 1 ? key_lo + 127 : it.k1 - 1;
+      const bool both = it.key0 + 128 < it.k1;  // keys in the second half
+      const bool idle = half != 0 && !both;
+      // ---- the block's keys to tensor memory: this warp's 32 rows.  The products that
+      // read the block before have completed: the last of them was waited for below.
+      if (!(ok = warp_wait(k_full, k_phase, p.ctx, abort))) break;
+      k_phase ^= 1u;
+      if (!idle) {
+        constexpr int kChunks = D / 8;  // 16-byte pieces of a row
+        const uint8_t* src = smem + half * C::kHalfBytes + row_of_half * 128;
+#pragma unroll
+        for (int y = 0; y < kChunks; y += 4) {
+          uint32_t w[16];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const int chunk = y + z;
+            const uint4 v = *reinterpret_cast<const uint4*>(
+                src + (chunk >> 3) * kPanel + (((chunk & 7) ^ (lane & 7)) << 4));
+            w[4 * z] = v.x;
+            w[4 * z + 1] = v.y;
+            w[4 * z + 2] = v.z;
+            w[4 * z + 3] = v.w;
+          }
+          tmem_st_x16(t_lane + static_cast<uint32_t>(half * (D / 2) + 4 * y), w);
+        }
+        tmem_st_done();
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(k_empty);
+        if (!idle) mbar_arrive(&k_ready[half]);
+      }
       uint64_t sum[2] = {0u, 0u};
       for (int j = it.j0; j < it.j1; ++j) {
+        const Unit u = unit.plus(half);
         ok = warp_wait(&lse_full[ls], l_phase, p.ctx, abort) &&
-             warp_wait(&s_full[buf], s_phase, p.ctx, abort);
+             (idle || warp_wait(&s_full[u.bar()], u.phase(), p.ctx, abort));
         if (!ok) break;
         tc_fence_after();
         const Rows& rw = rows[ls];
+        const uint32_t t_s = t_lane + u.column();
+        // 32 rows: all of them see the keys, or each is looked at
+        const auto all = [&](const uint32_t (&s)[32]) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (rw.most[c] < key_lo || key_lo >= x.k1) continue;
-          uint32_t s[32];
-          tmem_ld_32x32b_x32(t_lane + 256u * buf + 32u * c, s);
+          for (int v = 0; v < 16; ++v) {
+            float e0, e1;
+            unpack2(mul2(pack2(__uint_as_float(s[2 * v]), __uint_as_float(s[2 * v + 1])), scale2),
+                    e0, e1);
+            sum[v & 1] = add2(sum[v & 1], pack2(ex2(e0), ex2(e1)));
+          }
+        };
+        const auto some = [&](const uint32_t (&s)[32], int c) {
+          const int2* z2 = reinterpret_cast<const int2*>(rw.sees + 32 * c);
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            const int2 z = z2[v];
+            float e0, e1;
+            unpack2(mul2(pack2(__uint_as_float(s[2 * v]), __uint_as_float(s[2 * v + 1])), scale2),
+                    e0, e1);
+            // (selected, not multiplied: a row that does not count may hold anything)
+            sum[v & 1] =
+                add2(sum[v & 1], pack2(key <= z.x ? ex2(e0) : 0.f, key <= z.y ? ex2(e1) : 0.f));
+          }
+        };
+        if (!idle) {
+          // All columns to registers, and the buffer back to the MMA issuer before they
+          // are summed.
+          uint32_t s[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(t_s + 32u * c, s[c]);
           tmem_ld_wait();
-          const ulonglong2* m2 = reinterpret_cast<const ulonglong2*>(rw.minus + 32 * c);
-          if (rw.least[c] >= key_hi) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_empty[u.bar()]);
+          const int least = min(min(rw.least[0], rw.least[1]), min(rw.least[2], rw.least[3]));
+          if (least >= key_hi) {
 #pragma unroll
-            for (int v = 0; v < 8; ++v) {
-              const ulonglong2 m = m2[v];
-              float e0, e1, e2, e3;
-              unpack2(fma2(pack2(__uint_as_float(s[4 * v]), __uint_as_float(s[4 * v + 1])), scale2,
-                           m.x), e0, e1);
-              unpack2(fma2(pack2(__uint_as_float(s[4 * v + 2]), __uint_as_float(s[4 * v + 3])),
-                           scale2, m.y), e2, e3);
-              sum[0] = add2(sum[0], pack2(ex2(e0), ex2(e1)));
-              sum[1] = add2(sum[1], pack2(ex2(e2), ex2(e3)));
-            }
+            for (int c = 0; c < 4; ++c) all(s[c]);
           } else {
-            const int4* sees = reinterpret_cast<const int4*>(rw.sees + 32 * c);
 #pragma unroll
-            for (int v = 0; v < 8; ++v) {
-              const ulonglong2 m = m2[v];
-              const int4 z = sees[v];
-              float e0, e1, e2, e3;
-              unpack2(fma2(pack2(__uint_as_float(s[4 * v]), __uint_as_float(s[4 * v + 1])), scale2,
-                           m.x), e0, e1);
-              unpack2(fma2(pack2(__uint_as_float(s[4 * v + 2]), __uint_as_float(s[4 * v + 3])),
-                           scale2, m.y), e2, e3);
-              // (selected, not multiplied: a row that does not count may hold anything)
-              sum[0] = add2(sum[0], pack2(key <= z.x ? ex2(e0) : 0.f, key <= z.y ? ex2(e1) : 0.f));
-              sum[1] = add2(sum[1], pack2(key <= z.z ? ex2(e2) : 0.f, key <= z.w ? ex2(e3) : 0.f));
-            }
+            for (int c = 0; c < 4; ++c)
+              if (rw.most[c] >= key_lo) some(s[c], c);
           }
         }
-        tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&s_empty[buf]);
-          mbar_arrive(&lse_empty[ls]);
-        }
-        if ((buf ^= 1) == 0) s_phase ^= 1u;
+        if (lane == 0) mbar_arrive(&lse_empty[ls]);
+        unit.skip(both ? 2 : 1);
         if (++ls == kLseStages) {
           ls = 0;
           l_phase ^= 1u;
@@ -333,96 +491,130 @@ __global__ void __launch_bounds__(kThreads, 1)
       unpack2(add2(sum[0], sum[1]), a0, a1);
       const float a = a0 + a1;
       if (it.j0 == 0 && it.j1 == it.n) {
-        if (key < x.k1) {
-          const int64_t row = weigh_row(b, x.seq, key, it.h);
-          if (row >= 0) weigh_add(p, x, key, row, a);
+        if (key < it.k1) {
+          const int64_t row = weigh_row(b, it.seq, key, it.h);
+          if (row >= 0) weigh_add(p, it.seq, it.fresh, key, row, a);
         }
       } else {
         const int slot = 2 * static_cast<int>(blockIdx.x) + (started ? 1 : 0);
         p.parts[static_cast<int64_t>(slot) * kWeighBlockKeys + mine] = a;
         if (tid == 0)
-          p.records[slot] = WeighRecord{1, walk.run, it.h, it.i, it.j0 == 0, it.j1 == it.n, 0, 0};
+          p.records[slot] = WeighRecord{1, it.run, it.h, it.i, it.j0 == 0, it.j1 == it.n, 0, 0};
       }
       started = true;
     }
-  } else if (warp == kMmaWarp) {
-    // ============================================================ MMA issuer
+  } else {
+  reg_dec<kOtherRegs>();
+  if (warp < kTmaWarp) {
+    // ============================================================ MMA issuers
+    const int half = warp - kMmaWarp;
     const bool lead = elect_one();
     constexpr uint32_t idesc = idesc_bf16_f32(128, kRows);
     const uint32_t base = smem_addr(smem);
-    int kb = 0, qs = 0, buf = 0;
-    uint32_t k_phase = 0, q_phase = 0, s_phase = 1;
+    const uint32_t t_k = tmem + static_cast<uint32_t>(half * (D / 2));
+    int qs = 0, ls = 0;
+    Unit unit;
+    uint32_t k_phase = 0, q_phase = 0, l_phase = 0;
+    const uint64_t ones = sdesc_k_sw64(base + C::kOffOnes);
     bool issued = false;
-    while (ok && walk.next(p, tok, it)) {
-      ok = warp_wait(&k_full[kb], k_phase, p.ctx, abort);
-      const bool both = it.key0 + 128 < walk.t.x.k1;  // keys in the second half
-      for (int j = it.j0; ok && j < it.j1; ++j) {
-        ok = warp_wait(&q_full[qs], q_phase, p.ctx, abort) &&
-             warp_wait(&s_empty[buf], s_phase, p.ctx, abort);
+    while (ok && items.take(it, p.ctx, abort)) {
+      const bool both = it.key0 + 128 < it.k1;
+      const bool idle = half != 0 && !both;
+      if (!idle) {
+        if (!(ok = warp_wait(&k_ready[half], k_phase, p.ctx, abort))) break;
+        k_phase ^= 1u;
+      }
+      for (int j = it.j0; j < it.j1; ++j) {
+        const Unit u = unit.plus(half);
+        const Unit last = u.plus(2 * kUnits - kBuffers);  // in this buffer, three units ago
+        // (one that is idle takes no part in the lse ring, which does not wait for it)
+        ok = (idle || (warp_wait(&s_empty[last.bar()], last.phase(), p.ctx, abort) &&
+                       warp_wait(&lse_full[ls], l_phase, p.ctx, abort))) &&
+             warp_wait(&q_full[qs], q_phase, p.ctx, abort);
         if (!ok) break;
         tc_fence_after();
-        issued = true;
         if (lead) {
-          const uint64_t qd = sdesc_k_sw128(base + C::kOffQ + qs * C::kHalfBytes);
-          for (int h = 0; h < (both ? 2 : 1); ++h) {
-            const uint64_t kd = sdesc_k_sw128(base + (2 * kb + h) * C::kHalfBytes);
+          if (idle) {
+            mbar_arrive(&q_empty[qs]);
+          } else {
+            const uint64_t qd = sdesc_k_sw128(base + C::kOffQ + qs * C::kHalfBytes);
+            const uint64_t ld = sdesc_k_sw64(base + C::kOffLse + ls * kLseBytes);
+            const uint32_t t_s = tmem + u.column();
+            mma_ss(t_s, ones, ld, idesc, 0u);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint64_t step = static_cast<uint64_t>((k >> 2) * (kPanel >> 4) + 2 * (k & 3));
-              mma_ss(tmem + 256u * buf + 128u * h, kd + step, qd + step, idesc, k > 0 ? 1u : 0u);
-            }
+            for (int k = 0; k < D / 16; ++k)
+              mma_ts(t_s, t_k + 8u * k,
+                     qd + static_cast<uint64_t>((k >> 2) * (kPanel >> 4) + 2 * (k & 3)), idesc, 1u);
+            mma_commit(&s_full[u.bar()]);
+            mma_commit(&q_empty[qs]);
           }
-          mma_commit(&s_full[buf]);
-          mma_commit(&q_empty[qs]);
-          if (j == it.j1 - 1) mma_commit(&k_empty[kb]);
         }
+        issued = issued || !idle;
         __syncwarp();
-        if ((buf ^= 1) == 0) s_phase ^= 1u;
+        unit.skip(both ? 2 : 1);
         if (++qs == C::kQStages) {
           qs = 0;
           q_phase ^= 1u;
         }
+        if (++ls == kLseStages) {
+          ls = 0;
+          l_phase ^= 1u;
+        }
       }
-      if ((kb ^= 1) == 0) k_phase ^= 1u;
     }
     if (issued) {
-      if (lead) mma_commit(drain);
-      mbar_wait(drain, 0, p.ctx, nullptr);
+      if (lead) mma_commit(&drain[half]);
+      mbar_wait(&drain[half], 0, p.ctx, nullptr);
     }
     __syncwarp();
   } else if (warp == kTmaWarp) {
     // ============================================================ TMA producer
     const int page_shift = 31 - __clz(b.page_size);
-    int kb = 0, qs = 0, k_fill = 0, q_fill = 0;
+    int qs = 0, k_fill = 0, q_fill = 0;
     uint32_t k_phase = 1, q_phase = 1;
-    while (ok && walk.next(p, tok, it)) {
-      const WeighRun& x = walk.t.x;
-      const int keys = x.k1 - it.key0 < kWeighBlockKeys ? x.k1 - it.key0 : kWeighBlockKeys;
+    Walk walk{};
+    if (hi > lo) walk = s_walk;
+    int put = 0;
+    uint32_t put_phase = 1;
+    while (ok) {
+      walk.next(p, tok, it);
+      if (!(ok = warp_wait(&item_empty[put], put_phase, p.ctx, abort))) break;
+      if (lane == 0) {
+        item_slots[put] = it;
+        mbar_arrive(&item_full[put]);
+      }
+      __syncwarp();
+      if (++put == kItemStages) {
+        put = 0;
+        put_phase ^= 1u;
+      }
+      if (it.h < 0) break;
+      const int keys = it.k1 - it.key0 < kWeighBlockKeys ? it.k1 - it.key0 : kWeighBlockKeys;
       const int n_pg = (keys + b.page_size - 1) >> page_shift;  // at most 16
       int page = -1;
       if (lane < n_pg) {
-        page = b.page_table[static_cast<int64_t>(x.seq) * b.table_stride +
+        page = b.page_table[static_cast<int64_t>(it.seq) * b.table_stride +
                             ((it.key0 >> page_shift) + lane)];
         if (page >= b.n_pages) page = -1;
         if (page < 0) record_error(p.ctx, kErrBounds);  // its sums go nowhere
       }
       const uint32_t live = __ballot_sync(0xFFFFFFFFu, page >= 0);
-      if (!(ok = warp_wait(&k_empty[kb], k_phase, p.ctx, abort))) break;
+      if (!(ok = warp_wait(k_empty, k_phase, p.ctx, abort))) break;
+      k_phase ^= 1u;
       if (lane == 0)
-        mbar_arrive_expect_tx(&k_full[kb], static_cast<uint32_t>(__popc(live) * b.page_size * 128 *
-                                                                 C::kPanels));
+        mbar_arrive_expect_tx(k_full, static_cast<uint32_t>(__popc(live) * b.page_size * 128 *
+                                                            C::kPanels));
       __syncwarp();
       if (page >= 0) {
         const int at = lane << page_shift;  // key of the block
-        uint8_t* dst = smem + (2 * kb + (at >> 7)) * C::kHalfBytes + (at & 127) * 128;
+        uint8_t* dst = smem + (at >> 7) * C::kHalfBytes + (at & 127) * 128;
 #pragma unroll
         for (int c = 0; c < C::kPanels; ++c)
-          tma_load_3d(dst + c * kPanel, &maps.k, &k_full[kb], 0,
+          tma_load_3d(dst + c * kPanel, &maps.k, k_full, 0,
                       (page * b.n_kv_heads + it.h) << page_shift, c);
       }
       __syncwarp();
       ++k_fill;
-      if ((kb ^= 1) == 0) k_phase ^= 1u;
       for (int j = it.j0; j < it.j1; ++j) {
         if (!(ok = warp_wait(&q_empty[qs], q_phase, p.ctx, abort))) break;
         if (lane == 0) {
@@ -442,8 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // See every issued load land (bounded, also after an abort).
     if (lane == 0) {
-      for (int f = k_fill > 2 ? k_fill - 2 : 0; f < k_fill; ++f)
-        mbar_wait(&k_full[f & 1], static_cast<uint32_t>(f >> 1 & 1), p.ctx, nullptr);
+      if (k_fill > 0) mbar_wait(k_full, static_cast<uint32_t>(k_fill - 1 & 1), p.ctx, nullptr);
       for (int f = q_fill > C::kQStages ? q_fill - C::kQStages : 0; f < q_fill; ++f)
         mbar_wait(&q_full[f % C::kQStages], static_cast<uint32_t>(f / C::kQStages & 1), p.ctx,
                   nullptr);
@@ -454,31 +645,56 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool windowed = p.window > 0 && p.window < b.max_q_len;
     int ls = 0;
     uint32_t phase = 1;
-    while (ok && walk.next(p, tok, it)) {
-      const WeighRun& x = walk.t.x;
-      const int s1 = walk.t.group ? b.group_offsets[walk.run - b.n_seq + 1] : 0;
+    // −lse/scale as the sum of three bf16 numbers (24 bits), to be added by the product
+    const float to_score = -kWeighLog2e / p.scale_log2;
+    const auto put = [&](int stage, int row, float v) {
+      const uint32_t hi = pack_bf16x2_rn(v, 0.f);
+      const float r = v - bf16lo_to_f32(hi);
+      const uint32_t mid = pack_bf16x2_rn(r, 0.f);
+      const uint32_t lo = pack_bf16x2_rn(r - bf16lo_to_f32(mid), 0.f);
+      *reinterpret_cast<uint2*>(smem + C::kOffLse + stage * kLseBytes + row * 64 +
+                                ((row >> 1 & 3) << 4)) = make_uint2(hi | mid << 16, lo);
+    };
+    int row_tok[4], row_head[4];  // of the lane's four rows; the token −1: no row
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int row = 32 * c + lane;
+      row_tok[c] = row < tok * G ? row / G : -1;
+      row_head[c] = row % G;
+    }
+    while (ok && items.take(it, p.ctx, abort)) {
+      const float* lse = p.lse + it.h * G;
+      float l[4];  // of the next tile, on their way while this one waits
+      const auto load = [&](int j) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int t = it.first + j * tok + row_tok[c];
+          l[c] = row_tok[c] >= 0 && t < it.tok1
+                     ? lse[static_cast<int64_t>(t) * b.n_q_heads + row_head[c]]
+                     : INFINITY;
+        }
+      };
+      load(it.j0);
       for (int j = it.j0; j < it.j1; ++j) {
-        float minus[4];
+        float x[4];
         int sees[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const int row = 32 * c + lane;
-          const int t = it.first + j * tok + row / G;
-          minus[c] = 0.f;
+          const int t = it.first + j * tok + row_tok[c];
+          x[c] = 0.f;
           sees[c] = -1;
-          if (row < tok * G && t < x.tok1) {
-            const float l = p.lse[static_cast<int64_t>(t) * b.n_q_heads + it.h * G + row % G];
-            if (isfinite(l) && (!walk.t.group || !windowed || weigh_in_window(p, t, x.seq, s1))) {
-              minus[c] = -l * kWeighLog2e;
-              sees[c] = walk.t.group ? INT32_MAX : t + x.causal;
-            }
+          if (isfinite(l[c]) &&
+              (it.s1 == 0 || !windowed || weigh_in_window(p, t, it.seq, it.s1))) {
+            x[c] = fminf(fmaxf(l[c] * to_score, -3e38f), 3e38f);
+            sees[c] = it.s1 > 0 ? INT32_MAX : t + it.causal;
           }
         }
+        if (j + 1 < it.j1) load(j + 1);
         if (!(ok = warp_wait(&lse_empty[ls], phase, p.ctx, abort))) break;
         Rows& rw = rows[ls];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          rw.minus[32 * c + lane] = minus[c];
+          put(ls, 32 * c + lane, x[c]);
           rw.sees[32 * c + lane] = sees[c];
           const int least = __reduce_min_sync(0xFFFFFFFFu, sees[c]);
           const int most = __reduce_max_sync(0xFFFFFFFFu, sees[c]);
@@ -487,6 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             rw.most[c] = most;
           }
         }
+        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&lse_full[ls]);
         if (++ls == kLseStages) {
@@ -495,6 +712,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+  }
+
   }
 
   tc_fence_before();
