@@ -34,17 +34,14 @@
 namespace bd {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kWarps = kThreads / 32;
-constexpr int kSumWarps = 8;
-constexpr int kMmaWarp = 8, kTmaWarp = 10, kLseWarp = 11;  // MMA: 8 and 9, a half each
-// 384 threads launch with 168 registers each; the two epilogue warpgroups take 208 and
-// leave 88 for the third: 2·208 + 88 = 3·168.
-constexpr int kSumRegs = 208;
-constexpr int kOtherRegs = 88;
+constexpr int kSumWarps = 16;
+constexpr int kMmaWarp = 16, kTmaWarp = 18, kLseWarp = 19;  // MMA: 16 and 17, a half each
+constexpr int kWarps = 20;
+constexpr int kThreads = 32 * kWarps;
 constexpr int kRows = 128;          // query rows of a tile
 constexpr int kPanel = 128 * 128;   // 128 rows x 128 bytes
 constexpr int kLseStages = 4;
+constexpr int kSumStages = 4;
 constexpr int kBuffers = 3;  // of a half's product
 // The products ("units") are numbered in the order of tiles and halves; unit u goes to
 // buffer u % 3.  It has barriers u % 6 of its own: one that two units of different
@@ -84,10 +81,12 @@ struct Cfg {
   static constexpr int kOffOnes = kOffLse + kLseStages * kLseBytes;
   static constexpr int kOffRows = kOffOnes + kLseBytes;
   static constexpr int kOffItem = kOffRows + kLseStages * static_cast<int>(sizeof(Rows));
-  static constexpr int kOffBar = kOffItem + 4 * 64;  // items
+  static constexpr int kOffSum = kOffItem + 4 * 64;  // items
+  static constexpr int kOffBar = kOffSum + kSumStages * kWeighBlockKeys * 4;
   // k_full, k_empty, k_ready[2], s_full[], s_empty[], lse_full[], lse_empty[], q_full[],
-  // q_empty[], item_full[], item_empty[], drain[2]
-  static constexpr int kBars = 4 + 4 * kBuffers + 2 * kLseStages + 2 * kQStages + 2 * 4 + 2;
+  // q_empty[], item_full[], item_empty[], sum_full[],
+  // drain[2]
+  static constexpr int kBars = 4 + 4 * kBuffers + 2 * kLseStages + 2 * kQStages + 2 * 4 + kSumStages + 2;
   static constexpr int kOffMisc = (kOffBar + 8 * kBars + 15) / 16 * 16;
   static constexpr int kSmem = kOffMisc + 16 + 1024;  // with slack for alignment
 };
@@ -247,7 +246,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* q_empty = q_full + C::kQStages;
   uint64_t* item_full = q_empty + C::kQStages;
   uint64_t* item_empty = item_full + kItemStages;
-  uint64_t* drain = item_empty + kItemStages;
+  uint64_t* sum_full = item_empty + kItemStages;
+  uint64_t* drain = sum_full + kSumStages;
   Item* item_slots = reinterpret_cast<Item*>(smem + C::kOffItem);
   Rows* rows = reinterpret_cast<Rows*>(smem + C::kOffRows);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
@@ -278,6 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&item_full[i], 1);
       mbar_init(&item_empty[i], kItemReaders);
     }
+    for (int i = 0; i < kSumStages; ++i) mbar_init(&sum_full[i], kSumWarps / 2);
     for (int i = 0; i < 2; ++i) mbar_init(&drain[i], 1);
     *abort = 0;
     fence_mbar_init();
@@ -380,8 +381,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kSumWarps) {
     // ============================================================ sums
-    reg_inc<kSumRegs>();
-    const int half = warp >> 2;
+    const int half = warp >> 2 & 1;
+    const int c0 = warp >> 3 << 1;  // of the tile's four groups of 32 rows
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     const int row_of_half = 32 * (warp & 3) + lane;
     const int mine = 128 * half + row_of_half;  // key of the block
@@ -390,10 +391,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     int ls = 0;
     Unit unit;  // the tile's first
     bool started = false;  // an item before this one
+    // Sums over a tile's later 64 rows, for the warps of the first ones.  With three
+    // buffers of products a warp is at most three tiles, and items, ahead of another:
+    // four of these need no wait to be written.
+    float* others = reinterpret_cast<float*>(smem + C::kOffSum);
+    int ss = 0;
+    uint32_t sum_phase = 0;
     while (ok && items.take(it, p.ctx, abort)) {
       const int key = it.key0 + mine;
-      const int key_lo = it.key0 + 128 * half;  // the half's
-      const int key_hi = key_lo + 127 < it.k1 - 1 ? key_lo + 127 : it.k1 - 1;
+      const int key_lo = it.key0 + 128 * half + 32 * (warp & 3);  // the warp's
+      const int key_hi = key_lo + 31 < it.k1 - 1 ? key_lo + 31 : it.k1 - 1;
       const bool both = it.key0 + 128 < it.k1;  // keys in the second half
       const bool idle = half != 0 && !both;
       // ---- the block's keys to tensor memory: this warp's 32 rows.  The products that
@@ -401,14 +408,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = warp_wait(k_full, k_phase, p.ctx, abort))) break;
       k_phase ^= 1u;
       if (!idle) {
-        constexpr int kChunks = D / 8;  // 16-byte pieces of a row
+        constexpr int kChunks = D / 16;  // 16-byte pieces of a row's half, which this warp moves
+        const int x0 = (c0 >> 1) * kChunks;
         const uint8_t* src = smem + half * C::kHalfBytes + row_of_half * 128;
 #pragma unroll
         for (int y = 0; y < kChunks; y += 4) {
           uint32_t w[16];
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
-            const int chunk = y + z;
+            const int chunk = x0 + y + z;
             const uint4 v = *reinterpret_cast<const uint4*>(
                 src + (chunk >> 3) * kPanel + (((chunk & 7) ^ (lane & 7)) << 4));
             w[4 * z] = v.x;
@@ -416,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             w[4 * z + 2] = v.z;
             w[4 * z + 3] = v.w;
           }
-          tmem_st_x16(t_lane + static_cast<uint32_t>(half * (D / 2) + 4 * y), w);
+          tmem_st_x16(t_lane + static_cast<uint32_t>(half * (D / 2) + 4 * (x0 + y)), w);
         }
         tmem_st_done();
         tc_fence_before();
@@ -435,47 +443,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const Rows& rw = rows[ls];
         const uint32_t t_s = t_lane + u.column();
-        // 32 rows: all of them see the keys, or each is looked at
-        const auto all = [&](const uint32_t (&s)[32]) {
-#pragma unroll
-          for (int v = 0; v < 16; ++v) {
-            float e0, e1;
-            unpack2(mul2(pack2(__uint_as_float(s[2 * v]), __uint_as_float(s[2 * v + 1])), scale2),
-                    e0, e1);
-            sum[v & 1] = add2(sum[v & 1], pack2(ex2(e0), ex2(e1)));
-          }
-        };
-        const auto some = [&](const uint32_t (&s)[32], int c) {
-          const int2* z2 = reinterpret_cast<const int2*>(rw.sees + 32 * c);
-#pragma unroll
-          for (int v = 0; v < 16; ++v) {
-            const int2 z = z2[v];
-            float e0, e1;
-            unpack2(mul2(pack2(__uint_as_float(s[2 * v]), __uint_as_float(s[2 * v + 1])), scale2),
-                    e0, e1);
-            // (selected, not multiplied: a row that does not count may hold anything)
-            sum[v & 1] =
-                add2(sum[v & 1], pack2(key <= z.x ? ex2(e0) : 0.f, key <= z.y ? ex2(e1) : 0.f));
-          }
-        };
         if (!idle) {
-          // All columns to registers, and the buffer back to the MMA issuer before they
-          // are summed.
-          uint32_t s[4][32];
+          // 32 rows at a time; the buffer goes back to the MMA issuer before the last of
+          // them are summed.
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(t_s + 32u * c, s[c]);
-          tmem_ld_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s_empty[u.bar()]);
-          const int least = min(min(rw.least[0], rw.least[1]), min(rw.least[2], rw.least[3]));
-          if (least >= key_hi) {
+          for (int c = c0; c < c0 + 2; ++c) {
+            uint32_t s[32];
+            tmem_ld_32x32b_x32(t_s + 32u * c, s);
+            tmem_ld_wait();
+            if (c == c0 + 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&s_empty[u.bar()]);
+            }
+            if (rw.least[c] >= key_hi) {  // all of them see all of the warp's keys
 #pragma unroll
-            for (int c = 0; c < 4; ++c) all(s[c]);
-          } else {
+              for (int v = 0; v < 16; ++v) {
+                float e0, e1;
+                unpack2(mul2(pack2(__uint_as_float(s[2 * v]), __uint_as_float(s[2 * v + 1])),
+                             scale2), e0, e1);
+                sum[v & 1] = add2(sum[v & 1], pack2(ex2(e0), ex2(e1)));
+              }
+            } else if (rw.most[c] >= key_lo) {
+              const int2* z2 = reinterpret_cast<const int2*>(rw.sees + 32 * c);
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if (rw.most[c] >= key_lo) some(s[c], c);
+              for (int v = 0; v < 16; ++v) {
+                const int2 z = z2[v];
+                float e0, e1;
+                unpack2(mul2(pack2(__uint_as_float(s[2 * v]), __uint_as_float(s[2 * v + 1])),
+                             scale2), e0, e1);
+                // (selected, not multiplied: a row that does not count may hold anything)
+                sum[v & 1] = add2(sum[v & 1],
+                                  pack2(key <= z.x ? ex2(e0) : 0.f, key <= z.y ? ex2(e1) : 0.f));
+              }
+            }
           }
         }
         __syncwarp();
@@ -489,22 +490,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       float a0, a1;
       unpack2(add2(sum[0], sum[1]), a0, a1);
-      const float a = a0 + a1;
+      float a = a0 + a1;
+      if (c0 != 0) {
+        others[ss * kWeighBlockKeys + mine] = a;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sum_full[ss]);
+      } else {
+        if (!(ok = warp_wait(&sum_full[ss], sum_phase, p.ctx, abort))) break;
+        a += others[ss * kWeighBlockKeys + mine];
+      }
+      if (++ss == kSumStages) {
+        ss = 0;
+        sum_phase ^= 1u;
+      }
+      const bool first_item = !started;
+      started = true;
+      if (c0 != 0) continue;
       if (it.j0 == 0 && it.j1 == it.n) {
         if (key < it.k1) {
           const int64_t row = weigh_row(b, it.seq, key, it.h);
           if (row >= 0) weigh_add(p, it.seq, it.fresh, key, row, a);
         }
       } else {
-        const int slot = 2 * static_cast<int>(blockIdx.x) + (started ? 1 : 0);
+        const int slot = 2 * static_cast<int>(blockIdx.x) + (first_item ? 0 : 1);
         p.parts[static_cast<int64_t>(slot) * kWeighBlockKeys + mine] = a;
         if (tid == 0)
           p.records[slot] = WeighRecord{1, it.run, it.h, it.i, it.j0 == 0, it.j1 == it.n, 0, 0};
       }
-      started = true;
     }
   } else {
-  reg_dec<kOtherRegs>();
   if (warp < kTmaWarp) {
     // ============================================================ MMA issuers
     const int half = warp - kMmaWarp;
