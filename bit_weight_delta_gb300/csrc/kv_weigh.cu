@@ -10,12 +10,11 @@
 // reading the keys; longer ones are kv_weigh_tile.cu's, on the tensor cores, whose
 // parts of blocks are joined here.
 //
-// A unit is 32 keys of a run and key head, worked on by one warp: the keys are the
-// rows of mma.sync tiles (16 keys by 8 query rows by 16 elements) and stay in
-// registers while the query rows pass, 8 at a time, so that a key's sum stays
-// in its lanes.  Both operands are loaded straight from memory, 16 bytes a lane:
-// which of a row's elements a lane holds is the same for both, and a product's
-// sum does not care about their order.
+// A unit is 16 keys of a run and key head; every warp has an even share of all units,
+// in the order of runs, heads and keys.  The keys are the rows of mma.sync tiles (16
+// keys by 8 query rows by 16 elements), so that a key's sum stays in its four lanes,
+// and are loaded straight from memory to registers, 16 bytes a lane: which of a row's elements a lane holds is the same for keys and
+// queries, and a product's sum does not care about their order.
 #include <cmath>
 #include <cstdint>
 
@@ -29,7 +28,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnitKeys = 32;
+constexpr int kUnitKeys = 16;
 static_assert(kThreads == kWeighBlockKeys, "the join takes a key per thread");
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -41,17 +40,11 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// A run with its units per key head: none where the tile kernel has it.
-struct Run : WeighRun {
-  int units;
-};
-__device__ __forceinline__ Run run_of(const WeighArgs& p, int r, bool* bad) {
-  Run x{};
-  static_cast<WeighRun&>(x) = weigh_run(p, r, bad);
+// Units per key head of a run: none where the tile kernel has it.
+__device__ __forceinline__ int units_of(const WeighArgs& p, const WeighRun& x) {
   const int64_t rows =
       static_cast<int64_t>(x.tok1 - x.tok0) * (p.b.n_q_heads / p.b.n_kv_heads);
-  x.units = rows <= kWeighShortRows && x.k1 > x.k0 ? (x.k1 - x.k0 + kUnitKeys - 1) / kUnitKeys : 0;
-  return x;
+  return rows <= kWeighShortRows && x.k1 > x.k0 ? (x.k1 - x.k0 + kUnitKeys - 1) / kUnitKeys : 0;
 }
 
 // The blocks that several CTAs of the tile kernel share: their parts in their
@@ -79,26 +72,48 @@ __device__ void join_parts(const WeighArgs& p) {
   }
 }
 
+// A unit on its way: its rows g8 and g8 + 8, 8 elements of every 32 per lane, where it
+// lies in the cache (−1: nowhere) and what the lane's key had.
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv_weigh_kernel(const WeighArgs p) {
+struct Tile {
+  uint4 k[2][D / 32];
+  int row;
+  float old;
+};
+
+// CTAs per SM, by the registers that the keys and queries take.
+template <int D, int NT>
+constexpr int kCtas = NT == 1 ? (D == 128 ? 3 : 4) : (D == 128 ? 2 : 3);
+
+// NT: query rows in tiles of 8, at most.
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, kCtas<D, NT>) kv_weigh_kernel(const WeighArgs p) {
   __shared__ int64_t s_sum[kWarps];
+  __shared__ WeighRun s_run[kThreads];
+  __shared__ int64_t s_before[kThreads + 1];  // units before each run of the round
   const bd_attention_batch& b = p.b;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int H = b.n_kv_heads;
-  const uint32_t G = b.n_q_heads / H;
+  const int G = b.n_q_heads / H;
   const int n_run = b.n_seq + b.n_group;
   // The tile kernel ahead, where there is one, lets this one start only when it has
   // seen all before it complete: the units here need nothing of it, and run while
   // its last CTAs do.
   if (p.tile_ctas == 0) griddep_wait();
   griddep_launch_dependents();
-  // ---- an even share of all units for each warp
+  // ---- an even share of all units for each warp; the first runs, a run per thread
   bool bad = false;
-  int64_t mine = 0;
-  for (int r = tid; r < n_run; r += kThreads) mine += run_of(p, r, &bad).units;
+  WeighRun mine{};
+  int units = 0;
+  if (tid < n_run) {
+    mine = weigh_run(p, tid, &bad);
+    units = units_of(p, mine);
+  }
+  int64_t all = units;
+  for (int r = tid + kThreads; r < n_run; r += kThreads) all += units_of(p, weigh_run(p, r, &bad));
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, off);
-  if (lane == 0) s_sum[warp] = mine;
+  for (int off = 16; off > 0; off >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, off);
+  if (lane == 0) s_sum[warp] = all;
   bad = __syncthreads_or(bad);
   int64_t total = 0;
   for (int i = 0; i < kWarps; ++i) total += s_sum[i];
@@ -106,139 +121,177 @@ __global__ void __launch_bounds__(kThreads) kv_weigh_kernel(const WeighArgs p) {
   if (bad && tid == 0 && blockIdx.x == 0) record_error(p.ctx, kErrBounds);
   const int64_t gw = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
   const int64_t n_warps = static_cast<int64_t>(gridDim.x) * kWarps;
-  const int64_t u0 = total * gw / n_warps, u1 = total * (gw + 1) / n_warps;
+  const int64_t each = (total + n_warps - 1) / n_warps;
+  int64_t u = each * gw < total ? each * gw : total;
+  const int64_t u1 = u + each < total ? u + each : total;
+  const int64_t cta_end = each * kWarps * (blockIdx.x + 1) < total
+                              ? each * kWarps * (blockIdx.x + 1) : total;
 
   const int g8 = lane >> 2, quad = lane & 3;
   const int page_shift = 31 - __clz(b.page_size);
   const bool windowed = p.window > 0 && p.window < b.max_q_len;
-  // 32 runs at a time: a lane holds one of them and the units before it
   int64_t before = 0;
-  int64_t u = u0;
-  for (int r0 = 0; r0 < n_run && u < u1; r0 += 32) {
-    Run own{};
-    if (r0 + lane < n_run) own = run_of(p, r0 + lane, &bad);
-    int64_t inc = static_cast<int64_t>(own.units) * H;
+  for (int base = 0; base < n_run && before < cta_end; base += kThreads) {
+    if (base > 0) {
+      mine = WeighRun{};
+      units = 0;
+      if (base + tid < n_run) {
+        mine = weigh_run(p, base + tid, &bad);
+        units = units_of(p, mine);
+      }
+    }
+    int64_t inc = units;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int64_t o = __shfl_up_sync(0xFFFFFFFFu, inc, off);
       if (lane >= off) inc += o;
     }
-    const int64_t end = before + __shfl_sync(0xFFFFFFFFu, inc, 31);
-    for (; u < u1 && u < end; ++u) {
-      const int src = __ffs(__ballot_sync(0xFFFFFFFFu, before + inc > u)) - 1;
-      Run x;
-      x.seq = __shfl_sync(0xFFFFFFFFu, own.seq, src);
-      x.k0 = __shfl_sync(0xFFFFFFFFu, own.k0, src);
-      x.k1 = __shfl_sync(0xFFFFFFFFu, own.k1, src);
-      x.tok0 = __shfl_sync(0xFFFFFFFFu, own.tok0, src);
-      x.tok1 = __shfl_sync(0xFFFFFFFFu, own.tok1, src);
-      x.causal = __shfl_sync(0xFFFFFFFFu, own.causal, src);
-      x.fresh = __shfl_sync(0xFFFFFFFFu, own.fresh, src);
-      x.units = __shfl_sync(0xFFFFFFFFu, own.units, src);
-      const bool group = r0 + src >= b.n_seq;
-      const int64_t first = __shfl_sync(0xFFFFFFFFu, before + inc - static_cast<int64_t>(own.units) * H, src);
-      const int at = static_cast<int>(u - first);
-      const int h = at / x.units;
-      const int key0 = x.k0 + (at - h * x.units) * kUnitKeys;
-
-      // ---- the unit's keys: tiles of 16, each within a page
-      const int32_t* table = b.page_table + static_cast<int64_t>(x.seq) * b.table_stride;
-      uint4 k[2][2][D / 32];
-      int64_t tile_row[2];  // of the tile's first key in the cache, or −1
+    __syncthreads();  // sums and the round before have been read
+    if (lane == 31) s_sum[warp] = inc;
+    __syncthreads();
+    for (int i = 0; i < warp; ++i) inc += s_sum[i];
+    s_run[tid] = mine;
+    s_before[tid + 1] = before + inc * H;
+    if (tid == 0) s_before[0] = before;
+    __syncthreads();
+    before = s_before[kThreads];
+    // the run that holds the warp's first unit: the last that begins at or before it
+    int r = -1;
+    if (u < u1 && u < before) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int key = key0 + 16 * i;
-        tile_row[i] = -1;
-        if (key < x.k1) {
-          const int page = table[key >> page_shift];
+      for (int i = 0; i < kWarps; ++i)
+        r += __popc(__ballot_sync(0xFFFFFFFFu, s_before[32 * i + lane] <= u));
+    }
+    while (u < u1 && u < before) {
+      while (s_before[r + 1] <= u) ++r;  // runs without units
+      const WeighRun x = s_run[r];
+      const bool group = base + r >= b.n_seq;
+      const int per_head = (x.k1 - x.k0 + kUnitKeys - 1) / kUnitKeys;
+      const int64_t at = u - s_before[r];
+      const int h = static_cast<int>(at < (1ll << 31) ? static_cast<uint32_t>(at) / per_head
+                                                      : at / per_head);
+      const int blk0 = static_cast<int>(at - static_cast<int64_t>(h) * per_head);
+      const int blk1 = u1 - u < per_head - blk0 ? blk0 + static_cast<int>(u1 - u) : per_head;
+      u += blk1 - blk0;
+
+      // ---- the units blk0 .. blk1 of run x and head h
+      const int32_t* table = b.page_table + static_cast<int64_t>(x.seq) * b.table_stride;
+      const auto page_of = [&](int blk) {
+        return blk < blk1 ? table[(x.k0 + blk * kUnitKeys) >> page_shift] : 0;
+      };
+      const auto fetch = [&](Tile<D>& t, int blk, int page) {
+        const int key = x.k0 + blk * kUnitKeys;
+        t.row = -1;
+        t.old = 0.f;
+        if (blk < blk1) {
           if (page >= 0 && page < b.n_pages)
-            tile_row[i] = ((static_cast<int64_t>(page) * H + h) << page_shift) +
-                          (key & (b.page_size - 1));
+            t.row = ((page * H + h) << page_shift) + (key & (b.page_size - 1));  // below 2^31
           else
             record_error(p.ctx, kErrBounds);
         }
+        const uint16_t* src = p.k_pages + static_cast<int64_t>(t.row + g8) * D + 8 * quad;
 #pragma unroll
         for (int y = 0; y < 2; ++y)
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) {
-            k[i][y][j] = make_uint4(0u, 0u, 0u, 0u);
-            if (tile_row[i] >= 0 && key + g8 + 8 * y < x.k1)
-              k[i][y][j] = ldg_stream_v4(p.k_pages + (tile_row[i] + g8 + 8 * y) * D + 32 * j + 8 * quad);
+            t.k[y][j] = make_uint4(0u, 0u, 0u, 0u);
+            if (t.row >= 0 && key + g8 + 8 * y < x.k1)
+              t.k[y][j] = ldg_stream_v4(src + y * (8 * D) + 32 * j);
           }
-      }
-      // ---- the query rows, 8 at a time
-      float sum[2][2] = {};
-      const uint32_t rows = static_cast<uint32_t>(x.tok1 - x.tok0) * G;
-      // rows before the first that sees a key of the unit are left out
-      const int t_lo = group ? x.tok0 : max(x.tok0, key0 - x.causal);
-      for (uint32_t r = static_cast<uint32_t>(t_lo - x.tok0) * G & ~7u; r < rows; r += 8) {
-        uint4 q[D / 32];
-        {
-          const uint32_t row = r + g8;
-          const int t = x.tok0 + row / G;
-          const uint16_t* src_q =
-              p.q + (static_cast<int64_t>(t) * b.n_q_heads + h * G + row % G) * D + 8 * quad;
+        if (t.row >= 0 && quad < 2 && key + g8 + 8 * quad < x.k1)
+          t.old = p.weights[t.row + g8 + 8 * quad];
+      };
+      int page = page_of(blk0);
+      Tile<D> t;
+      fetch(t, blk0, page);
+      page = page_of(blk0 + 1);
+      // the query rows, as the products' other operand
+      const int rows = (x.tok1 - x.tok0) * G;  // at most 8·NT
+      uint4 q[NT][D / 32];
+      float minus[NT][2];
+      int sees[NT][2];
 #pragma unroll
-          for (int j = 0; j < D / 32; ++j)
-            q[j] = row < rows ? ldg_v4(src_q + 32 * j) : make_uint4(0u, 0u, 0u, 0u);
-        }
-        float lse[2];
-        int sees[2];
+      for (int i = 0; i < NT; ++i) {
+        const int row = 8 * i + g8;
+        const uint16_t* src = p.q +
+            (static_cast<int64_t>(x.tok0 + row / G) * b.n_q_heads + h * G + row % G) * D + 8 * quad;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j)
+          q[i][j] = row < rows ? ldg_v4(src + 32 * j) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const uint32_t row = r + 2 * quad + y;
-          lse[y] = INFINITY;
-          sees[y] = -1;
-          if (row < rows) {
-            const int t = x.tok0 + row / G;
-            const float l = p.lse[static_cast<int64_t>(t) * b.n_q_heads + h * G + row % G];
-            const bool counts =
-                !group || !windowed ||
-                weigh_in_window(p, t, x.seq, b.group_offsets[r0 + src - b.n_seq + 1]);
-            if (isfinite(l) && counts) {
-              lse[y] = l * kWeighLog2e;
-              sees[y] = group ? INT32_MAX : t + x.causal;
+          const int c = 8 * i + 2 * quad + y;
+          minus[i][y] = 0.f;
+          sees[i][y] = -1;
+          if (c < rows) {
+            const int tok = x.tok0 + c / G;
+            const float l = p.lse[static_cast<int64_t>(tok) * b.n_q_heads + h * G + c % G];
+            if (isfinite(l) &&
+                (!group || !windowed ||
+                 weigh_in_window(p, tok, x.seq, b.group_offsets[base + r - b.n_seq + 1]))) {
+              minus[i][y] = -l * kWeighLog2e;
+              sees[i][y] = group ? INT32_MAX : tok + x.causal;
             }
           }
         }
+      }
+      const auto weigh = [&](const Tile<D>& t, int blk) {
+        const int key = x.k0 + blk * kUnitKeys + g8;
+        float sum[2] = {0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float c[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < NT; ++i) {
+          float c[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) {
-            mma_16816(c, k[i][0][j].x, k[i][1][j].x, k[i][0][j].y, k[i][1][j].y, q[j].x, q[j].y);
-            mma_16816(c, k[i][0][j].z, k[i][1][j].z, k[i][0][j].w, k[i][1][j].w, q[j].z, q[j].w);
+            mma_16816(c, t.k[0][j].x, t.k[1][j].x, t.k[0][j].y, t.k[1][j].y, q[i][j].x, q[i][j].y);
+            mma_16816(d, t.k[0][j].z, t.k[1][j].z, t.k[0][j].w, t.k[1][j].w, q[i][j].z, q[i][j].w);
           }
-          const int key = key0 + 16 * i + g8;
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            const float w = ex2(fmaf(c[y], p.scale_log2, -lse[y & 1]));
-            if (key + 8 * (y >> 1) <= sees[y & 1]) sum[i][y >> 1] += w;
+            const float w = ex2(fmaf(c[y] + d[y], p.scale_log2, minus[i][y & 1]));
+            // (selected, not multiplied: a row that does not count may hold anything)
+            sum[y >> 1] += key + 8 * (y >> 1) <= sees[i][y & 1] ? w : 0.f;
           }
         }
-      }
-      // ---- a key's four lanes together; each then writes one key
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          sum[i][y] += __shfl_xor_sync(0xFFFFFFFFu, sum[i][y], 1);
-          sum[i][y] += __shfl_xor_sync(0xFFFFFFFFu, sum[i][y], 2);
+          sum[y] += __shfl_xor_sync(0xFFFFFFFFu, sum[y], 1);
+          sum[y] += __shfl_xor_sync(0xFFFFFFFFu, sum[y], 2);
         }
-      const int i = quad >> 1, y = quad & 1;
-      const float a = i == 0 ? (y == 0 ? sum[0][0] : sum[0][1]) : (y == 0 ? sum[1][0] : sum[1][1]);
-      const int key = key0 + 16 * i + 8 * y + g8;
-      const int64_t tile = i == 0 ? tile_row[0] : tile_row[1];
-      if (key < x.k1 && tile >= 0) {
-        weigh_add(p, x.seq, x.fresh, key, tile + 8 * y + g8, a);
+        const int mine_key = key + 8 * quad;  // of the first two lanes of four
+        if (t.row >= 0 && quad < 2 && mine_key < x.k1) {
+          const int row = t.row + g8 + 8 * quad;
+          const float a = quad == 0 ? sum[0] : sum[1];
+          if (mine_key >= x.fresh) {
+            p.weights[row] = a;
+            p.positions[row] = mine_key + (p.pos_offset != nullptr ? p.pos_offset[x.seq] : 0);
+          } else {
+            p.weights[row] = t.old + a;
+          }
+        }
+      };
+#pragma unroll 1
+      for (int blk = blk0; blk < blk1; ++blk) {
+        weigh(t, blk);
+        fetch(t, blk + 1, page);
+        page = page_of(blk + 2);
       }
     }
-    before = end;
   }
   if (p.tile_ctas > 0) {
     griddep_wait();
     join_parts(p);
   }
+}
+
+template <int D>
+cudaError_t launch_short(const WeighArgs& p, int sms, cudaStream_t s) {
+  const dim3 block(kThreads);
+  const int64_t rows = static_cast<int64_t>(p.b.max_q_len) * (p.b.n_q_heads / p.b.n_kv_heads);
+  // (a group of few members has up to 16 rows of single tokens)
+  return rows <= 8 && p.b.n_group == 0
+             ? launch_pdl(kv_weigh_kernel<D, 1>, dim3(kCtas<D, 1> * sms), block, 0, s, p)
+             : launch_pdl(kv_weigh_kernel<D, 2>, dim3(kCtas<D, 2> * sms), block, 0, s, p);
 }
 
 bool off(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) != 0; }
@@ -274,10 +327,8 @@ bd_status run_weigh(WeighArgs& p, int sms, cudaStream_t s) {
       return BD_ERR_CUDA;
     if (launch_weigh_tile(p, m, s) != cudaSuccess) return BD_ERR_CUDA;
   }
-  const dim3 grid(2 * sms), block(kThreads);
-  const cudaError_t e = b.head_dim == 128
-                            ? launch_pdl(kv_weigh_kernel<128>, grid, block, 0, s, p)
-                            : launch_pdl(kv_weigh_kernel<64>, grid, block, 0, s, p);
+  const cudaError_t e = b.head_dim == 128 ? launch_short<128>(p, sms, s)
+                                          : launch_short<64>(p, sms, s);
   return e == cudaSuccess ? BD_OK : BD_ERR_CUDA;
 }
 
