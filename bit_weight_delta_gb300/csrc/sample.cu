@@ -2,7 +2,7 @@
 //
 // A bf16 row has fewer than 2^16 different values, so all that the cuts and the
 // choice need of it is how often each value occurs: one pass over the row counts
-// its values in shared memory, 16 bits a value.  A value's weight
+// its values in shared memory.  A value's weight
 //   w = exp((v − largest)/T)
 // is then formed once per value instead of once per token, to about 2^-40 and as
 // a whole number of 2^-44 steps, and every cut is a prefix of the order (largest value
@@ -11,11 +11,20 @@
 // however a row is spread.  The chosen value and its number r among its equals
 // give the token: a second look at one CTA's part of the row finds the r-th.
 //
+// Values are numbered by their bin: 0x7FFF − bits for positive ones and bits for
+// negative ones, the largest value first.  Counted are the values from 2^-24 to 2^16 in
+// size, and zero: 10241 counters, of 32 bits.  (All bins' would fill an SM's shared
+// memory with 16-bit ones, and their phases of few threads would stand alone: 500
+// rows of 99991 took 161 us.)  A row with another value among those that may be taken
+// goes through all bins in several passes, by one CTA.
+//
+// Logits whose weight is less than 2^-46 next to the largest of the part's first
+// ones cannot be taken and are not counted: masked ones above all, which would be
+// additions to one address.
+//
 // A row is shared by a cluster of CTAs, each with counts of its own part, which
-// are added where they are read (distributed shared memory).  Values lie in the
-// order of the bins: bin = 0x7FFF − bits for positive ones and bits for
-// negative ones, a bin's count in half of a 32-bit word (bin & 0x7FFF): the low
-// half for positive values.  Segments are 32 bins; most are empty.
+// are added where they are read (distributed shared memory); a cluster takes row
+// after row.  Segments are 128 bins; most are empty.
 #include <cooperative_groups.h>
 
 #include <cstdint>
@@ -30,7 +39,7 @@ namespace cg = cooperative_groups;
 
 struct SampleArgs {
   const uint16_t* logits;
-  int64_t V, stride;
+  int64_t M, V, stride;
   const float *u, *temperature, *top_p, *min_p;
   const int32_t* top_k;
   int32_t* tokens;
@@ -38,16 +47,23 @@ struct SampleArgs {
   DevCtx ctx;
 };
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kWords = 32768;   // counts, two bins each
-constexpr int kSegs = 2048;     // of 32 bins
+constexpr int kCtas = 2;          // per SM
 constexpr int kMaxCluster = 8;
-constexpr int kMaxChunks = 8190;  // 8-element chunks of a CTA: counts stay below 2^16
 constexpr int kOneBits = 44;      // a weight of 1 is 2^44; 2^19 of them stay below 2^63
 constexpr int kBinFirst = 0x7F;   // +inf; NaN lies below
 constexpr int kBinLast = 0xFF7F;  // −inf and NaN lie above
 constexpr int kZeroBin = 0x7FFF;
+constexpr int kSegs = 512;        // of 128 bins, of all bins
+
+// The counted values: kSpan bins of either sign, with the zero in a segment of its own
+// between them.
+constexpr int kSpan = 40 * 128;
+constexpr int kPosBin = 0x8000 - ((127 + 16) << 7);  // of the largest, just below 2^16
+constexpr int kNegBin = 0x8000 + ((127 - 24) << 7);  // of −2^-24
+constexpr int kZeroSlot = kSpan, kNegSlot = kSpan + 128;
+constexpr int kSlots = 2 * kSpan + 128;
 
 // 2^(j/64) to 48 bits, from the exponential's series.
 constexpr double exp_series(double x) {
@@ -73,20 +89,23 @@ constexpr Pow2Table make_pow2_table() {
 __device__ constexpr Pow2Table kPow2 = make_pow2_table();
 
 struct Shared {
-  uint32_t counts[kWords];
-  uint64_t mass[kSegs];     // rank 0: sums before each listed segment
+  uint32_t counts[kSlots];
+  uint64_t mass[kSegs];            // rank 0: sums before each listed segment
   uint32_t number[kSegs];
-  uint16_t list[kSegs];     // segments that are not empty, in order
-  uint32_t occupied[kSegs / 32];   // this CTA's
+  uint16_t list[kSegs];            // segments that are not empty, in order
+  uint32_t seg_counts[128];        // one segment's, where all bins are gone through
+  uint32_t occupied[(kSlots / 128 + 31) / 32];   // this CTA's
   float pow2_hi[64], pow2_lo[64];
   uint64_t scan_mass[kWarps];
   uint32_t scan_number[kWarps];
-  float c_hi, c_lo;         // 2·log2(e)/T
-  int first;                // the largest value's bin, of this CTA's part
-  int all_first;
+  float half, c_hi, c_lo;          // 1/2 and 2·log2(e)/T (2^-65 and 2^64 of it for large T)
+  int guess;                       // the largest of the first logits, of this CTA's part
+  int first, all_first;            // the largest value's bin, of this part and of the row
+  int wide, all_wide;              // values outside of the counted ones
   int n_list;
-  int find_bin;             // the token's value, or −1: not in this CTA's part
-  uint32_t find_rank;       // its number among this CTA's tokens of that value
+  int asked;                       // the segment that the CTA is to count, or −1
+  int find_bin;                    // the token's value, or −1: not in this CTA's part
+  uint32_t find_rank;              // its number among this CTA's tokens of that value
   float find_prob;
   uint32_t warp_hits[kWarps];
 };
@@ -100,10 +119,10 @@ __device__ __forceinline__ float value_of(int bin) {
 // (v − max)·log2(e)/T held in two floats (half the difference, so that it stays
 // finite; 2·log2(e)/T for it).  2^y = 2^n · 2^(j/64) · e^t with |t| < 0.0055, where
 // e^t − 1 = t + t²/2 + … needs only its first term in two floats.
-__device__ uint64_t weight_of(const Shared& sh, int bin, int first) {
+__device__ __forceinline__ uint64_t weigh(const Shared& sh, int bin, int first) {
   if (bin == first) return uint64_t{1} << kOneBits;
   if (first == kBinFirst) return 0;  // +inf takes all
-  const float a = 0.5f * value_of(bin), b = -0.5f * value_of(first);
+  const float a = sh.half * value_of(bin), b = -sh.half * value_of(first);
   const float dh = __fadd_rn(a, b);
   const float bb = __fsub_rn(dh, a);
   const float dl = __fadd_rn(__fsub_rn(a, __fsub_rn(dh, bb)), __fsub_rn(b, bb));
@@ -132,6 +151,9 @@ __device__ uint64_t weight_of(const Shared& sh, int bin, int first) {
   const float unit = __int_as_float((127 + kOneBits + (ki >> 6)) << 23);
   return static_cast<uint64_t>(__float2ll_rn(s * unit) + __float2ll_rn(rest * unit));
 }
+__device__ __noinline__ uint64_t weight_of(const Shared& sh, int bin, int first) {
+  return weigh(sh, bin, first);
+}
 
 template <typename T>
 __device__ __forceinline__ T warp_inclusive(T v) {
@@ -144,7 +166,7 @@ __device__ __forceinline__ T warp_inclusive(T v) {
   return v;
 }
 
-// Eight logits from a 16-byte boundary on; those outside the row are NaN.
+// Eight logits from a 16-byte boundary on; those outside the row are −NaN.
 __device__ __forceinline__ uint4 load_chunk(const uint16_t* row, int64_t V, int mis, int chunk) {
   const int64_t i0 = static_cast<int64_t>(chunk) * 8 - mis;
   if (i0 >= 0 && i0 + 8 <= V) return ldg_stream_v4(row + i0);
@@ -152,8 +174,8 @@ __device__ __forceinline__ uint4 load_chunk(const uint16_t* row, int64_t V, int 
 #pragma unroll
   for (int x = 0; x < 4; ++x) {
     const int64_t i = i0 + 2 * x;
-    const uint32_t lo = i >= 0 && i < V ? row[i] : 0x7FFFu;
-    const uint32_t hi = i + 1 >= 0 && i + 1 < V ? row[i + 1] : 0x7FFFu;
+    const uint32_t lo = i >= 0 && i < V ? row[i] : 0xFFFFu;
+    const uint32_t hi = i + 1 >= 0 && i + 1 < V ? row[i + 1] : 0xFFFFu;
     w[x] = lo | hi << 16;
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
@@ -166,8 +188,45 @@ __device__ __forceinline__ uint32_t bins_of(uint32_t w) {
   return w ^ (0x7FFF7FFFu & ~negative);
 }
 
-__device__ __forceinline__ void count(uint32_t* counts, uint32_t bin) {
-  atomicAdd(counts + (bin & 0x7FFFu), bin & 0x8000u ? 0x10000u : 1u);
+// The bin of a slot of the counters (any, where a slot has none).
+__device__ __forceinline__ int bin_of_slot(int slot) {
+  return slot < kSpan ? slot + kPosBin : slot < kNegSlot ? kZeroBin : slot - kNegSlot + kNegBin;
+}
+
+// Counts a logit; true for one that has no counter.  (Additions of 1 to one address
+// are merged by the hardware: 17 a clock, and 8 to different ones.)
+__device__ __forceinline__ bool count(uint32_t* counts, int bin, int limit) {
+  const bool negative = bin >= 0x8000;
+  const uint32_t at = static_cast<uint32_t>(bin - (negative ? kNegBin : kPosBin));
+  if (bin > limit) return false;
+  if (at < kSpan) {
+    atomicAdd(counts + at + (negative ? kNegSlot : 0), 1u);
+    return false;
+  }
+  if (bin != kZeroBin && bin != kZeroBin + 1) return true;
+  atomicAdd(counts + kZeroSlot, 1u);
+  return false;
+}
+
+// The last bin whose logits can have a weight, where the largest lies in `guess` or
+// before it: 33·T below it, which is 47 powers of two.
+__device__ int limit_of(int guess, float t) {
+  if (guess < kBinFirst || guess > kBinLast) return kBinLast;  // nothing is known
+  const float v = value_of(guess) - 33.f * t;
+  if (!(t >= 0.f) || !(v > -INFINITY)) return kBinLast;
+  uint32_t bits = __float_as_uint(v) >> 16;
+  if (bits & 0x8000u) ++bits;  // a step further down (for positive ones the cut is one)
+  const int bin = static_cast<int>(bits & 0x8000u ? bits : 0x7FFFu - bits);
+  return bin == kZeroBin ? kZeroBin + 1 : (bin < kBinLast ? bin : kBinLast);  // with −0
+}
+
+// a / b, below 2^20; 0 where b is.
+__device__ __forceinline__ uint32_t quotient(uint64_t a, uint64_t b) {
+  if (b == 0) return 0;
+  uint32_t q = static_cast<uint32_t>(__fdividef(static_cast<float>(a), static_cast<float>(b)));
+  while (static_cast<uint64_t>(q) * b > a) --q;
+  while ((static_cast<uint64_t>(q) + 1) * b <= a) ++q;
+  return q;
 }
 
 // What a position in the order needs: the bin that holds it and what lies before.
@@ -179,348 +238,292 @@ struct Place {
   uint32_t count;    // of them
 };
 
-// Tokens of `bin` in the whole row.
-__device__ __forceinline__ uint32_t count_of(const uint32_t* const (&counts)[kMaxCluster],
-                                             int ranks, int bin) {
-  const int shift = bin & 0x8000 ? 16 : 0;
-  uint32_t n = 0;
-#pragma unroll
-  for (int r = 0; r < kMaxCluster; ++r)
-    if (r < ranks) n += counts[r][bin & 0x7FFF] >> shift & 0xFFFFu;
-  return n;
-}
+// ---- where the counts of a listed segment come from
 
+// The cluster's counters.
 template <int C>
-__global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs p) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  Shared& sh = *reinterpret_cast<Shared*>(smem);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = C == 1 ? 0 : static_cast<int>(cluster.block_rank());
-  const int64_t m = blockIdx.x / C;
-  const uint16_t* row = p.logits + m * p.stride;
-  const auto meet = [&] {
-    if constexpr (C == 1)
-      __syncthreads();
-    else
-      cluster.sync();
-  };
-
-  for (int i = tid; i < kWords / 4; i += kThreads)
-    reinterpret_cast<uint4*>(sh.counts)[i] = make_uint4(0u, 0u, 0u, 0u);
-  if (tid < 64) {
-    sh.pow2_hi[tid] = kPow2.hi[tid];
-    sh.pow2_lo[tid] = kPow2.lo[tid];
-    sh.occupied[tid] = 0u;
-  }
-  if (tid == 0) sh.first = kBinLast + 1;
-  griddep_wait();
-  griddep_launch_dependents();
-  if (tid == 0) {
-    const double c = 2.8853900817779268 /  // 2·log2(e)
-                     static_cast<double>(p.temperature != nullptr ? p.temperature[m] : 1.f);
-    sh.c_hi = static_cast<float>(c);
-    sh.c_lo = isinf(sh.c_hi) ? 0.f : static_cast<float>(c - static_cast<double>(sh.c_hi));
-  }
-  __syncthreads();
-
-  // ---- counts of this CTA's part
-  const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(row) >> 1 & 7);
-  const int chunks = static_cast<int>((p.V + mis + 7) >> 3);
-  const int per = (chunks + C - 1) / C;
-  const int c0 = rank * per < chunks ? rank * per : chunks;
-  const int c1 = c0 + per < chunks ? c0 + per : chunks;
-  constexpr int kUnroll = 4;
-  for (int c = c0 + tid; c < c1; c += kUnroll * kThreads) {
-    uint4 v[kUnroll];
+struct Counters {
+  const uint32_t* counts[C];
+  __device__ __forceinline__ int bin(int seg, int i) const { return bin_of_slot(128 * seg + i); }
+  // the lane's four bins
+  __device__ __forceinline__ void get(int seg, uint32_t (&n)[4]) const {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int x = 0; x < kUnroll; ++x)
-      if (c + x * kThreads < c1) v[x] = load_chunk(row, p.V, mis, c + x * kThreads);
-#pragma unroll
-    for (int x = 0; x < kUnroll; ++x) {
-      if (c + x * kThreads >= c1) break;
-      const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const uint32_t b = bins_of(w[y]);
-        count(sh.counts, b & 0xFFFFu);
-        count(sh.counts, b >> 16);
-      }
-    }
-  }
-  __syncthreads();
-  if (tid == 0) {  // −0 counts as 0
-    const uint32_t minus = sh.counts[0] >> 16;  // bin 0x8000
-    sh.counts[0] &= 0xFFFFu;
-    sh.counts[kZeroBin] += minus;
-  }
-  __syncthreads();
-
-  // ---- which segments hold anything
-  for (int s = warp; s < kSegs / 2; s += kWarps) {
-    const uint32_t w = sh.counts[32 * s + lane];
-    const uint32_t pos = __ballot_sync(0xFFFFFFFFu, (w & 0xFFFFu) != 0 && 32 * s + lane >= kBinFirst);
-    const uint32_t neg =
-        __ballot_sync(0xFFFFFFFFu, (w >> 16) != 0 && 0x8000 + 32 * s + lane <= kBinLast);
-    if (lane == 0) {
-      if (pos != 0) {
-        atomicOr(&sh.occupied[s >> 5], 1u << (s & 31));
-        atomicMin(&sh.first, 32 * s + __ffs(pos) - 1);
-      }
-      if (neg != 0) {
-        atomicOr(&sh.occupied[32 + (s >> 5)], 1u << (s & 31));
-        atomicMin(&sh.first, 0x8000 + 32 * s + __ffs(neg) - 1);
-      }
-    }
-  }
-  meet();
-  const uint32_t* counts[kMaxCluster];
-#pragma unroll
-  for (int r = 0; r < C; ++r)
-    counts[r] = C == 1 ? sh.counts : cluster.map_shared_rank(sh.counts, r);
-  if (warp == 0) {
-    int first = kBinLast + 1;
-    uint32_t w[2] = {0u, 0u};
+    for (int x = 0; x < 4; ++x) n[x] = 0;
 #pragma unroll
     for (int r = 0; r < C; ++r) {
-      const Shared* o = C == 1 ? &sh : cluster.map_shared_rank(&sh, r);
-      first = o->first < first ? o->first : first;
-      w[0] |= o->occupied[lane];
-      w[1] |= o->occupied[32 + lane];
+      const uint4 w = reinterpret_cast<const uint4*>(counts[r])[seg * 32 + lane];
+      n[0] += w.x;
+      n[1] += w.y;
+      n[2] += w.z;
+      n[3] += w.w;
     }
-    int at = 0;
+  }
+};
+
+__device__ __forceinline__ void cta_barrier() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+}
+
+// Tokens of the bins [base, base + n) in the whole row; a barrier lies before and
+// behind it.
+__device__ void count_range(const SampleArgs& p, const uint16_t* row, int mis, int base, int n,
+                            uint32_t* counts) {
+  const int chunks = static_cast<int>((p.V + mis + 7) >> 3);
+  for (int c = threadIdx.x; c < chunks; c += kThreads) {
+    const uint4 v = load_chunk(row, p.V, mis, c);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int inc = warp_inclusive(__popc(w[x]));
-      int to = at + inc - __popc(w[x]);
-      for (uint32_t bits = w[x]; bits != 0; bits &= bits - 1)
-        sh.list[to++] = static_cast<uint16_t>(1024 * x + 32 * lane + __ffs(bits) - 1);
-      at += __shfl_sync(0xFFFFFFFFu, inc, 31);
+    for (int y = 0; y < 8; ++y) {
+      const uint32_t b = bins_of(w[y >> 1]);
+      int bin = static_cast<int>(y & 1 ? b >> 16 : b & 0xFFFFu);
+      if (bin == kZeroBin + 1) bin = kZeroBin;
+      if (bin >= base && bin < base + n && bin >= kBinFirst && bin <= kBinLast)
+        atomicAdd(counts + (bin - base), 1u);
     }
-    if (lane == 0) {
-      sh.n_list = at;
-      sh.all_first = first;
-      sh.find_bin = -1;
+  }
+}
+
+// A segment of all bins, counted by the whole CTA when it is asked for.
+struct Recount {
+  const SampleArgs& p;
+  Shared& sh;
+  const uint16_t* row;
+  int mis;
+  __device__ __forceinline__ int bin(int seg, int i) const { return 128 * seg + i; }
+  __device__ void count() const {  // every thread
+    count_range(p, row, mis, 128 * sh.asked, 128, sh.seg_counts);
+    cta_barrier();
+  }
+  __device__ __forceinline__ void get(int seg, uint32_t (&n)[4]) const {  // the first warp
+    const int lane = threadIdx.x & 31;
+    reinterpret_cast<uint4*>(sh.seg_counts)[lane] = make_uint4(0u, 0u, 0u, 0u);
+    if (lane == 0) sh.asked = seg;
+    cta_barrier();
+    count();
+    const uint4 w = reinterpret_cast<const uint4*>(sh.seg_counts)[lane];
+    n[0] = w.x;
+    n[1] = w.y;
+    n[2] = w.z;
+    n[3] = w.w;
+    __syncwarp();
+  }
+  // the other warps, until the first has what it needs
+  __device__ void serve() const {
+    while (true) {
+      cta_barrier();
+      if (sh.asked < 0) return;
+      count();
     }
+  }
+  __device__ void done() const {
+    if ((threadIdx.x & 31) == 0) sh.asked = -1;
+    cta_barrier();
+  }
+};
+
+// Exclusive sums over the listed segments, in place, and those of all; the CTA.
+__device__ void sum_list(Shared& sh, int n_list) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  static_assert(kThreads >= kSegs, "a segment per thread");
+  const uint32_t n = tid < n_list ? sh.number[tid] : 0u;
+  const uint64_t w = tid < n_list ? sh.mass[tid] : 0u;
+  const uint32_t ni = warp_inclusive(n);
+  const uint64_t wi = warp_inclusive(w);
+  if (lane == 31) {
+    sh.scan_number[warp] = ni;
+    sh.scan_mass[warp] = wi;
   }
   __syncthreads();
-  const int n_list = sh.n_list, first = sh.all_first;
+  uint32_t nb = ni - n;
+  uint64_t wb = wi - w;
+  for (int i = 0; i < warp; ++i) {
+    nb += sh.scan_number[i];
+    wb += sh.scan_mass[i];
+  }
+  if (tid < n_list) {
+    sh.number[tid] = nb;
+    sh.mass[tid] = wb;
+  }
+  __syncthreads();
+  if (tid == kThreads - 1) {
+    sh.scan_number[0] = nb + n;
+    sh.scan_mass[0] = wb + w;
+  }
+  __syncthreads();
+}
 
-  // ---- the segments' numbers of tokens and weights, to the first CTA
-  Shared* lead = C == 1 ? &sh : cluster.map_shared_rank(&sh, 0);
-  for (int j = rank * kWarps + warp; j < n_list; j += C * kWarps) {
-    const int bin = 32 * sh.list[j] + lane;
-    uint32_t n = bin >= kBinFirst && bin <= kBinLast ? count_of(counts, C, bin) : 0u;
-    uint64_t w = n != 0 ? n * weight_of(sh, bin, first) : 0;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      n += __shfl_xor_sync(0xFFFFFFFFu, n, off);
-      w += __shfl_xor_sync(0xFFFFFFFFu, w, off);
+struct Settings {
+  float u, t, top_p, min_p;
+  int k;
+};
+
+// The cuts and the choice, by one warp: the value of the row's token, its number among
+// its equals and its probability.  False where there is none.
+template <class Source>
+__device__ __noinline__ bool choose(const SampleArgs& p, const Shared& sh, const Source& source,
+                                    const Settings& set, int n_list, int first, int* bin_out,
+                                    uint32_t* rank_out, float* prob_out) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t all = sh.scan_number[0];
+  const uint64_t all_mass = sh.scan_mass[0];
+  const bool bad = !(set.t >= 0.f) || isnan(set.u) || isnan(set.top_p) || isnan(set.min_p);
+  if (bad || all == 0) {
+    if (bad && lane == 0) record_error(p.ctx, kErrBounds);
+    return false;
+  }
+  // The last listed segment for which `before` holds (it holds for the first, and for
+  // all before one that it holds for).
+  const auto search = [&](auto before) {
+    int lo = 0, hi = n_list;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) >> 5, at = lo + lane * step;
+      const uint32_t yes = __ballot_sync(0xFFFFFFFFu, at < hi && (lane == 0 || before(at)));
+      const int top = 31 - __clz(yes);
+      lo += top * step;
+      hi = lo + step < hi ? lo + step : hi;
     }
-    if (lane == 0) {
-      lead->number[j] = n;
-      lead->mass[j] = w;
+    return lo;
+  };
+  // The first bin of segment j for which `inside` holds, given the sums before it; all
+  // lanes receive it.
+  const auto bin_in = [&](int j, auto inside) {
+    const int seg = sh.list[j];
+    uint32_t c[4], n = 0;
+    uint64_t w[4], w_all = 0;
+    source.get(seg, c);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      w[x] = c[x] != 0 ? weight_of(sh, source.bin(seg, 4 * lane + x), first) : 0;
+      n += c[x];
+      w_all += c[x] * w[x];
+    }
+    Place pl, found{};
+    pl.number = sh.number[j] + warp_inclusive(n) - n;
+    pl.mass = sh.mass[j] + warp_inclusive(w_all) - w_all;
+    bool any = false;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      pl.bin = source.bin(seg, 4 * lane + x);
+      pl.weight = w[x];
+      pl.count = c[x];
+      if (!any && c[x] != 0 && inside(pl)) {
+        any = true;
+        found = pl;
+      }
+      pl.number += c[x];
+      pl.mass += c[x] * w[x];
+    }
+    const uint32_t yes = __ballot_sync(0xFFFFFFFFu, any);
+    const int src = yes != 0 ? __ffs(yes) - 1 : 0;
+    found.bin = __shfl_sync(0xFFFFFFFFu, found.bin, src);
+    found.number = __shfl_sync(0xFFFFFFFFu, found.number, src);
+    found.mass = __shfl_sync(0xFFFFFFFFu, found.mass, src);
+    found.weight = __shfl_sync(0xFFFFFFFFu, found.weight, src);
+    found.count = __shfl_sync(0xFFFFFFFFu, found.count, src);
+    return found;
+  };
+  const auto at_mass = [&](uint64_t reach) {  // the bin in which the sum reaches `reach`
+    const int j = search([&](int i) { return sh.mass[i] < reach; });
+    return bin_in(j, [&](const Place& x) { return x.mass + x.count * x.weight >= reach; });
+  };
+  // The weight of the first n tokens, 1 <= n <= all.
+  const auto mass_of = [&](uint32_t n) {
+    if (n == all) return all_mass;
+    const int j = search([&](int i) { return sh.number[i] < n; });
+    const Place pl = bin_in(j, [&](const Place& x) { return x.number + x.count >= n; });
+    return pl.mass + (n - pl.number) * pl.weight;
+  };
+  // floor(w·f), and whether that is all of it; f in [0, 1).
+  const auto share = [](uint64_t w, float f, bool* exact) {
+    const uint64_t fixed = __float2ull_rz(f * 18446744073709551616.f);
+    *exact = w * fixed == 0;
+    return __umul64hi(w, fixed);
+  };
+  uint32_t n = all;
+  uint64_t kept = all_mass;
+  bool exact;
+  if (set.k > 0 && static_cast<uint32_t>(set.k) < all) n = static_cast<uint32_t>(set.k);
+  if (set.t == 0.f) n = 1;
+  uint32_t cut = n;
+  if (cut > 1 && set.top_p < 1.f) {
+    kept = mass_of(n);
+    const uint64_t down = share(kept, set.top_p > 0.f ? set.top_p : 0.f, &exact);
+    const uint64_t want = down + (exact ? 0 : 1);
+    if (want == 0) {
+      cut = 1;
+    } else {
+      const Place pl = at_mass(want);
+      const uint32_t at = pl.number + quotient(want - pl.mass + pl.weight - 1, pl.weight);
+      cut = at < cut ? at : cut;
     }
   }
-  meet();
-
-  if (rank == 0) {
-    // exclusive sums over the listed segments, two per thread
-    uint32_t n[2];
-    uint64_t w[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      n[x] = 2 * tid + x < n_list ? sh.number[2 * tid + x] : 0u;
-      w[x] = 2 * tid + x < n_list ? sh.mass[2 * tid + x] : 0u;
+  if (cut > 1 && set.min_p > 0.f) {
+    constexpr uint64_t one = uint64_t{1} << kOneBits;
+    const uint64_t least =
+        set.min_p >= 1.f ? one : static_cast<uint64_t>(ceilf(set.min_p * static_cast<float>(one)));
+    const int j = search([&](int i) {
+      const int bin = source.bin(sh.list[i], 0);
+      return weight_of(sh, bin < first ? first : bin, first) >= least;
+    });
+    const int seg = sh.list[j];
+    uint32_t c[4], with = 0;
+    source.get(seg, c);
+#pragma unroll 1
+    for (int x = 0; x < 4; ++x) {
+      const uint32_t k = x == 0 ? c[0] : x == 1 ? c[1] : x == 2 ? c[2] : c[3];
+      if (k != 0 && weight_of(sh, source.bin(seg, 4 * lane + x), first) >= least) with += k;
     }
-    const uint32_t ni = warp_inclusive(n[0] + n[1]);
-    const uint64_t wi = warp_inclusive(w[0] + w[1]);
-    if (lane == 31) {
-      sh.scan_number[warp] = ni;
-      sh.scan_mass[warp] = wi;
-    }
-    __syncthreads();
-    if (warp == 0) {
-      const uint32_t a = sh.scan_number[lane];
-      const uint64_t b = sh.scan_mass[lane];
-      sh.scan_number[lane] = warp_inclusive(a) - a;
-      sh.scan_mass[lane] = warp_inclusive(b) - b;
-    }
-    __syncthreads();
-    uint32_t nb = sh.scan_number[warp] + ni - n[0] - n[1];
-    uint64_t wb = sh.scan_mass[warp] + wi - w[0] - w[1];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      if (2 * tid + x < n_list) {
-        sh.number[2 * tid + x] = nb;
-        sh.mass[2 * tid + x] = wb;
-      }
-      nb += n[x];
-      wb += w[x];
-    }
-    if (tid == kThreads - 1) {
-      sh.scan_number[0] = nb;  // the whole row
-      sh.scan_mass[0] = wb;
-    }
-    __syncthreads();
-
-    if (warp == 0) {
-      const uint32_t all = sh.scan_number[0];
-      const uint64_t all_mass = sh.scan_mass[0];
-      float u = p.u[m];
-      const float t = p.temperature != nullptr ? p.temperature[m] : 1.f;
-      const int k = p.top_k != nullptr ? p.top_k[m] : 0;
-      const float top_p = p.top_p != nullptr ? p.top_p[m] : 1.f;
-      const float min_p = p.min_p != nullptr ? p.min_p[m] : 0.f;
-      const bool bad = !(t >= 0.f) || isnan(u) || isnan(top_p) || isnan(min_p);
-      if (bad || all == 0) {
-        if (lane == 0) {
-          if (bad) record_error(p.ctx, kErrBounds);
-          p.tokens[m] = -1;
-          if (p.prob != nullptr) p.prob[m] = 0.f;
-        }
-      } else {
-        // The last listed segment for which `before` holds (it holds for the
-        // first, and for all before one that it holds for).
-        const auto search = [&](auto before) {
-          int lo = 0, hi = n_list;
-          while (hi - lo > 1) {
-            const int step = (hi - lo + 31) >> 5, at = lo + lane * step;
-            const uint32_t yes = __ballot_sync(0xFFFFFFFFu, at < hi && (lane == 0 || before(at)));
-            const int top = 31 - __clz(yes);
-            lo += top * step;
-            hi = lo + step < hi ? lo + step : hi;
-          }
-          return lo;
-        };
-        // The bin of segment j in which `inside` first holds of a lane's bin's sums
-        // before and after; all lanes receive it.
-        const auto bin_in = [&](int j, auto inside) {
-          const int bin = 32 * sh.list[j] + lane;
-          Place pl;
-          pl.bin = bin;
-          pl.count = bin >= kBinFirst && bin <= kBinLast ? count_of(counts, C, bin) : 0u;
-          pl.weight = pl.count != 0 ? weight_of(sh, bin, first) : 0;
-          const uint64_t w_all = pl.count * pl.weight;
-          pl.number = sh.number[j] + warp_inclusive(pl.count) - pl.count;
-          pl.mass = sh.mass[j] + warp_inclusive(w_all) - w_all;
-          const uint32_t yes = __ballot_sync(0xFFFFFFFFu, pl.count != 0 && inside(pl));
-          const int src = yes != 0 ? __ffs(yes) - 1 : 0;
-          pl.bin = __shfl_sync(0xFFFFFFFFu, pl.bin, src);
-          pl.number = __shfl_sync(0xFFFFFFFFu, pl.number, src);
-          pl.mass = __shfl_sync(0xFFFFFFFFu, pl.mass, src);
-          pl.weight = __shfl_sync(0xFFFFFFFFu, pl.weight, src);
-          pl.count = __shfl_sync(0xFFFFFFFFu, pl.count, src);
-          return pl;
-        };
-        // The weight of the first n tokens, 1 <= n <= all.
-        const auto mass_of = [&](uint32_t n) {
-          if (n == all) return all_mass;
-          const int j = search([&](int i) { return sh.number[i] < n; });
-          const Place pl = bin_in(j, [&](const Place& x) { return x.number + x.count >= n; });
-          return pl.mass + (n - pl.number) * pl.weight;
-        };
-        // floor(w·f), and whether that is all of it; f in [0, 1).
-        const auto share = [](uint64_t w, float f, bool* exact) {
-          const uint64_t fixed = __float2ull_rz(f * 18446744073709551616.f);
-          *exact = w * fixed == 0;
-          return __umul64hi(w, fixed);
-        };
-        uint32_t n = all;
-        uint64_t kept = all_mass;
-        bool exact;
-        if (k > 0 && static_cast<uint32_t>(k) < all) {
-          n = static_cast<uint32_t>(k);
-          kept = mass_of(n);
-        }
-        if (t == 0.f) n = 1;
-        uint32_t cut = n;
-        if (cut > 1 && top_p < 1.f) {
-          const uint64_t down = share(kept, top_p > 0.f ? top_p : 0.f, &exact);
-          const uint64_t want = down + (exact ? 0 : 1);
-          if (want == 0) {
-            cut = 1;
-          } else {
-            const int j = search([&](int i) { return sh.mass[i] < want; });
-            const Place pl = bin_in(j, [&](const Place& x) {
-              return x.mass + x.count * x.weight >= want;
-            });
-            const uint32_t at =
-                pl.number + static_cast<uint32_t>((want - pl.mass + pl.weight - 1) / pl.weight);
-            cut = at < cut ? at : cut;
-          }
-        }
-        if (cut > 1 && min_p > 0.f) {
-          const uint64_t least =
-              min_p >= 1.f ? uint64_t{1} << kOneBits
-                           : static_cast<uint64_t>(ceilf(min_p * static_cast<float>(uint64_t{1} << kOneBits)));
-          const int j = search([&](int i) {
-            const int bin = 32 * sh.list[i];
-            return weight_of(sh, bin < first ? first : bin, first) >= least;
-          });
-          // (a bin below the weight, or none in this segment)
-          const int bin = 32 * sh.list[j] + lane;
-          const uint32_t c = bin >= kBinFirst && bin <= kBinLast ? count_of(counts, C, bin) : 0u;
-          uint32_t with = c != 0 && weight_of(sh, bin, first) >= least ? c : 0u;
-          with = __reduce_add_sync(0xFFFFFFFFu, with);
-          const uint32_t at = sh.number[j] + with;
-          cut = at < cut ? (at > 0 ? at : 1) : cut;
-        }
-        if (cut != n || t == 0.f) kept = mass_of(cut);
-        u = u > 0.f ? u : 0.f;
-        uint64_t target = u < 1.f ? share(kept, u, &exact) : kept - 1;
-        const int j = search([&](int i) { return sh.mass[i] <= target; });
-        const Place pl = bin_in(j, [&](const Place& x) {
-          return x.mass + x.count * x.weight > target;
-        });
-        uint32_t r = static_cast<uint32_t>((target - pl.mass) / pl.weight);
-        // whose part holds the r-th token of that value
-        int owner = 0;
-        const int shift = pl.bin & 0x8000 ? 16 : 0;
-#pragma unroll
-        for (int i = 0; i < C - 1; ++i) {
-          const uint32_t c = counts[i][pl.bin & 0x7FFF] >> shift & 0xFFFFu;
-          if (owner == i && r >= c) {
-            r -= c;
-            ++owner;
-          }
-        }
-        if (lane == 0) {
-          Shared* o = C == 1 ? &sh : cluster.map_shared_rank(&sh, owner);
-          o->find_bin = pl.bin;
-          o->find_rank = r;
-          o->find_prob = static_cast<float>(static_cast<double>(pl.weight) /
-                                            static_cast<double>(kept));
-        }
-      }
-    }
+    with = __reduce_add_sync(0xFFFFFFFFu, with);
+    const uint32_t at = sh.number[j] + with;
+    cut = at < cut ? (at > 0 ? at : 1) : cut;
   }
-  meet();
+  kept = cut == 1 ? uint64_t{1} << kOneBits : mass_of(cut);
+  const float u = set.u > 0.f ? set.u : 0.f;
+  const uint64_t target = u < 1.f ? share(kept, u, &exact) : kept - 1;
+  const Place pl = at_mass(target + 1);
+  *bin_out = pl.bin;
+  *rank_out = quotient(target - pl.mass, pl.weight);
+  *prob_out = static_cast<float>(pl.weight) / static_cast<float>(kept);
+  return true;
+}
+
+// The r-th token of the chosen value among the chunks [c0, c1): each warp looks through
+// a range of them, and the one that holds the token through its own once more.
+__device__ __noinline__ void find(const SampleArgs& p, Shared& sh, const uint16_t* row, int64_t m,
+                                  int mis, int c0, int c1) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bin = sh.find_bin;
-  if (bin < 0) return;
-
-  // ---- the r-th token of that value in this CTA's part: each warp looks through
-  // a range of it, and the one that holds the token through its own once more
   const uint32_t bits = bin < 0x8000 ? 0x7FFFu - bin : static_cast<uint32_t>(bin);
   const uint32_t mask = bin == kZeroBin ? 0x7FFF7FFFu : 0xFFFFFFFFu;
   const uint32_t pattern = bits | bits << 16;
-  const int w_per = (c1 - c0 + kWarps - 1) / kWarps;
-  const int w0 = c0 + warp * w_per < c1 ? c0 + warp * w_per : c1;
-  const int w1 = w0 + w_per < c1 ? w0 + w_per : c1;
-  const auto hits_of = [&](int c) {  // two bits per pair of logits
-    const uint4 v = load_chunk(row, p.V, mis, c);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const int per = (c1 - c0 + kWarps - 1) / kWarps;
+  const int w0 = c0 + warp * per < c1 ? c0 + warp * per : c1;
+  const int w1 = w0 + per < c1 ? w0 + per : c1;
+  constexpr int kUnroll = 4;
+  // a bit for each logit of the lane's chunks c, c + 32, … that is it
+  const auto hits_of = [&](int c) {
+    uint4 v[kUnroll];
+#pragma unroll
+    for (int x = 0; x < kUnroll; ++x)
+      v[x] = c + 32 * x < w1 ? load_chunk(row, p.V, mis, c + 32 * x)
+                             : make_uint4(~0u, ~0u, ~0u, ~0u);
     uint32_t h = 0;
 #pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      const uint32_t x = (w[y] & mask) ^ pattern;
-      h |= ((x & 0xFFFFu) == 0 ? 1u : 0u) << (2 * y) | (x >> 16 == 0 ? 2u : 0u) << (2 * y);
+    for (int x = 0; x < kUnroll; ++x) {
+      const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const uint32_t d = (w[y] & mask) ^ pattern;
+        // the top bit of each half that is zero
+        const uint32_t z = ~(((d & 0x7FFF7FFFu) + 0x7FFF7FFFu) | d | 0x7FFF7FFFu);
+        h |= (z >> 15 & 1u | z >> 30) << (8 * x + 2 * y);
+      }
     }
     return h;
   };
   uint32_t hits = 0;
-#pragma unroll 4
-  for (int c = w0 + lane; c < w1; c += 32) hits += __popc(hits_of(c));
+  for (int c = w0 + lane; c - lane < w1; c += 32 * kUnroll) hits += __popc(hits_of(c));
   hits = __reduce_add_sync(0xFFFFFFFFu, hits);
   if (lane == 0) sh.warp_hits[warp] = hits;
   __syncthreads();
@@ -528,21 +531,342 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs p)
   for (int i = 0; i < warp; ++i) before += sh.warp_hits[i];
   const uint32_t r = sh.find_rank;
   if (r < before || r >= before + hits) return;
-  for (int c = w0; c < w1; c += 32) {
-    const uint32_t h = c + lane < w1 ? hits_of(c + lane) : 0u;
-    const uint32_t inc = before + warp_inclusive(static_cast<uint32_t>(__popc(h)));
-    if (r < inc && r >= inc - __popc(h)) {
-      uint32_t left = r - (inc - __popc(h)), x = h;
-      for (; left > 0; --left) x &= x - 1;
-      p.tokens[m] = static_cast<int32_t>(static_cast<int64_t>(c + lane) * 8 - mis + __ffs(x) - 1);
-      if (p.prob != nullptr) p.prob[m] = sh.find_prob;
+  for (int c = w0; c < w1; c += 32 * kUnroll) {
+    const uint32_t h = hits_of(c + lane);
+    const uint32_t batch = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(__popc(h)));
+    if (r >= before + batch) {
+      before += batch;
+      continue;
     }
-    before = __shfl_sync(0xFFFFFFFFu, inc, 31);
+#pragma unroll 1
+    for (int x = 0; x < kUnroll; ++x) {
+      uint32_t g = h >> (8 * x) & 0xFFu;
+      const uint32_t inc = before + warp_inclusive(static_cast<uint32_t>(__popc(g)));
+      if (r < inc && r >= inc - __popc(g)) {
+        for (uint32_t left = r - (inc - __popc(g)); left > 0; --left) g &= g - 1;
+        p.tokens[m] = static_cast<int32_t>(static_cast<int64_t>(c + 32 * x + lane) * 8 - mis +
+                                           __ffs(g) - 1);
+        if (p.prob != nullptr) p.prob[m] = sh.find_prob;
+      }
+      before = __shfl_sync(0xFFFFFFFFu, inc, 31);
+    }
+    return;
+  }
+}
+
+// A row through all bins, by one CTA.  Leaves the counters zero.
+__device__ __noinline__ void all_bins(const SampleArgs& p, Shared& sh, const uint16_t* row,
+                                      int64_t m, int mis, const Settings& set) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kStep = kSlots / 128;  // segments at a time
+  if (tid == 0) sh.all_first = kBinLast + 1;
+  for (int s0 = 0; s0 < kSegs; s0 += kStep) {
+    for (int i = tid; i < kSlots / 4; i += kThreads)
+      reinterpret_cast<uint4*>(sh.counts)[i] = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+    count_range(p, row, mis, 128 * s0, kSlots, sh.counts);
+    __syncthreads();
+    int first = kBinLast + 1;
+    for (int i = kSlots - 1 - tid; i >= 0; i -= kThreads)
+      if (sh.counts[i] != 0) first = 128 * s0 + i;
+    first = __reduce_min_sync(0xFFFFFFFFu, first);
+    if (lane == 0) atomicMin(&sh.all_first, first);
+    __syncthreads();
+    for (int s = warp; s < kStep && s0 + s < kSegs; s += kWarps) {
+      uint32_t n = 0;
+      uint64_t w = 0;
+      for (int x = 0; x < 4; ++x) {
+        const uint32_t k = sh.counts[128 * s + 32 * x + lane];
+        if (k != 0) w += k * weight_of(sh, 128 * (s0 + s) + 32 * x + lane, sh.all_first);
+        n += k;
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) {
+        n += __shfl_xor_sync(0xFFFFFFFFu, n, off);
+        w += __shfl_xor_sync(0xFFFFFFFFu, w, off);
+      }
+      if (lane == 0) {
+        sh.number[s0 + s] = n;
+        sh.mass[s0 + s] = w;
+      }
+    }
+    __syncthreads();
+  }
+  for (int i = tid; i < kSlots / 4; i += kThreads)
+    reinterpret_cast<uint4*>(sh.counts)[i] = make_uint4(0u, 0u, 0u, 0u);
+  // the segments that are not empty, closed up
+  if (warp == 0) {
+    int at = 0;
+    for (int s = lane; s < kSegs; s += 32) {
+      const uint32_t n = sh.number[s];
+      const uint64_t w = sh.mass[s];
+      const uint32_t live = __ballot_sync(0xFFFFFFFFu, n != 0);
+      if (n != 0) {
+        const int to = at + __popc(live & ((1u << lane) - 1u));
+        sh.number[to] = n;
+        sh.mass[to] = w;
+        sh.list[to] = static_cast<uint16_t>(s);
+      }
+      at += __popc(live);
+      __syncwarp();
+    }
+    if (lane == 0) {
+      sh.n_list = at;
+      sh.find_bin = -1;
+    }
+  }
+  __syncthreads();
+  sum_list(sh, sh.n_list);
+  const Recount source{p, sh, row, mis};
+  if (warp == 0) {
+    int bin;
+    uint32_t rank;
+    float prob;
+    const bool any =
+        choose(p, sh, source, set, sh.n_list, sh.all_first, &bin, &rank, &prob);
+    if (lane == 0) {
+      if (any) {
+        sh.find_bin = bin;
+        sh.find_rank = rank;
+        sh.find_prob = prob;
+      } else {
+        p.tokens[m] = -1;
+        if (p.prob != nullptr) p.prob[m] = 0.f;
+      }
+    }
+    source.done();
+  } else {
+    source.serve();
+  }
+  __syncthreads();
+  if (sh.find_bin >= 0) find(p, sh, row, m, mis, 0, static_cast<int>((p.V + mis + 7) >> 3));
+  __syncthreads();
+}
+
+template <int C>
+__global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArgs p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  Shared& sh = *reinterpret_cast<Shared*>(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = C == 1 ? 0 : static_cast<int>(cluster.block_rank());
+  const auto meet = [&] {
+    if constexpr (C == 1)
+      __syncthreads();
+    else
+      cluster.sync();
+  };
+  const auto peer = [&](int r) { return C == 1 ? &sh : cluster.map_shared_rank(&sh, r); };
+
+  for (int i = tid; i < kSlots / 4; i += kThreads)
+    reinterpret_cast<uint4*>(sh.counts)[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (tid < 64) {
+    sh.pow2_hi[tid] = kPow2.hi[tid];
+    sh.pow2_lo[tid] = kPow2.lo[tid];
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  Counters<C> source;
+#pragma unroll
+  for (int r = 0; r < C; ++r) source.counts[r] = peer(r)->counts;
+
+  for (int64_t m = blockIdx.x / C; m < p.M; m += gridDim.x / C) {
+    const uint16_t* row = p.logits + m * p.stride;
+    Settings set;
+    set.t = p.temperature != nullptr ? p.temperature[m] : 1.f;
+    set.u = p.u[m];
+    set.k = p.top_k != nullptr ? p.top_k[m] : 0;
+    set.top_p = p.top_p != nullptr ? p.top_p[m] : 1.f;
+    set.min_p = p.min_p != nullptr ? p.min_p[m] : 0.f;
+    const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(row) >> 1 & 7);
+    const int chunks = static_cast<int>((p.V + mis + 7) >> 3);
+    const int per = (chunks + C - 1) / C;
+    const int c0 = rank * per < chunks ? rank * per : chunks;
+    const int c1 = c0 + per < chunks ? c0 + per : chunks;
+    constexpr int kUnroll = 4;
+    uint4 v[kUnroll];
+    const auto load = [&](int c) {
+#pragma unroll
+      for (int x = 0; x < kUnroll; ++x)
+        v[x] = c + x * kThreads < c1 ? load_chunk(row, p.V, mis, c + x * kThreads)
+                                     : make_uint4(~0u, ~0u, ~0u, ~0u);
+    };
+    load(c0 + tid);
+    if (tid == 0) {
+      sh.guess = sh.first = kBinLast + 1;
+      sh.wide = 0;
+      // the cluster's next row on its way to the L2 cache
+      const int64_t next = m + gridDim.x / C;
+      if (next < p.M && c1 - c0 > 2)
+        prefetch_l2(reinterpret_cast<const void*>(
+                        (reinterpret_cast<uintptr_t>(p.logits + next * p.stride) & ~15ull) +
+                        16 * static_cast<int64_t>(c0 + 1)),
+                    16u * static_cast<uint32_t>(c1 - c0 - 2));
+    } else if (tid == 32) {  // 2·log2(e)/T, and what its rounding left
+      constexpr double a = 2.8853900817779268;
+      constexpr float ah = static_cast<float>(a), al = static_cast<float>(a - static_cast<double>(ah));
+      const bool hot = set.t > 0x1p64f;  // both sides smaller, or the quotient has no bits left
+      const float t = hot ? set.t * 0x1p-64f : set.t;
+      const float hi = ah / t;
+      sh.half = hot ? 0x1p-65f : 0.5f;
+      sh.c_hi = hi;
+      sh.c_lo = isinf(hi) || hi == 0.f ? 0.f : (__fmaf_rn(-hi, t, ah) + al) / t;
+    }
+    __syncthreads();  // the counts are zero, too
+    {
+      int guess = kBinLast + 1;
+      const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        const uint32_t b = bins_of(w[y >> 1]);
+        const int bin = static_cast<int>(y & 1 ? b >> 16 : b & 0xFFFFu);
+        guess = bin >= kBinFirst && bin < guess ? bin : guess;
+      }
+      guess = __reduce_min_sync(0xFFFFFFFFu, guess);
+      if (lane == 0) atomicMin(&sh.guess, guess);
+    }
+    __syncthreads();
+    const int limit = limit_of(sh.guess, set.t);
+
+    // ---- counts of this CTA's part
+    uint32_t low = 0xFFFFFFFFu;  // the smallest bins
+    bool wide = false;
+    for (int c = c0 + tid; c - tid < c1; c += kUnroll * kThreads) {
+#pragma unroll
+      for (int x = 0; x < kUnroll; ++x) {
+        const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const uint32_t b = bins_of(w[y]);
+          low = __vminu2(low, b);
+          wide |= count(sh.counts, static_cast<int>(b & 0xFFFFu), limit);
+          wide |= count(sh.counts, static_cast<int>(b >> 16), limit);
+        }
+      }
+      if (c - tid + kUnroll * kThreads < c1) load(c + kUnroll * kThreads);
+    }
+    {
+      int first = static_cast<int>((low & 0xFFFFu) < low >> 16 ? low & 0xFFFFu : low >> 16);
+      first = __reduce_min_sync(0xFFFFFFFFu, first);
+      if (lane == 0) atomicMin(&sh.first, first == kZeroBin + 1 ? kZeroBin : first);
+      if (wide) sh.wide = 1;
+    }
+    __syncthreads();
+    // ---- which segments hold anything
+    for (int s = warp; s < kSlots / 128; s += kWarps) {
+      const uint4 n = reinterpret_cast<const uint4*>(sh.counts)[s * 32 + lane];
+      const uint32_t any = __ballot_sync(0xFFFFFFFFu, (n.x | n.y | n.z | n.w) != 0);
+      if (lane == 0) reinterpret_cast<uint8_t*>(sh.seg_counts)[s] = any != 0;
+    }
+    __syncthreads();
+    if (warp < static_cast<int>(sizeof(sh.occupied) / 4)) {
+      const int s = 32 * warp + lane;
+      const uint32_t bits = __ballot_sync(
+          0xFFFFFFFFu, s < kSlots / 128 && reinterpret_cast<uint8_t*>(sh.seg_counts)[s] != 0);
+      if (lane == 0) sh.occupied[warp] = bits;
+    }
+    meet();
+    if (warp == 0) {
+      int first = kBinLast + 1, any_wide = 0, at = 0;
+      uint32_t w[sizeof(sh.occupied) / 4] = {};
+#pragma unroll
+      for (int r = 0; r < C; ++r) {
+        const Shared* o = peer(r);
+        first = o->first < first ? o->first : first;
+        any_wide |= o->wide;
+#pragma unroll
+        for (size_t i = 0; i < sizeof(sh.occupied) / 4; ++i) w[i] |= o->occupied[i];
+      }
+#pragma unroll
+      for (size_t i = 0; i < sizeof(sh.occupied) / 4; ++i) {
+        if (w[i] >> lane & 1u)
+          sh.list[at + __popc(w[i] & ((1u << lane) - 1u))] =
+              static_cast<uint16_t>(32 * i + lane);
+        at += __popc(w[i]);
+      }
+      if (lane == 0) {
+        sh.n_list = at;
+        sh.all_first = first;
+        sh.all_wide = any_wide;
+        sh.find_bin = -1;
+      }
+    }
+    __syncthreads();
+    const int n_list = sh.n_list, first = sh.all_first;
+    if (sh.all_wide != 0) {
+      meet();  // the others' flags have been read
+      if (rank == 0) all_bins(p, sh, row, m, mis, set);
+      else
+        for (int i = tid; i < kSlots / 4; i += kThreads)
+          reinterpret_cast<uint4*>(sh.counts)[i] = make_uint4(0u, 0u, 0u, 0u);
+      __syncthreads();
+      continue;
+    }
+
+    // ---- the segments' numbers of tokens and weights, to the first CTA
+    for (int j = rank * kWarps + warp; j < n_list; j += C * kWarps) {
+      const int seg = sh.list[j];
+      uint32_t c[4], n = 0;
+      uint64_t w = 0;
+      source.get(seg, c);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if (c[x] != 0) w += c[x] * weigh(sh, bin_of_slot(128 * seg + 4 * lane + x), first);
+        n += c[x];
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) {
+        n += __shfl_xor_sync(0xFFFFFFFFu, n, off);
+        w += __shfl_xor_sync(0xFFFFFFFFu, w, off);
+      }
+      if (lane == 0) {
+        peer(0)->number[j] = n;
+        peer(0)->mass[j] = w;
+      }
+    }
+    meet();
+    if (rank == 0) {
+      sum_list(sh, n_list);
+      if (warp == 0) {
+        int bin;
+        uint32_t r;
+        float prob;
+        if (choose(p, sh, source, set, n_list, first, &bin, &r, &prob)) {
+          // whose part holds the r-th token of that value
+          const int slot = bin < kPosBin + kSpan ? bin - kPosBin
+                           : bin < kNegBin       ? kZeroSlot
+                                                 : bin - kNegBin + kNegSlot;
+          int owner = 0;
+#pragma unroll
+          for (int i = 0; i < C - 1; ++i) {
+            const uint32_t c = source.counts[i][slot];
+            if (owner == i && r >= c) {
+              r -= c;
+              ++owner;
+            }
+          }
+          if (lane == 0) {
+            Shared* o = peer(owner);
+            o->find_bin = bin;
+            o->find_rank = r;
+            o->find_prob = prob;
+          }
+        } else if (lane == 0) {
+          p.tokens[m] = -1;
+          if (p.prob != nullptr) p.prob[m] = 0.f;
+        }
+      }
+    }
+    meet();
+    for (int i = tid; i < kSlots / 4; i += kThreads)
+      reinterpret_cast<uint4*>(sh.counts)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (sh.find_bin >= 0) find(p, sh, row, m, mis, c0, c1);
+    __syncthreads();
   }
 }
 
 template <int C>
-cudaError_t launch(const SampleArgs& p, int64_t M, cudaStream_t s) {
+cudaError_t launch(const SampleArgs& p, int sms, cudaStream_t s) {
   static bool done[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -556,8 +880,10 @@ cudaError_t launch(const SampleArgs& p, int64_t M, cudaStream_t s) {
       done[dev & 63] = true;
     }
   }
-  return launch_pdl_cluster(sample_kernel<C>, dim3(static_cast<unsigned>(M * C)), dim3(kThreads),
-                            C, sizeof(Shared), s, p);
+  const int64_t most = sms * kCtas >= C ? sms * kCtas / C : 1;
+  const int64_t clusters = p.M < most ? p.M : most;
+  return launch_pdl_cluster(sample_kernel<C>, dim3(static_cast<unsigned>(clusters * C)),
+                            dim3(kThreads), C, sizeof(Shared), s, p);
 }
 
 bool off(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) != 0; }
@@ -583,6 +909,7 @@ extern "C" bd_status bitdelta_sample(const uint16_t* logits, int64_t M, int64_t 
   const int st = bd::current_device_context(&p.ctx, &sms);
   if (st != BD_OK) return static_cast<bd_status>(st);
   p.logits = logits;
+  p.M = M;
   p.V = V;
   p.stride = row_stride;
   p.u = u;
@@ -592,17 +919,24 @@ extern "C" bd_status bitdelta_sample(const uint16_t* logits, int64_t M, int64_t 
   p.min_p = min_p;
   p.tokens = tokens;
   p.prob = prob;
-  // CTAs per row: as many as the counts' 16 bits need, and more while all rows'
-  // still fit the device at once.
-  const int64_t chunks = (V + 14) / 8;
+  // CTAs per row: the number with which all rounds of rows take least, at about 8 us a
+  // row and 1 us for each 6000 logits of a CTA's part (two CTAs share an SM's 8 additions
+  // to shared memory a clock).
   int c = 1;
-  while (c < bd::kMaxCluster &&
-         (chunks > static_cast<int64_t>(bd::kMaxChunks) * c || M * 2 * c <= sms))
-    c *= 2;
+  double best = 0;
+  for (int n = 1; n <= bd::kMaxCluster; n *= 2) {
+    const int64_t at_once = sms * bd::kCtas >= n ? sms * bd::kCtas / n : 1;
+    const double time =
+        static_cast<double>((M + at_once - 1) / at_once) * (8.0 + static_cast<double>(V) / n / 6e3);
+    if (n == 1 || time < best) {
+      c = n;
+      best = time;
+    }
+  }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = c == 1   ? bd::launch<1>(p, M, s)
-                        : c == 2 ? bd::launch<2>(p, M, s)
-                        : c == 4 ? bd::launch<4>(p, M, s)
-                                 : bd::launch<8>(p, M, s);
+  const cudaError_t e = c == 1   ? bd::launch<1>(p, sms, s)
+                        : c == 2 ? bd::launch<2>(p, sms, s)
+                        : c == 4 ? bd::launch<4>(p, sms, s)
+                                 : bd::launch<8>(p, sms, s);
   return e == cudaSuccess ? BD_OK : BD_ERR_CUDA;
 }
