@@ -12,15 +12,13 @@
 // give the token: a second look at one CTA's part of the row finds the r-th.
 //
 // Values are numbered by their bin: 0x7FFF − bits for positive ones and bits for
-// negative ones, the largest value first.  Counted are the values from 2^-24 to 2^16 in
-// size, and zero: 10241 counters, of 32 bits.  (All bins' would fill an SM's shared
-// memory with 16-bit ones, and their phases of few threads would stand alone: 500
-// rows of 99991 took 161 us.)  A row with another value among those that may be taken
-// goes through all bins in several passes, by one CTA.
-//
-// Logits whose weight is less than 2^-46 next to the largest of the part's first
-// ones cannot be taken and are not counted: masked ones above all, which would be
-// additions to one address.
+// negative ones, the largest value first.  Counted are the values from 2^-40 to 2^16 in
+// size, and zero: two tables of 7168 counters, of 32 bits, with one more at either end
+// for what lies outside.  (All bins' would fill an SM's shared memory with 16-bit ones,
+// and their phases of few threads would stand alone: 500 rows of 99991 took 161 us.)
+// Additions of 1 to one address are merged by the hardware (17 a clock, and 8 to different
+// ones), so that a masked row costs no more than another.  A row with a value outside
+// that may be taken goes through all bins in several passes, by one CTA.
 //
 // A row is shared by a cluster of CTAs, each with counts of its own part, which
 // are added where they are read (distributed shared memory); a cluster takes row
@@ -57,13 +55,19 @@ constexpr int kBinLast = 0xFF7F;  // −inf and NaN lie above
 constexpr int kZeroBin = 0x7FFF;
 constexpr int kSegs = 512;        // of 128 bins, of all bins
 
-// The counted values: kSpan bins of either sign, with the zero in a segment of its own
-// between them.
-constexpr int kSpan = 40 * 128;
-constexpr int kPosBin = 0x8000 - ((127 + 16) << 7);  // of the largest, just below 2^16
-constexpr int kNegBin = 0x8000 + ((127 - 24) << 7);  // of −2^-24
-constexpr int kZeroSlot = kSpan, kNegSlot = kSpan + 128;
-constexpr int kSlots = 2 * kSpan + 128;
+// The counters: of either sign kSpan bins, behind one for the bins before them and with
+// one for those that follow; 41 segments each.  Behind the positive ones (and before the
+// negative) lie zero and what is smaller than the counted values.
+constexpr int kSpan = 56 * 128;
+constexpr int kPosBin = 0x8000 - ((127 + 16) << 7) - 1;  // 2^16, of slot 0
+constexpr int kNegShift = 0x8000 + ((127 - 40) << 7) - 1 - kPosBin;  // to the negative bins
+constexpr int kNegSlot = kSpan + 128;
+constexpr int kSlots = 2 * kNegSlot;
+constexpr int kZeroSlot = kSpan + 1;
+constexpr int kFarSlot = kNegSlot + kSpan + 1;  // −2^16 and below, −inf, −NaN
+constexpr int kSlotSegs = kSlots / 128;
+// The least size that is counted, as a bf16 number's bits.
+constexpr uint32_t kLeastBits = (127 - 40) << 7;
 
 // 2^(j/64) to 48 bits, from the exponential's series.
 constexpr double exp_series(double x) {
@@ -94,14 +98,12 @@ struct Shared {
   uint32_t number[kSegs];
   uint16_t list[kSegs];            // segments that are not empty, in order
   uint32_t seg_counts[128];        // one segment's, where all bins are gone through
-  uint32_t occupied[(kSlots / 128 + 31) / 32];   // this CTA's
+  uint32_t occupied[(kSlotSegs + 31) / 32];   // this CTA's
   float pow2_hi[64], pow2_lo[64];
-  uint64_t scan_mass[kWarps];
-  uint32_t scan_number[kWarps];
   float half, c_hi, c_lo;          // 1/2 and 2·log2(e)/T (2^-65 and 2^64 of it for large T)
-  int guess;                       // the largest of the first logits, of this CTA's part
   int first, all_first;            // the largest value's bin, of this part and of the row
   int wide, all_wide;              // values outside of the counted ones
+  int far;                         // logits of −2^16 and below
   int n_list;
   int asked;                       // the segment that the CTA is to count, or −1
   int find_bin;                    // the token's value, or −1: not in this CTA's part
@@ -190,34 +192,24 @@ __device__ __forceinline__ uint32_t bins_of(uint32_t w) {
 
 // The bin of a slot of the counters (any, where a slot has none).
 __device__ __forceinline__ int bin_of_slot(int slot) {
-  return slot < kSpan ? slot + kPosBin : slot < kNegSlot ? kZeroBin : slot - kNegSlot + kNegBin;
+  return slot < kZeroSlot ? slot + kPosBin
+                          : slot < kNegSlot ? kZeroBin : slot - kNegSlot + kPosBin + kNegShift;
 }
 
-// Counts a logit; true for one that has no counter.  (Additions of 1 to one address
-// are merged by the hardware: 17 a clock, and 8 to different ones.)
-__device__ __forceinline__ bool count(uint32_t* counts, int bin, int limit) {
-  const bool negative = bin >= 0x8000;
-  const uint32_t at = static_cast<uint32_t>(bin - (negative ? kNegBin : kPosBin));
-  if (bin > limit) return false;
-  if (at < kSpan) {
-    atomicAdd(counts + at + (negative ? kNegSlot : 0), 1u);
-    return false;
-  }
-  if (bin != kZeroBin && bin != kZeroBin + 1) return true;
-  atomicAdd(counts + kZeroSlot, 1u);
-  return false;
-}
-
-// The last bin whose logits can have a weight, where the largest lies in `guess` or
-// before it: 33·T below it, which is 47 powers of two.
-__device__ int limit_of(int guess, float t) {
-  if (guess < kBinFirst || guess > kBinLast) return kBinLast;  // nothing is known
-  const float v = value_of(guess) - 33.f * t;
-  if (!(t >= 0.f) || !(v > -INFINITY)) return kBinLast;
-  uint32_t bits = __float_as_uint(v) >> 16;
-  if (bits & 0x8000u) ++bits;  // a step further down (for positive ones the cut is one)
-  const int bin = static_cast<int>(bits & 0x8000u ? bits : 0x7FFFu - bits);
-  return bin == kZeroBin ? kZeroBin + 1 : (bin < kBinLast ? bin : kBinLast);  // with −0
+// Counts two logits.  least: the smallest size of a logit that is not zero, of each half
+// (as a negative number: bits − 0x8001; zero is 0x7FFF).
+__device__ __forceinline__ void count2(uint32_t* counts, uint32_t w, uint32_t& least) {
+  constexpr uint32_t two = 0x10001u;
+  least = __vmins2(least, (w | 0x8000u * two) - two);
+  uint32_t negative;  // 0xFFFF where the sign is set: bytes 1 and 3's signs, twice each
+  asm("prmt.b32 %0, %1, 0, 0xBB99;" : "=r"(negative) : "r"(w));
+  const uint32_t bin = w ^ (0x7FFF7FFFu & ~negative);
+  uint32_t e = bin - (negative & kNegShift * two);
+  e = __vminu2(__vmaxu2(e, kPosBin * two), (kPosBin + kSpan + 1) * two) - kPosBin * two;
+  const uint32_t at = 4 * e + (negative & 4 * kNegSlot * two);  // bytes, below 2^16
+  uint8_t* base = reinterpret_cast<uint8_t*>(counts);
+  atomicAdd(reinterpret_cast<uint32_t*>(base + (at & 0xFFFFu)), 1u);
+  atomicAdd(reinterpret_cast<uint32_t*>(base + (at >> 16)), 1u);
 }
 
 // a / b, below 2^20; 0 where b is.
@@ -322,35 +314,34 @@ struct Recount {
   }
 };
 
-// Exclusive sums over the listed segments, in place, and those of all; the CTA.
-__device__ void sum_list(Shared& sh, int n_list) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  static_assert(kThreads >= kSegs, "a segment per thread");
-  const uint32_t n = tid < n_list ? sh.number[tid] : 0u;
-  const uint64_t w = tid < n_list ? sh.mass[tid] : 0u;
-  const uint32_t ni = warp_inclusive(n);
-  const uint64_t wi = warp_inclusive(w);
-  if (lane == 31) {
-    sh.scan_number[warp] = ni;
-    sh.scan_mass[warp] = wi;
+// Exclusive sums over the listed segments, in place; returns those of all.  One warp.
+__device__ void sum_list(Shared& sh, int n_list, uint32_t& all, uint64_t& all_mass) {
+  const int lane = threadIdx.x & 31;
+  all = 0;
+  all_mass = 0;
+  for (int i = lane; i - lane < n_list; i += 32) {
+    const uint32_t n = i < n_list ? sh.number[i] : 0u;
+    const uint64_t w = i < n_list ? sh.mass[i] : 0u;
+    const uint32_t ni = warp_inclusive(n);
+    const uint64_t wi = warp_inclusive(w);
+    if (i < n_list) {
+      sh.number[i] = all + ni - n;
+      sh.mass[i] = all_mass + wi - w;
+    }
+    all += __shfl_sync(0xFFFFFFFFu, ni, 31);
+    all_mass += __shfl_sync(0xFFFFFFFFu, wi, 31);
   }
-  __syncthreads();
-  uint32_t nb = ni - n;
-  uint64_t wb = wi - w;
-  for (int i = 0; i < warp; ++i) {
-    nb += sh.scan_number[i];
-    wb += sh.scan_mass[i];
-  }
-  if (tid < n_list) {
-    sh.number[tid] = nb;
-    sh.mass[tid] = wb;
-  }
-  __syncthreads();
-  if (tid == kThreads - 1) {
-    sh.scan_number[0] = nb + n;
-    sh.scan_mass[0] = wb + w;
-  }
-  __syncthreads();
+  __syncwarp();
+}
+
+// Sums over a warp's lanes; each w below 2^58.
+__device__ __forceinline__ void warp_sums(uint32_t& n, uint64_t& w) {
+  n = __reduce_add_sync(0xFFFFFFFFu, n);
+  const uint32_t a = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(w) & 0x1FFFFFFu);
+  const uint32_t b = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(w >> 25) & 0x1FFFFFFu);
+  const uint64_t hi = w >> 50;  // at most 2^14 a lane
+  const uint32_t c = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(hi));
+  w = a + (static_cast<uint64_t>(b) << 25) + (static_cast<uint64_t>(c) << 50);
 }
 
 struct Settings {
@@ -361,12 +352,13 @@ struct Settings {
 // The cuts and the choice, by one warp: the value of the row's token, its number among
 // its equals and its probability.  False where there is none.
 template <class Source>
-__device__ __noinline__ bool choose(const SampleArgs& p, const Shared& sh, const Source& source,
+__device__ __noinline__ bool choose(const SampleArgs& p, Shared& sh, const Source& source,
                                     const Settings& set, int n_list, int first, int* bin_out,
                                     uint32_t* rank_out, float* prob_out) {
   const int lane = threadIdx.x & 31;
-  const uint32_t all = sh.scan_number[0];
-  const uint64_t all_mass = sh.scan_mass[0];
+  uint32_t all;
+  uint64_t all_mass;
+  sum_list(sh, n_list, all, all_mass);
   const bool bad = !(set.t >= 0.f) || isnan(set.u) || isnan(set.top_p) || isnan(set.min_p);
   if (bad || all == 0) {
     if (bad && lane == 0) record_error(p.ctx, kErrBounds);
@@ -385,26 +377,37 @@ __device__ __noinline__ bool choose(const SampleArgs& p, const Shared& sh, const
     }
     return lo;
   };
-  // The first bin of segment j for which `inside` holds, given the sums before it; all
-  // lanes receive it.
-  const auto bin_in = [&](int j, auto inside) {
+  // The segment that was last looked at: the lane's four bins.
+  int have = -1;
+  uint32_t c[4], number = 0;
+  uint64_t w[4], mass = 0;
+  const auto look = [&](int j) {
+    if (j == have) return;
+    have = j;
     const int seg = sh.list[j];
-    uint32_t c[4], n = 0;
-    uint64_t w[4], w_all = 0;
     source.get(seg, c);
+    uint32_t n = 0;
+    uint64_t w_all = 0;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      w[x] = c[x] != 0 ? weight_of(sh, source.bin(seg, 4 * lane + x), first) : 0;
+      w[x] = weigh(sh, source.bin(seg, 4 * lane + x), first);
       n += c[x];
       w_all += c[x] * w[x];
     }
+    number = sh.number[j] + warp_inclusive(n) - n;
+    mass = sh.mass[j] + warp_inclusive(w_all) - w_all;
+  };
+  // The first bin of segment j for which `inside` holds, given the sums before it; all
+  // lanes receive it.
+  const auto bin_in = [&](int j, auto inside) {
+    look(j);
     Place pl, found{};
-    pl.number = sh.number[j] + warp_inclusive(n) - n;
-    pl.mass = sh.mass[j] + warp_inclusive(w_all) - w_all;
+    pl.number = number;
+    pl.mass = mass;
     bool any = false;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      pl.bin = source.bin(seg, 4 * lane + x);
+      pl.bin = x;
       pl.weight = w[x];
       pl.count = c[x];
       if (!any && c[x] != 0 && inside(pl)) {
@@ -416,11 +419,10 @@ __device__ __noinline__ bool choose(const SampleArgs& p, const Shared& sh, const
     }
     const uint32_t yes = __ballot_sync(0xFFFFFFFFu, any);
     const int src = yes != 0 ? __ffs(yes) - 1 : 0;
-    found.bin = __shfl_sync(0xFFFFFFFFu, found.bin, src);
+    found.bin = source.bin(sh.list[j], 4 * src + __shfl_sync(0xFFFFFFFFu, found.bin, src));
     found.number = __shfl_sync(0xFFFFFFFFu, found.number, src);
     found.mass = __shfl_sync(0xFFFFFFFFu, found.mass, src);
     found.weight = __shfl_sync(0xFFFFFFFFu, found.weight, src);
-    found.count = __shfl_sync(0xFFFFFFFFu, found.count, src);
     return found;
   };
   const auto at_mass = [&](uint64_t reach) {  // the bin in which the sum reaches `reach`
@@ -466,14 +468,11 @@ __device__ __noinline__ bool choose(const SampleArgs& p, const Shared& sh, const
       const int bin = source.bin(sh.list[i], 0);
       return weight_of(sh, bin < first ? first : bin, first) >= least;
     });
-    const int seg = sh.list[j];
-    uint32_t c[4], with = 0;
-    source.get(seg, c);
-#pragma unroll 1
-    for (int x = 0; x < 4; ++x) {
-      const uint32_t k = x == 0 ? c[0] : x == 1 ? c[1] : x == 2 ? c[2] : c[3];
-      if (k != 0 && weight_of(sh, source.bin(seg, 4 * lane + x), first) >= least) with += k;
-    }
+    look(j);
+    uint32_t with = 0;
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (w[x] >= least) with += c[x];
     with = __reduce_add_sync(0xFFFFFFFFu, with);
     const uint32_t at = sh.number[j] + with;
     cut = at < cut ? (at > 0 ? at : 1) : cut;
@@ -489,7 +488,7 @@ __device__ __noinline__ bool choose(const SampleArgs& p, const Shared& sh, const
 }
 
 // The r-th token of the chosen value among the chunks [c0, c1): each warp looks through
-// a range of them, and the one that holds the token through its own once more.
+// a range of them, in batches, and the one that holds the token at its batch once more.
 __device__ __noinline__ void find(const SampleArgs& p, Shared& sh, const uint16_t* row, int64_t m,
                                   int mis, int c0, int c1) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -497,60 +496,69 @@ __device__ __noinline__ void find(const SampleArgs& p, Shared& sh, const uint16_
   const uint32_t bits = bin < 0x8000 ? 0x7FFFu - bin : static_cast<uint32_t>(bin);
   const uint32_t mask = bin == kZeroBin ? 0x7FFF7FFFu : 0xFFFFFFFFu;
   const uint32_t pattern = bits | bits << 16;
-  const int per = (c1 - c0 + kWarps - 1) / kWarps;
-  const int w0 = c0 + warp * per < c1 ? c0 + warp * per : c1;
-  const int w1 = w0 + per < c1 ? w0 + per : c1;
-  constexpr int kUnroll = 4;
-  // a bit for each logit of the lane's chunks c, c + 32, … that is it
-  const auto hits_of = [&](int c) {
-    uint4 v[kUnroll];
+  constexpr int kBatch = 8;  // chunks of a lane
+  const int batches = (c1 - c0 + 32 * kBatch - 1) / (32 * kBatch);
+  const int per = (batches + kWarps - 1) / kWarps;
+  const int b0 = warp * per < batches ? warp * per : batches;
+  const int b1 = b0 + per < batches ? b0 + per : batches;
+  const auto load = [&](uint4 (&v)[kBatch], int b) {
+    const int c = c0 + 32 * kBatch * b + lane;
 #pragma unroll
-    for (int x = 0; x < kUnroll; ++x)
-      v[x] = c + 32 * x < w1 ? load_chunk(row, p.V, mis, c + 32 * x)
+    for (int x = 0; x < kBatch; ++x)
+      v[x] = c + 32 * x < c1 ? load_chunk(row, p.V, mis, c + 32 * x)
                              : make_uint4(~0u, ~0u, ~0u, ~0u);
-    uint32_t h = 0;
-#pragma unroll
-    for (int x = 0; x < kUnroll; ++x) {
-      const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const uint32_t d = (w[y] & mask) ^ pattern;
-        // the top bit of each half that is zero
-        const uint32_t z = ~(((d & 0x7FFF7FFFu) + 0x7FFF7FFFu) | d | 0x7FFF7FFFu);
-        h |= (z >> 15 & 1u | z >> 30) << (8 * x + 2 * y);
-      }
-    }
-    return h;
   };
-  uint32_t hits = 0;
-  for (int c = w0 + lane; c - lane < w1; c += 32 * kUnroll) hits += __popc(hits_of(c));
-  hits = __reduce_add_sync(0xFFFFFFFFu, hits);
+  // the top bit of each half of a chunk's word that is the value
+  const auto hit = [&](uint32_t w) {
+    const uint32_t d = (w & mask) ^ pattern;
+    return ~(((d & 0x7FFF7FFFu) + 0x7FFF7FFFu) | d | 0x7FFF7FFFu);
+  };
+  uint32_t hits = 0, mine = 0;  // of the warp; of batch b0 + lane
+  for (int b = b0; b < b1; ++b) {
+    uint4 v[kBatch];
+    load(v, b);
+    uint32_t n = 0;  // in both halves
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x)
+      n += (hit(v[x].x) >> 15) + (hit(v[x].y) >> 15) + (hit(v[x].z) >> 15) + (hit(v[x].w) >> 15);
+    n = __reduce_add_sync(0xFFFFFFFFu, (n & 0xFFFFu) + (n >> 16));
+    hits += n;
+    if (b - b0 == lane) mine = n;
+  }
   if (lane == 0) sh.warp_hits[warp] = hits;
   __syncthreads();
   uint32_t before = 0;
   for (int i = 0; i < warp; ++i) before += sh.warp_hits[i];
   const uint32_t r = sh.find_rank;
   if (r < before || r >= before + hits) return;
-  for (int c = w0; c < w1; c += 32 * kUnroll) {
-    const uint32_t h = hits_of(c + lane);
-    const uint32_t batch = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(__popc(h)));
-    if (r >= before + batch) {
-      before += batch;
-      continue;
-    }
-#pragma unroll 1
-    for (int x = 0; x < kUnroll; ++x) {
-      uint32_t g = h >> (8 * x) & 0xFFu;
-      const uint32_t inc = before + warp_inclusive(static_cast<uint32_t>(__popc(g)));
-      if (r < inc && r >= inc - __popc(g)) {
-        for (uint32_t left = r - (inc - __popc(g)); left > 0; --left) g &= g - 1;
-        p.tokens[m] = static_cast<int32_t>(static_cast<int64_t>(c + 32 * x + lane) * 8 - mis +
-                                           __ffs(g) - 1);
+  // (more than 32 batches of a warp: only where a CTA has a row of 131072 and more)
+  const uint32_t inc = before + warp_inclusive(mine);
+  const uint32_t over = __ballot_sync(0xFFFFFFFFu, inc > r);
+  int b = b0 + (over != 0 ? __ffs(over) - 1 : 32);
+  before = over != 0 ? __shfl_sync(0xFFFFFFFFu, inc - mine, __ffs(over) - 1)
+                     : __shfl_sync(0xFFFFFFFFu, inc, 31);
+  for (; b < b1; ++b) {
+    uint4 v[kBatch];
+    load(v, b);
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+      uint32_t g = 0;  // a bit for each logit
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const uint32_t z = hit(w[y]);
+        g |= (z >> 15 & 1u | z >> 30) << (2 * y);
+      }
+      const uint32_t to = before + warp_inclusive(static_cast<uint32_t>(__popc(g)));
+      if (r < to && r >= to - __popc(g)) {
+        for (uint32_t left = r - (to - __popc(g)); left > 0; --left) g &= g - 1;
+        const int c = c0 + 32 * (kBatch * b + x) + lane;
+        p.tokens[m] = static_cast<int32_t>(static_cast<int64_t>(c) * 8 - mis + __ffs(g) - 1);
         if (p.prob != nullptr) p.prob[m] = sh.find_prob;
       }
-      before = __shfl_sync(0xFFFFFFFFu, inc, 31);
+      before = __shfl_sync(0xFFFFFFFFu, to, 31);
     }
-    return;
+    if (before > r) return;
   }
 }
 
@@ -558,7 +566,7 @@ __device__ __noinline__ void find(const SampleArgs& p, Shared& sh, const uint16_
 __device__ __noinline__ void all_bins(const SampleArgs& p, Shared& sh, const uint16_t* row,
                                       int64_t m, int mis, const Settings& set) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kStep = kSlots / 128;  // segments at a time
+  constexpr int kStep = kSlotSegs;  // segments at a time
   if (tid == 0) sh.all_first = kBinLast + 1;
   for (int s0 = 0; s0 < kSegs; s0 += kStep) {
     for (int i = tid; i < kSlots / 4; i += kThreads)
@@ -580,11 +588,7 @@ __device__ __noinline__ void all_bins(const SampleArgs& p, Shared& sh, const uin
         if (k != 0) w += k * weight_of(sh, 128 * (s0 + s) + 32 * x + lane, sh.all_first);
         n += k;
       }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) {
-        n += __shfl_xor_sync(0xFFFFFFFFu, n, off);
-        w += __shfl_xor_sync(0xFFFFFFFFu, w, off);
-      }
+      warp_sums(n, w);
       if (lane == 0) {
         sh.number[s0 + s] = n;
         sh.mass[s0 + s] = w;
@@ -616,7 +620,6 @@ __device__ __noinline__ void all_bins(const SampleArgs& p, Shared& sh, const uin
     }
   }
   __syncthreads();
-  sum_list(sh, sh.n_list);
   const Recount source{p, sh, row, mis};
   if (warp == 0) {
     int bin;
@@ -693,7 +696,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
     };
     load(c0 + tid);
     if (tid == 0) {
-      sh.guess = sh.first = kBinLast + 1;
       sh.wide = 0;
       // the cluster's next row on its way to the L2 cache
       const int64_t next = m + gridDim.x / C;
@@ -713,67 +715,72 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
       sh.c_lo = isinf(hi) || hi == 0.f ? 0.f : (__fmaf_rn(-hi, t, ah) + al) / t;
     }
     __syncthreads();  // the counts are zero, too
-    {
-      int guess = kBinLast + 1;
-      const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-#pragma unroll
-      for (int y = 0; y < 8; ++y) {
-        const uint32_t b = bins_of(w[y >> 1]);
-        const int bin = static_cast<int>(y & 1 ? b >> 16 : b & 0xFFFFu);
-        guess = bin >= kBinFirst && bin < guess ? bin : guess;
-      }
-      guess = __reduce_min_sync(0xFFFFFFFFu, guess);
-      if (lane == 0) atomicMin(&sh.guess, guess);
-    }
-    __syncthreads();
-    const int limit = limit_of(sh.guess, set.t);
 
     // ---- counts of this CTA's part
-    uint32_t low = 0xFFFFFFFFu;  // the smallest bins
-    bool wide = false;
+    uint32_t least = 0x7FFF7FFFu;
     for (int c = c0 + tid; c - tid < c1; c += kUnroll * kThreads) {
+      uint4 now[kUnroll];
+#pragma unroll
+      for (int x = 0; x < kUnroll; ++x) now[x] = v[x];
+      if (c - tid + kUnroll * kThreads < c1) load(c + kUnroll * kThreads);
 #pragma unroll
       for (int x = 0; x < kUnroll; ++x) {
-        const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const uint32_t b = bins_of(w[y]);
-          low = __vminu2(low, b);
-          wide |= count(sh.counts, static_cast<int>(b & 0xFFFFu), limit);
-          wide |= count(sh.counts, static_cast<int>(b >> 16), limit);
-        }
+        count2(sh.counts, now[x].x, least);
+        count2(sh.counts, now[x].y, least);
+        count2(sh.counts, now[x].z, least);
+        count2(sh.counts, now[x].w, least);
       }
-      if (c - tid + kUnroll * kThreads < c1) load(c + kUnroll * kThreads);
     }
     {
-      int first = static_cast<int>((low & 0xFFFFu) < low >> 16 ? low & 0xFFFFu : low >> 16);
-      first = __reduce_min_sync(0xFFFFFFFFu, first);
-      if (lane == 0) atomicMin(&sh.first, first == kZeroBin + 1 ? kZeroBin : first);
-      if (wide) sh.wide = 1;
+      // (bits − 0x8001 below 0: a size, and one that is not counted)
+      const int lo = static_cast<int16_t>(least & 0xFFFFu), hi = static_cast<int16_t>(least >> 16);
+      const int bound = static_cast<int>(kLeastBits) - 0x8001;
+      if (lo < bound || hi < bound) sh.wide = 1;
+    }
+    __syncthreads();
+    if (tid == 0) {
+      // −0 is 0; larger values than the counted ones, and NaN, are another matter
+      sh.counts[kZeroSlot] += sh.counts[kNegSlot];
+      if (sh.counts[0] != 0) sh.wide = 1;
+      sh.far = sh.counts[kFarSlot] != 0;
+      sh.counts[kNegSlot] = sh.counts[0] = sh.counts[kFarSlot] = 0;
     }
     __syncthreads();
     // ---- which segments hold anything
-    for (int s = warp; s < kSlots / 128; s += kWarps) {
+    for (int s = warp; s < kSlotSegs; s += kWarps) {
       const uint4 n = reinterpret_cast<const uint4*>(sh.counts)[s * 32 + lane];
       const uint32_t any = __ballot_sync(0xFFFFFFFFu, (n.x | n.y | n.z | n.w) != 0);
       if (lane == 0) reinterpret_cast<uint8_t*>(sh.seg_counts)[s] = any != 0;
     }
     __syncthreads();
-    if (warp < static_cast<int>(sizeof(sh.occupied) / 4)) {
-      const int s = 32 * warp + lane;
-      const uint32_t bits = __ballot_sync(
-          0xFFFFFFFFu, s < kSlots / 128 && reinterpret_cast<uint8_t*>(sh.seg_counts)[s] != 0);
-      if (lane == 0) sh.occupied[warp] = bits;
+    if (warp == 0) {
+      int seg = kSlotSegs;  // of the largest value of this part
+#pragma unroll
+      for (int i = static_cast<int>(sizeof(sh.occupied) / 4) - 1; i >= 0; --i) {
+        const int s = 32 * i + lane;
+        const uint32_t bits = __ballot_sync(
+            0xFFFFFFFFu, s < kSlotSegs && reinterpret_cast<uint8_t*>(sh.seg_counts)[s] != 0);
+        if (lane == 0) sh.occupied[i] = bits;
+        if (bits != 0) seg = 32 * i + __ffs(bits) - 1;
+      }
+      int slot = kSlots;
+      if (seg < kSlotSegs)
+#pragma unroll
+        for (int x = 3; x >= 0; --x)
+          if (sh.counts[128 * seg + 4 * lane + x] != 0) slot = 128 * seg + 4 * lane + x;
+      slot = __reduce_min_sync(0xFFFFFFFFu, slot);
+      if (lane == 0) sh.first = slot < kSlots ? bin_of_slot(slot) : kBinLast + 1;
     }
     meet();
     if (warp == 0) {
-      int first = kBinLast + 1, any_wide = 0, at = 0;
+      int first = kBinLast + 1, any_wide = 0, any_far = 0, at = 0;
       uint32_t w[sizeof(sh.occupied) / 4] = {};
 #pragma unroll
       for (int r = 0; r < C; ++r) {
         const Shared* o = peer(r);
         first = o->first < first ? o->first : first;
         any_wide |= o->wide;
+        any_far |= o->far;
 #pragma unroll
         for (size_t i = 0; i < sizeof(sh.occupied) / 4; ++i) w[i] |= o->occupied[i];
       }
@@ -787,7 +794,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
       if (lane == 0) {
         sh.n_list = at;
         sh.all_first = first;
-        sh.all_wide = any_wide;
+        // logits of −2^16 and below have no weight next to one 33·T above that
+        sh.all_wide = any_wide != 0 ||
+                      (any_far != 0 && !(first <= kBinLast && value_of(first) > 33.f * set.t - 65536.f));
         sh.find_bin = -1;
       }
     }
@@ -811,31 +820,26 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
       source.get(seg, c);
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        if (c[x] != 0) w += c[x] * weigh(sh, bin_of_slot(128 * seg + 4 * lane + x), first);
+        w += c[x] * weigh(sh, bin_of_slot(128 * seg + 4 * lane + x), first);
         n += c[x];
       }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) {
-        n += __shfl_xor_sync(0xFFFFFFFFu, n, off);
-        w += __shfl_xor_sync(0xFFFFFFFFu, w, off);
-      }
+      warp_sums(n, w);
       if (lane == 0) {
         peer(0)->number[j] = n;
         peer(0)->mass[j] = w;
       }
     }
     meet();
-    if (rank == 0) {
-      sum_list(sh, n_list);
-      if (warp == 0) {
+    if (rank == 0 && warp == 0) {
+      {
         int bin;
         uint32_t r;
         float prob;
         if (choose(p, sh, source, set, n_list, first, &bin, &r, &prob)) {
           // whose part holds the r-th token of that value
-          const int slot = bin < kPosBin + kSpan ? bin - kPosBin
-                           : bin < kNegBin       ? kZeroSlot
-                                                 : bin - kNegBin + kNegSlot;
+          const int slot = bin <= kPosBin + kSpan ? bin - kPosBin
+                           : bin < 0x8000         ? kZeroSlot
+                                                  : bin - kPosBin - kNegShift + kNegSlot;
           int owner = 0;
 #pragma unroll
           for (int i = 0; i < C - 1; ++i) {
