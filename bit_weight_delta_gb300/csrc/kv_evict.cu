@@ -41,23 +41,20 @@ struct EvictArgs {
   DevCtx ctx;
 };
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kDigits = 2048;
-constexpr int kMaxCluster = 8;
 constexpr int kMaxKeys = 49152;  // of a CTA
+constexpr int kMaxLen = 8 * kMaxKeys;
 constexpr uint32_t kProtected = 0xFFFFFFFFu;
 
 struct Shared {
   uint32_t digits[3][kDigits];  // counts of the three passes
-  uint32_t bits[kMaxKeys / 32];  // the slots that stay
-  uint32_t warp_n[2][kWarps];
+  uint32_t warp_n[2][32];
   uint32_t found, above;         // a pass' digit, and the keys above it
   uint32_t equal;                // keys that equal the threshold
   uint32_t holes, movers;        // of this CTA
   int bad, prefix;
-  // then keys[cap + 64]; once they are no longer needed, the lists of holes and
-  // movers, (cap + 64) / 2 each
+  // then keys[cap + 64], once they are no longer needed the lists of holes and movers,
+  // (cap + 64) / 2 each; and a bit for each key that stays
 };
 
 // New length of a sequence of kv keys whose first `prefix` are shared.
@@ -89,11 +86,14 @@ __device__ __forceinline__ T warp_inclusive(T v) {
   return v;
 }
 
-template <int C>
-__global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs p) {
+// T threads: 256 for few keys, four CTAs an SM, and 1024 for many.
+template <int C, int T>
+__global__ void __launch_bounds__(T, T == 256 ? 4 : 1) kv_evict_kernel(const EvictArgs p) {
+  constexpr int kWarps = T / 32;
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& sh = *reinterpret_cast<Shared*>(smem);
   uint32_t* keys = reinterpret_cast<uint32_t*>(smem + sizeof(Shared));
+  uint32_t* stay = keys + p.cap + 64;  // bits
   const bd_attention_batch& b = p.b;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   cg::cluster_group cluster = cg::this_cluster();
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs p) {
   };
   const auto peer = [&](int r) { return C == 1 ? &sh : cluster.map_shared_rank(&sh, r); };
 
-  for (int i = tid; i < 3 * kDigits; i += kThreads) (&sh.digits[0][0])[i] = 0u;
+  for (int i = tid; i < 3 * kDigits; i += T) (&sh.digits[0][0])[i] = 0u;
   if (tid == 0) {
     sh.bad = 0;
     sh.prefix = 0;
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs p) {
   griddep_wait();
   griddep_launch_dependents();
   __syncthreads();
-  for (int g = tid; g < b.n_group; g += kThreads)
+  for (int g = tid; g < b.n_group; g += T)
     if (b.group_offsets[g] <= s && s < b.group_offsets[g + 1])
       atomicMax(&sh.prefix, b.prefix_len[g]);
   const int kv = b.kv_len[s], keep = p.keep[s];
@@ -139,18 +139,41 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs p) {
            (slot & (b.page_size - 1));
   };
   const bool apart = p.weights_out != p.weights || p.positions_out != p.positions;
-  const auto copy_entry = [&](int slot) {
-    const int64_t row = row_of(slot);
-    if (row < 0) {
-      record_error(p.ctx, kErrBounds);
-      return;
-    }
-    p.weights_out[row] = p.weights[row];
-    p.positions_out[row] = p.positions[row];
+  // kBatch slots of a thread at a time, T apart: their rows, weights and positions
+  constexpr int kBatch = 8;
+  struct Entries {
+    int64_t row[kBatch];
+    float w[kBatch];
+    int pos[kBatch];
   };
-  if (apart)  // what is not chosen from
-    for (int i = rank * kThreads + tid; i < (len == kv ? kv : prefix); i += C * kThreads)
-      copy_entry(i);
+  const auto fetch = [&](Entries& e, int slot, int end) {
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x)
+      e.row[x] = slot + x * T < end ? row_of(slot + x * T) : -2;
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      e.w[x] = e.row[x] >= 0 ? p.weights[e.row[x]] : 0.f;
+      e.pos[x] = e.row[x] >= 0 ? p.positions[e.row[x]] : 0;
+    }
+  };
+  bool bad = false;
+  if (apart) {  // what is not chosen from
+    const int end = len == kv ? kv : prefix;
+    for (int slot = rank * T * kBatch + tid; slot < end; slot += C * T * kBatch) {
+      Entries e;
+      fetch(e, slot, end);
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        if (e.row[x] >= 0) {
+          p.weights_out[e.row[x]] = e.w[x];
+          p.positions_out[e.row[x]] = e.pos[x];
+        }
+        bad |= e.row[x] == -1;
+      }
+    }
+    if (bad) record_error(p.ctx, kErrBounds);
+    bad = false;
+  }
   if (len == kv) return;
 
   // ---- the keys of slots prefix + [i0, i1)
@@ -162,17 +185,26 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs p) {
   const int late = static_cast<int>(late64 > INT32_MAX   ? INT32_MAX
                                     : late64 < INT32_MIN ? INT32_MIN
                                                          : late64);
-  bool bad = false;
-  for (int i = tid; i < n; i += kThreads) {
-    const int64_t row = row_of(prefix + i0 + i);
-    uint32_t key = 0u;
-    if (row < 0) {
-      bad = true;
-    } else {
-      key = key_of(p.weights[row], p.positions[row], late, p.sink);
-      atomicAdd(&sh.digits[0][key >> 21], 1u);
+  for (int i = tid; i < n; i += T * kBatch) {
+    Entries e;
+    fetch(e, prefix + i0 + i, prefix + i0 + n);
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      if (e.row[x] == -2) break;
+      uint32_t key = 0u;
+      if (e.row[x] < 0) {
+        bad = true;
+      } else {
+        key = key_of(e.w[x], e.pos[x], late, p.sink);
+        atomicAdd(&sh.digits[0][key >> 21], 1u);
+        // (all slots that go on; the movers' weights overwrite the freed ones' below)
+        if (apart && i0 + i + x * T < K) {
+          p.weights_out[e.row[x]] = e.w[x];
+          p.positions_out[e.row[x]] = e.pos[x];
+        }
+      }
+      keys[i + x * T] = key;
     }
-    keys[i] = key;
   }
   if (bad) sh.bad = 1;
   meet();
@@ -193,33 +225,40 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs p) {
     const int down = kShift[pass];
     if (pass > 0) {
       const int up = kShift[pass - 1];
-      for (int i = tid; i < n; i += kThreads) {
+      for (int i = tid; i < n; i += T) {
         const uint32_t key = keys[i];
         if (key >> up == threshold >> up) atomicAdd(&sh.digits[pass][key >> down & 0x7FFu], 1u);
       }
       meet();
     }
-    // four digits per thread, from the top
-    uint32_t c[4] = {0u, 0u, 0u, 0u};
+    // an even share of the digits per thread, from the top
+    constexpr int kEach = kDigits / T;
+    uint32_t c[kEach];
+#pragma unroll
+    for (int x = 0; x < kEach; ++x) c[x] = 0u;
 #pragma unroll
     for (int r = 0; r < C; ++r) {
-      const uint4 v =
-          reinterpret_cast<const uint4*>(peer(r)->digits[pass])[kDigits / 4 - 1 - tid];
-      c[0] += v.w;
-      c[1] += v.z;
-      c[2] += v.y;
-      c[3] += v.x;
+      const uint2* d = reinterpret_cast<const uint2*>(peer(r)->digits[pass] + kDigits - kEach * (tid + 1));
+#pragma unroll
+      for (int x = 0; x < kEach / 2; ++x) {
+        const uint2 v = d[x];
+        c[kEach - 1 - 2 * x] += v.x;
+        c[kEach - 2 - 2 * x] += v.y;
+      }
     }
-    const uint32_t sum = c[0] + c[1] + c[2] + c[3];
+    uint32_t sum = 0u;
+#pragma unroll
+    for (int x = 0; x < kEach; ++x) sum += c[x];
     const uint32_t inc = warp_inclusive(sum);
     if (lane == 31) sh.warp_n[0][warp] = inc;
     __syncthreads();
     uint32_t above = inc - sum;
-    for (int i = 0; i < warp; ++i) above += sh.warp_n[0][i];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
+    for (int i = 0; i < kWarps; ++i) above += i < warp ? sh.warp_n[0][i] : 0u;
+#pragma unroll
+    for (int x = 0; x < kEach; ++x) {
       if (above < left && left <= above + c[x]) {
-        sh.found = static_cast<uint32_t>(kDigits - 1 - 4 * tid - x);
+        sh.found = static_cast<uint32_t>(kDigits - 1 - kEach * tid - x);
         sh.above = above;
         sh.equal = c[x];
       }
@@ -273,7 +312,7 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs p) {
       stays = !split || equal_at + __popc(same & ((1u << lane) - 1u)) < left;
     equal_at += __popc(same);
     const uint32_t kept = __ballot_sync(0xFFFFFFFFu, stays);
-    if (lane == 0) sh.bits[i >> 5] = kept;
+    if (lane == 0) stay[i >> 5] = kept;
     holes += __popc(lives & ~kept & below(i));
     movers += __popc(kept & ~below(i));
   }
@@ -318,14 +357,13 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs p) {
   };
   for (int i = w0; i < w1; i += 32) {
     const uint32_t lives = w1 - i >= 32 ? 0xFFFFFFFFu : (1u << (w1 - i)) - 1u;
-    const uint32_t kept = sh.bits[i >> 5], low = below(i);
+    const uint32_t kept = stay[i >> 5], low = below(i);
     const uint32_t hole = lives & ~kept & low, mover = kept & ~low;
     const uint32_t before = (1u << lane) - 1u;
     if (hole >> lane & 1u) put(0, hole_at + __popc(hole & before), prefix + i0 + i + lane);
     if (mover >> lane & 1u) put(1, mover_at + __popc(mover & before), prefix + i0 + i + lane);
     hole_at += __popc(hole);
     mover_at += __popc(mover);
-    if (apart && (kept & low) >> lane & 1u) copy_entry(prefix + i0 + i + lane);
   }
   meet();
 
@@ -335,14 +373,14 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs p) {
   const int lanes = b.head_dim >> 3;  // per row
   const int rows = 32 / lanes;        // rows a warp moves at once, of keys or values
   const int sub = lane / lanes, at = lane - sub * lanes;
-  constexpr int kBatch = 4;
-  for (int e0 = warp * rows; e0 < mine; e0 += kBatch * kWarps * rows) {
-    uint4 k[kBatch], v[kBatch];
-    int64_t to[kBatch];
-    float w[kBatch];
-    int pos[kBatch];
+  constexpr int kMoves = 4;
+  for (int e0 = warp * rows; e0 < mine; e0 += kMoves * kWarps * rows) {
+    uint4 k[kMoves], v[kMoves];
+    int64_t to[kMoves];
+    float w[kMoves];
+    int pos[kMoves];
 #pragma unroll
-    for (int x = 0; x < kBatch; ++x) {
+    for (int x = 0; x < kMoves; ++x) {
       const int e = e0 + x * kWarps * rows + sub;
       to[x] = -1;
       if (e < mine) {
@@ -355,7 +393,7 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs p) {
       }
     }
 #pragma unroll
-    for (int x = 0; x < kBatch; ++x) {
+    for (int x = 0; x < kMoves; ++x) {
       if (to[x] < 0) continue;
       reinterpret_cast<uint4*>(p.k_pages + to[x] * b.head_dim)[at] = k[x];
       reinterpret_cast<uint4*>(p.v_pages + to[x] * b.head_dim)[at] = v[x];
@@ -388,9 +426,11 @@ __global__ void __launch_bounds__(256)
   pos_offset[s] += kv - len;
 }
 
-size_t smem_bytes(int cap) { return sizeof(Shared) + 4 * (static_cast<size_t>(cap) + 64); }
+size_t smem_bytes(int cap) {
+  return sizeof(Shared) + 4 * (static_cast<size_t>(cap) + 64) + static_cast<size_t>(cap) / 8;
+}
 
-template <int C>
+template <int C, int T>
 cudaError_t launch(const EvictArgs& p, cudaStream_t s) {
   static bool done[64] = {};
   int dev = 0;
@@ -399,16 +439,54 @@ cudaError_t launch(const EvictArgs& p, cudaStream_t s) {
   {
     std::lock_guard<std::mutex> lock(host_cache_mutex());
     if (!done[dev & 63]) {
-      e = cudaFuncSetAttribute(kv_evict_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      e = cudaFuncSetAttribute(kv_evict_kernel<C, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                static_cast<int>(smem_bytes(kMaxKeys)));
+      if (e == cudaSuccess && C > 8)
+        e = cudaFuncSetAttribute(kv_evict_kernel<C, T>,
+                                 cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       if (e != cudaSuccess) return e;
       done[dev & 63] = true;
     }
   }
-  static_assert(sizeof(Shared) + 4 * (kMaxKeys + 64) <= 227 * 1024, "shared memory of one CTA");
+  static_assert(sizeof(Shared) + 4 * (kMaxKeys + 64) + kMaxKeys / 8 <= 227 * 1024,
+                "shared memory of one CTA");
   const unsigned grid = static_cast<unsigned>(p.b.n_seq) * p.b.n_kv_heads * C;
-  return launch_pdl_cluster(kv_evict_kernel<C>, dim3(grid), dim3(kThreads), C, smem_bytes(p.cap),
-                            s, p);
+  return launch_pdl_cluster(kv_evict_kernel<C, T>, dim3(grid), dim3(T), C, smem_bytes(p.cap), s, p);
+}
+
+// Clusters of 16 that the device holds at once with the most shared memory that the
+// choice below gives them (half of the keys of the longest); 0 where it holds none.
+int large_clusters() {
+  static int known[64] = {};  // plus one
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> lock(host_cache_mutex());
+  int& n = known[dev & 63];
+  if (n == 0) {
+    const size_t bytes = smem_bytes(kMaxLen / 16);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(16);
+    cfg.blockDim = dim3(1024);
+    cfg.dynamicSmemBytes = bytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 16;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int count = 0;
+    const auto kernel = kv_evict_kernel<16, 1024>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(bytes)) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&count, kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      count = 0;
+    }
+    n = count + 1;
+  }
+  return n - 1;
 }
 
 bool off(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) != 0; }
@@ -437,7 +515,7 @@ bd_status bitdelta_kv_evict(const bd_attention_batch* batch, const int32_t* keep
   int st = bd::check_batch(batch, keep);
   if (st != BD_OK) return static_cast<bd_status>(st);
   if (recent < 0 || sink < 0) return BD_ERR_INVALID_ARG;
-  if (batch->max_kv_len > bd::kMaxCluster * bd::kMaxKeys) return BD_ERR_UNSUPPORTED_SHAPE;
+  if (batch->max_kv_len > bd::kMaxLen) return BD_ERR_UNSUPPORTED_SHAPE;
   if (static_cast<int64_t>(batch->n_seq) * batch->n_kv_heads > (1 << 27))
     return BD_ERR_UNSUPPORTED_SHAPE;
   if (batch->n_seq == 0) return BD_OK;
@@ -462,19 +540,26 @@ bd_status bitdelta_kv_evict(const bd_attention_batch* batch, const int32_t* keep
   p.positions = positions;
   p.weights_out = weights_out;
   p.positions_out = positions_out;
-  // CTAs per sequence and key head: as many as the keys need, and more while
-  // the device has SMs left for them and each still has a few thousand.
+  // CTAs per sequence and key head: as many as the keys need, and more while the device
+  // has SMs left for them and each still has 2048.  Where there are more CTAs than SMs,
+  // and few keys each, they have 256 threads, which leaves an SM four of them: their
+  // phases wait for one another.
   const int64_t items = static_cast<int64_t>(batch->n_seq) * batch->n_kv_heads;
+  const int len = batch->max_kv_len;
   int c = 1;
-  while (c < bd::kMaxCluster &&
-         (batch->max_kv_len > bd::kMaxKeys * c || (items * 2 * c <= sms && batch->max_kv_len > 2048 * c)))
-    c *= 2;
-  p.cap = ((batch->max_kv_len + c - 1) / c + 31) / 32 * 32;
+  while (c < 8 && (len > bd::kMaxKeys * c || (items * 2 * c <= sms && len > 2048 * c))) c *= 2;
+  if (c == 8 && items * 16 <= sms && len > 2048 * 8 && bd::large_clusters() >= items) c = 16;
+  p.cap = ((len + c - 1) / c + 31) / 32 * 32;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = c == 1   ? bd::launch<1>(p, s)
-                        : c == 2 ? bd::launch<2>(p, s)
-                        : c == 4 ? bd::launch<4>(p, s)
-                                 : bd::launch<8>(p, s);
+  const bool few = p.cap <= 8192 && items * c > sms;
+  cudaError_t e;
+  switch (c) {
+    case 1: e = few ? bd::launch<1, 256>(p, s) : bd::launch<1, 1024>(p, s); break;
+    case 2: e = few ? bd::launch<2, 256>(p, s) : bd::launch<2, 1024>(p, s); break;
+    case 4: e = few ? bd::launch<4, 256>(p, s) : bd::launch<4, 1024>(p, s); break;
+    case 8: e = few ? bd::launch<8, 256>(p, s) : bd::launch<8, 1024>(p, s); break;
+    default: e = few ? bd::launch<16, 256>(p, s) : bd::launch<16, 1024>(p, s); break;
+  }
   return e == cudaSuccess ? BD_OK : BD_ERR_CUDA;
 }
 

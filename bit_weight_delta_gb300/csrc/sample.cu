@@ -22,7 +22,7 @@
 //
 // A row is shared by a cluster of CTAs, each with counts of its own part, which
 // are added where they are read (distributed shared memory); a cluster takes row
-// after row.  Segments are 128 bins; most are empty.
+// after row.  Segments are 32 bins, a lane each; most are empty.
 #include <cooperative_groups.h>
 
 #include <cstdint>
@@ -53,19 +53,21 @@ constexpr int kOneBits = 44;      // a weight of 1 is 2^44; 2^19 of them stay be
 constexpr int kBinFirst = 0x7F;   // +inf; NaN lies below
 constexpr int kBinLast = 0xFF7F;  // −inf and NaN lie above
 constexpr int kZeroBin = 0x7FFF;
-constexpr int kSegs = 512;        // of 128 bins, of all bins
+constexpr int kSegs = 2048;       // of 32 bins, of all bins
 
 // The counters: of either sign kSpan bins, behind one for the bins before them and with
-// one for those that follow; 41 segments each.  Behind the positive ones (and before the
+// one for those that follow.  Behind the positive ones (and before the
 // negative) lie zero and what is smaller than the counted values.
 constexpr int kSpan = 56 * 128;
 constexpr int kPosBin = 0x8000 - ((127 + 16) << 7) - 1;  // 2^16, of slot 0
 constexpr int kNegShift = 0x8000 + ((127 - 40) << 7) - 1 - kPosBin;  // to the negative bins
-constexpr int kNegSlot = kSpan + 128;
+constexpr int kNegSlot = kSpan + 64;
 constexpr int kSlots = 2 * kNegSlot;
 constexpr int kZeroSlot = kSpan + 1;
 constexpr int kFarSlot = kNegSlot + kSpan + 1;  // −2^16 and below, −inf, −NaN
-constexpr int kSlotSegs = kSlots / 128;
+static_assert(kSlots % 128 == 0, "four segments at a time");
+constexpr int kSlotSegs = kSlots / 32;
+constexpr int kMasks = (kSlotSegs + 31) / 32;
 // The least size that is counted, as a bf16 number's bits.
 constexpr uint32_t kLeastBits = (127 - 40) << 7;
 
@@ -97,8 +99,9 @@ struct Shared {
   uint64_t mass[kSegs];            // rank 0: sums before each listed segment
   uint32_t number[kSegs];
   uint16_t list[kSegs];            // segments that are not empty, in order
-  uint32_t seg_counts[128];        // one segment's, where all bins are gone through
-  uint32_t occupied[(kSlotSegs + 31) / 32];   // this CTA's
+  uint32_t seg_counts[32];         // one segment's, where all bins are gone through
+  alignas(8) uint8_t flags[8 * kMasks];  // of four segments each: not empty (0 behind them)
+  uint32_t occupied[kMasks];       // this CTA's
   float pow2_hi[64], pow2_lo[64];
   float half, c_hi, c_lo;          // 1/2 and 2·log2(e)/T (2^-65 and 2^64 of it for large T)
   int first, all_first;            // the largest value's bin, of this part and of the row
@@ -236,20 +239,13 @@ struct Place {
 template <int C>
 struct Counters {
   const uint32_t* counts[C];
-  __device__ __forceinline__ int bin(int seg, int i) const { return bin_of_slot(128 * seg + i); }
-  // the lane's four bins
-  __device__ __forceinline__ void get(int seg, uint32_t (&n)[4]) const {
-    const int lane = threadIdx.x & 31;
+  // of the lane
+  __device__ __forceinline__ int bin(int seg, int i) const { return bin_of_slot(32 * seg + i); }
+  __device__ __forceinline__ uint32_t get(int seg) const {
+    uint32_t n = 0;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) n[x] = 0;
-#pragma unroll
-    for (int r = 0; r < C; ++r) {
-      const uint4 w = reinterpret_cast<const uint4*>(counts[r])[seg * 32 + lane];
-      n[0] += w.x;
-      n[1] += w.y;
-      n[2] += w.z;
-      n[3] += w.w;
-    }
+    for (int r = 0; r < C; ++r) n += counts[r][32 * seg + (threadIdx.x & 31)];
+    return n;
   }
 };
 
@@ -282,23 +278,20 @@ struct Recount {
   Shared& sh;
   const uint16_t* row;
   int mis;
-  __device__ __forceinline__ int bin(int seg, int i) const { return 128 * seg + i; }
+  __device__ __forceinline__ int bin(int seg, int i) const { return 32 * seg + i; }
   __device__ void count() const {  // every thread
-    count_range(p, row, mis, 128 * sh.asked, 128, sh.seg_counts);
+    count_range(p, row, mis, 32 * sh.asked, 32, sh.seg_counts);
     cta_barrier();
   }
-  __device__ __forceinline__ void get(int seg, uint32_t (&n)[4]) const {  // the first warp
+  __device__ __forceinline__ uint32_t get(int seg) const {  // the first warp
     const int lane = threadIdx.x & 31;
-    reinterpret_cast<uint4*>(sh.seg_counts)[lane] = make_uint4(0u, 0u, 0u, 0u);
+    sh.seg_counts[lane] = 0;
     if (lane == 0) sh.asked = seg;
     cta_barrier();
     count();
-    const uint4 w = reinterpret_cast<const uint4*>(sh.seg_counts)[lane];
-    n[0] = w.x;
-    n[1] = w.y;
-    n[2] = w.z;
-    n[3] = w.w;
+    const uint32_t n = sh.seg_counts[lane];
     __syncwarp();
+    return n;
   }
   // the other warps, until the first has what it needs
   __device__ void serve() const {
@@ -377,52 +370,32 @@ __device__ __noinline__ bool choose(const SampleArgs& p, Shared& sh, const Sourc
     }
     return lo;
   };
-  // The segment that was last looked at: the lane's four bins.
+  // The segment that was last looked at: the lane's bin.
   int have = -1;
-  uint32_t c[4], number = 0;
-  uint64_t w[4], mass = 0;
+  Place mine{};
   const auto look = [&](int j) {
     if (j == have) return;
     have = j;
     const int seg = sh.list[j];
-    source.get(seg, c);
-    uint32_t n = 0;
-    uint64_t w_all = 0;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      w[x] = weigh(sh, source.bin(seg, 4 * lane + x), first);
-      n += c[x];
-      w_all += c[x] * w[x];
-    }
-    number = sh.number[j] + warp_inclusive(n) - n;
-    mass = sh.mass[j] + warp_inclusive(w_all) - w_all;
+    mine.count = source.get(seg);
+    mine.bin = source.bin(seg, lane);
+    mine.weight = weigh(sh, mine.bin, first);
+    const uint64_t w = mine.count * mine.weight;
+    mine.number = sh.number[j] + warp_inclusive(mine.count) - mine.count;
+    mine.mass = sh.mass[j] + warp_inclusive(w) - w;
   };
   // The first bin of segment j for which `inside` holds, given the sums before it; all
   // lanes receive it.
   const auto bin_in = [&](int j, auto inside) {
     look(j);
-    Place pl, found{};
-    pl.number = number;
-    pl.mass = mass;
-    bool any = false;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      pl.bin = x;
-      pl.weight = w[x];
-      pl.count = c[x];
-      if (!any && c[x] != 0 && inside(pl)) {
-        any = true;
-        found = pl;
-      }
-      pl.number += c[x];
-      pl.mass += c[x] * w[x];
-    }
-    const uint32_t yes = __ballot_sync(0xFFFFFFFFu, any);
+    const uint32_t yes = __ballot_sync(0xFFFFFFFFu, mine.count != 0 && inside(mine));
     const int src = yes != 0 ? __ffs(yes) - 1 : 0;
-    found.bin = source.bin(sh.list[j], 4 * src + __shfl_sync(0xFFFFFFFFu, found.bin, src));
-    found.number = __shfl_sync(0xFFFFFFFFu, found.number, src);
-    found.mass = __shfl_sync(0xFFFFFFFFu, found.mass, src);
-    found.weight = __shfl_sync(0xFFFFFFFFu, found.weight, src);
+    Place found;
+    found.bin = __shfl_sync(0xFFFFFFFFu, mine.bin, src);
+    found.number = __shfl_sync(0xFFFFFFFFu, mine.number, src);
+    found.mass = __shfl_sync(0xFFFFFFFFu, mine.mass, src);
+    found.weight = __shfl_sync(0xFFFFFFFFu, mine.weight, src);
+    found.count = __shfl_sync(0xFFFFFFFFu, mine.count, src);
     return found;
   };
   const auto at_mass = [&](uint64_t reach) {  // the bin in which the sum reaches `reach`
@@ -469,10 +442,7 @@ __device__ __noinline__ bool choose(const SampleArgs& p, Shared& sh, const Sourc
       return weight_of(sh, bin < first ? first : bin, first) >= least;
     });
     look(j);
-    uint32_t with = 0;
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-      if (w[x] >= least) with += c[x];
+    uint32_t with = mine.weight >= least ? mine.count : 0;
     with = __reduce_add_sync(0xFFFFFFFFu, with);
     const uint32_t at = sh.number[j] + with;
     cut = at < cut ? (at > 0 ? at : 1) : cut;
@@ -572,22 +542,17 @@ __device__ __noinline__ void all_bins(const SampleArgs& p, Shared& sh, const uin
     for (int i = tid; i < kSlots / 4; i += kThreads)
       reinterpret_cast<uint4*>(sh.counts)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
-    count_range(p, row, mis, 128 * s0, kSlots, sh.counts);
+    count_range(p, row, mis, 32 * s0, kSlots, sh.counts);
     __syncthreads();
     int first = kBinLast + 1;
     for (int i = kSlots - 1 - tid; i >= 0; i -= kThreads)
-      if (sh.counts[i] != 0) first = 128 * s0 + i;
+      if (sh.counts[i] != 0) first = 32 * s0 + i;
     first = __reduce_min_sync(0xFFFFFFFFu, first);
     if (lane == 0) atomicMin(&sh.all_first, first);
     __syncthreads();
     for (int s = warp; s < kStep && s0 + s < kSegs; s += kWarps) {
-      uint32_t n = 0;
-      uint64_t w = 0;
-      for (int x = 0; x < 4; ++x) {
-        const uint32_t k = sh.counts[128 * s + 32 * x + lane];
-        if (k != 0) w += k * weight_of(sh, 128 * (s0 + s) + 32 * x + lane, sh.all_first);
-        n += k;
-      }
+      uint32_t n = sh.counts[32 * s + lane];
+      uint64_t w = n != 0 ? n * weight_of(sh, 32 * (s0 + s) + lane, sh.all_first) : 0;
       warp_sums(n, w);
       if (lane == 0) {
         sh.number[s0 + s] = n;
@@ -663,6 +628,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
 
   for (int i = tid; i < kSlots / 4; i += kThreads)
     reinterpret_cast<uint4*>(sh.counts)[i] = make_uint4(0u, 0u, 0u, 0u);
+  for (int i = tid; i < 8 * kMasks; i += kThreads) sh.flags[i] = 0;
   if (tid < 64) {
     sh.pow2_hi[tid] = kPow2.hi[tid];
     sh.pow2_lo[tid] = kPow2.lo[tid];
@@ -746,53 +712,61 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
       sh.counts[kNegSlot] = sh.counts[0] = sh.counts[kFarSlot] = 0;
     }
     __syncthreads();
-    // ---- which segments hold anything
-    for (int s = warp; s < kSlotSegs; s += kWarps) {
+    // ---- which segments hold anything: four at a time, eight lanes each
+    for (int s = warp; s < kSlots / 128; s += kWarps) {
       const uint4 n = reinterpret_cast<const uint4*>(sh.counts)[s * 32 + lane];
       const uint32_t any = __ballot_sync(0xFFFFFFFFu, (n.x | n.y | n.z | n.w) != 0);
-      if (lane == 0) reinterpret_cast<uint8_t*>(sh.seg_counts)[s] = any != 0;
+      if (lane == 0)
+        sh.flags[s] = static_cast<uint8_t>((any & 0xFFu ? 1 : 0) | (any & 0xFF00u ? 2 : 0) |
+                                           (any & 0xFF0000u ? 4 : 0) | (any >> 24 ? 8 : 0));
     }
     __syncthreads();
     if (warp == 0) {
-      int seg = kSlotSegs;  // of the largest value of this part
-#pragma unroll
-      for (int i = static_cast<int>(sizeof(sh.occupied) / 4) - 1; i >= 0; --i) {
-        const int s = 32 * i + lane;
-        const uint32_t bits = __ballot_sync(
-            0xFFFFFFFFu, s < kSlotSegs && reinterpret_cast<uint8_t*>(sh.seg_counts)[s] != 0);
-        if (lane == 0) sh.occupied[i] = bits;
-        if (bits != 0) seg = 32 * i + __ffs(bits) - 1;
+      uint32_t bits = 0;
+      if (lane < kMasks) {
+        const uint32_t* f = reinterpret_cast<const uint32_t*>(sh.flags) + 2 * lane;
+        // a nibble of each byte
+        const auto pack = [](uint32_t x) {
+          x = (x | x >> 4) & 0x00FF00FFu;
+          return (x | x >> 8) & 0xFFFFu;
+        };
+        bits = pack(f[0]) | pack(f[1]) << 16;
+        sh.occupied[lane] = bits;
       }
-      int slot = kSlots;
-      if (seg < kSlotSegs)
-#pragma unroll
-        for (int x = 3; x >= 0; --x)
-          if (sh.counts[128 * seg + 4 * lane + x] != 0) slot = 128 * seg + 4 * lane + x;
-      slot = __reduce_min_sync(0xFFFFFFFFu, slot);
+      const uint32_t live = __ballot_sync(0xFFFFFFFFu, bits != 0);
+      int slot = kSlots;  // of the largest value of this part
+      if (live != 0) {
+        const int at = __ffs(live) - 1;
+        const int seg = 32 * at + __ffs(__shfl_sync(0xFFFFFFFFu, bits, at)) - 1;
+        const uint32_t some = __ballot_sync(0xFFFFFFFFu, sh.counts[32 * seg + lane] != 0);
+        slot = 32 * seg + __ffs(some) - 1;
+      }
       if (lane == 0) sh.first = slot < kSlots ? bin_of_slot(slot) : kBinLast + 1;
     }
     meet();
     if (warp == 0) {
-      int first = kBinLast + 1, any_wide = 0, any_far = 0, at = 0;
-      uint32_t w[sizeof(sh.occupied) / 4] = {};
+      int first = kBinLast + 1, any_wide = 0, any_far = 0;
+      uint32_t w = 0;
 #pragma unroll
       for (int r = 0; r < C; ++r) {
         const Shared* o = peer(r);
         first = o->first < first ? o->first : first;
         any_wide |= o->wide;
         any_far |= o->far;
-#pragma unroll
-        for (size_t i = 0; i < sizeof(sh.occupied) / 4; ++i) w[i] |= o->occupied[i];
+        if (lane < kMasks) w |= o->occupied[lane];
       }
+      int n_list = 0;
 #pragma unroll
-      for (size_t i = 0; i < sizeof(sh.occupied) / 4; ++i) {
-        if (w[i] >> lane & 1u)
-          sh.list[at + __popc(w[i] & ((1u << lane) - 1u))] =
+      for (int i = 0; i < kMasks; ++i) {
+        const uint32_t bits = __shfl_sync(0xFFFFFFFFu, w, i);
+        if (bits >> lane & 1u)
+          sh.list[n_list + __popc(bits & ((1u << lane) - 1u))] =
               static_cast<uint16_t>(32 * i + lane);
-        at += __popc(w[i]);
+        n_list += __popc(bits);
       }
+      __syncwarp();
       if (lane == 0) {
-        sh.n_list = at;
+        sh.n_list = n_list;
         sh.all_first = first;
         // logits of −2^16 and below have no weight next to one 33·T above that
         sh.all_wide = any_wide != 0 ||
@@ -815,14 +789,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
     // ---- the segments' numbers of tokens and weights, to the first CTA
     for (int j = rank * kWarps + warp; j < n_list; j += C * kWarps) {
       const int seg = sh.list[j];
-      uint32_t c[4], n = 0;
-      uint64_t w = 0;
-      source.get(seg, c);
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        w += c[x] * weigh(sh, bin_of_slot(128 * seg + 4 * lane + x), first);
-        n += c[x];
-      }
+      uint32_t n = source.get(seg);
+      uint64_t w = n * weigh(sh, source.bin(seg, lane), first);
       warp_sums(n, w);
       if (lane == 0) {
         peer(0)->number[j] = n;
