@@ -37,24 +37,25 @@ struct EvictArgs {
   const int32_t* positions;
   float* weights_out;
   int32_t* positions_out;
-  int32_t cap;  // keys of a CTA, a multiple of 32
+  int32_t cap;  // keys of a CTA, a multiple of 128
   DevCtx ctx;
 };
 
 constexpr int kDigits = 2048;
-constexpr int kMaxKeys = 49152;  // of a CTA
+constexpr int kMaxKeys = 43008;  // of a CTA
 constexpr int kMaxLen = 8 * kMaxKeys;
 constexpr uint32_t kProtected = 0xFFFFFFFFu;
 
-struct Shared {
+struct alignas(16) Shared {  // what follows it is read 16 bytes at a time
   uint32_t digits[3][kDigits];  // counts of the three passes
   uint32_t warp_n[2][32];
   uint32_t found, above;         // a pass' digit, and the keys above it
   uint32_t equal;                // keys that equal the threshold
   uint32_t holes, movers;        // of this CTA
   int bad, prefix;
-  // then keys[cap + 64], once they are no longer needed the lists of holes and movers,
-  // (cap + 64) / 2 each; and a bit for each key that stays
+  // then keys[cap + 256], once they are no longer needed the lists of holes' and movers'
+  // rows, (cap + 256) / 2 each; a byte for four slots: holes, movers; and in a cluster
+  // total[kDigits], a pass' counts in all of it
 };
 
 // New length of a sequence of kv keys whose first `prefix` are shared.
@@ -93,7 +94,8 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) kv_evict_kernel(const Evi
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& sh = *reinterpret_cast<Shared*>(smem);
   uint32_t* keys = reinterpret_cast<uint32_t*>(smem + sizeof(Shared));
-  uint32_t* stay = keys + p.cap + 64;  // bits
+  uint8_t* stay = reinterpret_cast<uint8_t*>(keys + p.cap + 256);  // two bits a slot
+  uint32_t* total = reinterpret_cast<uint32_t*>(stay + p.cap / 4);
   const bd_attention_batch& b = p.b;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   cg::cluster_group cluster = cg::this_cluster();
@@ -132,42 +134,56 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) kv_evict_kernel(const Evi
   const int32_t* table = b.page_table + static_cast<int64_t>(s) * b.table_stride;
   const int page_shift = 31 - __clz(b.page_size);
   // a slot's row (of this head) in the cache, or −1
-  const auto row_of = [&](int slot) -> int64_t {
+  const auto row_of = [&](int slot) {
     const int page = table[slot >> page_shift];
     if (page < 0 || page >= b.n_pages) return -1;
-    return ((static_cast<int64_t>(page) * b.n_kv_heads + h) << page_shift) +
-           (slot & (b.page_size - 1));
+    return ((page * b.n_kv_heads + h) << page_shift) + (slot & (b.page_size - 1));
   };
   const bool apart = p.weights_out != p.weights || p.positions_out != p.positions;
-  // kBatch slots of a thread at a time, T apart: their rows, weights and positions
-  constexpr int kBatch = 8;
+  // Four neighbouring slots of a thread, which lie in one page (slots are counted from a
+  // page's start, pages hold 16 and more), and kBatch of these at a time, T apart.
+  constexpr int kBatch = 2;
   struct Entries {
-    int64_t row[kBatch];
-    float w[kBatch];
-    int pos[kBatch];
+    int row[kBatch];  // of the first slot (below 2^31), −1: no such page, −2: past the end
+    float4 w[kBatch];
+    int4 pos[kBatch];
   };
   const auto fetch = [&](Entries& e, int slot, int end) {
 #pragma unroll
     for (int x = 0; x < kBatch; ++x)
-      e.row[x] = slot + x * T < end ? row_of(slot + x * T) : -2;
+      e.row[x] = slot + 4 * x * T < end ? row_of(slot + 4 * x * T) : -2;
 #pragma unroll
-    for (int x = 0; x < kBatch; ++x) {
-      e.w[x] = e.row[x] >= 0 ? p.weights[e.row[x]] : 0.f;
-      e.pos[x] = e.row[x] >= 0 ? p.positions[e.row[x]] : 0;
+    for (int x = 0; x < kBatch; ++x)
+      if (e.row[x] >= 0) {
+        e.w[x] = *reinterpret_cast<const float4*>(p.weights + e.row[x]);
+        e.pos[x] = *reinterpret_cast<const int4*>(p.positions + e.row[x]);
+      }
+  };
+  // the first `live` of four
+  const auto put = [&](int row, int live, const float4& w, const int4& pos) {
+    if (live >= 4) {
+      *reinterpret_cast<float4*>(p.weights_out + row) = w;
+      *reinterpret_cast<int4*>(p.positions_out + row) = pos;
+      return;
     }
+    const float ws[3] = {w.x, w.y, w.z};
+    const int ps[3] = {pos.x, pos.y, pos.z};
+#pragma unroll
+    for (int y = 0; y < 3; ++y)
+      if (y < live) {
+        p.weights_out[row + y] = ws[y];
+        p.positions_out[row + y] = ps[y];
+      }
   };
   bool bad = false;
   if (apart) {  // what is not chosen from
     const int end = len == kv ? kv : prefix;
-    for (int slot = rank * T * kBatch + tid; slot < end; slot += C * T * kBatch) {
+    for (int slot = 4 * (rank * T * kBatch + tid); slot < end; slot += 4 * C * T * kBatch) {
       Entries e;
       fetch(e, slot, end);
 #pragma unroll
       for (int x = 0; x < kBatch; ++x) {
-        if (e.row[x] >= 0) {
-          p.weights_out[e.row[x]] = e.w[x];
-          p.positions_out[e.row[x]] = e.pos[x];
-        }
+        if (e.row[x] >= 0) put(e.row[x], end - slot - 4 * x * T, e.w[x], e.pos[x]);
         bad |= e.row[x] == -1;
       }
     }
@@ -178,32 +194,36 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) kv_evict_kernel(const Evi
 
   // ---- the keys of slots prefix + [i0, i1)
   const int m = kv - prefix, K = len - prefix;
-  const int per = ((m + C - 1) / C + 31) & ~31;
+  const int per = ((m + C - 1) / C + 127) & ~127;
   const int i0 = rank * per < m ? rank * per : m;
   const int n = (i0 + per < m ? i0 + per : m) - i0;
   const int64_t late64 = static_cast<int64_t>(kv) + shift - p.recent;
   const int late = static_cast<int>(late64 > INT32_MAX   ? INT32_MAX
                                     : late64 < INT32_MIN ? INT32_MIN
                                                          : late64);
-  for (int i = tid; i < n; i += T * kBatch) {
+  for (int i = 4 * tid; i < n; i += 4 * T * kBatch) {
     Entries e;
     fetch(e, prefix + i0 + i, prefix + i0 + n);
 #pragma unroll
     for (int x = 0; x < kBatch; ++x) {
       if (e.row[x] == -2) break;
-      uint32_t key = 0u;
+      const int at = i + 4 * x * T;
+      uint32_t key[4] = {0u, 0u, 0u, 0u};
       if (e.row[x] < 0) {
         bad = true;
       } else {
-        key = key_of(e.w[x], e.pos[x], late, p.sink);
-        atomicAdd(&sh.digits[0][key >> 21], 1u);
-        // (all slots that go on; the movers' weights overwrite the freed ones' below)
-        if (apart && i0 + i + x * T < K) {
-          p.weights_out[e.row[x]] = e.w[x];
-          p.positions_out[e.row[x]] = e.pos[x];
+        const float w[4] = {e.w[x].x, e.w[x].y, e.w[x].z, e.w[x].w};
+        const int pos[4] = {e.pos[x].x, e.pos[x].y, e.pos[x].z, e.pos[x].w};
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          if (at + y >= n) continue;
+          key[y] = key_of(w[y], pos[y], late, p.sink);
+          atomicAdd(&sh.digits[0][key[y] >> 21], 1u);
         }
+        // (all slots that go on; the movers' weights overwrite the freed ones' below)
+        if (apart && i0 + at < K) put(e.row[x], K - i0 - at, e.w[x], e.pos[x]);
       }
-      keys[i + x * T] = key;
+      *reinterpret_cast<uint4*>(keys + at) = make_uint4(key[0], key[1], key[2], key[3]);
     }
   }
   if (bad) sh.bad = 1;
@@ -225,25 +245,41 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) kv_evict_kernel(const Evi
     const int down = kShift[pass];
     if (pass > 0) {
       const int up = kShift[pass - 1];
-      for (int i = tid; i < n; i += T) {
-        const uint32_t key = keys[i];
-        if (key >> up == threshold >> up) atomicAdd(&sh.digits[pass][key >> down & 0x7FFu], 1u);
+      for (int i = 4 * tid; i < n; i += 4 * T) {
+        const uint4 v = *reinterpret_cast<const uint4*>(keys + i);
+        const uint32_t key[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          if (i + y < n && key[y] >> up == threshold >> up)
+            atomicAdd(&sh.digits[pass][key[y] >> down & 0x7FFu], 1u);
+      }
+      meet();
+    }
+    // The cluster's counts: every CTA adds up a share of the digits and gives it to all.
+    // (All digits of all CTAs read by each took 64 KB of the others' memory a pass, 13 us
+    // of three passes by eight CTAs.)
+    if constexpr (C > 1) {
+      constexpr int kShare = kDigits / C;
+      for (int d = rank * kShare + tid; d < (rank + 1) * kShare; d += T) {
+        uint32_t count = 0u;
+#pragma unroll
+        for (int r = 0; r < C; ++r) count += peer(r)->digits[pass][d];
+#pragma unroll
+        for (int r = 0; r < C; ++r) cluster.map_shared_rank(total, r)[d] = count;
       }
       meet();
     }
     // an even share of the digits per thread, from the top
     constexpr int kEach = kDigits / T;
     uint32_t c[kEach];
-#pragma unroll
-    for (int x = 0; x < kEach; ++x) c[x] = 0u;
-#pragma unroll
-    for (int r = 0; r < C; ++r) {
-      const uint2* d = reinterpret_cast<const uint2*>(peer(r)->digits[pass] + kDigits - kEach * (tid + 1));
+    {
+      const uint2* d = reinterpret_cast<const uint2*>((C > 1 ? total : sh.digits[pass]) +
+                                                      kDigits - kEach * (tid + 1));
 #pragma unroll
       for (int x = 0; x < kEach / 2; ++x) {
         const uint2 v = d[x];
-        c[kEach - 1 - 2 * x] += v.x;
-        c[kEach - 2 - 2 * x] += v.y;
+        c[kEach - 1 - 2 * x] = v.x;
+        c[kEach - 2 - 2 * x] = v.y;
       }
     }
     uint32_t sum = 0u;
@@ -274,48 +310,74 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) kv_evict_kernel(const Evi
   const uint32_t equals = K > 0 ? sh.equal : 0u;
   const bool split = left < equals;  // not all of the threshold's equals stay
 
-  // ---- which slots stay: a warp owns a run of them
-  const int w_per = ((n + kWarps - 1) / kWarps + 31) & ~31;
+  // ---- which slots stay: a warp owns a run of them, a lane four neighbours
+  const int w_per = ((n + kWarps - 1) / kWarps + 127) & ~127;
   const int w0 = warp * w_per < n ? warp * w_per : n;
   const int w1 = w0 + w_per < n ? w0 + w_per : n;
   uint32_t equal_at = 0u;  // equals before this warp's slots
   if (split) {
     uint32_t e = 0u;
-    for (int i = w0; i < w1; i += 32)
-      e += __popc(__ballot_sync(0xFFFFFFFFu, i + lane < w1 && keys[i + lane] == threshold));
+    for (int i = w0 + 4 * lane; i < w1; i += 128) {
+      const uint4 v = *reinterpret_cast<const uint4*>(keys + i);
+      const uint32_t key[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int y = 0; y < 4; ++y) e += i + y < w1 && key[y] == threshold;
+    }
+    e = __reduce_add_sync(0xFFFFFFFFu, e);
     if (lane == 0) sh.warp_n[0][warp] = e;
     __syncthreads();
-    if (tid == 0) {
-      uint32_t all = 0u;
-      for (int i = 0; i < kWarps; ++i) all += sh.warp_n[0][i];
-      sh.equal = all;
+    uint32_t all = 0u;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      if (i == warp) equal_at = all;
+      all += sh.warp_n[0][i];
     }
-    for (int i = 0; i < warp; ++i) equal_at += sh.warp_n[0][i];
+    if (tid == 0) sh.equal = all;
     meet();
 #pragma unroll
     for (int r = 0; r < C; ++r)
       if (r < rank) equal_at += peer(r)->equal;
   }
-  uint32_t holes = 0u, movers = 0u;
-  // bits of the 32 slots from i on that lie below K
+  // of four slots from i on, those that lie below K
   const auto below = [&](int i) {
     const int d = K - (i0 + i);
-    return d >= 32 ? 0xFFFFFFFFu : d <= 0 ? 0u : (1u << d) - 1u;
+    return d >= 4 ? 15u : d <= 0 ? 0u : (1u << d) - 1u;
   };
-  for (int i = w0; i < w1; i += 32) {
-    const bool live = i + lane < w1;
-    const uint32_t key = live ? keys[i + lane] : 0u;
-    const uint32_t lives = __ballot_sync(0xFFFFFFFFu, live);
-    const uint32_t same = __ballot_sync(0xFFFFFFFFu, live && K > 0 && key == threshold);
-    bool stays = live && K > 0 && key > threshold;
-    if (same >> lane & 1u)
-      stays = !split || equal_at + __popc(same & ((1u << lane) - 1u)) < left;
-    equal_at += __popc(same);
-    const uint32_t kept = __ballot_sync(0xFFFFFFFFu, stays);
-    if (lane == 0) stay[i >> 5] = kept;
-    holes += __popc(lives & ~kept & below(i));
-    movers += __popc(kept & ~below(i));
+  uint32_t holes = 0u, movers = 0u;
+  for (int i = w0 + 4 * lane; i - 4 * lane < w1; i += 128) {
+    uint32_t key[4] = {0u, 0u, 0u, 0u}, lives = 0u, same = 0u, kept = 0u;
+    if (i < w1) {
+      const uint4 v = *reinterpret_cast<const uint4*>(keys + i);
+      key[0] = v.x, key[1] = v.y, key[2] = v.z, key[3] = v.w;
+      lives = w1 - i >= 4 ? 15u : (1u << (w1 - i)) - 1u;
+    }
+    if (K > 0) {
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        kept |= (key[y] > threshold ? 1u : 0u) << y;
+        same |= (key[y] == threshold ? 1u : 0u) << y;
+      }
+      same &= lives;
+      if (!split) {
+        kept |= same;
+      } else {
+        const uint32_t inc = warp_inclusive(static_cast<uint32_t>(__popc(same)));
+        uint32_t at = equal_at + inc - __popc(same);
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          if (same >> y & 1u) kept |= (at++ < left ? 1u : 0u) << y;
+        equal_at += __shfl_sync(0xFFFFFFFFu, inc, 31);
+      }
+      kept &= lives;
+    }
+    const uint32_t low = below(i);
+    const uint32_t hole = lives & ~kept & low, mover = kept & ~low;
+    if (i < w1) stay[i >> 2] = static_cast<uint8_t>(hole | mover << 4);
+    holes += __popc(hole);
+    movers += __popc(mover);
   }
+  holes = __reduce_add_sync(0xFFFFFFFFu, holes);
+  movers = __reduce_add_sync(0xFFFFFFFFu, movers);
   __syncthreads();  // the sums of equals have been read
   if (lane == 0) {
     sh.warp_n[0][warp] = holes;
@@ -323,6 +385,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) kv_evict_kernel(const Evi
   }
   __syncthreads();
   uint32_t hole_at = 0u, mover_at = 0u, all_holes = 0u, all_movers = 0u;
+#pragma unroll
   for (int i = 0; i < kWarps; ++i) {
     if (i == warp) {
       hole_at = all_holes;
@@ -347,23 +410,33 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) kv_evict_kernel(const Evi
     moves += o->movers;
   }
 
-  // ---- their numbers: entry e of both lists lies in CTA e / share
+  // ---- their rows: entry e of both lists lies in CTA e / share
   const uint32_t share = (moves + C - 1) / C;
-  const int half = (p.cap + 64) / 2;
-  const auto put = [&](int list, uint32_t e, int slot) {
+  const int half = (p.cap + 256) / 2;
+  const auto note = [&](int list, uint32_t e, int row) {
     const uint32_t r = C == 1 ? 0u : e / share;
     uint32_t* to = C == 1 ? keys : cluster.map_shared_rank(keys, r);
-    to[list * half + (e - r * share)] = static_cast<uint32_t>(slot);
+    to[list * half + (e - r * share)] = static_cast<uint32_t>(row);
   };
-  for (int i = w0; i < w1; i += 32) {
-    const uint32_t lives = w1 - i >= 32 ? 0xFFFFFFFFu : (1u << (w1 - i)) - 1u;
-    const uint32_t kept = stay[i >> 5], low = below(i);
-    const uint32_t hole = lives & ~kept & low, mover = kept & ~low;
-    const uint32_t before = (1u << lane) - 1u;
-    if (hole >> lane & 1u) put(0, hole_at + __popc(hole & before), prefix + i0 + i + lane);
-    if (mover >> lane & 1u) put(1, mover_at + __popc(mover & before), prefix + i0 + i + lane);
-    hole_at += __popc(hole);
-    mover_at += __popc(mover);
+  for (int i = w0 + 4 * lane; i - 4 * lane < w1; i += 128) {
+    const uint32_t bits = i < w1 ? stay[i >> 2] : 0u;
+    if (__ballot_sync(0xFFFFFFFFu, bits != 0) == 0) continue;
+    const uint32_t hole = bits & 15u, mover = bits >> 4;
+    // both numbers in one sum
+    const uint32_t mine = __popc(hole) | __popc(mover) << 16;
+    const uint32_t inc = warp_inclusive(mine);
+    uint32_t e = hole_at + ((inc - mine) & 0xFFFFu), f = mover_at + ((inc - mine) >> 16);
+    if (bits != 0) {
+      const int row = row_of(prefix + i0 + i);
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        if (hole >> y & 1u) note(0, e++, row + y);
+        if (mover >> y & 1u) note(1, f++, row + y);
+      }
+    }
+    const uint32_t all = __shfl_sync(0xFFFFFFFFu, inc, 31);
+    hole_at += all & 0xFFFFu;
+    mover_at += all >> 16;
   }
   meet();
 
@@ -384,8 +457,8 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) kv_evict_kernel(const Evi
       const int e = e0 + x * kWarps * rows + sub;
       to[x] = -1;
       if (e < mine) {
-        to[x] = row_of(static_cast<int>(keys[e]));
-        const int64_t from = row_of(static_cast<int>(keys[half + e]));
+        to[x] = keys[e];
+        const int64_t from = keys[half + e];
         k[x] = reinterpret_cast<const uint4*>(p.k_pages + from * b.head_dim)[at];
         v[x] = reinterpret_cast<const uint4*>(p.v_pages + from * b.head_dim)[at];
         w[x] = p.weights[from];
@@ -426,8 +499,9 @@ __global__ void __launch_bounds__(256)
   pos_offset[s] += kv - len;
 }
 
-size_t smem_bytes(int cap) {
-  return sizeof(Shared) + 4 * (static_cast<size_t>(cap) + 64) + static_cast<size_t>(cap) / 8;
+constexpr size_t smem_bytes(int cap, int c) {
+  return sizeof(Shared) + 4 * (static_cast<size_t>(cap) + 256) + static_cast<size_t>(cap) / 4 +
+         (c > 1 ? 4 * kDigits : 0);
 }
 
 template <int C, int T>
@@ -440,7 +514,7 @@ cudaError_t launch(const EvictArgs& p, cudaStream_t s) {
     std::lock_guard<std::mutex> lock(host_cache_mutex());
     if (!done[dev & 63]) {
       e = cudaFuncSetAttribute(kv_evict_kernel<C, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(smem_bytes(kMaxKeys)));
+                               static_cast<int>(smem_bytes(kMaxKeys, C)));
       if (e == cudaSuccess && C > 8)
         e = cudaFuncSetAttribute(kv_evict_kernel<C, T>,
                                  cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -448,10 +522,9 @@ cudaError_t launch(const EvictArgs& p, cudaStream_t s) {
       done[dev & 63] = true;
     }
   }
-  static_assert(sizeof(Shared) + 4 * (kMaxKeys + 64) + kMaxKeys / 8 <= 227 * 1024,
-                "shared memory of one CTA");
+  static_assert(smem_bytes(kMaxKeys, C) <= 227 * 1024, "shared memory of one CTA");
   const unsigned grid = static_cast<unsigned>(p.b.n_seq) * p.b.n_kv_heads * C;
-  return launch_pdl_cluster(kv_evict_kernel<C, T>, dim3(grid), dim3(T), C, smem_bytes(p.cap), s, p);
+  return launch_pdl_cluster(kv_evict_kernel<C, T>, dim3(grid), dim3(T), C, smem_bytes(p.cap, C), s, p);
 }
 
 // Clusters of 16 that the device holds at once with the most shared memory that the
@@ -463,7 +536,7 @@ int large_clusters() {
   std::lock_guard<std::mutex> lock(host_cache_mutex());
   int& n = known[dev & 63];
   if (n == 0) {
-    const size_t bytes = smem_bytes(kMaxLen / 16);
+    const size_t bytes = smem_bytes(kMaxLen / 16, 16);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(16);
     cfg.blockDim = dim3(1024);
@@ -523,8 +596,8 @@ bd_status bitdelta_kv_evict(const bd_attention_batch* batch, const int32_t* keep
       !positions_out)
     return BD_ERR_INVALID_ARG;
   if (bd::off(batch->page_table, 4) || bd::off(pos_offset, 4) || bd::off(k_pages, 16) ||
-      bd::off(v_pages, 16) || bd::off(weights, 4) || bd::off(positions, 4) ||
-      bd::off(weights_out, 4) || bd::off(positions_out, 4))
+      bd::off(v_pages, 16) || bd::off(weights, 16) || bd::off(positions, 16) ||
+      bd::off(weights_out, 16) || bd::off(positions_out, 16))
     return BD_ERR_MISALIGNED;
   bd::EvictArgs p{};
   int sms = 0;
@@ -549,7 +622,7 @@ bd_status bitdelta_kv_evict(const bd_attention_batch* batch, const int32_t* keep
   int c = 1;
   while (c < 8 && (len > bd::kMaxKeys * c || (items * 2 * c <= sms && len > 2048 * c))) c *= 2;
   if (c == 8 && items * 16 <= sms && len > 2048 * 8 && bd::large_clusters() >= items) c = 16;
-  p.cap = ((len + c - 1) / c + 31) / 32 * 32;
+  p.cap = ((len + c - 1) / c + 127) / 128 * 128;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool few = p.cap <= 8192 && items * c > sms;
   cudaError_t e;

@@ -119,7 +119,7 @@ bd_status bitdelta_kv_weigh(const bd_attention_batch* batch, const uint16_t* q, 
  *                sequence of the batch (below kv_len[s] of one that stays).
  * kv_len is not changed: every layer is cut with the same lengths, and
  * bitdelta_kv_evict_lengths then sets them.  The batch's query tokens are not
- * looked at.  max_kv_len: at most 393216.
+ * looked at.  The tables start on 16-byte boundaries.  max_kv_len: at most 344064.
  * A kv_len outside the batch's bounds, or a page outside [0, n_pages), sets
  * BD_ERR_DEVICE_BOUNDS and leaves the sequence's key head as it was.
  */

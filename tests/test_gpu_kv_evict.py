@@ -331,6 +331,6 @@ def test_refusals():
             bd.bitdelta_kv_evict(c.batch, keep, c.k, c.v, c.w, c.pos, **kw)
     with pytest.raises(TypeError):
         bd.bitdelta_kv_evict(c.batch, keep, c.k, c.v, c.w, c.pos, recent=1.5)
-    big = c.make(max_kv_len=393217)
+    big = c.make(max_kv_len=344065)
     with pytest.raises(bd.BitDeltaError):
         bd.bitdelta_kv_evict(big, keep, c.k, c.v, c.w, c.pos)
