@@ -307,22 +307,32 @@ struct Recount {
   }
 };
 
-// Exclusive sums over the listed segments, in place; returns those of all.  One warp.
+// Exclusive sums over the listed segments, in place; returns those of all.  One warp,
+// neighbouring segments to a lane: one scan over the lanes, whatever their number.
 __device__ void sum_list(Shared& sh, int n_list, uint32_t& all, uint64_t& all_mass) {
   const int lane = threadIdx.x & 31;
-  all = 0;
-  all_mass = 0;
-  for (int i = lane; i - lane < n_list; i += 32) {
-    const uint32_t n = i < n_list ? sh.number[i] : 0u;
-    const uint64_t w = i < n_list ? sh.mass[i] : 0u;
-    const uint32_t ni = warp_inclusive(n);
-    const uint64_t wi = warp_inclusive(w);
-    if (i < n_list) {
-      sh.number[i] = all + ni - n;
-      sh.mass[i] = all_mass + wi - w;
-    }
-    all += __shfl_sync(0xFFFFFFFFu, ni, 31);
-    all_mass += __shfl_sync(0xFFFFFFFFu, wi, 31);
+  const int per = (n_list + 31) >> 5;
+  const int i0 = lane * per < n_list ? lane * per : n_list;
+  const int i1 = i0 + per < n_list ? i0 + per : n_list;
+  uint32_t n = 0;
+  uint64_t w = 0;
+  for (int i = i0; i < i1; ++i) {
+    n += sh.number[i];
+    w += sh.mass[i];
+  }
+  uint32_t n_at = warp_inclusive(n);
+  uint64_t w_at = warp_inclusive(w);
+  all = __shfl_sync(0xFFFFFFFFu, n_at, 31);
+  all_mass = __shfl_sync(0xFFFFFFFFu, w_at, 31);
+  n_at -= n;
+  w_at -= w;
+  for (int i = i0; i < i1; ++i) {
+    const uint32_t x = sh.number[i];
+    const uint64_t y = sh.mass[i];
+    sh.number[i] = n_at;
+    sh.mass[i] = w_at;
+    n_at += x;
+    w_at += y;
   }
   __syncwarp();
 }
@@ -344,116 +354,138 @@ struct Settings {
 
 // The cuts and the choice, by one warp: the value of the row's token, its number among
 // its equals and its probability.  False where there is none.
+//
+// All of it are questions for the place in the order at which something is reached: a
+// number of tokens, a sum, or a weight below `goal`.  One loop asks them: this runs
+// once a row, and its instructions are fetched from memory for that.
 template <class Source>
 __device__ __noinline__ bool choose(const SampleArgs& p, Shared& sh, const Source& source,
                                     const Settings& set, int n_list, int first, int* bin_out,
                                     uint32_t* rank_out, float* prob_out) {
   const int lane = threadIdx.x & 31;
   uint32_t all;
-  uint64_t all_mass;
-  sum_list(sh, n_list, all, all_mass);
+  uint64_t kept;  // the weight of the first `cut` tokens, once it is known
+  sum_list(sh, n_list, all, kept);
   const bool bad = !(set.t >= 0.f) || isnan(set.u) || isnan(set.top_p) || isnan(set.min_p);
   if (bad || all == 0) {
     if (bad && lane == 0) record_error(p.ctx, kErrBounds);
     return false;
   }
-  // The last listed segment for which `before` holds (it holds for the first, and for
-  // all before one that it holds for).
-  const auto search = [&](auto before) {
-    int lo = 0, hi = n_list;
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) >> 5, at = lo + lane * step;
-      const uint32_t yes = __ballot_sync(0xFFFFFFFFu, at < hi && (lane == 0 || before(at)));
-      const int top = 31 - __clz(yes);
-      lo += top * step;
-      hi = lo + step < hi ? lo + step : hi;
-    }
-    return lo;
-  };
-  // The segment that was last looked at: the lane's bin.
-  int have = -1;
-  Place mine{};
-  const auto look = [&](int j) {
-    if (j == have) return;
-    have = j;
-    const int seg = sh.list[j];
-    mine.count = source.get(seg);
-    mine.bin = source.bin(seg, lane);
-    mine.weight = weigh(sh, mine.bin, first);
-    const uint64_t w = mine.count * mine.weight;
-    mine.number = sh.number[j] + warp_inclusive(mine.count) - mine.count;
-    mine.mass = sh.mass[j] + warp_inclusive(w) - w;
-  };
-  // The first bin of segment j for which `inside` holds, given the sums before it; all
-  // lanes receive it.
-  const auto bin_in = [&](int j, auto inside) {
-    look(j);
-    const uint32_t yes = __ballot_sync(0xFFFFFFFFu, mine.count != 0 && inside(mine));
-    const int src = yes != 0 ? __ffs(yes) - 1 : 0;
-    Place found;
-    found.bin = __shfl_sync(0xFFFFFFFFu, mine.bin, src);
-    found.number = __shfl_sync(0xFFFFFFFFu, mine.number, src);
-    found.mass = __shfl_sync(0xFFFFFFFFu, mine.mass, src);
-    found.weight = __shfl_sync(0xFFFFFFFFu, mine.weight, src);
-    found.count = __shfl_sync(0xFFFFFFFFu, mine.count, src);
-    return found;
-  };
-  const auto at_mass = [&](uint64_t reach) {  // the bin in which the sum reaches `reach`
-    const int j = search([&](int i) { return sh.mass[i] < reach; });
-    return bin_in(j, [&](const Place& x) { return x.mass + x.count * x.weight >= reach; });
-  };
-  // The weight of the first n tokens, 1 <= n <= all.
-  const auto mass_of = [&](uint32_t n) {
-    if (n == all) return all_mass;
-    const int j = search([&](int i) { return sh.number[i] < n; });
-    const Place pl = bin_in(j, [&](const Place& x) { return x.number + x.count >= n; });
-    return pl.mass + (n - pl.number) * pl.weight;
-  };
-  // floor(w·f), and whether that is all of it; f in [0, 1).
+  constexpr uint64_t one = uint64_t{1} << kOneBits;
+  uint32_t cut = set.k > 0 && static_cast<uint32_t>(set.k) < all ? static_cast<uint32_t>(set.k) : all;
+  if (set.t == 0.f) cut = 1;
+  if (cut != all) kept = cut == 1 ? one : 0;  // 0: to be asked for
+  // floor(w·f); f in [0, 1)
   const auto share = [](uint64_t w, float f, bool* exact) {
     const uint64_t fixed = __float2ull_rz(f * 18446744073709551616.f);
     *exact = w * fixed == 0;
     return __umul64hi(w, fixed);
   };
-  uint32_t n = all;
-  uint64_t kept = all_mass;
-  bool exact;
-  if (set.k > 0 && static_cast<uint32_t>(set.k) < all) n = static_cast<uint32_t>(set.k);
-  if (set.t == 0.f) n = 1;
-  uint32_t cut = n;
-  if (cut > 1 && set.top_p < 1.f) {
-    kept = mass_of(n);
-    const uint64_t down = share(kept, set.top_p > 0.f ? set.top_p : 0.f, &exact);
-    const uint64_t want = down + (exact ? 0 : 1);
-    if (want == 0) {
-      cut = 1;
+  enum Step { kTopP, kMinP, kChoose };
+  enum Kind { kNumber, kMass, kWeight };
+  int have = -1;  // the segment that was last looked at: the lane's bin of it
+  Place mine{};
+  uint64_t target = 0;
+#pragma unroll 1
+  for (int step = kTopP; step <= kChoose;) {
+    // ---- the next question
+    Kind kind = kMass;
+    uint64_t goal;
+    bool exact;
+    if (step == kMinP) {
+      if (cut == 1 || !(set.min_p > 0.f)) {
+        ++step;
+        continue;
+      }
+      kind = kWeight;
+      goal = set.min_p >= 1.f
+                 ? one : static_cast<uint64_t>(ceilf(set.min_p * static_cast<float>(one)));
     } else {
-      const Place pl = at_mass(want);
-      const uint32_t at = pl.number + quotient(want - pl.mass + pl.weight - 1, pl.weight);
-      cut = at < cut ? at : cut;
+      if (step == kTopP && (cut == 1 || !(set.top_p < 1.f))) {
+        ++step;
+        continue;
+      }
+      if (kept == 0) {
+        kind = kNumber;
+        goal = cut;
+      } else if (step == kTopP) {
+        goal = share(kept, set.top_p > 0.f ? set.top_p : 0.f, &exact);
+        if (!exact) ++goal;
+        if (goal == 0) goal = 1;
+      } else {
+        const float u = set.u > 0.f ? set.u : 0.f;
+        target = u < 1.f ? share(kept, u, &exact) : kept - 1;
+        goal = target + 1;
+      }
+    }
+    // ---- the last listed segment before it: that holds for the first, and for all before
+    // one that it holds for
+    int lo = 0, hi = n_list;
+#pragma unroll 1
+    while (hi - lo > 1) {
+      const int width = (hi - lo + 31) >> 5, at = lo + lane * width;
+      bool before = at < hi;
+      if (before && lane > 0) {
+        if (kind == kNumber) {
+          before = sh.number[at] < goal;
+        } else if (kind == kMass) {
+          before = sh.mass[at] < goal;
+        } else {
+          const int bin = source.bin(sh.list[at], 0);
+          before = weight_of(sh, bin < first ? first : bin, first) >= goal;
+        }
+      }
+      const int top = 31 - __clz(__ballot_sync(0xFFFFFFFFu, before));
+      lo += top * width;
+      hi = lo + width < hi ? lo + width : hi;
+    }
+    // ---- its bins, a lane each, and the first that reaches it
+    if (lo != have) {
+      have = lo;
+      const int seg = sh.list[lo];
+      mine.count = source.get(seg);
+      mine.bin = source.bin(seg, lane);
+      mine.weight = weight_of(sh, mine.bin, first);
+      const uint64_t w = mine.count * mine.weight;
+      mine.number = sh.number[lo] + warp_inclusive(mine.count) - mine.count;
+      mine.mass = sh.mass[lo] + warp_inclusive(w) - w;
+    }
+    if (kind == kWeight) {
+      const uint32_t with = __reduce_add_sync(
+          0xFFFFFFFFu, mine.weight >= goal ? mine.count : 0u);
+      uint32_t at = sh.number[lo] + with;
+      at = at > 0 ? at : 1;
+      if (at < cut) {
+        cut = at;
+        kept = cut == 1 ? one : 0;
+      }
+      ++step;
+      continue;
+    }
+    const bool reaches = kind == kNumber ? mine.number + mine.count >= goal
+                                         : mine.mass + mine.count * mine.weight >= goal;
+    const uint32_t yes = __ballot_sync(0xFFFFFFFFu, mine.count != 0 && reaches);
+    const int src = yes != 0 ? __ffs(yes) - 1 : 0;
+    const int bin = __shfl_sync(0xFFFFFFFFu, mine.bin, src);
+    const uint32_t number = __shfl_sync(0xFFFFFFFFu, mine.number, src);
+    const uint64_t mass = __shfl_sync(0xFFFFFFFFu, mine.mass, src);
+    const uint64_t weight = __shfl_sync(0xFFFFFFFFu, mine.weight, src);
+    if (kind == kNumber) {
+      kept = mass + (goal - number) * weight;
+    } else if (step == kTopP) {
+      const uint32_t at = number + quotient(goal - mass + weight - 1, weight);
+      if (at < cut) {
+        cut = at;
+        kept = cut == 1 ? one : 0;
+      }
+      ++step;
+    } else {
+      *bin_out = bin;
+      *rank_out = quotient(target - mass, weight);
+      *prob_out = static_cast<float>(weight) / static_cast<float>(kept);
+      ++step;
     }
   }
-  if (cut > 1 && set.min_p > 0.f) {
-    constexpr uint64_t one = uint64_t{1} << kOneBits;
-    const uint64_t least =
-        set.min_p >= 1.f ? one : static_cast<uint64_t>(ceilf(set.min_p * static_cast<float>(one)));
-    const int j = search([&](int i) {
-      const int bin = source.bin(sh.list[i], 0);
-      return weight_of(sh, bin < first ? first : bin, first) >= least;
-    });
-    look(j);
-    uint32_t with = mine.weight >= least ? mine.count : 0;
-    with = __reduce_add_sync(0xFFFFFFFFu, with);
-    const uint32_t at = sh.number[j] + with;
-    cut = at < cut ? (at > 0 ? at : 1) : cut;
-  }
-  kept = cut == 1 ? uint64_t{1} << kOneBits : mass_of(cut);
-  const float u = set.u > 0.f ? set.u : 0.f;
-  const uint64_t target = u < 1.f ? share(kept, u, &exact) : kept - 1;
-  const Place pl = at_mass(target + 1);
-  *bin_out = pl.bin;
-  *rank_out = quotient(target - pl.mass, pl.weight);
-  *prob_out = static_cast<float>(pl.weight) / static_cast<float>(kept);
   return true;
 }
 
@@ -466,68 +498,74 @@ __device__ __noinline__ void find(const SampleArgs& p, Shared& sh, const uint16_
   const uint32_t bits = bin < 0x8000 ? 0x7FFFu - bin : static_cast<uint32_t>(bin);
   const uint32_t mask = bin == kZeroBin ? 0x7FFF7FFFu : 0xFFFFFFFFu;
   const uint32_t pattern = bits | bits << 16;
-  constexpr int kBatch = 8;  // chunks of a lane
+  constexpr int kBatch = 8;  // chunks of a lane, 32 apart
   const int batches = (c1 - c0 + 32 * kBatch - 1) / (32 * kBatch);
   const int per = (batches + kWarps - 1) / kWarps;
   const int b0 = warp * per < batches ? warp * per : batches;
   const int b1 = b0 + per < batches ? b0 + per : batches;
-  const auto load = [&](uint4 (&v)[kBatch], int b) {
-    const int c = c0 + 32 * kBatch * b + lane;
-#pragma unroll
-    for (int x = 0; x < kBatch; ++x)
-      v[x] = c + 32 * x < c1 ? load_chunk(row, p.V, mis, c + 32 * x)
-                             : make_uint4(~0u, ~0u, ~0u, ~0u);
-  };
   // the top bit of each half of a chunk's word that is the value
   const auto hit = [&](uint32_t w) {
     const uint32_t d = (w & mask) ^ pattern;
     return ~(((d & 0x7FFF7FFFu) + 0x7FFF7FFFu) | d | 0x7FFF7FFFu);
   };
-  uint32_t hits = 0, mine = 0;  // of the warp; of batch b0 + lane
-  for (int b = b0; b < b1; ++b) {
-    uint4 v[kBatch];
-    load(v, b);
-    uint32_t n = 0;  // in both halves
-#pragma unroll
-    for (int x = 0; x < kBatch; ++x)
-      n += (hit(v[x].x) >> 15) + (hit(v[x].y) >> 15) + (hit(v[x].z) >> 15) + (hit(v[x].w) >> 15);
-    n = __reduce_add_sync(0xFFFFFFFFu, (n & 0xFFFFu) + (n >> 16));
-    hits += n;
-    if (b - b0 == lane) mine = n;
-  }
-  if (lane == 0) sh.warp_hits[warp] = hits;
-  __syncthreads();
-  uint32_t before = 0;
-  for (int i = 0; i < warp; ++i) before += sh.warp_hits[i];
   const uint32_t r = sh.find_rank;
-  if (r < before || r >= before + hits) return;
-  // (more than 32 batches of a warp: only where a CTA has a row of 131072 and more)
-  const uint32_t inc = before + warp_inclusive(mine);
-  const uint32_t over = __ballot_sync(0xFFFFFFFFu, inc > r);
-  int b = b0 + (over != 0 ? __ffs(over) - 1 : 32);
-  before = over != 0 ? __shfl_sync(0xFFFFFFFFu, inc - mine, __ffs(over) - 1)
-                     : __shfl_sync(0xFFFFFFFFu, inc, 31);
-  for (; b < b1; ++b) {
-    uint4 v[kBatch];
-    load(v, b);
+  uint32_t before = 0;          // of the token, in the part
+  uint32_t counts = 0;          // the lane's hits in the last batch, four bits a chunk
+  int b = b0, end = b1, last = b0;  // the batch of `counts`
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    uint32_t hits = 0, mine = 0;  // of the warp; of batch b0 + lane
+#pragma unroll 1
+    for (; b < end; ++b) {
+      const int c = c0 + 32 * kBatch * b + lane;
+      uint4 v[kBatch];
 #pragma unroll
-    for (int x = 0; x < kBatch; ++x) {
-      const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
-      uint32_t g = 0;  // a bit for each logit
+      for (int x = 0; x < kBatch; ++x)
+        v[x] = c + 32 * x < c1 ? load_chunk(row, p.V, mis, c + 32 * x)
+                               : make_uint4(~0u, ~0u, ~0u, ~0u);
+      counts = 0;
+      uint32_t n = 0;
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const uint32_t z = hit(w[y]);
-        g |= (z >> 15 & 1u | z >> 30) << (2 * y);
+      for (int x = 0; x < kBatch; ++x) {
+        const uint32_t k = (hit(v[x].x) >> 15) + (hit(v[x].y) >> 15) + (hit(v[x].z) >> 15) +
+                           (hit(v[x].w) >> 15);
+        const uint32_t both = (k + (k >> 16)) & 0xFu;  // up to eight
+        counts |= both << (4 * x);
+        n += both;
       }
-      const uint32_t to = before + warp_inclusive(static_cast<uint32_t>(__popc(g)));
-      if (r < to && r >= to - __popc(g)) {
-        for (uint32_t left = r - (to - __popc(g)); left > 0; --left) g &= g - 1;
-        const int c = c0 + 32 * (kBatch * b + x) + lane;
-        p.tokens[m] = static_cast<int32_t>(static_cast<int64_t>(c) * 8 - mis + __ffs(g) - 1);
-        if (p.prob != nullptr) p.prob[m] = sh.find_prob;
-      }
-      before = __shfl_sync(0xFFFFFFFFu, to, 31);
+      n = __reduce_add_sync(0xFFFFFFFFu, n);
+      hits += n;
+      last = b;
+      if (b - b0 == lane) mine = n;
     }
+    if (pass == 1) break;
+    if (lane == 0) sh.warp_hits[warp] = hits;
+    __syncthreads();
+    const uint32_t theirs = lane < kWarps ? sh.warp_hits[lane] : 0u;
+    before = __shfl_sync(0xFFFFFFFFu, warp_inclusive(theirs) - theirs, warp);
+    if (r < before || r >= before + hits) return;
+    // the batch (of the first 32 of the warp, which are all of a part below 1 M logits)
+    const uint32_t inc = before + warp_inclusive(mine);
+    const int at = __ffs(__ballot_sync(0xFFFFFFFFu, inc > r)) - 1;
+    before = __shfl_sync(0xFFFFFFFFu, inc - mine, at);
+    b = b0 + at;
+    end = last == b ? b : b + 1;
+  }
+#pragma unroll 1
+  for (int x = 0; x < kBatch; ++x) {
+    const uint32_t k = counts >> (4 * x) & 0xFu;
+    const uint32_t to = before + warp_inclusive(k);
+    if (r < to && r >= to - k) {
+      const int c = c0 + 32 * (kBatch * last + x) + lane;
+      const int64_t i0 = static_cast<int64_t>(c) * 8 - mis;
+      uint32_t left = r - (to - k);
+      for (int64_t i = i0 < 0 ? 0 : i0; i < i0 + 8 && i < p.V; ++i)
+        if ((row[i] & (mask & 0xFFFFu)) == bits && left-- == 0) {
+          p.tokens[m] = static_cast<int32_t>(i);
+          if (p.prob != nullptr) p.prob[m] = sh.find_prob;
+        }
+    }
+    before = __shfl_sync(0xFFFFFFFFu, to, 31);
     if (before > r) return;
   }
 }

@@ -97,6 +97,15 @@ class Layer(Block):
         return self.norm("next", self.linear("down", f, seg), h, seg)
 
 
+def bd_head(vocab, hidden, g):
+    """The head's base weight and two variants' deltas, as bitdelta_linear_grouped takes them."""
+    rn = lambda std: (torch.randn((vocab, hidden), generator=g, device="cuda") * std).to(torch.bfloat16)
+    base = rn(3.0 * hidden ** -0.5)
+    packs = [bd.bitdelta_compress(base, base + rn(0.1 * hidden ** -0.5), per_row=True)
+             for _ in range(2)]
+    return (base, *bd.variant_tables([p for p, _ in packs], [a for _, a in packs], "cuda"), packs)
+
+
 def main():
     hidden, ffn, hq, hkv, dim, page, vocab = 2048, 5632, 16, 4, 128, 16, 32000
     variant, prompts, steps = [0, 1, 2, 1], [512, 300, 77, 600], 48
@@ -104,13 +113,14 @@ def main():
     layers = [Layer(hidden, ffn, hq, hkv, dim, variants=2, seed=i) for i in range(2)]
     g = torch.Generator(device="cuda").manual_seed(9)
     embed = torch.randn((vocab, hidden), generator=g, device="cuda").to(torch.bfloat16)
-    head = (embed.float() * hidden ** -0.5).to(torch.bfloat16)
+    head = bd_head(vocab, hidden, g)
     seqs = Sequences(n, budget, slack, hq, hkv, dim, page)
     pages = seqs.room(max(prompts) + 1)
     caches = [LayerCache(pages, hkv, page, dim) for _ in layers]
     rope = rope_table(max(prompts) + steps + 1, dim)
     temperature = torch.tensor([0.7, 0.0, 1.0, 0.9], device="cuda")
     top_k, top_p = int32([50, 0, 0, 200]), torch.tensor([0.95, 1.0, 0.9, 1.0], device="cuda")
+    one_row = int32(range(n + 1))          # a sequence's last token is a segment
     tokens = torch.randint(0, vocab, (sum(prompts),), generator=g, device="cuda")
     for step in range(steps + 1):
         q_len = prompts if step == 0 else [1] * n
@@ -123,7 +133,8 @@ def main():
         for layer, cache in zip(layers, caches):
             # a prompt is weighed by its last tokens
             h, x = layer.forward(h, seg, batch, rope, cache, seqs.pos_offset, window=64)
-        logits = x[[o - 1 for o in offsets[1:]]] @ head.T
+        last = x[[o - 1 for o in offsets[1:]]].contiguous()
+        logits = bd.bitdelta_linear_grouped(last, one_row, int32(variant), *head[:3], 2, 1)
         tokens, _ = bd.bitdelta_sample(logits, torch.rand(n, generator=g, device="cuda"),
                                        temperature=temperature, top_k=top_k, top_p=top_p)
         before = list(seqs.lens)
