@@ -224,6 +224,16 @@ struct Items {
     }
     return it.h >= 0;
   }
+  // The next item's first slot and its run's end, before it is taken; false where
+  // there is none.
+  __device__ __forceinline__ bool peek(int& key0, int& k1, bool& ok, const DevCtx& ctx,
+                                       volatile int* abort) {
+    if (!(ok = warp_wait(&full[at], phase, ctx, abort))) return false;
+    const int h = __shfl_sync(0xFFFFFFFFu, slots[at].h, 0);
+    key0 = __shfl_sync(0xFFFFFFFFu, slots[at].key0, 0);
+    k1 = __shfl_sync(0xFFFFFFFFu, slots[at].k1, 0);
+    return h >= 0;
+  }
 };
 
 template <int D>
@@ -397,18 +407,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* others = reinterpret_cast<float*>(smem + C::kOffSum);
     int ss = 0;
     uint32_t sum_phase = 0;
-    while (ok && items.take(it, p.ctx, abort)) {
-      const int key = it.key0 + mine;
-      const int key_lo = it.key0 + 128 * half + 32 * (warp & 3);  // the warp's
-      const int key_hi = key_lo + 31 < it.k1 - 1 ? key_lo + 31 : it.k1 - 1;
-      const bool both = it.key0 + 128 < it.k1;  // keys in the second half
-      const bool idle = half != 0 && !both;
-      // ---- the block's keys to tensor memory: this warp's 32 rows.  The products that
-      // read the block before have completed: the last of them was waited for below.
-      if (!(ok = warp_wait(k_full, k_phase, p.ctx, abort))) break;
+    // A block's keys to tensor memory: this warp's 32 rows, half of their columns.  The
+    // products that read the block before have completed: the last of them has been
+    // waited for.
+    const auto stage = [&](int key0, int k1) {
+      if (!warp_wait(k_full, k_phase, p.ctx, abort)) return false;
       k_phase ^= 1u;
-      if (!idle) {
-        constexpr int kChunks = D / 16;  // 16-byte pieces of a row's half, which this warp moves
+      const bool live = half == 0 || key0 + 128 < k1;
+      if (live) {
+        constexpr int kChunks = D / 16;  // 16-byte pieces of a row's half
         const int x0 = (c0 >> 1) * kChunks;
         const uint8_t* src = smem + half * C::kHalfBytes + row_of_half * 128;
 #pragma unroll
@@ -432,7 +439,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(k_empty);
-        if (!idle) mbar_arrive(&k_ready[half]);
+        if (live) mbar_arrive(&k_ready[half]);
+      }
+      return true;
+    };
+    bool staged = false;  // the item's keys, while the one before was summed
+    while (ok && items.take(it, p.ctx, abort)) {
+      const int key = it.key0 + mine;
+      const int key_lo = it.key0 + 128 * half + 32 * (warp & 3);  // the warp's
+      const int key_hi = key_lo + 31 < it.k1 - 1 ? key_lo + 31 : it.k1 - 1;
+      const bool both = it.key0 + 128 < it.k1;  // keys in the second half
+      const bool idle = half != 0 && !both;
+      if (!staged && !(ok = stage(it.key0, it.k1))) break;
+      staged = false;
+      // what the key has, on its way while its sum is formed
+      int row = -1;
+      float old = 0.f;
+      if (c0 == 0 && key < it.k1 && it.j0 == 0 && it.j1 == it.n) {
+        row = static_cast<int>(weigh_row(b, it.seq, key, it.h));  // below 2^31
+        if (row >= 0 && key < it.fresh) old = p.weights[row];
       }
       uint64_t sum[2] = {0u, 0u};
       for (int j = it.j0; j < it.j1; ++j) {
@@ -441,6 +466,14 @@ __global__ void __launch_bounds__(kThreads, 1)
              (idle || warp_wait(&s_full[u.bar()], u.phase(), p.ctx, abort));
         if (!ok) break;
         tc_fence_after();
+        // The half's last product with this block: the next block's keys go to tensor
+        // memory now, and its products run while this tile is summed.  (Taken up after
+        // that, an item of two tiles took 8200 cycles.)
+        if (j == it.j1 - 1) {
+          int key0, k1;
+          if (items.peek(key0, k1, ok, p.ctx, abort)) staged = ok = stage(key0, k1);
+          if (!ok) break;
+        }
         const Rows& rw = rows[ls];
         const uint32_t t_s = t_lane + u.column();
         if (!idle) {
@@ -507,9 +540,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       started = true;
       if (c0 != 0) continue;
       if (it.j0 == 0 && it.j1 == it.n) {
-        if (key < it.k1) {
-          const int64_t row = weigh_row(b, it.seq, key, it.h);
-          if (row >= 0) weigh_add(p, it.seq, it.fresh, key, row, a);
+        if (row >= 0) {
+          p.weights[row] = old + a;
+          if (key >= it.fresh)
+            p.positions[row] = key + (p.pos_offset != nullptr ? p.pos_offset[it.seq] : 0);
         }
       } else {
         const int slot = 2 * static_cast<int>(blockIdx.x) + (first_item ? 0 : 1);
