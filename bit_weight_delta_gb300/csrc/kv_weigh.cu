@@ -202,14 +202,11 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) kv_weigh_kernel(const 
           t.old = p.weights[t.row + g8 + 8 * quad];
       };
       int page = page_of(blk0);
-      Tile<D> t;
-      fetch(t, blk0, page);
-      page = page_of(blk0 + 1);
-      // the query rows, as the products' other operand
+      // The query rows, as the products' other operand, and their lse: on their way before
+      // the first unit's page is known.
       const int rows = (x.tok1 - x.tok0) * G;  // at most 8·NT
       uint4 q[NT][D / 32];
-      float minus[NT][2];
-      int sees[NT][2];
+      float lse[NT][2];
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         const int row = 8 * i + g8;
@@ -221,20 +218,28 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) kv_weigh_kernel(const 
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           const int c = 8 * i + 2 * quad + y;
-          minus[i][y] = 0.f;
-          sees[i][y] = -1;
-          if (c < rows) {
-            const int tok = x.tok0 + c / G;
-            const float l = p.lse[static_cast<int64_t>(tok) * b.n_q_heads + h * G + c % G];
-            if (isfinite(l) &&
-                (!group || !windowed ||
-                 weigh_in_window(p, tok, x.seq, b.group_offsets[base + r - b.n_seq + 1]))) {
-              minus[i][y] = -l * kWeighLog2e;
-              sees[i][y] = group ? INT32_MAX : tok + x.causal;
-            }
-          }
+          lse[i][y] = c < rows ? p.lse[static_cast<int64_t>(x.tok0 + c / G) * b.n_q_heads + h * G +
+                                       c % G]
+                               : INFINITY;
         }
       }
+      Tile<D> t;
+      fetch(t, blk0, page);
+      page = page_of(blk0 + 1);
+      float minus[NT][2];
+      int sees[NT][2];
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int tok = x.tok0 + (8 * i + 2 * quad + y) / G;
+          const bool counts =
+              isfinite(lse[i][y]) &&
+              (!group || !windowed ||
+               weigh_in_window(p, tok, x.seq, b.group_offsets[base + r - b.n_seq + 1]));
+          minus[i][y] = counts ? -lse[i][y] * kWeighLog2e : 0.f;
+          sees[i][y] = counts ? (group ? INT32_MAX : tok + x.causal) : -1;
+        }
       const auto weigh = [&](const Tile<D>& t, int blk) {
         const int key = x.k0 + blk * kUnitKeys + g8;
         float sum[2] = {0.f, 0.f};
