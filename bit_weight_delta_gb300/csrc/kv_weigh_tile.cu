@@ -588,11 +588,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t qd = sdesc_k_sw128(base + C::kOffQ + qs * C::kHalfBytes);
             const uint64_t ld = sdesc_k_sw64(base + C::kOffLse + ls * kLseBytes);
             const uint32_t t_s = tmem + u.column();
-            mma_ss(t_s, ones, ld, idesc, 0u);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
               mma_ts(t_s, t_k + 8u * k,
-                     qd + static_cast<uint64_t>((k >> 2) * (kPanel >> 4) + 2 * (k & 3)), idesc, 1u);
+                     qd + static_cast<uint64_t>((k >> 2) * (kPanel >> 4) + 2 * (k & 3)), idesc,
+                     k > 0 ? 1u : 0u);
+            // (last: −lse/scale is the largest of the terms, and where it comes first all
+            // later sums are rounded at its size: weights of a 4096-key prompt were 1.4e-6 off, not 2.3e-7)
+            mma_ss(t_s, ones, ld, idesc, 1u);
             mma_commit(&s_full[u.bar()]);
             mma_commit(&q_empty[qs]);
           }
