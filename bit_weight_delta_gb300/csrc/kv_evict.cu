@@ -624,14 +624,15 @@ bd_status bitdelta_kv_evict(const bd_attention_batch* batch, const int32_t* keep
   if (c == 8 && items * 16 <= sms && len > 2048 * 8 && bd::large_clusters() >= items) c = 16;
   p.cap = ((len + c - 1) / c + 127) / 128 * 128;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const bool few = p.cap <= 8192 && items * c > sms;
+  // (clusters come of fewer CTAs than SMs, or of more keys)
+  const bool few = c == 1 && p.cap <= 8192 && items > sms;
   cudaError_t e;
   switch (c) {
     case 1: e = few ? bd::launch<1, 256>(p, s) : bd::launch<1, 1024>(p, s); break;
-    case 2: e = few ? bd::launch<2, 256>(p, s) : bd::launch<2, 1024>(p, s); break;
-    case 4: e = few ? bd::launch<4, 256>(p, s) : bd::launch<4, 1024>(p, s); break;
-    case 8: e = few ? bd::launch<8, 256>(p, s) : bd::launch<8, 1024>(p, s); break;
-    default: e = few ? bd::launch<16, 256>(p, s) : bd::launch<16, 1024>(p, s); break;
+    case 2: e = bd::launch<2, 1024>(p, s); break;
+    case 4: e = bd::launch<4, 1024>(p, s); break;
+    case 8: e = bd::launch<8, 1024>(p, s); break;
+    default: e = bd::launch<16, 1024>(p, s); break;
   }
   return e == cudaSuccess ? BD_OK : BD_ERR_CUDA;
 }

@@ -357,7 +357,8 @@ bd_status bitdelta_kv_weigh(const bd_attention_batch* batch, const uint16_t* q, 
   int st = bd::check_attention_batch(batch);
   if (st != BD_OK) return static_cast<bd_status>(st);
   const float scale_log2 = scale * bd::kWeighLog2e;
-  if (!(scale > 0.f) || std::isinf(scale_log2) || window < 0) return BD_ERR_INVALID_ARG;
+  // (the tile kernel divides lse by the scale)
+  if (!(scale >= 0x1p-100f) || std::isinf(scale_log2) || window < 0) return BD_ERR_INVALID_ARG;
   if (batch->n_tokens == 0 || batch->n_seq == 0) return BD_OK;
   if (!q || !lse || !k_pages || !weights || !positions || batch->n_pages < 1)
     return BD_ERR_INVALID_ARG;

@@ -21,10 +21,22 @@
 // it at its full rate (128 bytes a clock), and the loads of Q and the epilogue's of
 // lse came on top (1650 cycles a tile).
 //
-// Warps: 0-3 and 4-7 the epilogues of the block's halves, 8 and 9 their MMA
-// issuers (a warp per half: one's waits are then the time of the other's products),
-// 10 the TMA producer of K and Q, 11 loads the rows' lse.  Tensor memory: the block's halves in columns 0-127, three buffers of 128
-// columns behind them that the halves' products go to in turn.
+// Warps: 0-15 the epilogue, of which a warp has 32 keys of one of the block's halves
+// and 64 of a tile's 128 rows (eight warps with all rows took 59 us where these take
+// 48); 16 and 17 the halves' MMA issuers (one's waits are then the time of the other's
+// products); 18 the TMA producer of K and Q, which also walks through the CTA's share
+// and puts its items in a ring for the other roles; 19 loads the rows' lse.
+// Tensor memory: the block's halves in columns 0-127, three buffers of 128 columns
+// behind them that the halves' products go to in turn.
+//
+// A block and a tile of 128-element heads are 8.4 MFLOP of products, 1024 cycles of the
+// tensor pipe and an eighth more for lse, and 32768 exponentials, 1024 cycles of the
+// SM's special function units: the two bound it.  Measured (152 SMs, 64 query and 8 key
+// heads of 128): a prompt of 2048 tokens 48.1 us, the tensor pipe 39% and the special
+// function units 33% busy; it is a tile's chain of wait, load from tensor memory, sum
+// and release, about 2200 cycles, that the three buffers do not hide in full.  The last
+// 64 tokens of a prompt over its 8192 keys take 21 us, of which the start of a CTA (its
+// share, the first block and tile) is 5 and the join by the kernel that follows 3.
 #include <cstdint>
 
 #include "attention.cuh"
@@ -552,8 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           p.records[slot] = WeighRecord{1, it.run, it.h, it.i, it.j0 == 0, it.j1 == it.n, 0, 0};
       }
     }
-  } else {
-  if (warp < kTmaWarp) {
+  } else if (warp < kTmaWarp) {
     // ============================================================ MMA issuers
     const int half = warp - kMmaWarp;
     const bool lead = elect_one();
@@ -594,7 +605,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                      qd + static_cast<uint64_t>((k >> 2) * (kPanel >> 4) + 2 * (k & 3)), idesc,
                      k > 0 ? 1u : 0u);
             // (last: −lse/scale is the largest of the terms, and where it comes first all
-            // later sums are rounded at its size: weights of a 4096-key prompt were 1.4e-6 off, not 2.3e-7)
+            // later sums are rounded at its size: the weights of a prompt of 2048 were off by
+            // 1.4e-6 of the largest, now by 2.3e-7)
             mma_ss(t_s, ones, ld, idesc, 1u);
             mma_commit(&s_full[u.bar()]);
             mma_commit(&q_empty[qs]);
@@ -763,8 +775,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  }
-
   }
 
   tc_fence_before();

@@ -83,6 +83,7 @@ bd_status bitdelta_kv_append_at(const bd_attention_batch* batch, const int32_t* 
  * step and layer, after the attention that gave lse; q, lse and scale as there.
  * A row whose lse is not finite adds nothing.  Sums are in fp32, in an order
  * that the batch alone decides.
+ *   scale        2^-100 and more.
  *   pos_offset   device int32 [n_seq]: tokens that evictions took from the
  *                sequence; NULL: 0.
  *   workspace    device memory of bitdelta_kv_weigh_workspace_bytes(batch) bytes
@@ -121,7 +122,9 @@ bd_status bitdelta_kv_weigh(const bd_attention_batch* batch, const uint16_t* q, 
  * bitdelta_kv_evict_lengths then sets them.  The batch's query tokens are not
  * looked at.  The tables start on 16-byte boundaries.  max_kv_len: at most 344064.
  * A kv_len outside the batch's bounds, or a page outside [0, n_pages), sets
- * BD_ERR_DEVICE_BOUNDS and leaves the sequence's key head as it was.
+ * BD_ERR_DEVICE_BOUNDS and leaves the sequence's key head as it was; of other
+ * weights_out and positions_out some of its slots may have been set.  Two
+ * sequences that share a page outside of a group are not supported.
  */
 bd_status bitdelta_kv_evict(const bd_attention_batch* batch, const int32_t* keep, int32_t recent,
                             int32_t sink, const int32_t* pos_offset, uint16_t* k_pages,

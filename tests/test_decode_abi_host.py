@@ -118,6 +118,7 @@ def test_kv_weigh(lib):
     assert call(b=None) == INVALID
     for scale in (0.0, -1.0, float("inf"), float("nan"), 3e38):
         assert call(scale=scale) == INVALID
+    assert call(scale=2.0 ** -101) == INVALID
     assert call(window=-1) == INVALID
     for name in ("q", "lse", "k", "w", "pos"):
         assert call(**{name: None}) == INVALID

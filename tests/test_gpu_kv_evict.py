@@ -152,6 +152,25 @@ def test_one_long_sequence_over_a_cluster(kv, keep, apart):
     Case([kv], [keep], hkv=2, dim=64, page=128, recent=100, sink=4, seed=kv).check(apart)
 
 
+def test_a_cache_past_32_bits():
+    """The same pages behind 65536 others, more than 2^31 elements into the cache."""
+    c = Case([300, 5000, 129], [100, 2000, 128], hkv=2, dim=128, page=128, recent=5, sink=2, seed=40)
+    small = [t.clone() for t in (c.k, c.v, c.w, c.pos)]
+    c.call()
+    first, far = 65536, []
+    for t in small:
+        far.append(torch.zeros((first + c.n_pages, *t.shape[1:]), dtype=t.dtype, device="cuda"))
+        far[-1][first:] = t
+    near = (c.k, c.v, c.w, c.pos)
+    c.k, c.v, c.w, c.pos = far
+    c.table = (np.minimum(c.table, 2 ** 29) + first).astype(np.int32)
+    c.batch = c.make()
+    c.call()
+    assert bd.bitdelta_check_error() == 0
+    for a, b in zip(far, near):
+        assert torch.equal(a[first:], b) and not a[:first].any()
+
+
 @pytest.mark.parametrize("n", [40, 80, 160, 400])
 def test_many_sequences(n):
     rng = np.random.default_rng(n)

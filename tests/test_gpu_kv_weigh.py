@@ -281,6 +281,64 @@ def test_scales():
         assert ((c.w.double() - want).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("scale", [2.0 ** -100, 1e-20, 1e-3, 40.0])
+@pytest.mark.parametrize("lens", [[(1, 90), (2, 33)], [(50, 300), (17, 17)]])
+def test_scales_far_from_the_usual(scale, lens):
+    c = Case(lens, hq=8, hkv=2, seed=30)
+    c.scale = scale
+    for s in range(len(lens)):
+        for h in range(c.hkv):
+            sc, seen, _ = c.score(s, h)
+            c.lse[c.off[s]:c.off[s + 1], 4 * h:4 * h + 4] = torch.logsumexp(
+                torch.where(seen, sc, -INF), -1).T.float()
+    want, tol, pos = c.want()
+    c.call(scale=scale)
+    assert bd.bitdelta_check_error() == 0
+    # a term below fp32's least normal number, 2^-126, may come out as 0; a key has at most
+    # 50·4 < 2^8 terms
+    tol += 2.0 ** -118
+    assert ((c.w.double() - want).abs() <= tol).all() and torch.equal(c.pos, pos)
+
+
+def test_a_cache_past_32_bits():
+    """The same pages behind 65536 others, more than 2^31 elements into the cache."""
+    c = Case([(1, 300), (60, 200), (3, 40), (1, 129), (1, 140)], hq=8, hkv=2, dim=128, page=128,
+             seed=31)
+    first, w, pos = 65536, c.w.clone(), c.pos.clone()
+    c.call()
+    kp = torch.zeros((first + c.n_pages, 2, 128, 128), dtype=torch.bfloat16, device="cuda")
+    kp[first:] = c.kp
+    far_w = torch.zeros(kp.shape[:3], device="cuda")
+    far_w[first:] = w
+    far_pos = torch.zeros(kp.shape[:3], dtype=torch.int32, device="cuda")
+    far_pos[first:] = pos
+    c.table = (np.minimum(c.table, 2 ** 29) + first).astype(np.int32)
+    bd.bitdelta_kv_weigh(c.make(), c.q, c.lse, kp, far_w, far_pos, pos_offset=c.shift)
+    assert bd.bitdelta_check_error() == 0
+    assert torch.equal(far_w[first:].view(torch.int32), c.w.view(torch.int32))
+    assert torch.equal(far_pos[first:], c.pos)
+    assert not far_w[:first].any() and not far_pos[:first].any()
+
+
+def test_a_graph_of_prompts_and_shared_prefixes():
+    """Both kernels of a call captured, replayed twice over the same tables, and an eager call
+    between."""
+    c = Case([(1, 70), (5, 90), (1, 66), (130, 300), (1, 1000)], groups=[(3, 64)], seed=32)
+    c.call()
+    start, pos = torch.nan_to_num(c.w), c.pos.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.call()
+    for _ in range(2):
+        c.w.copy_(start)
+        c.call()
+        want = c.w.clone()
+        c.w.copy_(start)
+        graph.replay()
+        assert torch.equal(c.w, want) and torch.equal(c.pos, pos)
+    assert bd.bitdelta_check_error() == 0
+
+
 @pytest.mark.parametrize("bad", ["kv", "order", "tokens", "prefix", "odd prefix", "table"])
 def test_broken_tables_change_nothing(bad):
     c = Case([(1, 70), (2, 90), (1, 40)], groups=[(2, 64)], seed=19)

@@ -42,8 +42,13 @@ def choose(x, u, t=1.0, k=0, p=1.0, m=0.0):
     if p < 1:
         want = max(p, 0.0) * total[n - 1]
         cut = int(np.searchsorted(total[:n], want, side="left")) + 1
-        if w[1:].any():            # sums of nothing but the largest are exact
-            near = min(near, np.abs(total[:n] - want).min() / total[n - 1])
+        # The weight 1 is exact, another one off by 2^-40 of itself and its two roundings to
+        # 2^-44 steps, half a step each: a nearness of len(x)·2^-40 is that of their sum.
+        # (Sums of nothing but the largest are exact.)
+        less = w[(w > 0) & (w < 1)]
+        off = less.sum() * 2.0 ** -40 + len(less) * 2.0 ** -44
+        if off > 0:
+            near = min(near, np.abs(total[:n] - want).min() / off * len(x) * 2.0 ** -40)
     else:
         cut = n
     if m > 0:
@@ -208,6 +213,42 @@ def test_extreme_values_and_temperatures():
 
 def test_tiny_and_huge_temperatures():
     check(rand_logits(6, 2000, seed=3), rand_u(6, 14), t=[1e-45, 1e-38, 1e-10, 1e6, 1e30, INF])
+
+
+# bf16 neighbours around 2^16, −2^16, ±2^-40 and zero, where the counters of values end
+LARGE = [49152.0, 65024.0, 65280.0, 65536.0, 66048.0, 131072.0]
+SMALL = [2.0 ** e for e in (-39, -40, -41, -42, -126, -133)] + [2.0 ** -40 * 1.0078125,
+                                                               2.0 ** -41 * 1.9921875, 0.0]
+
+
+@pytest.mark.parametrize("vocab", [64, 20011])
+@pytest.mark.parametrize("sign", [1.0, -1.0, 0.0])  # 0: of both signs
+@pytest.mark.parametrize("values_of, t", [
+    (LARGE[:3], 3000.0), (LARGE, 3000.0), (LARGE, 3e5), (LARGE, 1.0), (LARGE[3:], 4e4),
+    (SMALL, 2.0 ** -40), (SMALL, 2.0 ** -42), (SMALL, 1.0), (SMALL[2:], 2.0 ** -42),
+    (SMALL[:2], 2.0 ** -40), (LARGE[1:5] + SMALL, 2e3), (LARGE[:3] + [0.0, 8.0], 2e3)])
+def test_values_at_the_ends_of_the_counters(values_of, t, sign, vocab):
+    rows = 6
+    rng = np.random.default_rng(len(values_of))
+    x = rng.choice(np.array(values_of), (rows, vocab))
+    x *= rng.choice([1.0, -1.0], x.shape) if sign == 0 else sign
+    x[1, 5:] = -INF                       # few logits, the rest masked
+    x[2, ::2] = -NAN
+    x[3, 1:] = np.where(rng.random(vocab - 1) < 0.9, 1.0, x[3, 1:])
+    logits = torch.from_numpy(x).to(torch.bfloat16).cuda()
+    assert torch.equal(logits.double().cpu().nan_to_num(7.0), torch.from_numpy(x).nan_to_num(7.0))
+    check(logits, rand_u(rows, 8), t=[t] * rows, k=[0, 0, 0, 0, vocab // 3, 0],
+          p=[1, 1, 1, 1, 1, 0.7])
+
+
+def test_far_values_count_at_high_temperatures():
+    """−2^16 and below, with the largest 33 temperatures above them and less."""
+    x = np.full((8, 5000), -65536.0)
+    x[:, 100:200] = -70144.0
+    x[:, 7] = [0.0, 0.0, 0.0, 0.0, -32768.0, -65280.0, 60160.0, -131072.0]
+    t = [1e3, 1.9e3, 2.2e3, 1e5, 1e3, 1e3, 1e5, 1e4]
+    for seed in range(3):
+        check(torch.from_numpy(x).to(torch.bfloat16).cuda(), rand_u(8, seed), t=t)
 
 
 def test_bad_parameters_are_reported():
