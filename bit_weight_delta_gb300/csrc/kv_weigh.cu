@@ -47,28 +47,38 @@ __device__ __forceinline__ int units_of(const WeighArgs& p, const WeighRun& x) {
   return rows <= kWeighShortRows && x.k1 > x.k0 ? (x.k1 - x.k0 + kUnitKeys - 1) / kUnitKeys : 0;
 }
 
-// The blocks that several CTAs of the tile kernel share: their parts in their
-// order.
+// The blocks that several CTAs of the tile kernel share: their parts in their order.
+// (As a rule two, of neighbouring CTAs, in the next place or the one behind it: these are
+// loaded before it is known which.)
 __device__ void join_parts(const WeighArgs& p) {
   const int n = 2 * p.tile_ctas;
   for (int i = blockIdx.x; i < n; i += gridDim.x) {
-    const WeighRecord r = p.records[i];
-    if (!r.used || !r.begins) continue;
-    float a = p.parts[static_cast<int64_t>(i) * kWeighBlockKeys + threadIdx.x];
-    bool more = !r.ends;
-    for (int j = i + 1; more && j < n; ++j) {
-      const WeighRecord o = p.records[j];
-      if (!o.used) continue;
+    constexpr int kAhead = 3;
+    uint32_t f[kAhead];
+    float v[kAhead];
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) {
+      f[x] = i + x < n ? p.records[i + x] : 0u;
+      v[x] = i + x < n ? p.parts[static_cast<int64_t>(i + x) * kWeighBlockKeys + threadIdx.x] : 0.f;
+    }
+    const int32_t to = p.rows[static_cast<int64_t>(i) * kWeighBlockKeys + threadIdx.x];
+    if ((f[0] & kWeighBegins) == 0) continue;
+    const float old = to >= 0 ? p.weights[to] : 0.f;
+    float a = v[0];
+    bool more = (f[0] & kWeighEnds) == 0;
+#pragma unroll
+    for (int x = 1; x < kAhead; ++x)
+      if (more && f[x] != 0) {
+        a += v[x];
+        more = (f[x] & kWeighEnds) == 0;
+      }
+    for (int j = i + kAhead; more && j < n; ++j) {
+      const uint32_t o = p.records[j];
+      if (o == 0) continue;
       a += p.parts[static_cast<int64_t>(j) * kWeighBlockKeys + threadIdx.x];
-      more = !o.ends;
+      more = (o & kWeighEnds) == 0;
     }
-    bool bad = false;  // (the kernel that left the parts has looked)
-    const WeighRun x = weigh_run(p, r.run, &bad);
-    const int key = x.k0 + r.block * kWeighBlockKeys + static_cast<int>(threadIdx.x);
-    if (key < x.k1) {
-      const int64_t row = weigh_row(p.b, x.seq, key, r.head);
-      if (row >= 0) weigh_add(p, x.seq, x.fresh, key, row, a);
-    }
+    if (to != kWeighNowhere) p.weights[to >= 0 ? to : ~to] = old + a;
   }
 }
 
@@ -307,11 +317,12 @@ bool may_tile(const bd_attention_batch& b) {
          static_cast<int64_t>(b.max_q_len) * (b.n_q_heads / b.n_kv_heads) > kWeighShortRows;
 }
 size_t records_bytes(int ctas) {
-  return (sizeof(WeighRecord) * 2 * static_cast<size_t>(ctas) + 255) / 256 * 256;
+  return (sizeof(uint32_t) * 2 * static_cast<size_t>(ctas) + 255) / 256 * 256;
 }
-size_t workspace_bytes(int ctas) {
-  return records_bytes(ctas) + sizeof(float) * 2 * static_cast<size_t>(ctas) * kWeighBlockKeys;
+size_t parts_bytes(int ctas) {
+  return sizeof(float) * 2 * static_cast<size_t>(ctas) * kWeighBlockKeys;
 }
+size_t workspace_bytes(int ctas) { return records_bytes(ctas) + 2 * parts_bytes(ctas); }
 
 bd_status run_weigh(WeighArgs& p, int sms, cudaStream_t s) {
   const bd_attention_batch& b = p.b;
@@ -381,8 +392,10 @@ bd_status bitdelta_kv_weigh(const bd_attention_batch* batch, const uint16_t* q, 
   p.weights = weights;
   p.positions = positions;
   p.tile_ctas = bd::may_tile(*batch) ? sms : 0;
-  p.records = static_cast<bd::WeighRecord*>(workspace);
-  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + bd::records_bytes(sms));
+  uint8_t* at = static_cast<uint8_t*>(workspace);
+  p.records = reinterpret_cast<uint32_t*>(at);
+  p.parts = reinterpret_cast<float*>(at += bd::records_bytes(sms));
+  p.rows = reinterpret_cast<int32_t*>(at + bd::parts_bytes(sms));
   return bd::run_weigh(p, sms, reinterpret_cast<cudaStream_t>(stream));
 }
 

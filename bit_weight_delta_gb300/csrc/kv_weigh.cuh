@@ -17,13 +17,12 @@ constexpr int kWeighShortRows = 16;
 constexpr int kWeighBlockKeys = 256;  // keys of a block of the tile kernel
 
 // A block of keys that several CTAs share: the sums of CTA c's tiles are in
-// parts[2c] (of the block that it began in) or parts[2c + 1] (that it ended in).
-struct WeighRecord {
-  int32_t used;        // 0: no part
-  int32_t run, head, block;
-  int32_t begins, ends;  // the block's first tiles, its last ones
-  int32_t pad0, pad1;
-};
+// parts[2c] (of the block that it began in) or parts[2c + 1] (that it ended in), and
+// what they are is in records[2c], [2c + 1].
+constexpr uint32_t kWeighPart = 1, kWeighBegins = 2, kWeighEnds = 4;  // the block's first tiles, its last
+// Where a key's sum goes, beside a part that begins a block: its row in the tables, to be
+// added to; ~row for a slot of the step's own tokens, to be set; or kWeighNowhere.
+constexpr int32_t kWeighNowhere = INT32_MIN;
 
 struct WeighArgs {
   bd_attention_batch b;
@@ -36,8 +35,9 @@ struct WeighArgs {
   float* weights;
   int32_t* positions;
   int32_t tile_ctas;      // of the tile kernel; 0 where it is not launched
-  WeighRecord* records;   // [2·tile_ctas]
+  uint32_t* records;      // [2·tile_ctas]
   float* parts;           // [2·tile_ctas][kWeighBlockKeys]
+  int32_t* rows;          // the same
   DevCtx ctx;
 };
 
@@ -129,24 +129,6 @@ __device__ __forceinline__ bool weigh_in_window(const WeighArgs& p, int t, int s
       s1 = mid;
   }
   return p.b.seq_offsets[s0 + 1] - t <= p.window;
-}
-
-// The row of slot `key` and head h in the tables beside the cache, or −1.
-__device__ __forceinline__ int64_t weigh_row(const bd_attention_batch& b, int seq, int key, int h) {
-  const int page = b.page_table[static_cast<int64_t>(seq) * b.table_stride + key / b.page_size];
-  if (page < 0 || page >= b.n_pages) return -1;
-  return (static_cast<int64_t>(page) * b.n_kv_heads + h) * b.page_size + key % b.page_size;
-}
-
-// A key's sum to the table.
-__device__ __forceinline__ void weigh_add(const WeighArgs& p, int seq, int fresh, int key,
-                                          int64_t row, float a) {
-  if (key >= fresh) {
-    p.weights[row] = a;
-    p.positions[row] = key + (p.pos_offset != nullptr ? p.pos_offset[seq] : 0);
-  } else {
-    p.weights[row] += a;
-  }
 }
 
 #endif  // __CUDACC__

@@ -103,6 +103,13 @@ struct Cfg {
   static constexpr int kSmem = kOffMisc + 16 + 1024;  // with slack for alignment
 };
 
+// The row of slot `key` and head h in the tables beside the cache, or −1.
+__device__ __forceinline__ int64_t weigh_row(const bd_attention_batch& b, int seq, int key, int h) {
+  const int page = b.page_table[static_cast<int64_t>(seq) * b.table_stride + key / b.page_size];
+  if (page < 0 || page >= b.n_pages) return -1;
+  return (static_cast<int64_t>(page) * b.n_kv_heads + h) * b.page_size + key % b.page_size;
+}
+
 // a / b of numbers that are not negative, in 32 bits where they fit.
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   return (a | b) >> 32 == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
@@ -393,8 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   if (tid < 2) {
-    WeighRecord none{};
-    p.records[2 * blockIdx.x + tid] = none;
+    p.records[2 * blockIdx.x + tid] = 0;
   }
   __syncthreads();
   Items items{item_slots, item_full, item_empty};
@@ -464,12 +470,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool idle = half != 0 && !both;
       if (!staged && !(ok = stage(it.key0, it.k1))) break;
       staged = false;
-      // what the key has, on its way while its sum is formed
+      // the key's place and what it has, on their way while its sum is formed
       int row = -1;
       float old = 0.f;
-      if (c0 == 0 && key < it.k1 && it.j0 == 0 && it.j1 == it.n) {
+      if (c0 == 0 && key < it.k1 && it.j0 == 0) {
         row = static_cast<int>(weigh_row(b, it.seq, key, it.h));  // below 2^31
-        if (row >= 0 && key < it.fresh) old = p.weights[row];
+        if (row >= 0 && key < it.fresh && it.j1 == it.n) old = p.weights[row];
       }
       uint64_t sum[2] = {0u, 0u};
       for (int j = it.j0; j < it.j1; ++j) {
@@ -551,17 +557,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool first_item = !started;
       started = true;
       if (c0 != 0) continue;
+      if (row >= 0 && key >= it.fresh)
+        p.positions[row] = key + (p.pos_offset != nullptr ? p.pos_offset[it.seq] : 0);
       if (it.j0 == 0 && it.j1 == it.n) {
-        if (row >= 0) {
-          p.weights[row] = old + a;
-          if (key >= it.fresh)
-            p.positions[row] = key + (p.pos_offset != nullptr ? p.pos_offset[it.seq] : 0);
-        }
+        if (row >= 0) p.weights[row] = old + a;
       } else {
         const int slot = 2 * static_cast<int>(blockIdx.x) + (first_item ? 0 : 1);
-        p.parts[static_cast<int64_t>(slot) * kWeighBlockKeys + mine] = a;
+        const int64_t at = static_cast<int64_t>(slot) * kWeighBlockKeys + mine;
+        p.parts[at] = a;
+        if (it.j0 == 0) p.rows[at] = row < 0 ? kWeighNowhere : key < it.fresh ? row : ~row;
         if (tid == 0)
-          p.records[slot] = WeighRecord{1, it.run, it.h, it.i, it.j0 == 0, it.j1 == it.n, 0, 0};
+          p.records[slot] = kWeighPart | (it.j0 == 0 ? kWeighBegins : 0) |
+                            (it.j1 == it.n ? kWeighEnds : 0);
       }
     }
   } else if (warp < kTmaWarp) {

@@ -87,7 +87,7 @@ bd_status bitdelta_kv_append_at(const bd_attention_batch* batch, const int32_t* 
  *   pos_offset   device int32 [n_seq]: tokens that evictions took from the
  *                sequence; NULL: 0.
  *   workspace    device memory of bitdelta_kv_weigh_workspace_bytes(batch) bytes
- *                (0.3 MB) on a 256-byte boundary.  Calls that can overlap on the
+ *                (0.6 MB) on a 256-byte boundary.  Calls that can overlap on the
  *                GPU need workspaces of their own.
  * A batch whose tables break its bounds, or a group with a prefix_len that is
  * not a multiple of page_size or reaches into a member's query tokens, sets
