@@ -51,6 +51,7 @@ struct alignas(16) Shared {  // what follows it is read 16 bytes at a time
   uint32_t warp_n[2][32];
   uint32_t found, above;         // a pass' digit, and the keys above it
   uint32_t equal;                // keys that equal the threshold
+  uint32_t n_list, n_few;        // keys with the threshold's digits so far: of this CTA, of all
   uint32_t holes, movers;        // of this CTA
   int bad, prefix;
   // then keys[cap + 256], once they are no longer needed the lists of holes' and movers'
@@ -115,6 +116,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) kv_evict_kernel(const Evi
   if (tid == 0) {
     sh.bad = 0;
     sh.prefix = 0;
+    sh.n_list = 0;
   }
   griddep_wait();
   griddep_launch_dependents();
@@ -237,28 +239,47 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) kv_evict_kernel(const Evi
     return;
   }
 
-  // ---- the K-th largest key, and how many of its equals stay
-  uint32_t threshold = 0u, left = static_cast<uint32_t>(K);
+  // the sum of what the warps before this one have
+  const auto before = [&](const uint32_t* n) {
+    return __reduce_add_sync(0xFFFFFFFFu, lane < warp ? n[lane] : 0u);
+  };
+  // ---- the K-th largest key, and how many of its equals stay (K = 0: none of them), by
+  // digits from the top.  (Rolled: this runs once, and its instructions are fetched for it.)
+  // Where the keys that have the digits so far are few, every CTA of a cluster takes them
+  // all, and the passes that are left need nothing of the others.  (Over all keys two passes
+  // took 10600 cycles by a cluster of four, so 4700, and four prompts 19.1 -> 15.0 us.  A
+  // CTA by itself passes over 4160 keys in 2300, and making the list took it 3700.)
+  constexpr int kFew = 1024, kPer = kFew / T;
+  uint32_t threshold = 0u, left = static_cast<uint32_t>(K), equals = 0u;
+  bool few = false;
+  uint32_t cand[kPer];
+#pragma unroll 1
+  for (int pass = 0; pass < 3 && K > 0; ++pass) {
+    const int down = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const int up = pass == 1 ? 21 : 10;  // of the pass before
+    uint32_t* digits = sh.digits[pass];
+    if (few) {
 #pragma unroll
-  for (int pass = 0; pass < 3; ++pass) {
-    constexpr int kShift[3] = {21, 10, 0};
-    const int down = kShift[pass];
-    if (pass > 0) {
-      const int up = kShift[pass - 1];
+      for (int x = 0; x < kPer; ++x)
+        if (static_cast<uint32_t>(tid + x * T) < sh.n_few && cand[x] >> up == threshold >> up)
+          atomicAdd(&digits[cand[x] >> down & 0x7FFu], 1u);
+      __syncthreads();
+    } else if (pass > 0) {
+#pragma unroll 2
       for (int i = 4 * tid; i < n; i += 4 * T) {
         const uint4 v = *reinterpret_cast<const uint4*>(keys + i);
         const uint32_t key[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int y = 0; y < 4; ++y)
           if (i + y < n && key[y] >> up == threshold >> up)
-            atomicAdd(&sh.digits[pass][key[y] >> down & 0x7FFu], 1u);
+            atomicAdd(&digits[key[y] >> down & 0x7FFu], 1u);
       }
       meet();
     }
     // The cluster's counts: every CTA adds up a share of the digits and gives it to all.
     // (All digits of all CTAs read by each took 64 KB of the others' memory a pass, 13 us
     // of three passes by eight CTAs.)
-    if constexpr (C > 1) {
+    if (C > 1 && !few) {
       constexpr int kShare = kDigits / C;
       for (int d = rank * kShare + tid; d < (rank + 1) * kShare; d += T) {
         uint32_t count = 0u;
@@ -273,8 +294,8 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) kv_evict_kernel(const Evi
     constexpr int kEach = kDigits / T;
     uint32_t c[kEach];
     {
-      const uint2* d = reinterpret_cast<const uint2*>((C > 1 ? total : sh.digits[pass]) +
-                                                      kDigits - kEach * (tid + 1));
+      const uint2* d = reinterpret_cast<const uint2*>((C > 1 && !few ? total : digits) + kDigits -
+                                                      kEach * (tid + 1));
 #pragma unroll
       for (int x = 0; x < kEach / 2; ++x) {
         const uint2 v = d[x];
@@ -288,9 +309,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) kv_evict_kernel(const Evi
     const uint32_t inc = warp_inclusive(sum);
     if (lane == 31) sh.warp_n[0][warp] = inc;
     __syncthreads();
-    uint32_t above = inc - sum;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) above += i < warp ? sh.warp_n[0][i] : 0u;
+    uint32_t above = inc - sum + before(sh.warp_n[0]);
 #pragma unroll
     for (int x = 0; x < kEach; ++x) {
       if (above < left && left <= above + c[x]) {
@@ -301,13 +320,43 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) kv_evict_kernel(const Evi
       above += c[x];
     }
     __syncthreads();
-    if (K > 0) {
-      threshold |= sh.found << down;
-      left -= sh.above;
+    threshold |= sh.found << down;
+    left -= sh.above;
+    equals = sh.equal;
+    if (C == 1 || few || pass == 2 || equals > kFew) continue;
+    few = true;
+    // this CTA's in place of the pass' digits, which all have read
+    for (int i = 4 * tid; i - 4 * lane < n; i += 4 * T) {
+      uint32_t key[4] = {0u, 0u, 0u, 0u}, hit = 0u;
+      if (i < n) {
+        const uint4 v = *reinterpret_cast<const uint4*>(keys + i);
+        key[0] = v.x, key[1] = v.y, key[2] = v.z, key[3] = v.w;
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          hit |= (i + y < n && key[y] >> down == threshold >> down ? 1u : 0u) << y;
+      }
+      if (!__any_sync(0xFFFFFFFFu, hit != 0)) continue;
+      const uint32_t inc = warp_inclusive(static_cast<uint32_t>(__popc(hit)));
+      uint32_t at = lane == 31 ? atomicAdd(&sh.n_list, inc) : 0u;
+      at = __shfl_sync(0xFFFFFFFFu, at, 31) + inc - __popc(hit);
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        if (hit >> y & 1u) digits[at++] = key[y];
+    }
+    if (tid == 0) sh.n_few = equals;
+    meet();
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+      uint32_t at = tid + x * T;  // of all CTAs' lists
+      cand[x] = 0u;
+#pragma unroll
+      for (int r = 0; r < C; ++r) {
+        const uint32_t n_list = peer(r)->n_list;
+        if (at < n_list) cand[x] = peer(r)->digits[pass][at];
+        at = at < n_list ? UINT32_MAX : at - n_list;
+      }
     }
   }
-  // (K = 0: nothing of the candidates stays)
-  const uint32_t equals = K > 0 ? sh.equal : 0u;
   const bool split = left < equals;  // not all of the threshold's equals stay
 
   // ---- which slots stay: a warp owns a run of them, a lane four neighbours
@@ -326,13 +375,8 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) kv_evict_kernel(const Evi
     e = __reduce_add_sync(0xFFFFFFFFu, e);
     if (lane == 0) sh.warp_n[0][warp] = e;
     __syncthreads();
-    uint32_t all = 0u;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      if (i == warp) equal_at = all;
-      all += sh.warp_n[0][i];
-    }
-    if (tid == 0) sh.equal = all;
+    equal_at = before(sh.warp_n[0]);
+    if (tid == T - 1) sh.equal = equal_at + e;
     meet();
 #pragma unroll
     for (int r = 0; r < C; ++r)
@@ -384,19 +428,10 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) kv_evict_kernel(const Evi
     sh.warp_n[1][warp] = movers;
   }
   __syncthreads();
-  uint32_t hole_at = 0u, mover_at = 0u, all_holes = 0u, all_movers = 0u;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    if (i == warp) {
-      hole_at = all_holes;
-      mover_at = all_movers;
-    }
-    all_holes += sh.warp_n[0][i];
-    all_movers += sh.warp_n[1][i];
-  }
-  if (tid == 0) {
-    sh.holes = all_holes;
-    sh.movers = all_movers;
+  uint32_t hole_at = before(sh.warp_n[0]), mover_at = before(sh.warp_n[1]);
+  if (tid == T - 1) {
+    sh.holes = hole_at + holes;
+    sh.movers = mover_at + movers;
   }
   meet();  // and all keys have been read
   uint32_t moves = 0u;
