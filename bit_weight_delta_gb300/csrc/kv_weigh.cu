@@ -13,8 +13,15 @@
 // A unit is 16 keys of a run and key head; every warp has an even share of all units,
 // in the order of runs, heads and keys.  The keys are the rows of mma.sync tiles (16
 // keys by 8 query rows by 16 elements), so that a key's sum stays in its four lanes,
-// and are loaded straight from memory to registers, 16 bytes a lane: which of a row's elements a lane holds is the same for keys and
-// queries, and a product's sum does not care about their order.
+// and are loaded straight from memory to registers, 16 bytes a lane: which of a row's
+// elements a lane holds is the same for keys and queries, and a product's sum does not
+// care about their order.  Scores, powers and sums are fp32; keys and queries are the
+// cache's bf16.
+//
+// Bound by the keys' bytes.  Measured (152 SMs, 64 query and 8 key heads of 128):
+// 64 tokens over 500 to 8000 keys 92.9 us, 575 MB at 91% of the copy rate; one over
+// 131071 keys 46.2 us, 88%; 8 over 120 to 1000 keys 7.2 us, most of it five accesses
+// in a row (lengths, page, key, product, store).
 #include <cmath>
 #include <cstdint>
 

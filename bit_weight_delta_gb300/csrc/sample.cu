@@ -23,6 +23,10 @@
 // A row is shared by a cluster of CTAs, each with counts of its own part, which
 // are added where they are read (distributed shared memory); a cluster takes row
 // after row.  Segments are 32 bins, a lane each; most are empty.
+//
+// Bound by the counters' additions where rows are many (500 of 99991 80.5 us, where their
+// bytes are 15), and by the chain of short phases where they are few (one of 32000
+// 15.9 us, 64 of 128000 26.8).
 #include <cooperative_groups.h>
 
 #include <cstdint>
