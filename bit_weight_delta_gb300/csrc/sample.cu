@@ -933,15 +933,25 @@ extern "C" bd_status bitdelta_sample(const uint16_t* logits, int64_t M, int64_t 
   p.min_p = min_p;
   p.tokens = tokens;
   p.prob = prob;
-  // CTAs per row: the number with which all rounds of rows take least, at about 8 us a
-  // row and 1 us for each 6000 logits of a CTA's part (two CTAs share an SM's 8 additions
-  // to shared memory a clock).
+  // CTAs per row: the number with which all rounds of rows take least.  A round takes about
+  // 8 us, 3 more in clusters, 2 more where two CTAs share an SM, and 1 us for each 8000
+  // logits of an SM (10000 in clusters: of their parts the second look takes one).  Clusters
+  // do not fill the device: 0.85 of it, 0.75 with one CTA an SM.  Over 94 sizes (1 to 1000
+  // rows of 5000 to 262144) the choice costs 0.9% more than the best number.  (us with 1, 2,
+  // 4 and 8: 1 row of 128000 28.7 23.7 18.8 17.2; 38 of 32000 18.4 18.8 20.1 33.6; 64 of
+  // 128000 31.0 27.1 25.8 40.9; 152 of 128000 33.3 35.2 79.1 135.4.)
   int c = 1;
   double best = 0;
   for (int n = 1; n <= bd::kMaxCluster; n *= 2) {
-    const int64_t at_once = sms * bd::kCtas >= n ? sms * bd::kCtas / n : 1;
-    const double time =
-        static_cast<double>((M + at_once - 1) / at_once) * (8.0 + static_cast<double>(V) / n / 6e3);
+    const bool alone = n == 1;
+    const int64_t room = static_cast<int64_t>((alone ? 1.0 : 0.85) * bd::kCtas * sms / n);
+    const int64_t at_once = room > 1 ? room : 1;
+    const int64_t rows = M < at_once ? M : at_once;
+    const int share = rows * n <= (alone ? 1.0 : 0.75) * sms ? 1 : bd::kCtas;  // of an SM
+    const double logits = static_cast<double>(share) * static_cast<double>(V) / n;
+    const double time = static_cast<double>((M + at_once - 1) / at_once) *
+                        (8.0 + (alone ? 0.0 : 3.0) + (share > 1 ? 2.0 : 0.0) +
+                         logits / (alone ? 8e3 : 10e3));
     if (n == 1 || time < best) {
       c = n;
       best = time;
