@@ -121,6 +121,8 @@ struct TileRun {
   bool group;
   int blocks;
   int n_full, m_full;  // the first m_full blocks are seen from the first token on
+  int step;            // of the others each has so many tiles fewer than the one before it
+                       // (0: it depends)
   int64_t per_head;    // tiles
   // first token that sees block i
   __device__ __forceinline__ int first_token(int i) const {
@@ -145,7 +147,12 @@ __device__ TileRun tile_run(const WeighArgs& p, int r, int tok, bool* bad) {
                      : static_cast<int>(ahead < 0 ? 0 : ahead / kWeighBlockKeys + 1);
   if (t.m_full > t.blocks) t.m_full = t.blocks;
   t.per_head = static_cast<int64_t>(t.m_full) * t.n_full;
-  for (int i = t.m_full; i < t.blocks; ++i) t.per_head += t.tiles(i, tok);
+  t.step = kWeighBlockKeys % tok == 0 ? kWeighBlockKeys / tok : 0;
+  const int64_t n = t.blocks - t.m_full;
+  if (n > 0 && t.step > 0)
+    t.per_head += n * t.tiles(t.m_full, tok) - t.step * (n * (n - 1) / 2);
+  else
+    for (int i = t.m_full; i < t.blocks; ++i) t.per_head += t.tiles(i, tok);
   return t;
 }
 
@@ -182,7 +189,11 @@ struct Walk {
       at -= static_cast<int64_t>(i) * t.n_full;
     } else {
       at -= full;
-      for (i = t.m_full; at >= t.tiles(i, tok); ++i) at -= t.tiles(i, tok);
+      i = t.m_full;
+      for (int n = t.tiles(i, tok); at >= n; n = t.step > 0 ? n - t.step : t.tiles(i, tok)) {
+        at -= n;
+        ++i;
+      }
     }
     j = static_cast<int>(at);
   }
@@ -341,10 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int64_t more = 0;
   for (int r = tid + kThreads; r < n_run; r += kThreads)
     more += tile_run(p, r, tok, &bad).per_head;
-#pragma unroll
-  for (int off = 16; off > 0 && n_run > kThreads; off >>= 1)
-    more += __shfl_xor_sync(0xFFFFFFFFu, more, off);
-  // inclusive sums over the round's runs
+  // inclusive sums over the lanes
   const auto scan = [&](int64_t n) {
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -353,19 +361,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return n;
   };
+  // the sum of all warps' n, and of those before this one
+  const auto of_warps = [&](const int64_t* n, int64_t& before) {
+    const int64_t mine = lane < kWarps ? n[lane] : 0, inc = scan(mine);
+    before = __shfl_sync(0xFFFFFFFFu, inc - mine, warp);
+    return __shfl_sync(0xFFFFFFFFu, inc, 31);
+  };
   int64_t inc = scan(mine.per_head);
-  if (lane == 31) {
-    s_sum[warp] = inc;
-    s_more[warp] = more;
+  if (lane == 31) s_sum[warp] = inc;
+  if (n_run > kThreads) {
+    more = scan(more);
+    if (lane == 31) s_more[warp] = more;
   }
   bad = __syncthreads_or(bad);
-  int64_t round = 0, total = 0;
-#pragma unroll 1
-  for (int i = 0; i < kWarps; ++i) {
-    if (i == warp) inc += round;
-    round += s_sum[i];
-    total += s_more[i];
-  }
+  int64_t others;
+  int64_t round = of_warps(s_sum, others);  // over the round's runs
+  inc += others;
+  int64_t total = n_run > kThreads ? of_warps(s_more, others) : 0;
   total = bad ? 0 : (total + round) * b.n_kv_heads;
   if (bad && tid == 0 && blockIdx.x == 0) record_error(p.ctx, kErrBounds);
   const int64_t each = quotient(total, gridDim.x), extra = total - each * gridDim.x;
@@ -381,11 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();  // the sums before have been read
         if (lane == 31) s_sum[warp] = inc;
         __syncthreads();
-        round = 0;
-        for (int i = 0; i < kWarps; ++i) {
-          if (i == warp) inc += round;
-          round += s_sum[i];
-        }
+        round = of_warps(s_sum, others);
+        inc += others;
       }
       const int64_t first = before + (inc - mine.per_head) * b.n_kv_heads;
       if (first <= lo && lo < before + inc * b.n_kv_heads) {
