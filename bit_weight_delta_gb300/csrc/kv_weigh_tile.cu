@@ -133,7 +133,7 @@ struct TileRun {
   }
 };
 
-__device__ TileRun tile_run(const WeighArgs& p, int r, int tok, bool* bad) {
+__device__ __forceinline__ TileRun tile_run(const WeighArgs& p, int r, int tok, bool* bad) {
   TileRun t{};
   t.x = weigh_run(p, r, bad);
   t.group = r >= p.b.n_seq;
@@ -154,6 +154,11 @@ __device__ TileRun tile_run(const WeighArgs& p, int r, int tok, bool* bad) {
   else
     for (int i = t.m_full; i < t.blocks; ++i) t.per_head += t.tiles(i, tok);
   return t;
+}
+
+// The same where it is seldom needed.
+__device__ __noinline__ TileRun further_run(const WeighArgs& p, int r, int tok, bool* bad) {
+  return tile_run(p, r, tok, bad);
 }
 
 // Tiles [j0, j1) of a block, as the roles read it from shared memory; h < 0 ends the
@@ -203,7 +208,7 @@ struct Walk {
     if (left <= 0) return;
     while (h == p.b.n_kv_heads) {  // (there is a further run: left counts its tiles)
       bool bad = false;
-      t = tile_run(p, ++run, tok, &bad);
+      t = further_run(p, ++run, tok, &bad);
       if (t.per_head > 0) h = 0;
     }
     it.h = h;
@@ -268,7 +273,8 @@ struct Items {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    weigh_tile_kernel(const __grid_constant__ WeighMaps maps, const WeighArgs p) {
+    weigh_tile_kernel(const __grid_constant__ WeighMaps maps,
+                      const __grid_constant__ WeighArgs p) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int64_t s_sum[kWarps], s_more[kWarps];
@@ -351,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid < n_run) mine = tile_run(p, tid, tok, &bad);
   int64_t more = 0;
   for (int r = tid + kThreads; r < n_run; r += kThreads)
-    more += tile_run(p, r, tok, &bad).per_head;
+    more += further_run(p, r, tok, &bad).per_head;
   // inclusive sums over the lanes
   const auto scan = [&](int64_t n) {
 #pragma unroll
@@ -388,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int base = 0; base < n_run && before <= lo; base += kThreads) {
       if (base > 0) {
         mine = TileRun{};
-        if (base + tid < n_run) mine = tile_run(p, base + tid, tok, &bad);
+        if (base + tid < n_run) mine = further_run(p, base + tid, tok, &bad);
         inc = scan(mine.per_head);
         __syncthreads();  // the sums before have been read
         if (lane == 31) s_sum[warp] = inc;
