@@ -176,9 +176,7 @@ __device__ __forceinline__ T warp_inclusive(T v) {
 }
 
 // Eight logits from a 16-byte boundary on; those outside the row are −NaN.
-__device__ __forceinline__ uint4 load_chunk(const uint16_t* row, int64_t V, int mis, int chunk) {
-  const int64_t i0 = static_cast<int64_t>(chunk) * 8 - mis;
-  if (i0 >= 0 && i0 + 8 <= V) return ldg_stream_v4(row + i0);
+__device__ __noinline__ uint4 edge_chunk(const uint16_t* row, int64_t V, int64_t i0) {
   uint32_t w[4];
 #pragma unroll
   for (int x = 0; x < 4; ++x) {
@@ -188,6 +186,11 @@ __device__ __forceinline__ uint4 load_chunk(const uint16_t* row, int64_t V, int 
     w[x] = lo | hi << 16;
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 load_chunk(const uint16_t* row, int64_t V, int mis, int chunk) {
+  const int64_t i0 = static_cast<int64_t>(chunk) * 8 - mis;
+  if (i0 >= 0 && i0 + 8 <= V) return ldg_stream_v4(row + i0);
+  return edge_chunk(row, V, i0);
 }
 
 // The bins of two logits.
