@@ -19,8 +19,8 @@
 // cache's bf16.
 //
 // Bound by the keys' bytes.  Measured (152 SMs, 64 query and 8 key heads of 128):
-// 64 tokens over 500 to 8000 keys 92.9 us, 575 MB at 91% of the copy rate; one over
-// 131071 keys 46.2 us, 88%; 8 over 120 to 1000 keys 7.2 us, most of it five accesses
+// 64 tokens over 500 to 8000 keys 93.5 us, 575 MB at 91% of the copy rate; one over
+// 131071 keys 46.6 us, 88%; 8 over 120 to 1000 keys 7.2 us, most of it five accesses
 // in a row (lengths, page, key, product, store).
 #include <cmath>
 #include <cstdint>

@@ -22,8 +22,8 @@
 // lse came on top (1650 cycles a tile).
 //
 // Warps: 0-15 the epilogue, of which a warp has 32 keys of one of the block's halves
-// and 64 of a tile's 128 rows (eight warps with all rows took 59 us where these take
-// 46); 16 and 17 the halves' MMA issuers (one's waits are then the time of the other's
+// and 64 of a tile's 128 rows (eight warps with all rows took 59 us where these took
+// 49); 16 and 17 the halves' MMA issuers (one's waits are then the time of the other's
 // products); 18 the TMA producer of K and Q, which also walks through the CTA's share
 // and puts its items in a ring for the other roles; 19 loads the rows' lse.
 // Tensor memory: the block's halves in columns 0-127, three buffers of 128 columns
@@ -32,11 +32,12 @@
 // A block and a tile of 128-element heads are 8.4 MFLOP of products, 1024 cycles of the
 // tensor pipe and an eighth more for lse, and 32768 exponentials, 1024 cycles of the
 // SM's special function units: the two bound it.  Measured (152 SMs, 64 query and 8 key
-// heads of 128): a prompt of 2048 tokens 46.3 us, the tensor pipe 36% and the special
+// heads of 128): a prompt of 2048 tokens 43.7 us, the tensor pipe 36% and the special
 // function units 30% busy; it is a tile's chain of wait, load from tensor memory, sum
 // and release, about 2200 cycles, that the three buffers do not hide in full.  The last
-// 64 tokens of a prompt over its 8192 keys take 20 us, of which the start of a CTA (its
-// share, the first block and tile) is 5 and the join by the kernel that follows 3.
+// 64 tokens of a prompt over its 8192 keys take 19.6 us, of which the start of a CTA
+// (lengths, share, page) is 4, its first block and product 3 and the join by the kernel
+// that follows 3.
 #include <cstdint>
 
 #include "attention.cuh"

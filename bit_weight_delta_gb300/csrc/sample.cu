@@ -24,9 +24,9 @@
 // are added where they are read (distributed shared memory); a cluster takes row
 // after row.  Segments are 32 bins, a lane each; most are empty.
 //
-// Bound by the counters' additions where rows are many (500 of 99991 80.5 us, where their
+// Bound by the counters' additions where rows are many (500 of 99991 80.2 us, where their
 // bytes are 15), and by the chain of short phases where they are few (one of 32000
-// 15.9 us, 64 of 128000 26.8).
+// 16.0 us, 64 of 128000 26.0).
 #include <cooperative_groups.h>
 
 #include <cstdint>
