@@ -93,9 +93,9 @@ __device__ __forceinline__ T warp_inclusive(T v) {
   return v;
 }
 
-// T threads: 256 for few keys, four CTAs an SM, and 1024 for many.
+// T threads: 256, 512 or 1024, and four, two or one CTA an SM.
 template <int C, int T>
-__global__ void __launch_bounds__(T, T == 256 ? 4 : 1) kv_evict_kernel(const EvictArgs p) {
+__global__ void __launch_bounds__(T, 1024 / T) kv_evict_kernel(const EvictArgs p) {
   constexpr int kWarps = T / 32;
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& sh = *reinterpret_cast<Shared*>(smem);
@@ -654,24 +654,34 @@ bd_status bitdelta_kv_evict(const bd_attention_batch* batch, const int32_t* keep
   p.weights_out = weights_out;
   p.positions_out = positions_out;
   // CTAs per sequence and key head: as many as the keys need, and more while the device
-  // has SMs left for them and each still has 2048.  Where there are more CTAs than SMs,
-  // and few keys each, they have 256 threads, which leaves an SM four of them: their
-  // phases wait for one another.
+  // has SMs left for them (clusters fill 0.85 of it) and each still has 2048.  Threads:
+  // where each SM has a CTA, as many as its keys keep busy; where there are more CTAs, few,
+  // so that several share an SM, whose phases wait for one another.  Over 164 sizes (8 to
+  // 1024 items of 300 to 32768 keys) the choice costs 2.3% more than the best of 1 to 8
+  // CTAs of 256, 512 and 1024 threads.  (us, keys x items to 98%, CTAs of threads: 4160 x
+  // 512 29.3 by 1 of 256, 33.4 of 512, 45.7 of 1024; 16384 x 512 103, 83 and 97; 8192 x 64
+  // 27.3, 21.2 and 19.1; 32768 x 16 25.2 by 4 of 1024, 43.6 by 8, of which not all run at
+  // once.)
   const int64_t items = static_cast<int64_t>(batch->n_seq) * batch->n_kv_heads;
   const int len = batch->max_kv_len;
   int c = 1;
-  while (c < 8 && (len > bd::kMaxKeys * c || (items * 2 * c <= sms && len > 2048 * c))) c *= 2;
+  while (c < 8 && (len > bd::kMaxKeys * c || (items * 2 * c <= 0.85 * sms && len > 2048 * c)))
+    c *= 2;
   if (c == 8 && items * 16 <= sms && len > 2048 * 8 && bd::large_clusters() >= items) c = 16;
   p.cap = ((len + c - 1) / c + 127) / 128 * 128;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  // (clusters come of fewer CTAs than SMs, or of more keys)
-  const bool few = c == 1 && p.cap <= 8192 && items > sms;
+  const int few = items <= sms ? 512 : 4608, some = items <= sms ? 2048 : 16384;
+  const bool half = p.cap <= 4096;
   cudaError_t e;
   switch (c) {
-    case 1: e = few ? bd::launch<1, 256>(p, s) : bd::launch<1, 1024>(p, s); break;
-    case 2: e = bd::launch<2, 1024>(p, s); break;
-    case 4: e = bd::launch<4, 1024>(p, s); break;
-    case 8: e = bd::launch<8, 1024>(p, s); break;
+    case 1:
+      e = len <= few    ? bd::launch<1, 256>(p, s)
+          : len <= some ? bd::launch<1, 512>(p, s)
+                        : bd::launch<1, 1024>(p, s);
+      break;
+    case 2: e = half ? bd::launch<2, 512>(p, s) : bd::launch<2, 1024>(p, s); break;
+    case 4: e = half ? bd::launch<4, 512>(p, s) : bd::launch<4, 1024>(p, s); break;
+    case 8: e = half ? bd::launch<8, 512>(p, s) : bd::launch<8, 1024>(p, s); break;
     default: e = bd::launch<16, 1024>(p, s); break;
   }
   return e == cudaSuccess ? BD_OK : BD_ERR_CUDA;

@@ -178,6 +178,18 @@ def test_many_sequences(n):
     Case(kv, rng.integers(-1, 300, n), hkv=1, recent=3, sink=1, seed=n).check()
 
 
+@pytest.mark.parametrize("others,kv", [(160, 700), (160, 5000), (160, 17000), (39, 9000), (30, 17000),
+                                       (15, 33000), (3, 5000)])
+@pytest.mark.parametrize("apart", [False, True])
+def test_one_long_sequence_among_short_ones(others, kv, apart):
+    """One to eight CTAs of every number of threads, most of them with next to nothing to do."""
+    rng = np.random.default_rng(others)
+    short = rng.integers(1, 60, others)
+    at = others // 2
+    Case([*short[:at], kv, *short[at:]], [*(short[:at] // 2), kv // 3, *(short[at:] - 1)], hkv=1,
+         page=32, recent=2, sink=1, seed=kv).check(apart)
+
+
 def test_equal_weights_go_by_their_slot():
     Case([1000, 257], [500, 100], ties=True, recent=10, sink=1, seed=3).check()
     c = Case([5000], [2000], hkv=1, seed=4)      # all alike: nothing moves
