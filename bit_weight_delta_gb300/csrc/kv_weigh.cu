@@ -20,7 +20,7 @@
 //
 // Bound by the keys' bytes.  Measured (152 SMs, 64 query and 8 key heads of 128):
 // 64 tokens over 500 to 8000 keys 93.5 us, 575 MB at 91% of the copy rate; one over
-// 131071 keys 46.6 us, 88%; 8 over 120 to 1000 keys 7.2 us, most of it five accesses
+// 131071 keys 46.6 us, 88%; 8 over 120 to 1000 keys 7.0 us, most of it five accesses
 // in a row (lengths, page, key, product, store).
 #include <cmath>
 #include <cstdint>
@@ -306,14 +306,31 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, NT>) kv_weigh_kernel(const 
   }
 }
 
+// CTAs of the short runs' kernel.  Behind the tile kernel, and where the batch may have many
+// units, as many as the SMs hold; for few of them fewer, which start sooner and ask less
+// often for the same lengths.  (us, 8 key heads of 128, one CTA for two SMs, one an SM, two
+// and three: 1 token over 1000 keys 4.2 4.3 5.4 5.7; 8 over 500 7.5 5.8 6.7 6.8; 1 over
+// 8000 10.7 8.1 8.4 8.6; 64 over 300 20.2 14.0 13.5 12.1.  Of 64, where four fit: 64 over
+// 300 17.9 12.0 9.7, 10.6 by four; 64 over 2000 88 48 32, 27.5 by four.)
+template <int D>
+unsigned short_ctas(const WeighArgs& p, int sms, int most) {
+  if (p.tile_ctas > 0) return static_cast<unsigned>(most * sms);
+  const int64_t units = static_cast<int64_t>(p.b.n_seq) * p.b.n_kv_heads *
+                        ((p.b.max_kv_len + kUnitKeys - 1) / kUnitKeys);
+  if (units <= 4ll * sms) return static_cast<unsigned>((sms + 1) / 2);
+  if (units <= (D == 128 ? 32ll : 16ll) * sms) return static_cast<unsigned>(sms);
+  if (D == 64 && units <= 80ll * sms) return static_cast<unsigned>(2 * sms);
+  return static_cast<unsigned>(most * sms);
+}
+
 template <int D>
 cudaError_t launch_short(const WeighArgs& p, int sms, cudaStream_t s) {
   const dim3 block(kThreads);
   const int64_t rows = static_cast<int64_t>(p.b.max_q_len) * (p.b.n_q_heads / p.b.n_kv_heads);
   // (a group of few members has up to 16 rows of single tokens)
   return rows <= 8 && p.b.n_group == 0
-             ? launch_pdl(kv_weigh_kernel<D, 1>, dim3(kCtas<D, 1> * sms), block, 0, s, p)
-             : launch_pdl(kv_weigh_kernel<D, 2>, dim3(kCtas<D, 2> * sms), block, 0, s, p);
+             ? launch_pdl(kv_weigh_kernel<D, 1>, dim3(short_ctas<D>(p, sms, kCtas<D, 1>)), block, 0, s, p)
+             : launch_pdl(kv_weigh_kernel<D, 2>, dim3(short_ctas<D>(p, sms, kCtas<D, 2>)), block, 0, s, p);
 }
 
 bool off(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) != 0; }
