@@ -16,7 +16,7 @@
 //
 // Bound by the weights' bytes and the moves at best; with few of either by the chain of
 // phases between barriers.  Measured (152 SMs, 8 key heads of 128): 64 sequences of 4097
-// to 4160 keys to 4096 21.1 us; four of 8192 to 1024 15.1 us; one of 131071 to 65536
+// to 4160 keys to 4096 21.0 us; four of 8192 to 1024 14.8 us; one of 131071 to 65536
 // 83 us, of which 52 are 270 MB of moves (70% of the copy rate in rows of 256 bytes).
 #include <cooperative_groups.h>
 

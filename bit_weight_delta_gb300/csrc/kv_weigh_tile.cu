@@ -32,8 +32,8 @@
 // A block and a tile of 128-element heads are 8.4 MFLOP of products, 1024 cycles of the
 // tensor pipe and an eighth more for lse, and 32768 exponentials, 1024 cycles of the
 // SM's special function units: the two bound it.  Measured (152 SMs, 64 query and 8 key
-// heads of 128): a prompt of 2048 tokens 43.7 us, the tensor pipe 36% and the special
-// function units 30% busy; it is a tile's chain of wait, load from tensor memory, sum
+// heads of 128): a prompt of 2048 tokens 43.7 us, the tensor pipe 38% and the special
+// function units 31% busy; it is a tile's chain of wait, load from tensor memory, sum
 // and release, about 2200 cycles, that the three buffers do not hide in full.  The last
 // 64 tokens of a prompt over its 8192 keys take 19.6 us, of which the start of a CTA
 // (lengths, share, page) is 4, its first block and product 3 and the join by the kernel
