@@ -64,6 +64,15 @@ struct alignas(16) Shared {  // what follows it is read 16 bytes at a time
   // total[kDigits], a pass' counts in all of it
 };
 
+// Whether a length lies within the batch's bounds, and a page within the cache.  A sequence
+// of which one of them does not (of the pages, those that are chosen from) is refused, by
+// the eviction and by the update of the lengths alike.
+__device__ __forceinline__ bool length_fits(const bd_attention_batch& b, int kv) {
+  return kv >= 0 && kv <= b.max_kv_len && kv <= b.table_stride * b.page_size;
+}
+__device__ __forceinline__ bool page_fits(const bd_attention_batch& b, int page) {
+  return page >= 0 && page < b.n_pages;
+}
 // New length of a sequence of kv keys whose first `prefix` are shared.
 __device__ __forceinline__ int evicted_length(int kv, int keep, int prefix) {
   if (keep < 0 || keep >= kv) return kv;
@@ -131,7 +140,7 @@ __global__ void __launch_bounds__(T, 1024 / T) kv_evict_kernel(const EvictArgs p
       atomicMax(&sh.prefix, b.prefix_len[g]);
   const int kv = b.kv_len[s], keep = p.keep[s];
   const int shift = p.pos_offset != nullptr ? p.pos_offset[s] : 0;
-  if (kv < 0 || kv > b.max_kv_len || kv > b.table_stride * b.page_size) {
+  if (!length_fits(b, kv)) {
     if (tid == 0) record_error(p.ctx, kErrBounds);
     return;  // every CTA of the cluster
   }
@@ -143,7 +152,7 @@ __global__ void __launch_bounds__(T, 1024 / T) kv_evict_kernel(const EvictArgs p
   // a slot's row (of this head) in the cache, or −1
   const auto row_of = [&](int slot) {
     const int page = table[slot >> page_shift];
-    if (page < 0 || page >= b.n_pages) return -1;
+    if (!page_fits(b, page)) return -1;
     return ((page * b.n_kv_heads + h) << page_shift) + (slot & (b.page_size - 1));
   };
   const bool apart = p.weights_out != p.weights || p.positions_out != p.positions;
@@ -518,25 +527,37 @@ __global__ void __launch_bounds__(T, 1024 / T) kv_evict_kernel(const EvictArgs p
   }
 }
 
-__global__ void __launch_bounds__(256)
+constexpr int kLengthThreads = 128;
+
+// A CTA per sequence.
+__global__ void __launch_bounds__(kLengthThreads)
     evict_lengths_kernel(const bd_attention_batch b, const int32_t* keep, int32_t* kv_len_out,
                          int32_t* pos_offset, DevCtx ctx) {
+  __shared__ int s_prefix;
+  const int s = static_cast<int>(blockIdx.x), tid = threadIdx.x;
+  if (tid == 0) s_prefix = 0;
   griddep_wait();
   griddep_launch_dependents();
-  const int s = blockIdx.x * blockDim.x + threadIdx.x;
-  if (s >= b.n_seq) return;
-  const int kv = b.kv_len[s];
-  if (kv < 0 || kv > b.max_kv_len) {
-    record_error(ctx, kErrBounds);
-    return;
+  __syncthreads();
+  for (int g = tid; g < b.n_group; g += kLengthThreads)
+    if (b.group_offsets[g] <= s && s < b.group_offsets[g + 1])
+      atomicMax(&s_prefix, b.prefix_len[g]);
+  const int kv = b.kv_len[s], keeps = keep[s];
+  __syncthreads();
+  bool fits = length_fits(b, kv);
+  const int prefix = fits ? prefix_keys(b, s_prefix, kv) : 0;
+  const int len = fits ? evicted_length(kv, keeps, prefix) : kv;
+  if (len != kv && b.page_table != nullptr && b.n_pages > 0) {
+    const int32_t* table = b.page_table + static_cast<int64_t>(s) * b.table_stride;
+    const int page_shift = 31 - __clz(b.page_size);
+    for (int i = (prefix >> page_shift) + tid; i <= (kv - 1) >> page_shift; i += kLengthThreads)
+      fits &= page_fits(b, table[i]);
   }
-  int prefix = 0;
-  for (int g = 0; g < b.n_group; ++g)
-    if (b.group_offsets[g] <= s && s < b.group_offsets[g + 1] && b.prefix_len[g] > prefix)
-      prefix = b.prefix_len[g];
-  const int len = evicted_length(kv, keep[s], prefix_keys(b, prefix, kv));
-  kv_len_out[s] = len;
-  pos_offset[s] += kv - len;
+  fits = __syncthreads_and(fits);  // and kv_len[s], which may be kv_len_out[s], has been read
+  if (tid != 0) return;
+  if (!fits) record_error(ctx, kErrBounds);
+  kv_len_out[s] = fits ? len : kv;
+  if (fits) pos_offset[s] += kv - len;
 }
 
 constexpr size_t smem_bytes(int cap, int c) {
@@ -608,6 +629,8 @@ bool off(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % 
 int check_batch(const bd_attention_batch* b, const int32_t* keep) {
   const int st = check_attention_batch(b);
   if (st != BD_OK) return st;
+  if (b->max_kv_len > kMaxLen || static_cast<int64_t>(b->n_seq) * b->n_kv_heads > (1 << 27))
+    return BD_ERR_UNSUPPORTED_SHAPE;
   if (b->n_seq == 0) return BD_OK;
   if (!b->kv_len || !keep) return BD_ERR_INVALID_ARG;
   if (b->n_group > 0 && (!b->group_offsets || !b->prefix_len)) return BD_ERR_INVALID_ARG;
@@ -628,9 +651,6 @@ bd_status bitdelta_kv_evict(const bd_attention_batch* batch, const int32_t* keep
   int st = bd::check_batch(batch, keep);
   if (st != BD_OK) return static_cast<bd_status>(st);
   if (recent < 0 || sink < 0) return BD_ERR_INVALID_ARG;
-  if (batch->max_kv_len > bd::kMaxLen) return BD_ERR_UNSUPPORTED_SHAPE;
-  if (static_cast<int64_t>(batch->n_seq) * batch->n_kv_heads > (1 << 27))
-    return BD_ERR_UNSUPPORTED_SHAPE;
   if (batch->n_seq == 0) return BD_OK;
   if (!batch->page_table || !k_pages || !v_pages || !weights || !positions || !weights_out ||
       !positions_out)
@@ -694,15 +714,15 @@ bd_status bitdelta_kv_evict_lengths(const bd_attention_batch* batch, const int32
   if (st != BD_OK) return static_cast<bd_status>(st);
   if (batch->n_seq == 0) return BD_OK;
   if (!kv_len_out || !pos_offset) return BD_ERR_INVALID_ARG;
-  if (bd::off(kv_len_out, 4) || bd::off(pos_offset, 4)) return BD_ERR_MISALIGNED;
+  if (bd::off(batch->page_table, 4) || bd::off(kv_len_out, 4) || bd::off(pos_offset, 4))
+    return BD_ERR_MISALIGNED;
   bd::DevCtx ctx;
   int sms = 0;
   if ((st = bd::current_device_context(&ctx, &sms)) != BD_OK) return static_cast<bd_status>(st);
-  const unsigned grid = (static_cast<unsigned>(batch->n_seq) + 255) / 256;
   const cudaError_t e =
-      bd::launch_pdl(bd::evict_lengths_kernel, dim3(grid), dim3(256), 0,
-                     reinterpret_cast<cudaStream_t>(stream), *batch, keep, kv_len_out, pos_offset,
-                     ctx);
+      bd::launch_pdl(bd::evict_lengths_kernel, dim3(static_cast<unsigned>(batch->n_seq)),
+                     dim3(bd::kLengthThreads), 0, reinterpret_cast<cudaStream_t>(stream), *batch,
+                     keep, kv_len_out, pos_offset, ctx);
   return e == cudaSuccess ? BD_OK : BD_ERR_CUDA;
 }
 

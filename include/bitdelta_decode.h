@@ -121,8 +121,9 @@ bd_status bitdelta_kv_weigh(const bd_attention_batch* batch, const uint16_t* q, 
  * kv_len is not changed: every layer is cut with the same lengths, and
  * bitdelta_kv_evict_lengths then sets them.  The batch's query tokens are not
  * looked at.  The tables start on 16-byte boundaries.  max_kv_len: at most 344064.
- * A kv_len outside the batch's bounds, or a page outside [0, n_pages), sets
- * BD_ERR_DEVICE_BOUNDS and leaves the sequence's key head as it was; of other
+ * A kv_len outside the batch's bounds (or past its page table's row), or a page
+ * outside [0, n_pages) among those that are chosen from, sets BD_ERR_DEVICE_BOUNDS
+ * and leaves the sequence as it was, with its length; of other
  * weights_out and positions_out some of its slots may have been set.  Two
  * sequences that share a page outside of a group are not supported.
  */
@@ -134,7 +135,10 @@ bd_status bitdelta_kv_evict(const bd_attention_batch* batch, const int32_t* keep
 /*
  * The lengths after an eviction of every layer: kv_len_out[s] = n' and
  * pos_offset[s] += kv_len[s] − n'.  kv_len_out may be the batch's own kv_len;
- * the attention's plan has to be made again.
+ * the attention's plan has to be made again.  What the eviction refuses is
+ * refused here too, for the same batch, keep and n_pages: a sequence that it left as
+ * it was sets BD_ERR_DEVICE_BOUNDS and keeps its length and offset (kv_len_out[s] =
+ * kv_len[s]).  With n_pages = 0 or no page_table the pages are not looked at.
  */
 bd_status bitdelta_kv_evict_lengths(const bd_attention_batch* batch, const int32_t* keep,
                                     int32_t* kv_len_out, int32_t* pos_offset,

@@ -172,3 +172,14 @@ def test_kv_evict_lengths(lib):
     assert lib.bitdelta_kv_evict_lengths(ref, GOOD, GOOD, ODD, None) == MISALIGNED
     empty = batch(n_seq=0)
     assert lib.bitdelta_kv_evict_lengths(ctypes.addressof(empty), None, None, None, None) == OK
+
+
+def test_lengths_refuse_the_batches_that_the_eviction_refuses(lib):
+    for bad in (dict(max_kv_len=344065),
+                dict(n_seq=1 << 20, n_q_heads=1024, n_kv_heads=1024, n_pages=1)):
+        ref = batch(**bad)
+        assert lib.bitdelta_kv_evict(ctypes.addressof(ref), GOOD, 0, 0, None, GOOD, GOOD, GOOD, GOOD,
+                                     GOOD, GOOD, None) == SHAPE
+        assert lib.bitdelta_kv_evict_lengths(ctypes.addressof(ref), GOOD, GOOD, GOOD, None) == SHAPE
+    odd = batch(n_tokens=0, page_table=ODD)
+    assert lib.bitdelta_kv_evict_lengths(ctypes.addressof(odd), GOOD, GOOD, GOOD, None) == MISALIGNED

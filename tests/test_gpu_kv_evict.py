@@ -365,3 +365,74 @@ def test_refusals():
     big = c.make(max_kv_len=344065)
     with pytest.raises(bd.BitDeltaError):
         bd.bitdelta_kv_evict(big, keep, c.k, c.v, c.w, c.pos)
+
+
+def lengths_of(c):
+    """(kv_len, pos_offset) after bitdelta_kv_evict_lengths into outputs of their own."""
+    kv, shift = torch.full((len(c.kv),), 77, dtype=torch.int32, device="cuda"), torch.from_numpy(c.shift).cuda()
+    bd.bitdelta_kv_evict_lengths(c.batch, torch.from_numpy(c.keep).cuda(), kv, shift)
+    return kv.tolist(), (shift.cpu().numpy() - c.shift).tolist()
+
+
+@pytest.mark.parametrize("max_kv,kv", [(50, 60), (100, -3), (1000, 500)])
+def test_lengths_of_a_refused_sequence_stay(max_kv, kv):
+    """Past the bound, negative, and past the page table's row (of 5 pages)."""
+    c = Case([60, 20], [10, 10], seed=50)
+    c.kv = np.array([kv, 20], np.int32)
+    c.batch = c.make(max_kv_len=max_kv)
+    bd.bitdelta_check_error()
+    c.call()
+    assert bd.bitdelta_check_error() == 7
+    assert lengths_of(c) == ([kv, 10], [0, 10])
+    assert bd.bitdelta_check_error() == 7
+    own, shift = torch.from_numpy(c.kv).cuda(), torch.from_numpy(c.shift).cuda()
+    batch = bd.AttentionBatch(torch.arange(3, dtype=torch.int32, device="cuda"), own,
+                              torch.from_numpy(c.table).cuda(), 2, 1, max_kv, 2, 2, 64, 16)
+    bd.bitdelta_kv_evict_lengths(batch, torch.from_numpy(c.keep).cuda(), own, shift)   # in place
+    assert own.tolist() == [kv, 10] and (shift.cpu().numpy() - c.shift).tolist() == [0, 10]
+    assert bd.bitdelta_check_error() == 7
+
+
+@pytest.mark.parametrize("where", [0, 3, 6])
+def test_lengths_of_a_sequence_with_a_bad_page_stay(where):
+    """The eviction left it alone; once its table is right, it is cut like any other."""
+    c, good = (Case([100, 100], [40, 40], seed=51) for _ in range(2))
+    page, c.table[0, where] = c.table[0, where], c.n_pages
+    c.batch = c.make()
+    c.call()
+    assert bd.bitdelta_check_error() == 7
+    assert lengths_of(c) == ([100, 40], [0, 60])
+    assert bd.bitdelta_check_error() == 7
+    want = good.want(False)
+    c.table[0, where], c.keep[1] = page, -1
+    c.batch = c.make()
+    c.call()
+    assert lengths_of(c) == ([40, 100], [60, 0])
+    assert bd.bitdelta_check_error() == 0
+    for got, t in zip((c.k, c.v, c.w, c.pos), want):
+        assert torch.equal(got.cpu(), t)
+
+
+def test_lengths_with_a_bad_page_that_is_not_chosen_from():
+    """In a shared prefix, behind the last key, or of a sequence that is not cut: none of
+    them stops the eviction or the lengths."""
+    c = Case([100, 90, 70], [64, 80, 70], groups=[(2, 32)], seed=52)
+    c.table[0, 1] = -1
+    c.table[1, 6] = c.n_pages
+    c.table[2, 2] = -1
+    c.batch = c.make()
+    c.call()
+    assert lengths_of(c) == ([64, 80, 70], [36, 10, 0])
+    assert bd.bitdelta_check_error() == 0
+
+
+def test_lengths_of_many_sequences_and_groups():
+    n = 700
+    rng = np.random.default_rng(53)
+    kv = rng.integers(64, 400, n)
+    keep = rng.integers(-1, 300, n)
+    c = Case(kv, keep, hkv=1, groups=[(2, 16 * (1 + i % 4)) for i in range(300)], seed=53)
+    c.call()
+    want = [c.length(s) for s in range(n)]
+    assert lengths_of(c) == (want, [int(k) - w for k, w in zip(kv, want)])
+    assert bd.bitdelta_check_error() == 0
