@@ -433,3 +433,44 @@ def test_refusals():
     for scale in (0.0, -1.0, NAN, INF):
         with pytest.raises(bd.BitDeltaError):
             bd.bitdelta_kv_weigh(c.batch, *args, scale=scale)
+
+
+@pytest.mark.parametrize("grouped", [False, True])
+def test_prompts_with_many_runs_between_them(grouped):
+    """What a role waits for another does not grow by the runs without tiles between two that
+    have some: all waits end within 5 ms, with 40000 single tokens of one key each there."""
+    n, g, dim, page, q = 40000, 8, 64, 16, 2000
+    lens = np.array([q] + [1] * n + [q])
+    need = -(-lens // page)
+    first = np.concatenate([[0], np.cumsum(need)])
+    table = (first[:-1, None] + np.minimum(np.arange(need.max()), need[:, None] - 1)).astype(np.int32)
+    off = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    i32 = lambda a: torch.from_numpy(np.asarray(a, np.int32)).cuda()
+    kw = {}
+    if grouped:                            # pairs that share nothing
+        kw = {"group_offsets": i32(np.arange(0, n + 3, 2)), "prefix_len": i32([0] * (n // 2 + 1))}
+    batch = bd.AttentionBatch(i32(off), i32(lens), i32(table), int(off[-1]), q, q, g, 1, dim, page, **kw)
+    gen = torch.Generator(device="cuda").manual_seed(36)
+    rn = lambda *s: torch.randn(s, generator=gen, device="cuda").to(torch.bfloat16)
+    qs, kp = rn(int(off[-1]), g, dim), rn(int(first[-1]), 1, page, dim)
+    _, lse = bd.bitdelta_attention(batch, qs, kp, kp)
+    weights = torch.zeros((int(first[-1]), 1, page), device="cuda")
+    positions = torch.full(weights.shape, -1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    bd.bitdelta_set_wait_limit_ns(5_000_000)
+    try:
+        bd.bitdelta_kv_weigh(batch, qs, lse, kp, weights, positions)
+        assert bd.bitdelta_check_error() == 0
+    finally:
+        bd.bitdelta_set_wait_limit_ns(2_000_000_000)
+    # every row's weights sum to one, within lse's own error, 2^-16·(1 + |lse|) at most with
+    # |lse| below 10, and a score's, 2^-19 of less than 16
+    w, pages = weights.view(-1).double(), int(need[0]) * page
+    for part in (w[:pages], w[-pages:]):
+        assert abs(part.sum().item() - q * g) <= q * g * 2.0 ** -12
+    single = w[pages:-pages].view(n, page)
+    assert ((single[:, 0] - g).abs() <= g * 2.0 ** -12).all() and not single[:, 1:].any()
+    pos = positions.view(-1)
+    for part in (pos[:pages], pos[-pages:]):
+        assert torch.equal(part[:q], torch.arange(q, device="cuda", dtype=torch.int32))
+    assert (pos[pages:-pages].view(n, page)[:, 0] == 0).all()
