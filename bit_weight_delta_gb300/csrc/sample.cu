@@ -344,13 +344,13 @@ __device__ void sum_list(Shared& sh, int n_list, uint32_t& all, uint64_t& all_ma
   __syncwarp();
 }
 
-// Sums over a warp's lanes; each w below 2^58.
+// Sums over a warp's lanes, in pieces of 25, 25 and 14 bits (32 of each fit 32 bits).  Any w
+// will do whose sum over the lanes fits 64: a row's is below 2^63.
 __device__ __forceinline__ void warp_sums(uint32_t& n, uint64_t& w) {
   n = __reduce_add_sync(0xFFFFFFFFu, n);
   const uint32_t a = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(w) & 0x1FFFFFFu);
   const uint32_t b = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(w >> 25) & 0x1FFFFFFu);
-  const uint64_t hi = w >> 50;  // at most 2^14 a lane
-  const uint32_t c = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(hi));
+  const uint32_t c = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(w >> 50));
   w = a + (static_cast<uint64_t>(b) << 25) + (static_cast<uint64_t>(c) << 50);
 }
 

@@ -344,3 +344,10 @@ def test_refused_settings():
             bd.bitdelta_sample(x, u, **{name: v.cuda()})
     with pytest.raises(bd.BitDeltaError):
         bd.bitdelta_sample(torch.zeros((1, 524033), dtype=torch.bfloat16, device="cuda"), u[:1])
+
+
+@pytest.mark.parametrize("value", [0.0, 1.5, -1.5, 2.0 ** 20, -2.0 ** 20])
+def test_one_value_over_the_largest_vocabulary(value):
+    """The largest sum that a row can have, 524032 weights of 2^44 in one bin."""
+    x = torch.full((4, 524032), value, dtype=torch.bfloat16, device="cuda")
+    check(x, rand_u(4, 60), k=[0, 0, 400001, 1000], p=[1.0, 0.3, 0.7, 0.5], m=[0.0, 0.5, 1.0, 0.0])
