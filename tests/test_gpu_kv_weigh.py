@@ -474,3 +474,32 @@ def test_prompts_with_many_runs_between_them(grouped):
     for part in (pos[:pages], pos[-pages:]):
         assert torch.equal(part[:q], torch.arange(q, device="cuda", dtype=torch.int32))
     assert (pos[pages:-pages].view(n, page)[:, 0] == 0).all()
+
+
+@pytest.mark.parametrize("at", [[0, 5, 639, 640, 641, 1279, 1280, 1499], [700], [1499], [3, 4]])
+@pytest.mark.parametrize("window", [0, 20])
+def test_prompts_spread_among_many_single_tokens(at, window):
+    """More runs than a CTA of the tile kernel has threads, and than one of the short runs'."""
+    rng = np.random.default_rng(33)
+    lens = [(1, int(k)) for k in rng.integers(1, 60, 1500)]
+    for i in at:
+        lens[i] = (17 + i % 40, 60 + i % 300)
+    Case(lens, hq=4, hkv=1, dim=64, window=window, seed=33).check()
+
+
+@pytest.mark.parametrize("members,groups", [(3, 250), (2, 400), (5, 1)])
+def test_groups_behind_many_sequences(members, groups):
+    rng = np.random.default_rng(34)
+    lens = [(1, int(k)) for k in rng.integers(65, 120, members * groups)]
+    lens += [(1, int(k)) for k in rng.integers(1, 50, 900)]
+    lens[-1], lens[-400] = (30, 70), (9, 300)
+    Case(lens, hq=8, hkv=1, dim=64, seed=34,
+         groups=[(members, 16 * (1 + g % 4)) for g in range(groups)]).check()
+
+
+@pytest.mark.parametrize("lens,groups", [([(1, 100), (4, 60), (40, 130), (1, 7)], ()),
+                                         ([(1, 70), (2, 90), (1, 101), (20, 80)], [(3, 64)])])
+def test_each_further_call_adds_as_much(lens, groups):
+    c = Case(lens, groups=groups, window=0, seed=35)
+    for _ in range(3):
+        c.check()
