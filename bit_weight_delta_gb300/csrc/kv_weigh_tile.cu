@@ -94,7 +94,7 @@ struct Cfg {
   static constexpr int kOffOnes = kOffLse + kLseStages * kLseBytes;
   static constexpr int kOffRows = kOffOnes + kLseBytes;
   static constexpr int kOffItem = kOffRows + kLseStages * static_cast<int>(sizeof(Rows));
-  static constexpr int kOffSum = kOffItem + 4 * 64;  // items
+  static constexpr int kOffSum = kOffItem + 4 * 48;  // items
   static constexpr int kOffBar = kOffSum + kSumStages * kWeighBlockKeys * 4;
   // k_full, k_empty, k_ready[2], s_full[], s_empty[], lse_full[], lse_empty[], q_full[],
   // q_empty[], item_full[], item_empty[], sum_full[],
@@ -175,17 +175,14 @@ __device__ __forceinline__ TileRun run_of_lane(TileRun t, int src) {
 // Tiles [j0, j1) of a block, as the roles read it from shared memory; h < 0 ends the
 // work.
 struct Item {
-  int h, i;
+  int h;
   int key0;       // the block's first slot
   int first;      // token of tile 0
   int j0, j1, n;  // n: tiles of the block
-  int run, seq;
-  int k1, tok1;   // the run's
-  int causal, fresh;
+  int seq, k1, tok1, causal, fresh;  // the run's
   int s1;         // a group's end, 0 for a sequence
-  int pad[2];
 };
-static_assert(sizeof(Item) == 64, "four 16-byte words");
+static_assert(sizeof(Item) == 48, "as the ring's place in shared memory has it");
 constexpr int kItemStages = 4;
 constexpr int kItemReaders = kSumWarps + 3;  // the MMA issuers and the loader of lse
 
@@ -239,13 +236,11 @@ struct Walk {
     it.h = -1;
     if (left <= 0 || (h == p.b.n_kv_heads && !next_run(p, tok))) return;
     it.h = h;
-    it.i = i;
     it.key0 = t.x.k0 + kWeighBlockKeys * i;
     it.first = t.first_token(i);
     it.n = t.tiles(i, tok);
     it.j0 = j;
     it.j1 = left < it.n - j ? j + static_cast<int>(left) : it.n;
-    it.run = run;
     it.seq = t.x.seq;
     it.k1 = t.x.k1;
     it.tok1 = t.x.tok1;
@@ -275,8 +270,8 @@ struct Items {
     it = slots[at];
     // (a value from lane 0 is known to be the same in all lanes: what it decides stays
     // in uniform registers, which the tensor instructions take)
-    for (int* f : {&it.h, &it.i, &it.key0, &it.first, &it.j0, &it.j1, &it.n, &it.run, &it.seq,
-                   &it.k1, &it.tok1, &it.causal, &it.fresh, &it.s1})
+    for (int* f : {&it.h, &it.key0, &it.first, &it.j0, &it.j1, &it.n, &it.seq, &it.k1, &it.tok1,
+                   &it.causal, &it.fresh, &it.s1})
       *f = __shfl_sync(0xFFFFFFFFu, *f, 0);
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[at]);
@@ -461,9 +456,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     int ls = 0;
     Unit unit;  // the tile's first
     bool started = false;  // an item before this one
-    // Sums over a tile's later 64 rows, for the warps of the first ones.  With three
-    // buffers of products a warp is at most three tiles, and items, ahead of another:
-    // four of these need no wait to be written.
+    // Sums over a tile's later 64 rows, for the warps of the first ones.  Four of these need
+    // no wait to be written: an item's keys arrive when all warps have staged those of the
+    // one before it, which they do at the end of the item before that one at the earliest.
+    // So a warp that sums item n has all others behind the end of item n − 3.  (The products'
+    // buffers alone would not bound it: the warps of a half without keys wait for none.)
     float* others = reinterpret_cast<float*>(smem + C::kOffSum);
     int ss = 0;
     uint32_t sum_phase = 0;
