@@ -83,7 +83,7 @@ __device__ __forceinline__ WeighRun weigh_run(const WeighArgs& p, int r, bool* b
     const int prefix = b.n_group > 0 ? weigh_prefix(b, r) : 0;
     if (lo < 0 || hi < lo || hi > b.n_tokens || hi - lo > b.max_q_len || kv < 0 ||
         kv > b.max_kv_len || kv > b.table_stride * b.page_size ||
-        (prefix > 0 && kv - (hi - lo) < prefix)) {
+        (prefix > 0 && hi > lo && kv - (hi - lo) < prefix)) {
       *bad = true;
       return x;
     }

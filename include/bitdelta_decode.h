@@ -90,7 +90,8 @@ bd_status bitdelta_kv_append_at(const bd_attention_batch* batch, const int32_t* 
  *                (0.6 MB) on a 256-byte boundary.  Calls that can overlap on the
  *                GPU need workspaces of their own.
  * A batch whose tables break its bounds, or a group with a prefix_len that is
- * not a multiple of page_size or reaches into a member's query tokens, sets
+ * not a multiple of page_size or reaches into a member's query tokens (a member
+ * without any may have fewer keys), sets
  * BD_ERR_DEVICE_BOUNDS and changes nothing; a page outside [0, n_pages) sets it and
  * is skipped.  Two sequences that share a page outside of a group are not
  * supported (the page would have two writers).

@@ -503,3 +503,20 @@ def test_each_further_call_adds_as_much(lens, groups):
     c = Case(lens, groups=groups, window=0, seed=35)
     for _ in range(3):
         c.check()
+
+
+@pytest.mark.parametrize("at", [0, 1, 3])
+@pytest.mark.parametrize("kv", [0, 5, 64])
+@pytest.mark.parametrize("q", [1, 30])
+def test_a_member_of_a_group_without_tokens(at, kv, q):
+    """A server's empty place in a group: a prefix longer than its keys reaches into no query
+    tokens of its own, and the others' weights are what they are without it."""
+    lens = [(1, 70), (q, 110), (2, 90), (1, 65)]
+    lens[at] = (0, 64)
+    c = Case(lens + [(1, 40)], groups=[(4, 64)], seed=37)
+    c.kv[at], c.lens[at] = kv, (0, kv)
+    c.batch = c.make()
+    vp = torch.nan_to_num(c.kp)
+    bd.bitdelta_attention(c.batch, c.q, c.kp, vp)
+    assert bd.bitdelta_check_error() == 0
+    c.check()
