@@ -865,8 +865,8 @@ def bitdelta_kv_evict(batch: AttentionBatch, keep, k_pages, v_pages, weights, po
 def bitdelta_kv_evict_lengths(batch: AttentionBatch, keep, kv_len, pos_offset, stream=None):
     """The lengths after bitdelta_kv_evict: kv_len (int32 [n_seq], the batch's own tensor
     or another) gets the new ones, pos_offset grows by what was dropped.  A sequence that the
-    eviction refused keeps both.  Call batch.plan() before the next attention.  Returns
-    (kv_len, pos_offset)."""
+    eviction by the same batch and keep refused keeps both.  Call batch.plan() before the
+    next attention.  Returns (kv_len, pos_offset)."""
     if stream is not None:
         with _on(stream, kv_len.device):
             return bitdelta_kv_evict_lengths(batch, keep, kv_len, pos_offset)

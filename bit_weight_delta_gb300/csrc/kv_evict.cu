@@ -529,7 +529,9 @@ __global__ void __launch_bounds__(T, 1024 / T) kv_evict_kernel(const EvictArgs p
 
 constexpr int kLengthThreads = 128;
 
-// A CTA per sequence.
+// A CTA per sequence, as the page-table row of one that is cut has to be read (a thread per
+// sequence without that took 2.3 us for 64 sequences, this 2.4; one of 131071 keys in pages
+// of 16 takes 4.8).
 __global__ void __launch_bounds__(kLengthThreads)
     evict_lengths_kernel(const bd_attention_batch b, const int32_t* keep, int32_t* kv_len_out,
                          int32_t* pos_offset, DevCtx ctx) {

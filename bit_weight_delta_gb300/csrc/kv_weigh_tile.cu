@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                      k > 0 ? 1u : 0u);
             // (last: −lse/scale is the largest of the terms, and where it comes first all
             // later sums are rounded at its size: the weights of a prompt of 2048 were off by
-            // 1.4e-6 of the largest, now by 2.3e-7)
+            // 1.4e-6 of the largest, now by 2.4e-7)
             mma_ss(t_s, ones, ld, idesc, 1u);
             mma_commit(&s_full[u.bar()]);
             mma_commit(&q_empty[qs]);
